@@ -282,7 +282,8 @@ float* llm_logits_buffer(llm_handle* h);
 int32_t llm_filled(const llm_handle* h, int32_t b);
 
 /* A message for the last failure on h (owned by h; valid until the next call); with h == NULL,
- * why the last llm_create on the calling thread failed.  And a name for a status code. */
+ * why the last llm_create, llm_qcache_* or llm_verify on the calling thread failed.  And a name
+ * for a status code. */
 const char* llm_last_error(const llm_handle* h);
 const char* llm_status_string(llm_status s);
 
@@ -363,6 +364,108 @@ llm_status llm_step_kernels(llm_handle* h, int32_t B, float temp, int32_t k, int
 #define LLM_SAMPLE_NOALLOC_MAX_ELEMS 262144
 llm_status llm_sample_noalloc(const float* logits_dev, int32_t B, int32_t V, float temp, int32_t k,
                               float p, const float* u_dev, int32_t* ids_dev, void* cuda_stream);
+
+/*
+ * 8-bit key/value caches without a handle.  The pages have no counterpart; a cache in half the
+ * bytes of a bf16 one is an addition of this library.
+ *
+ * A cache holds e4m3 codes (one byte: sign, 4 exponent bits of bias 7, 3 mantissa bits; largest 448)
+ * and one f32 scale for each block of LLM_QCACHE_BLOCK positions of a cache row and key/value head,
+ * keys and values apart.  Scales are powers of two; a value is its code's value times its block's
+ * scale.  The memory is the caller's: device memory of the current device, zeroed before its first
+ * use.  Codes are [rows][kv_heads][max_seq][head], 16-byte aligned; scales
+ * [rows][kv_heads][max_seq / LLM_QCACHE_BLOCK].  max_seq is a multiple of LLM_QCACHE_BLOCK (of 64
+ * with page tables), head 16, 32, 64, 128 or 256, rows x kv_heads x max_seq < 2^31, else
+ * LLM_ERR_CONFIG.
+ *
+ * The calls below share these arguments:
+ *   B, S          rows of the call, and tokens per row at most; buffers of tokens are [B][S] rows of
+ *                 `stride` elements (at least the row's width; pointers and strides are multiples of
+ *                 16 bytes), of type dtype (LLM_DTYPE_F32 or LLM_DTYPE_BF16).
+ *   count_dev     [B] tokens that row b really has, 0..S (NULL: S); the others are neither read nor
+ *                 written.
+ *   table_dev     [B][pages_per_row] pages as for llm_decode_paged, over a pool of rows * (max_seq / 64)
+ *                 pages (NULL: row b of the call is cache row b, and B <= rows).  Rows may share pages
+ *                 that none of them writes.
+ *   status_dev    one int32 (may be NULL): where a position, length or count is out of range, or a
+ *                 page outside the pool, the first such error is stored there if it holds 0
+ *                 (LLM_ERR_POS_RANGE, LLM_ERR_ARG), and a wait that gave up (LLM_ERR_DEVICE_TIMEOUT).
+ *                 Nothing out of range is read or written: a write or read skips the row (the block,
+ *                 for a page), an attention treats the row as empty (the page's positions as unseen).
+ *   cuda_stream   the stream the work is ordered on (NULL: the legacy default stream).  The calls
+ *                 return without waiting, allocate nothing and may be captured into a graph.
+ * B < 1 (or B > rows without a table) is LLM_ERR_BATCH; other bad arguments are LLM_ERR_ARG, and
+ * llm_last_error(NULL) says which.
+ */
+#define LLM_QCACHE_BLOCK 16
+typedef struct llm_qcache {
+  void* k;          /* codes of the keys   */
+  void* v;          /* codes of the values */
+  float* k_scale;
+  float* v_scale;
+  int32_t rows, kv_heads, max_seq, head;
+} llm_qcache;
+
+/*
+ * Write keys and values (rows of kv_heads * head elements) at positions pos_dev[b] .. + count - 1 of
+ * row b.  In each block that the tokens touch, need is the least power of two >= 2^-126 with
+ * max |x| / need <= 448 over the new values; the block's scale becomes need where its first position
+ * is written, else max(scale, need), the codes of its positions before pos_dev[b] being rounded again
+ * when it grows; new codes are x / scale to nearest even.  So writing at a position ends what the
+ * block held after the new tokens (their codes stay, their scale may not).  A value that is not
+ * finite makes its block's scale NaN: all of it reads as NaN until its first position is written anew.
+ * Two rows of one call must not write the same block.
+ */
+llm_status llm_qcache_write(const llm_qcache* cache, const void* k_dev, const void* v_dev, int32_t dtype,
+                            int64_t stride, int32_t B, int32_t S, const int32_t* pos_dev,
+                            const int32_t* count_dev, const int32_t* table_dev, int32_t pages_per_row,
+                            int32_t* status_dev, void* cuda_stream);
+
+/* Read back the values at positions pos_dev[b] .. + count - 1 of row b (exact in both types, but for
+ * bf16 values below 2^-126). */
+llm_status llm_qcache_read(const llm_qcache* cache, int32_t B, int32_t S, const int32_t* pos_dev,
+                           const int32_t* count_dev, const int32_t* table_dev, int32_t pages_per_row,
+                           void* k_dev, void* v_dev, int32_t dtype, int64_t stride, int32_t* status_dev,
+                           void* cuda_stream);
+
+/*
+ * Grouped-query attention over the cache: query head j*group + n of token i of row b attends, with
+ * key/value head j, to positions 0 .. length_dev[b] - count + i of the row (its own tokens are the
+ * last `count` of the length, so a token sees those before it and itself):
+ *   out = sum softmax(scale * q . k) v,  statistics and sums in f32; a token that sees nothing gets 0.
+ * q and out are rows of kv_heads * group * head elements at q_stride and out_stride, both of type
+ * dtype; they must not overlap.  group is 1..16 with group * head <= 1024 (else LLM_ERR_CONFIG).
+ * workspace_dev: at least llm_qcache_workspace bytes for the same cache, group, B and S (16-byte
+ * aligned; may be NULL where that is 0), all zero before its first use; every call leaves it ready
+ * for the next.  Calls that overlap on the GPU, captured graphs among them, need workspaces of their
+ * own; after LLM_ERR_DEVICE_TIMEOUT, zero it again.
+ */
+llm_status llm_qcache_workspace(const llm_qcache* cache, int32_t group, int32_t B, int32_t S, uint64_t* bytes);
+llm_status llm_qcache_attend(const llm_qcache* cache, const void* q_dev, int32_t dtype, int64_t q_stride,
+                             int32_t group, int32_t B, int32_t S, const int32_t* length_dev,
+                             const int32_t* count_dev, const int32_t* table_dev, int32_t pages_per_row,
+                             float scale, void* out_dev, int64_t out_stride, void* workspace_dev,
+                             uint64_t workspace_bytes, int32_t* status_dev, void* cuda_stream);
+
+/*
+ * Verify drafted tokens, without a handle (speculative sampling: the tokens that come out are
+ * distributed as if the target model had drawn them one by one).  Row b has n = count_dev[b] drafts
+ * (NULL: S; clamped to 0..S) drafts_dev [B][S], the target's probabilities p_dev [B][S + 1][V] (row
+ * i: after the first i drafts), the draft model's q_dev [B][S][V] or NULL (deterministic drafts:
+ * q_i(x_i) = 1), and draws u_dev [B][S + 1] in [0, 1).  Draft i is kept while
+ * u[i] * q_i(x_i) < p_i(x_i) (an exact comparison; an id outside 0..V-1 is never kept).  After the r
+ * kept drafts one token is drawn with u[S] from the weights max(p_r - q_r, 0) if r < n (without q:
+ * p_r without x_r), else p_n: with w in whole multiples of 2^-61 (p - q is one f32 subtraction; NaN,
+ * negative and smaller values weigh 0, values above 1 weigh 1) and total their sum, the first id whose
+ * running sum is above floor(floor(u * 2^24) * total / 2^24).  If the difference leaves no weight, p_r
+ * is drawn from instead; if that has none either, the id is 0.  ids_dev [B][S + 1] receives the kept
+ * drafts, the drawn token and then -1; accepted_dev [B] receives r.  Rows of p and q sum to about 1
+ * (for rows that sum to 8 or more the drawn id is in range but unspecified).  Device memory of the
+ * current device; ordered on cuda_stream, returns without waiting, allocates nothing.
+ */
+llm_status llm_verify(const float* p_dev, const float* q_dev, const int32_t* drafts_dev,
+                      const int32_t* count_dev, int32_t B, int32_t S, int32_t V, const float* u_dev,
+                      int32_t* ids_dev, int32_t* accepted_dev, void* cuda_stream);
 
 #ifdef __cplusplus
 }

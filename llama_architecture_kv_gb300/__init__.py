@@ -25,7 +25,8 @@ EXPORTS = ("llm_weight_count", "llm_create", "llm_destroy", "llm_reset", "llm_pr
            "llm_step_kernels", "llm_decode_rows", "llm_decode_rows_dev", "llm_step_rows",
            "llm_step_rows_dev", "llm_generate", "llm_generate_dev", "llm_decode_paged",
            "llm_decode_paged_dev", "llm_step_paged", "llm_step_paged_dev", "llm_check_wait_timeout",
-           "llm_prefill_packed")
+           "llm_prefill_packed", "llm_qcache_write", "llm_qcache_read", "llm_qcache_workspace",
+           "llm_qcache_attend", "llm_verify")
 
 
 class LlmConfig(ctypes.Structure):
@@ -40,6 +41,12 @@ class LlmConfig(ctypes.Structure):
                 ("max_tokens", ctypes.c_int32), ("step_kernel", ctypes.c_int32)]
 
 
+class LlmQcache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("rows", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("max_seq", ctypes.c_int32), ("head", ctypes.c_int32)]
+
+
 class LlmError(RuntimeError):
     def __init__(self, status, msg):
         super().__init__(f"{msg} (status {status})")
@@ -49,6 +56,7 @@ class LlmError(RuntimeError):
 # argument and result types of every entry point (ctypes)
 _i32, _i64, _u64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float, ctypes.c_void_p
 _pcfg = ctypes.POINTER(LlmConfig)
+_pqc = ctypes.POINTER(LlmQcache)
 SIGNATURES = {
     "llm_weight_count": ([_pcfg], _u64),
     "llm_create": ([_pcfg, _vp, _u64, _i32, _vp, ctypes.POINTER(_vp)], _i32),
@@ -86,6 +94,12 @@ SIGNATURES = {
     "llm_sample_noalloc": ([_vp, _i32, _i32, _f32, _i32, _f32, _vp, _vp, _vp], _i32),
     "llm_step_kernels": ([_vp, _i32, _f32, _i32, ctypes.POINTER(_i32)], _i32),
     "llm_check_wait_timeout": ([_vp, _i64], _i32),
+    "llm_qcache_write": ([_pqc, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp], _i32),
+    "llm_qcache_read": ([_pqc, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i64, _vp, _vp], _i32),
+    "llm_qcache_workspace": ([_pqc, _i32, _i32, _i32, ctypes.POINTER(_u64)], _i32),
+    "llm_qcache_attend": ([_pqc, _vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _f32, _vp, _i64, _vp, _u64,
+                           _vp, _vp], _i32),
+    "llm_verify": ([_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp], _i32),
     }
 
 _lib = None
@@ -306,6 +320,167 @@ def llm_sample_noalloc(logits, B, V, temp, k, p, u, ids, stream=None):
     st = lib().llm_sample_noalloc(_ptr(logits), B, V, temp, k, p, _ptr(u), _ptr(ids), stream)
     if st != LLM_OK:
         raise LlmError(st, f"llm_sample_noalloc: {lib().llm_status_string(st).decode()}")
+
+
+# ---- operators on torch CUDA tensors, without a handle (include/llm.h) --------------------
+# Shapes, types, contiguity and the device are checked here; the library checks the rest.
+
+def _refused(name, st):
+    why = lib().llm_last_error(None)
+    raise LlmError(st, f"{name}: {lib().llm_status_string(st).decode()}: {why.decode() if why else ''}")
+
+
+def _need(ok, what):
+    if not ok:
+        raise LlmError(LLM_ERR_ARG, what)
+
+
+def _int32(t, name, device, shape):
+    """The address of an int32 tensor of the given shape (None: 0)."""
+    if t is None:
+        return None
+    _need(str(t.dtype) == "torch.int32" and t.device == device and t.is_contiguous() and tuple(t.shape) == shape,
+          f"{name} must be a contiguous int32 tensor {shape} on {device}")
+    return t.data_ptr()
+
+
+def _here(device):
+    """Launches go to the current device, which has to be the tensors' own."""
+    import torch
+    _need(device.type == "cuda" and device.index == torch.cuda.current_device(),
+          f"tensors on {device} while the current CUDA device is another")
+
+
+def _rows(t, name, device, dtype, shape):
+    """Token rows [B, S, heads, head] (or [B, S, heads * head]) of one type: the address and the
+    distance between tokens in elements; rows of a wider tensor may be given as a slice."""
+    import torch
+    B, S, width = shape
+    heads = t.dim() == 4
+    _need(t.dim() in (3, 4) and t.device == device and t.dtype in (torch.float32, torch.bfloat16)
+          and (dtype is None or t.dtype == dtype), f"{name} must be f32 or bf16 rows on {device}, all of one type")
+    _need(t.shape[0] == B and t.shape[1] == S and t.numel() == B * S * width,
+          f"{name} must hold {B} x {S} rows of {width} elements, not {tuple(t.shape)}")
+    st = t.stride()
+    _need(st[-1] == 1 and (not heads or st[2] == t.shape[3] or t.shape[2] == 1),
+          f"{name}: the elements of a row must be contiguous")
+    # (the stride of a dimension of size 1 carries no meaning)
+    step = st[1] if S > 1 else st[0] if B > 1 else width
+    _need(B == 1 or S == 1 or st[0] == S * step, f"{name}: rows must be evenly spaced")
+    return t.data_ptr(), step
+
+
+def _bf16(t):
+    return LLM_DTYPE_BF16 if t.element_size() == 2 else LLM_DTYPE_F32
+
+
+class QCache:
+    """An 8-bit key/value cache over torch tensors: codes k, v [rows, kv_heads, max_seq, head]
+    (uint8 or float8_e4m3fn) and scales [rows, kv_heads, max_seq // 16] (float32), all zeroed before
+    their first use.  The tensors stay the caller's; calls are ordered on `stream` (a cudaStream_t,
+    None: the legacy default stream) and return without waiting.  `pos`, `length`, `count` [B] and
+    `table` [B, pages] are int32 CUDA tensors, `status` one int32."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        for t, name in ((k, "k"), (v, "v")):
+            _need(t.dim() == 4 and str(t.dtype) in ("torch.uint8", "torch.float8_e4m3fn") and t.is_contiguous()
+                  and t.device == k.device and t.shape == k.shape,
+                  f"{name} must be contiguous codes [rows, kv_heads, max_seq, head] (uint8 or float8_e4m3fn)")
+        rows, kv, cap, hd = k.shape
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _need(tuple(t.shape) == (rows, kv, cap // 16) and str(t.dtype) == "torch.float32" and t.is_contiguous()
+                  and t.device == k.device, f"{name} must be contiguous float32 [rows, kv_heads, max_seq // 16]")
+        _need(k.is_cuda, "a cache lies in CUDA memory")
+        self.tensors = (k, v, k_scale, v_scale)  # kept alive with the addresses below
+        self.device, self.kv, self.hd = k.device, kv, hd
+        self.c = LlmQcache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), rows, kv, cap, hd)
+        self._c = ctypes.byref(self.c)
+
+    @classmethod
+    def empty(cls, rows, kv_heads, max_seq, head, device="cuda"):
+        """A zeroed cache in new tensors."""
+        import torch
+        code = lambda: torch.zeros(rows, kv_heads, max_seq, head, dtype=torch.uint8, device=device)  # noqa: E731
+        scale = lambda: torch.zeros(rows, kv_heads, max_seq // 16, device=device)  # noqa: E731
+        return cls(code(), code(), scale(), scale())
+
+    def _call_rows(self, B, S, first, name, count, table, status):
+        _here(self.device)
+        _need(first is not None, f"{name} is missing")
+        return (_int32(first, name, self.device, (B,)), _int32(count, "count", self.device, (B,)),
+                _int32(table, "table", self.device, (B, table.shape[1]) if table is not None and table.dim() == 2 else ()),
+                0 if table is None else table.shape[1],
+                None if status is None else _int32(status, "status", self.device, tuple(status.shape)[:1] if status.numel() == 1 else ()))
+
+    def write(self, k, v, pos, count=None, table=None, status=None, stream=None):
+        """Keys and values [B, S, kv_heads, head] at positions pos[b] + i of row b (llm_qcache_write)."""
+        B, S = k.shape[0], k.shape[1]
+        first, count, table, pages, status = self._call_rows(B, S, pos, "pos", count, table, status)
+        kp, step = _rows(k, "k", self.device, None, (B, S, self.kv * self.hd))
+        vp, vstep = _rows(v, "v", self.device, k.dtype, (B, S, self.kv * self.hd))
+        _need(step == vstep, "k and v must have the same row stride")
+        st = lib().llm_qcache_write(self._c, kp, vp, _bf16(k), step, B, S, first, count, table, pages, status, stream)
+        if st != LLM_OK:
+            _refused("llm_qcache_write", st)
+
+    def read(self, pos, k, v, count=None, table=None, status=None, stream=None):
+        """Positions pos[b] + i of row b into k and v [B, S, kv_heads, head] (llm_qcache_read)."""
+        B, S = k.shape[0], k.shape[1]
+        first, count, table, pages, status = self._call_rows(B, S, pos, "pos", count, table, status)
+        kp, step = _rows(k, "k", self.device, None, (B, S, self.kv * self.hd))
+        vp, vstep = _rows(v, "v", self.device, k.dtype, (B, S, self.kv * self.hd))
+        _need(step == vstep, "k and v must have the same row stride")
+        st = lib().llm_qcache_read(self._c, B, S, first, count, table, pages, kp, vp, _bf16(k), step, status, stream)
+        if st != LLM_OK:
+            _refused("llm_qcache_read", st)
+
+    def workspace(self, group, B, S):
+        """A zeroed workspace for attend() with this group, rows and tokens per row."""
+        import torch
+        _here(self.device)
+        n = ctypes.c_uint64()
+        st = lib().llm_qcache_workspace(self._c, group, B, S, ctypes.byref(n))
+        if st != LLM_OK:
+            _refused("llm_qcache_workspace", st)
+        return torch.zeros(max(16, n.value), dtype=torch.uint8, device=self.device)
+
+    def attend(self, q, length, out, workspace, count=None, table=None, scale=None, status=None, stream=None):
+        """Attention of q [B, S, heads, head] over the first length[b] positions of row b, the tokens
+        themselves being the last of them, into out (llm_qcache_attend); scale defaults to
+        head ** -0.5."""
+        B, S = q.shape[0], q.shape[1]
+        width = q.numel() // (B * S) if B * S else 0
+        group = width // (self.kv * self.hd)
+        _need(group * self.kv * self.hd == width and width > 0, "q must hold a whole number of heads per key/value head")
+        first, count, table, pages, status = self._call_rows(B, S, length, "length", count, table, status)
+        qp, qstep = _rows(q, "q", self.device, None, (B, S, width))
+        op, ostep = _rows(out, "out", self.device, q.dtype, (B, S, width))
+        _need(workspace.device == self.device and workspace.is_contiguous(), "workspace must be contiguous CUDA memory")
+        st = lib().llm_qcache_attend(self._c, qp, _bf16(q), qstep, group, B, S, first, count, table, pages,
+                                     self.hd ** -0.5 if scale is None else scale, op, ostep, workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), status, stream)
+        if st != LLM_OK:
+            _refused("llm_qcache_attend", st)
+
+
+def llm_verify(p, q, drafts, u, ids, accepted, count=None, stream=None):
+    """Verification of drafts [B, S] against the target's probabilities p [B, S + 1, V], the draft
+    model's q [B, S, V] (None: deterministic drafts) and draws u [B, S + 1], into ids [B, S + 1] and
+    accepted [B] (see include/llm.h); CUDA tensors, f32 and int32."""
+    import torch
+    _need(drafts.dim() == 2 and p.dim() == 3, "drafts must be [B, S] and p [B, S + 1, V]")
+    (B, S), V, dev = drafts.shape, p.shape[2], p.device
+    _here(dev)
+    for t, name, shape in ((p, "p", (B, S + 1, V)), (q, "q", (B, S, V)), (u, "u", (B, S + 1))):
+        _need((t is None and name == "q") or (t is not None and tuple(t.shape) == shape and t.dtype == torch.float32
+                                              and t.is_contiguous() and t.device == dev),
+              f"{name} must be a contiguous float32 tensor {shape} on {dev}")
+    _need(ids is not None and accepted is not None, "ids and accepted are missing")
+    st = lib().llm_verify(p.data_ptr(), None if q is None else q.data_ptr(), _int32(drafts, "drafts", dev, (B, S)),
+                          _int32(count, "count", dev, (B,)), B, S, V, u.data_ptr(), _int32(ids, "ids", dev, (B, S + 1)),
+                          _int32(accepted, "accepted", dev, (B,)), stream)
+    if st != LLM_OK:
+        _refused("llm_verify", st)
 
 
 # ---- a small convenience wrapper --------------------------------------------------------

@@ -331,7 +331,7 @@ struct llm_handle {
 
 namespace {
 
-thread_local std::string g_create_err;  // why the last llm_create on this thread failed
+thread_local std::string g_create_err;  // why the last llm_create (or entry without a handle) on this thread failed
 
 llm_status fail(llm_handle* h, llm_status s, const char* fmt, ...) {
   if (h) {
@@ -900,6 +900,14 @@ llm_status check_row_positions(llm_handle* h, int B, const int32_t* pos) {
 }
 
 }  // namespace
+
+namespace llm {
+// the message of an entry without a handle, for llm_last_error(NULL)
+llm_status fail_thread(llm_status s, const char* why) {
+  g_create_err = why;
+  return s;
+}
+}  // namespace llm
 
 // ---------------------------------------------------------------------------------------
 // C ABI

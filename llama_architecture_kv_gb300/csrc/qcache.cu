@@ -1,0 +1,277 @@
+// Writing into and reading from an 8-bit key/value cache, and its attention on CUDA cores.
+//
+// A block is kQBlock consecutive positions of one cache row and key/value head.  Its scale s is a
+// power of two, so dividing by it, multiplying by it and moving a code from one scale to another
+// are exact in f32 but for the rounding to e4m3 itself (to nearest even, off by at most 2^-4 of the
+// value while |x| / s >= 2^-6, by at most 2^-10 s below).  A float format keeps its relative error
+// over 14 binades below the largest value of the block, so the scale only has to place the largest
+// value near 448 and a power of two loses at most a factor of two of the range.
+//
+// Writing tokens p0 .. p0 + n - 1 of a row, per block that they touch:
+//   need = the least power of two >= 2^-126 with max |x| / need <= 448 over the new values;
+//   s    = need if the call writes the block's first position, else max(s_old, need), and the
+//          codes of the block's positions before p0 are rounded again from s_old to s;
+//   code = e4m3(x / s).
+// Values that are not finite make need NaN (their codes are 0): the block then reads as NaN until
+// its first position is written anew, and no code is ever NaN, so a product over codes stays finite
+// for every token that does not see the block.  Codes of positions after the new tokens are not
+// touched.
+//
+// Bounds: both directions are HBM-bound for long inputs and launch-latency-bound for one token per
+// row.  One warp owns a (block, head, keys or values): its 16 tokens' rows are all loaded at once
+// (16 independent 16-byte loads a lane at hd 128, f32), reduced in registers and stored as codes, so
+// each value is read once and the maximum costs no second pass.
+#include <algorithm>
+#include <type_traits>
+
+#include "qcache.cuh"
+
+namespace llm {
+
+namespace {
+
+constexpr int kQThreads = 128;
+
+// four consecutive elements of a row of type ST (0 f32, 1 bf16) as f32
+template <int ST>
+LLM_D float4 load_quad(const void* p, int64_t i) {
+  if constexpr (ST == 0) {
+    return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+    return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+  }
+}
+
+// One warp: n tokens (1 <= t0 + n <= kQBlock) at positions t0 .. t0 + n - 1 of a block, whose codes
+// start at `codes` and whose scale is *scale; token i's values are the HD elements at src + i * stride
+template <int HD, int ST>
+LLM_D void quantise_run(uint8_t* codes, float* scale, int t0, int n, const void* src, int64_t base, int64_t stride) {
+  constexpr int QR = HD / 4;                  // groups of four values per token
+  constexpr int NQ = kQBlock * QR / 32;       // groups per lane
+  const int lane = threadIdx.x & 31;
+  const int nq = n * QR;
+  const float s_old = t0 > 0 ? *scale : 0.0f;
+  float4 x[NQ];
+  uint32_t top = 0u;                          // largest |x| as bits (ordered; not finite: >= 0x7f800000)
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    const int q = lane + 32 * i;
+    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (q < nq) x[i] = load_quad<ST>(src, base + (int64_t)(q / QR) * stride + (q % QR) * 4);
+  }
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    const uint32_t a = max(__float_as_uint(x[i].x) & 0x7fffffffu, __float_as_uint(x[i].y) & 0x7fffffffu);
+    const uint32_t b = max(__float_as_uint(x[i].z) & 0x7fffffffu, __float_as_uint(x[i].w) & 0x7fffffffu);
+    top = max(top, max(a, b));
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  const bool fine = top < 0x7f800000u && s_old == s_old;
+  float s = fine ? q_scale(__uint_as_float(top)) : __uint_as_float(0x7fc00000u);
+  if (fine && t0 > 0) s = fmaxf(s, s_old);
+  if (fine && s > s_old && t0 > 0) {
+    // the tokens before, from s_old to s: their values times s_old / s < 1 (both powers of two)
+    const float f = s_old * q_recip(s);
+    uint32_t* c4 = reinterpret_cast<uint32_t*>(codes);
+    for (int q = lane; q < t0 * QR; q += 32) {
+      const float4 v = e4m3_quad(c4[q]);
+      c4[q] = e4m3x2(v.x * f, v.y * f) | e4m3x2(v.z * f, v.w * f) << 16;
+    }
+  }
+  const float r = fine ? q_recip(s) : 0.0f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(codes + t0 * HD);
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    const int q = lane + 32 * i;
+    if (q < nq)
+      dst[q] = fine ? e4m3x2(x[i].x * r, x[i].y * r) | e4m3x2(x[i].z * r, x[i].w * r) << 16 : 0u;
+  }
+  __syncwarp();  // every lane has read the old scale
+  if (lane == 0) *scale = s;
+}
+
+// warp w of the grid: (row, touched block, kv head, keys or values), the last the fastest
+template <int HD, int ST>
+__global__ void __launch_bounds__(kQThreads)
+    qcache_write_kernel(const QCacheView c, const QRows r, const void* k, const void* v, int64_t stride, int span) {
+  const int64_t w = (int64_t)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
+  const int side = (int)(w & 1);
+  const int h = (int)((w >> 1) % c.kv);
+  const int64_t bj = (w >> 1) / c.kv;
+  const int b = (int)(bj / span), j = (int)(bj - (int64_t)b * span);
+  if (b >= r.B) return;
+  const int p0 = r.first[b], n = q_count(r, b);
+  if (n == 0) return;
+  if (p0 < 0 || p0 > r.limit - n) {
+    q_report(r.status, kErrPosRange);
+    return;
+  }
+  const int blk = p0 / kQBlock + j;           // the block in the row
+  const int lo = max(p0, blk * kQBlock), hi = min(p0 + n, (blk + 1) * kQBlock);
+  if (lo >= hi) return;
+  int row, pp;
+  if (!q_place(r, c, b, blk * kQBlock, row, pp)) return;
+  const size_t head = (size_t)row * c.kv + h;
+  uint8_t* codes = (side ? c.v : c.k) + (head * c.cap + pp) * HD;
+  float* scale = (side ? c.vs : c.ks) + head * (c.cap / kQBlock) + pp / kQBlock;
+  quantise_run<HD, ST>(codes, scale, lo - blk * kQBlock, hi - lo, side ? v : k,
+                       ((int64_t)b * r.S + (lo - p0)) * stride + (int64_t)h * HD, stride);
+}
+
+// Rows of a handle's step: warp (entry, kv head, keys or values); staged values [B][kv][HD].  A
+// prefill pass lists the entries of a cache row in position order, so the entries of one block
+// follow one another: the first of them (the leader) writes all, run by run of consecutive
+// positions, and the others' warps leave.
+template <int HD, int ST>
+__global__ void __launch_bounds__(kQThreads)
+    qcache_write_step_kernel(const QCacheView c, const QRows r, const void* k, const void* v) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t w = (int64_t)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
+  const int side = (int)(w & 1);
+  const int h = (int)((w >> 1) % c.kv);
+  const int64_t e64 = (w >> 1) / c.kv;
+  if (e64 >= r.B) return;
+  const int e = (int)e64;
+  auto slot = [&](int i, int& row, int& pp) { cache_slot(r.step, c.cap, i, row_pos(r.step, i), row, pp); };
+  int row, pp;
+  slot(e, row, pp);
+  int n = 1;
+  if (r.step->rowmap) {
+    int pr, pq;
+    if (e > 0) {
+      slot(e - 1, pr, pq);
+      if (pr == row && pq / kQBlock == pp / kQBlock) return;
+    }
+    n = 0;
+    while (n < kQBlock && e + n < r.B) {
+      slot(e + n, pr, pq);
+      if (pr != row || pq / kQBlock != pp / kQBlock) break;
+      ++n;
+    }
+  }
+  const size_t head = (size_t)row * c.kv + h;
+  const int blk = pp / kQBlock;
+  uint8_t* codes = (side ? c.v : c.k) + (head * c.cap + (size_t)blk * kQBlock) * HD;
+  float* scale = (side ? c.vs : c.ks) + head * (c.cap / kQBlock) + blk;
+  const int64_t stride = (int64_t)c.kv * HD;
+  for (int i = 0; i < n;) {
+    int r0, q0, len = 1;
+    slot(e + i, r0, q0);
+    while (i + len < n) {
+      int r1, q1;
+      slot(e + i + len, r1, q1);
+      if (q1 != q0 + len) break;
+      ++len;
+    }
+    quantise_run<HD, ST>(codes, scale, q0 - blk * kQBlock, len, side ? v : k, (int64_t)(e + i) * stride + (int64_t)h * HD,
+                         stride);
+    __syncwarp();
+    i += len;
+  }
+}
+
+// thread: 16 consecutive dimensions of one (row, token, kv head), keys and values
+template <int HD, int ST>
+__global__ void __launch_bounds__(256) qcache_read_kernel(const QCacheView c, const QRows r, void* k, void* v, int64_t stride) {
+  constexpr int PR = HD / 16;
+  const int64_t total = (int64_t)r.B * r.S * c.kv * PR;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+    const int e = (int)(i % PR);
+    const int h = (int)(i / PR % c.kv);
+    const int64_t bt = i / PR / c.kv;
+    const int b = (int)(bt / r.S), t = (int)(bt - (int64_t)b * r.S);
+    const int p0 = r.first[b], n = q_count(r, b);
+    if (t >= n) continue;
+    if (p0 < 0 || p0 > r.limit - n) {
+      q_report(r.status, kErrPosRange);
+      continue;
+    }
+    int row, pp;
+    if (!q_place(r, c, b, p0 + t, row, pp)) continue;
+    const size_t head = (size_t)row * c.kv + h;
+    const size_t at = (head * c.cap + pp) * HD + e * 16, sc = head * (c.cap / kQBlock) + pp / kQBlock;
+    const uint4 u[2] = {*reinterpret_cast<const uint4*>(c.k + at), *reinterpret_cast<const uint4*>(c.v + at)};
+    const float s[2] = {c.ks[sc], c.vs[sc]};
+    const int64_t o = bt * stride + (int64_t)h * HD + e * 16;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const uint32_t w[4] = {u[side].x, u[side].y, u[side].z, u[side].w};
+      void* dst = side ? v : k;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float4 f = e4m3_quad(w[q]);
+        f.x *= s[side]; f.y *= s[side]; f.z *= s[side]; f.w *= s[side];
+        if constexpr (ST == 0) {
+          *reinterpret_cast<float4*>(static_cast<float*>(dst) + o + 4 * q) = f;
+        } else {
+          // (codes hold four significant bits: rounding to bf16 changes only values below 2^-126)
+          const uint2 p = make_uint2((uint32_t)f32_to_bf16(f.x) | (uint32_t)f32_to_bf16(f.y) << 16,
+                                     (uint32_t)f32_to_bf16(f.z) | (uint32_t)f32_to_bf16(f.w) << 16);
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dst) + o + 4 * q) = p;
+        }
+      }
+    }
+  }
+}
+
+// calls f with the head size and the element type as compile-time numbers
+template <class F>
+cudaError_t with_shape(int hd, int st, F f) {
+#define LLM_CASE(HD) \
+  case HD: return st ? f(std::integral_constant<int, HD>{}, std::integral_constant<int, 1>{}) \
+                     : f(std::integral_constant<int, HD>{}, std::integral_constant<int, 0>{});
+  switch (hd) {
+    LLM_CASE(16)
+    LLM_CASE(32)
+    LLM_CASE(64)
+    LLM_CASE(128)
+    LLM_CASE(256)
+    default: return cudaErrorInvalidValue;
+  }
+#undef LLM_CASE
+}
+
+}  // namespace
+
+bool qcache_head_supported(int hd) { return hd == 16 || hd == 32 || hd == 64 || hd == 128 || hd == 256; }
+
+cudaError_t launch_qcache_write(const QCacheView& c, const QRows& r, const void* k, const void* v, int st,
+                                int64_t stride, cudaStream_t s) {
+  const int span = (r.S + kQBlock - 2) / kQBlock + 1;  // blocks that S tokens can touch
+  const int64_t warps = (int64_t)r.B * span * c.kv * 2, grid = (warps + kQThreads / 32 - 1) / (kQThreads / 32);
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  return with_shape(c.hd, st, [&](auto hd, auto t) {
+    qcache_write_kernel<hd.value, t.value><<<(unsigned)grid, kQThreads, 0, s>>>(c, r, k, v, stride, span);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_qcache_write_step(const QCacheView& c, const QRows& r, const void* k, const void* v, int st,
+                                     cudaStream_t s, bool pdl) {
+  const int64_t warps = (int64_t)r.B * c.kv * 2, grid = (warps + kQThreads / 32 - 1) / (kQThreads / 32);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kQThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return with_shape(c.hd, st, [&](auto hd, auto t) {
+    return cudaLaunchKernelEx(&cfg, qcache_write_step_kernel<hd.value, t.value>, c, r, k, v);
+  });
+}
+
+cudaError_t launch_qcache_read(const QCacheView& c, const QRows& r, void* k, void* v, int st, int64_t stride,
+                               cudaStream_t s) {
+  const int64_t threads = (int64_t)r.B * r.S * c.kv * (c.hd / 16), grid = std::min<int64_t>((threads + 255) / 256, 1 << 20);
+  return with_shape(c.hd, st, [&](auto hd, auto t) {
+    qcache_read_kernel<hd.value, t.value><<<(unsigned)grid, 256, 0, s>>>(c, r, k, v, stride);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace llm

@@ -1,0 +1,193 @@
+// Verification of drafted tokens against the target model's probabilities (speculative sampling).
+//
+// Row b brings n drafts x_0 .. x_{n-1}, the target's probabilities p_0 .. p_n after each of them,
+// the draft model's q_0 .. q_{n-1} (or none: a deterministic draft, q_i(x_i) = 1) and draws u.
+//   draft i is kept while u_i q_i(x_i) < p_i(x_i);
+//   after r kept drafts one more token is drawn with u_S from the weights
+//     w = max(p_r - q_r, 0)  (r < n; without q: p_r with x_r left out),  w = p_n  (r = n),
+// so the tokens are distributed as if the target had drawn them one by one.
+//
+// The products u q are exact in f64 and the weights are whole multiples of 2^-61 (p - q is one f32
+// subtraction; an f32 of at least 2^-38 is such a multiple), so every sum is an exact 64-bit integer
+// whatever its order: the drawn token is that of a sequential walk over the row, on any split.
+//
+// Bound: the two rows of V floats that the last token is drawn from (everything else is a few
+// scalars).  A cluster of 8 CTAs shares a row, since one SM's loads would need about 10 us for 1 MB:
+// each warp sums one contiguous stretch with coalesced loads, the stretches' sums meet through
+// distributed shared memory, and only the warp whose stretch holds the draw reads it again (from L2).
+#include <algorithm>
+
+#include "verify.cuh"
+
+namespace llm {
+
+namespace {
+
+constexpr int kVerThreads = 512;
+constexpr int kVerWarps = kVerThreads / 32;
+constexpr int kVerCluster = 8;
+
+LLM_D uint32_t ver_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+LLM_D void ver_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+LLM_D uint64_t ver_remote(const uint64_t* p, uint32_t rank) {
+  uint32_t local = (uint32_t)__cvta_generic_to_shared(p), remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote) : "memory");
+  return v;
+}
+
+// a weight in units of 2^-61 (NaN and negative values weigh nothing)
+LLM_D uint64_t ver_units(float w) {
+  w = w > 0.0f ? fminf(w, 1.0f) : 0.0f;
+  return (uint64_t)__float2ull_rz(w * 2305843009213693952.0f);
+}
+
+struct VerRow {
+  const float* p;   // [V]
+  const float* q;   // [V] or null
+  int skip;         // id left out, or -1
+};
+LLM_D uint64_t ver_weight(const VerRow& r, int v) {
+  float w = r.p[v];
+  if (r.q) w = __fsub_rn(w, r.q[v]);
+  return v == r.skip ? 0ull : ver_units(w);
+}
+
+// cluster = row; VEC: rows start on 16-byte boundaries
+template <bool VEC>
+__global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a) {
+  __shared__ int s_r;
+  __shared__ uint64_t s_warp[kVerWarps];   // sums of this CTA's stretches
+  __shared__ uint64_t s_cta;               // their sum
+  __shared__ uint64_t s_all[kVerCluster];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = ver_rank();
+  const int b = blockIdx.x / kVerCluster;
+  const int S = a.S, V = a.V;
+  int n = a.count ? a.count[b] : S;
+  n = n < 0 ? 0 : n > S ? S : n;
+  if (tid == 0) s_r = n;
+  __syncthreads();
+  for (int i = tid; i < n; i += kVerThreads) {
+    const int x = a.drafts[(size_t)b * S + i];
+    bool kept = false;
+    if (x >= 0 && x < V) {
+      const float p = a.p[((size_t)b * (S + 1) + i) * V + x];
+      const float q = a.q ? a.q[((size_t)b * S + i) * V + x] : 1.0f;
+      kept = (double)a.u[(size_t)b * (S + 1) + i] * (double)q < (double)p;
+    }
+    if (!kept) atomicMin(&s_r, i);
+  }
+  __syncthreads();
+  const int r = s_r;
+  VerRow row = {a.p + ((size_t)b * (S + 1) + r) * V, nullptr, -1};
+  if (r < n) {
+    if (a.q) row.q = a.q + ((size_t)b * S + r) * V;
+    else row.skip = a.drafts[(size_t)b * S + r];
+  }
+  // stretches of whole groups of 4 ids, warp by warp over the cluster
+  const int per = ((V + kVerCluster * kVerWarps - 1) / (kVerCluster * kVerWarps) + 3) & ~3;
+  const int64_t i0_ = (int64_t)((int)rank * kVerWarps + warp) * per;
+  const int i0 = (int)min((int64_t)V, i0_), i1 = (int)min((int64_t)V, i0_ + per);
+  int32_t* ids = a.ids + (size_t)b * (S + 1);
+  // no weight at all (not a row of probabilities): id 0; the draw's owner writes over it after the
+  // cluster barriers
+  if (rank == 0 && tid == 0) ids[r] = 0;
+  uint64_t total = 0;
+  for (int attempt = 0; attempt < 2; ++attempt) {
+    uint64_t sum = 0;
+    if (VEC) {
+      const int v4 = i1 & ~3;  // (i0 is a multiple of 4; only the last stretch can end off one)
+#pragma unroll 4
+      for (int v = i0 + 4 * lane; v < v4; v += 128) {
+        const float4 p = *reinterpret_cast<const float4*>(row.p + v);
+        float w[4] = {p.x, p.y, p.z, p.w};
+        if (row.q) {
+          const float4 q = *reinterpret_cast<const float4*>(row.q + v);
+          w[0] = __fsub_rn(w[0], q.x); w[1] = __fsub_rn(w[1], q.y);
+          w[2] = __fsub_rn(w[2], q.z); w[3] = __fsub_rn(w[3], q.w);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += v + i == row.skip ? 0ull : ver_units(w[i]);
+      }
+      for (int v = max(i0, v4) + lane; v < i1; v += 32) sum += ver_weight(row, v);
+    } else {
+#pragma unroll 4
+      for (int v = i0 + lane; v < i1; v += 32) sum += ver_weight(row, v);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s_warp[warp] = sum;
+    __syncthreads();
+    if (tid == 0) {
+      uint64_t t = 0;
+      for (int w = 0; w < kVerWarps; ++w) t += s_warp[w];
+      s_cta = t;
+    }
+    ver_cluster_sync();
+    if (tid < kVerCluster) s_all[tid] = ver_remote(&s_cta, (uint32_t)tid);
+    ver_cluster_sync();  // (also: nobody leaves or overwrites its sum before all have read it)
+    total = 0;
+    for (int c = 0; c < kVerCluster; ++c) total += s_all[c];
+    if (total > 0 || (!row.q && row.skip < 0)) break;
+    // nothing left over (p <= q everywhere): the target's own probabilities
+    row.q = nullptr;
+    row.skip = -1;
+  }
+  // floor(u * 2^24) * total / 2^24, below total
+  const float u = a.u[(size_t)b * (S + 1) + S];
+  const uint64_t d = u > 0.0f ? (uint64_t)(min(u, 0.99999994f) * 16777216.0f) : 0ull;
+  const uint64_t goal = d * (total >> 24) + ((d * (total & 0xffffffull)) >> 24);
+  uint64_t before = 0;
+  for (uint32_t c = 0; c < rank; ++c) before += s_all[c];
+  if (rank == 0) {
+    for (int i = tid; i <= S; i += kVerThreads)
+      if (i != r) ids[i] = i < r ? a.drafts[(size_t)b * S + i] : -1;
+    if (tid == 0) a.accepted[b] = r;
+  }
+  for (int w = 0; w < warp; ++w) before += s_warp[w];
+  if (goal < before || goal - before >= s_warp[warp]) return;
+  // this warp's stretch holds the draw: 32 ids at a time, a running sum over the lanes
+  for (int v0 = i0; v0 < i1; v0 += 32) {
+    const int v = v0 + lane;
+    uint64_t incl = v < i1 ? ver_weight(row, v) : 0ull;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const uint32_t above = __ballot_sync(0xffffffffu, before + incl > goal);
+    if (above) {
+      if (lane == 0) ids[r] = v0 + __ffs(above) - 1;
+      return;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
+  const bool vec = a.V % 4 == 0 && (reinterpret_cast<uintptr_t>(a.p) & 15) == 0 && (reinterpret_cast<uintptr_t>(a.q) & 15) == 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.B * kVerCluster);
+  cfg.blockDim = dim3(kVerThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kVerCluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, vec ? verify_kernel<true> : verify_kernel<false>, a);
+}
+
+}  // namespace llm
