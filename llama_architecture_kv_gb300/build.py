@@ -12,7 +12,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libllm.so")
 SOURCES = ["llm.cu", "gemv.cu", "gemm.cu", "attention.cu", "sampler.cu", "noalloc.cu", "mega.cu", "qcache.cu",
-           "qattn.cu", "verify.cu", "ops.cu"]
+           "qattn.cu", "qattn_tc64.cu", "qattn_tc128.cu", "verify.cu", "ops.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE]
 

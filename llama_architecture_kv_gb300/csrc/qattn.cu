@@ -15,6 +15,8 @@
 #include <type_traits>
 
 #include "attention.cuh"
+#include "gemm.cuh"
+#include "qattn_tc.cuh"
 #include "qcache.cuh"
 
 namespace llm {
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(kSimpleThreads) qattn_simple_kernel(const QAtt
       if (a.splits == 1) {
         store_o<QT>(a.out, t64 * a.out_stride + (int64_t)head * HD + e, L == 0.f ? 0.f : O / L);
       } else {
-        float* dst = reinterpret_cast<float*>(a.ws) + ((t64 * a.c.kv * g + head) * a.splits + split) * (HD + 2);
+        float* dst = reinterpret_cast<float*>(a.ws + kQattnTickets) + ((t64 * a.c.kv * g + head) * a.splits + split) * (HD + 2);
         dst[e] = O;
         if (e == 0) {
           dst[HD] = M;
@@ -212,7 +214,7 @@ __global__ void qattn_merge_kernel(const QAttnArgs a) {
   for (int64_t t = blockIdx.y; t < (int64_t)a.r.B * a.r.S; t += gridDim.y) {
     int b, start, end;
     if (!token_range(a.r, (int)t, b, start, end)) continue;
-    const float* src = reinterpret_cast<const float*>(a.ws) + (t * H + head) * a.splits * (HD + 2);
+    const float* src = reinterpret_cast<const float*>(a.ws + kQattnTickets) + (t * H + head) * a.splits * (HD + 2);
     float M = -INFINITY, O = 0.f, L = 0.f;
     for (int s = 0; s < a.splits; ++s) M = fmaxf(M, src[s * (HD + 2) + HD]);
     for (int s = 0; s < a.splits; ++s) {
@@ -236,7 +238,7 @@ template <int HD, int QT>
 cudaError_t launch_simple(const QAttnArgs& a0, int num_sms, cudaStream_t s, bool pdl) {
   QAttnArgs a = a0;
   const int64_t tokens = (int64_t)a.r.B * a.r.S;
-  a.splits = simple_splits(a.c, tokens, a.r.limit, num_sms);
+  a.splits = simple_splits(a.c, tokens, std::min(a.r.limit, a.c.rows * a.c.cap), num_sms);
   void (*fn)(const QAttnArgs) = nullptr;
   if (a.g <= 4) fn = qattn_simple_kernel<HD, 4, QT>;
   else if constexpr (HD <= 128) {
@@ -261,18 +263,72 @@ cudaError_t launch_simple(const QAttnArgs& a0, int num_sms, cudaStream_t s, bool
 
 }  // namespace
 
-uint64_t qattn_workspace(const QCacheView& c, int g, int B, int S, int num_sms) {
-  const int64_t tokens = (int64_t)B * S;
-  const int splits = simple_splits(c, tokens, c.cap * c.rows, num_sms);
-  return splits == 1 ? 0 : (uint64_t)tokens * c.kv * g * splits * (c.hd + 2) * 4;
+namespace {
+
+// the tensor-core kernel's tiles: 16 nc accumulator columns of np pieces, the smallest that holds all
+// of a row's (token, head) columns, else the largest
+struct TcPlanQ {
+  int nc, cols, tokens, grid;
+};
+TcPlanQ plan_tc_q(const QCacheView& c, int g, int qt, int64_t rows, int S, int limit, int num_sms) {
+  const int np = qt ? 2 : 4, most = qt ? 4 : 8;
+  TcPlanQ p;
+  p.nc = 1;
+  while (p.nc < most && (int64_t)p.nc * 16 / np < (int64_t)S * g) p.nc *= 2;
+  p.cols = p.nc * 16 / np;
+  p.tokens = p.cols / g;
+  const int64_t units = rows * ((S + p.tokens - 1) / p.tokens) * c.kv;
+  const int64_t tiles = units * ((limit + kQaTile - 1) / kQaTile);
+  const int64_t ctas = std::min(num_sms * (p.nc <= 2 ? 2 : 1), kQattnTickets / 4);
+  p.grid = (int)std::max<int64_t>(1, std::min(tiles, ctas));
+  return p;
 }
 
-cudaError_t launch_qattn(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s, bool pdl) {
+}  // namespace
+
+bool qattn_uses_tc(int hd) { return hd == 64 || hd == 128; }
+int qattn_tile_tokens(int g) { return 32 / g; }
+
+bool qattn_make_map(CUtensorMap* map, const void* codes, int hd, uint64_t rows) {
+  return make_map_2d(map, codes, 1, (uint64_t)hd, rows, (uint32_t)hd, 64,
+                     hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+uint64_t qattn_workspace(const QCacheView& c, int g, int B, int S, int num_sms) {
+  const int64_t tokens = (int64_t)B * S;
+  const int limit = c.rows * c.cap;
+  if (qattn_uses_tc(c.hd)) {
+    uint64_t most = 0;
+    for (int qt = 0; qt < 2; ++qt) {
+      const TcPlanQ p = plan_tc_q(c, g, qt, B, S, limit, num_sms);
+      most = std::max(most, (uint64_t)p.grid * 2 * p.cols * (c.hd + 2) * 4);
+    }
+    return kQattnTickets + most;
+  }
+  const int splits = simple_splits(c, tokens, limit, num_sms);
+  return splits == 1 ? 0 : kQattnTickets + (uint64_t)tokens * c.kv * g * splits * (c.hd + 2) * 4;
+}
+
+cudaError_t launch_qattn(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s, bool pdl, const CUtensorMap* kmap,
+                         const CUtensorMap* vmap) {
+  if (qattn_uses_tc(a.c.hd)) {
+    CUtensorMap maps[2];
+    if (!kmap) {
+      const uint64_t rows = (uint64_t)a.c.rows * a.c.kv * a.c.cap;
+      if (!qattn_make_map(&maps[0], a.c.k, a.c.hd, rows) || !qattn_make_map(&maps[1], a.c.v, a.c.hd, rows))
+        return cudaErrorInvalidValue;
+      kmap = &maps[0];
+      vmap = &maps[1];
+    }
+    const int S = a.tiles ? qattn_tile_tokens(a.g) : a.r.S;  // (a tile is a row of its own)
+    // (a page table can name a page more than once: rows longer than the pool get no more CTAs)
+    const TcPlanQ p = plan_tc_q(a.c, a.g, qt, a.r.B, S, std::min(a.r.limit, a.c.rows * a.c.cap), num_sms);
+    return a.c.hd == 64 ? launch_qattn_tc64(*kmap, *vmap, a, qt, p.nc, p.grid, s, pdl)
+                        : launch_qattn_tc128(*kmap, *vmap, a, qt, p.nc, p.grid, s, pdl);
+  }
   switch (a.c.hd) {
     case 16: return qt ? launch_simple<16, 1>(a, num_sms, s, pdl) : launch_simple<16, 0>(a, num_sms, s, pdl);
     case 32: return qt ? launch_simple<32, 1>(a, num_sms, s, pdl) : launch_simple<32, 0>(a, num_sms, s, pdl);
-    case 64: return qt ? launch_simple<64, 1>(a, num_sms, s, pdl) : launch_simple<64, 0>(a, num_sms, s, pdl);
-    case 128: return qt ? launch_simple<128, 1>(a, num_sms, s, pdl) : launch_simple<128, 0>(a, num_sms, s, pdl);
     case 256: return qt ? launch_simple<256, 1>(a, num_sms, s, pdl) : launch_simple<256, 0>(a, num_sms, s, pdl);
     default: return cudaErrorInvalidValue;
   }

@@ -1,0 +1,781 @@
+// Attention over an 8-bit cache on the 5th-generation tensor cores, head sizes 64 and 128: the
+// kernel template (instantiated in qattn_tc64.cu and qattn_tc128.cu).
+//
+// The codes go from HBM to shared memory by TMA and from there into e4m3 MMAs as they are: no code
+// is ever widened.  The f32 (bf16) operands that meet them, queries and softmax weights, enter as NP
+// e4m3 pieces, x = 2^e (x_0 + x_1 / 16 + x_2 / 256 + ...), each piece the rounding of what the ones
+// before left over (four bits a piece: four pieces for f32, 2^-19 of a query's largest element and
+// 2^-16 of a weight; two for bf16, which hold a bf16 query's eight bits and a weight to 2^-8).  The
+// pieces are columns of their own, so every accumulator sums like with like in f32 and the powers of 16
+// are applied once, in registers.
+//
+// A tile is 128 positions of one row and key/value head against up to C = 16 NC / NP columns, the
+// (token, query head) pairs of up to C / g tokens that share the codes:
+//   S [128 positions][16 NC]  = K [128][HD] Q^T      A = keys, K-major as stored; B = query pieces
+//   softmax                     thread = position: pieces summed, block scales applied, weights split
+//   O [HD][16 NC]            += V^T [HD][128] P^T     A = values, M-major as stored; B = weight pieces
+// With the positions on the M side a tile costs 8 MMAs however few columns there are, and a thread
+// writes its position's pieces with one 16-byte store per 16 columns (B's N-major layout).
+//
+// Running maxima are lazy: a column's reference moves only when a score exceeds it by 2^8 (pieces
+// reach 448, weights stay below 2^8), so the accumulators in tensor memory are hardly ever rescaled.
+// The values' block scales ride on the weights, relative to the largest scale seen (also lazy).
+//
+// One CTA: a producer warp (TMA, a ring of tiles), a warp that issues the MMAs, and two groups of four
+// softmax warps that take the tiles of a segment in turn, each with its own accumulators, so that one
+// group's softmax overlaps the other's loads and products.  The (row, token tile, kv head, tile)
+// sequence is cut into one equal run per CTA; the parts of a unit cut across CTAs meet in global
+// memory, where the last CTA to arrive (a ticket, nobody waits) adds them in CTA order.  So rows of
+// any lengths fill the SMs evenly and the result does not depend on timing.
+#pragma once
+#include "attention.cuh"
+#include "qcache.cuh"
+#include "tc.cuh"
+
+namespace llm {
+
+constexpr int kQaTile = 128;                       // positions per tile
+constexpr int kQaThreads = 320;                    // producer, MMA issuer, 2 x 4 softmax warps
+constexpr uint64_t kQaWaitCycles = 1000000000ull;  // about 0.5 s
+constexpr float kQaLazy = 8.0f;                    // log2 of how far a weight may exceed the reference
+constexpr size_t kQaSmem = 232448;                 // shared memory a CTA can have
+
+template <int HD, int NP, int NC>
+struct QaShape {
+  static constexpr int N = 16 * NC;                // accumulator columns
+  static constexpr int C = N / NP;                 // (token, head) columns
+  static constexpr int CPC = 16 / NP;              // of them per 16 accumulator columns
+  static constexpr int KB = kQaTile * HD;          // bytes of a tile of keys (or values)
+  static constexpr int STAGE = 2 * KB;
+  static constexpr int QB = N * HD;                // query pieces
+  static constexpr int PB = kQaTile * N;           // weight pieces of one group
+  // two CTAs per SM where their tensor memory (4 N columns each) and rings fit: their segment ends
+  // and starts overlap (measured: profiles/qcache_attention.md)
+  static constexpr int CTAS = NC <= 2 ? 2 : 1;
+  static constexpr size_t MISC = 4096;
+  static constexpr size_t BUDGET = kQaSmem / CTAS - (CTAS > 1 ? 1024 : 0);
+  static constexpr int FIT = (int)((BUDGET - QB - 2 * PB - MISC - 1024) / STAGE);
+  static constexpr int ST = FIT < 8 ? FIT : 8;     // ring stages
+  static constexpr size_t SMEM = 1024 + (size_t)ST * STAGE + QB + 2 * PB + MISC;
+  static constexpr uint32_t SWZ = HD == 128 ? 2 : 4;  // 128- or 64-byte swizzle
+  static_assert(ST >= 2, "ring");
+};
+
+// one tile of tokens: ntok tokens whose queries are rows qrow .. of q; token i sees start <= t < end0 + i
+struct QaUnit {
+  int b;          // the row (or pass entry) whose places hold the positions
+  int ntok;
+  int64_t qrow;
+  int start, end0, last;  // last: positions the last token sees end here
+  int tile0, nt;  // its position tiles
+};
+
+LLM_D QaUnit qa_unit(const QAttnArgs& a, int t, int tpt, int nct) {
+  QaUnit u;
+  if (a.r.step) {
+    if (a.tiles) {
+      const int32_t* e = a.tiles + 4 + 4 * (size_t)t;
+      u.b = e[0];
+      u.ntok = e[1];
+      u.start = e[3];
+    } else {
+      u.b = t;
+      u.ntok = 1;
+      u.start = row_start(a.r.step, t);
+    }
+    u.qrow = u.b;
+    u.end0 = row_pos(a.r.step, u.b) + 1;
+  } else {
+    u.b = t / nct;
+    const int n = q_count(a.r, u.b), i0 = (t - u.b * nct) * tpt;
+    int len = a.r.first[u.b];
+    if (len < 0 || len > a.r.limit) {
+      q_report(a.r.status, kErrPosRange);
+      len = 0;
+    }
+    u.ntok = max(0, min(tpt, n - i0));
+    u.qrow = (int64_t)u.b * a.r.S + i0;
+    u.start = 0;
+    u.end0 = len - n + i0 + 1;
+  }
+  u.last = u.end0 + u.ntok - 1;
+  u.tile0 = u.start / kQaTile;
+  u.nt = u.ntok > 0 && u.last > u.start ? (u.last + kQaTile - 1) / kQaTile - u.tile0 : 0;
+  return u;
+}
+
+LLM_D bool qa_place(const QAttnArgs& a, int b, int pos, int& row, int& pp) {
+  if (!a.r.step) return q_place(a.r, a.c, b, pos, row, pp);
+  cache_slot(a.r.step, a.c.cap, b, pos, row, pp);
+  return true;
+}
+
+LLM_D float qa_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// the walk of one CTA's run over (token tile, kv head, position tiles)
+struct QaWalk {
+  QaUnit u;
+  int t, j, k0, k1;
+  long long st, end, off;  // off: place of (t, head 0) in the sequence
+  int tpt, nct;
+  LLM_D void begin(const QAttnArgs& a, int t_, long long off_, long long c0, long long c1, int tpt_, int nct_) {
+    t = t_; off = off_; st = c0; end = c1; tpt = tpt_; nct = nct_;
+    if (st >= end) return;
+    u = qa_unit(a, t, tpt, nct);
+    j = (int)((st - off) / u.nt);
+    k0 = (int)(st - off - (long long)j * u.nt);
+    cut();
+  }
+  LLM_D void cut() { k1 = (int)min((long long)u.nt, k0 + (end - st)); }
+  LLM_D bool there() const { return st < end; }
+  LLM_D long long unit0() const { return off + (long long)j * u.nt; }
+  LLM_D void next(const QAttnArgs& a) {
+    st += k1 - k0;
+    if (st >= end) return;  // (a unit that goes on belongs to the next CTA)
+    k0 = 0;
+    if (++j == a.c.kv) {
+      j = 0;
+      off += (long long)a.c.kv * u.nt;
+      do u = qa_unit(a, ++t, tpt, nct);
+      while (u.nt == 0);
+    }
+    cut();
+  }
+};
+
+template <int HD, int NP, int NC, int QT>
+__global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
+    qattn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const QAttnArgs a) {
+  using X = QaShape<HD, NP, NC>;
+  constexpr int N = X::N, C = X::C, CPC = X::CPC, ST = X::ST;
+  extern __shared__ unsigned char qraw[];
+  const uint32_t s_raw = smem_u32(qraw);
+  unsigned char* base = qraw + (((s_raw + 1023u) & ~1023u) - s_raw);
+  const uint32_t s_ring = smem_u32(base);
+  unsigned char* qbuf = base + (size_t)ST * X::STAGE;
+  unsigned char* pbuf = qbuf + X::QB;              // [2][PB]
+  float* qsc = reinterpret_cast<float*>(pbuf + 2 * X::PB);  // [C] query scale, in units of log2
+  int* cend = reinterpret_cast<int*>(qsc + C);     // [C] end of the positions a column sees
+  float* wmax = reinterpret_cast<float*>(cend + C);  // [2][4][C] warps' maxima; at a segment's end, sums
+  float* gref = wmax + 8 * C;                      // [2][C] the groups' references
+  float* wvs = gref + 2 * C;                       // [2][4] warps' largest value scales
+  float* gvs = wvs + 8;                            // [2] the groups' value scales
+  const uint32_t bars = (smem_u32(gvs + 2) + 7u) & ~7u;
+  const uint32_t b_full = bars, b_empty = b_full + 8 * ST, b_s = b_empty + 8 * ST, b_p = b_s + 16, b_pv = b_p + 16,
+                 b_q = b_pv + 16;
+  static_assert((size_t)C * (4 + 4 + 32 + 8) + 64 + 16 * ST + 64 <= X::MISC, "shared memory");
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_t, s_last;
+  __shared__ long long s_off, s_total;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x;
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(b_full + 8u * i, 1);
+      mbar_init(b_empty + 8u * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b_s + 8u * i, 1);
+      mbar_init(b_p + 8u * i, 128);
+      mbar_init(b_pv + 8u * i, 1);
+    }
+    mbar_init(b_q, 1);
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&s_tmem), 4 * N);
+    tmem_relinquish();
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // this CTA's run: the token tiles' position tiles are counted lane by lane (contiguous stretches),
+  // and the lane whose stretch holds the run's start finds its token tile
+  const int tpt = C / a.g;
+  const int nct = a.r.step ? 1 : (a.r.S + tpt - 1) / tpt;
+  const int nq = a.r.step ? (a.tiles ? a.tiles[1] : a.r.B) : a.r.B * nct;
+  if (warp == 0) {
+    const int per = (nq + 31) / 32, t0 = min(nq, lane * per), t1 = min(nq, t0 + per);
+    long long sum = 0;
+    for (int t = t0; t < t1; ++t) sum += qa_unit(a, t, tpt, nct).nt;
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const long long total = __shfl_sync(0xffffffffu, incl, 31) * a.c.kv;
+    const long long ge = min((long long)gridDim.x, total), c0 = cta < ge ? total * cta / ge : total;
+    long long off = (incl - sum) * a.c.kv;
+    if (lane == 0) s_total = total;
+    if (sum > 0 && c0 >= off && c0 < incl * a.c.kv) {
+      for (int t = t0; t < t1; ++t) {
+        const long long w = (long long)qa_unit(a, t, tpt, nct).nt * a.c.kv;
+        if (c0 < off + w) {
+          s_t = t;
+          s_off = off;
+          break;
+        }
+        off += w;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  // (never more runs than tiles, so that every CTA of a unit's range holds a part of it)
+  const long long T = s_total;
+  const int G = (int)min((long long)gridDim.x, T);
+  const long long c0 = cta < G ? T * cta / G : T, c1 = cta < G ? T * (cta + 1) / G : T;
+  QaWalk w;
+  w.begin(a, s_t, s_off, c0, c1, tpt, nct);
+  bool ok = true;  // a wait that gave up: no further waits, but every loop and barrier is still walked
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (ok && !mbar_wait(bar, parity, kQaWaitCycles)) {
+      ok = false;
+      q_report(a.r.status, kErrDeviceTimeout);
+    }
+  };
+
+  if (warp == 0) {
+    // ---- producer ----
+    if (lane == 0) {
+      tma_prefetch_map(&kmap);
+      tma_prefetch_map(&vmap);
+      long long it = 0;
+      int slot = 0;
+      uint32_t par = 1u;
+      for (; w.there(); w.next(a)) {
+        for (int k = w.k0; k < w.k1; ++k, ++it) {
+          wait(b_empty + 8u * slot, par);
+          if (!ok) break;
+          const int p0 = (w.u.tile0 + k) * kQaTile;
+          int y[2];
+          uint32_t bytes = 0;
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            int row, pp;
+            y[hf] = -1;
+            if (p0 + 64 * hf < w.u.last && qa_place(a, w.u.b, p0 + 64 * hf, row, pp)) {
+              y[hf] = a.krow0 + (row * a.c.kv + w.j) * a.c.cap + pp;
+              bytes += 2 * 64 * HD;
+            }
+          }
+          const uint32_t dst = s_ring + (uint32_t)slot * X::STAGE;
+          const uint32_t bar = b_full + 8u * slot;
+          mbar_expect_tx(bar, bytes);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+            if (y[hf] >= 0) {
+              tma_load_2d(dst + hf * 64 * HD, &kmap, bar, 0, y[hf]);
+              tma_load_2d(dst + X::KB + hf * 64 * HD, &vmap, bar, 0, y[hf]);
+            }
+          if (++slot == ST) slot = 0, par ^= 1u;
+        }
+        if (!ok) break;
+      }
+      // no copy may still be writing shared memory when the CTA exits
+      ok = true;
+      const long long lo = it > ST ? it - ST : 0;
+      for (long long i = lo; i < it; ++i) wait(b_full + 8u * (uint32_t)(i % ST), (uint32_t)(i / ST) & 1u);
+    }
+  } else if (warp == 1) {
+    // ---- MMA issuer ----
+    if (lane == 0) {
+      const uint32_t id_s = idesc_e4m3_f32(kQaTile, N, 0), id_o = idesc_e4m3_f32(HD, N, 1);
+      const uint32_t q_addr = smem_u32(qbuf), p_addr = smem_u32(pbuf);
+      uint32_t cnt[2] = {0u, 0u};  // tiles whose weights each group has written
+      uint32_t qpar = 0u;
+      long long it = 0;            // tiles before this segment
+      for (; w.there(); w.next(a)) {
+        const int n = w.k1 - w.k0;
+        auto scores = [&](int t) {
+          const uint32_t slot = (uint32_t)((it + t) % ST);
+          wait(b_full + 8u * slot, (uint32_t)((it + t) / ST) & 1u);
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t k_addr = s_ring + slot * X::STAGE;
+#pragma unroll
+          for (int ks = 0; ks < HD / 32; ++ks)
+            tc_mma_e4m3(tmem + (t & 1) * N, smem_desc(k_addr + ks * 32, 16, 8 * HD, X::SWZ),
+                        smem_desc(q_addr + ks * 32, 16, 8 * HD, X::SWZ), id_s, ks > 0);
+          tc_commit(b_s + 8u * (t & 1));
+        };
+        wait(b_q, qpar);
+        qpar ^= 1u;
+        tc_fence_after();
+        scores(0);
+        if (n > 1) scores(1);
+        for (int t = 0; t < n; ++t) {
+          const int gp = t & 1;
+          wait(b_p + 8u * gp, cnt[gp]++ & 1u);
+          if (ok) {
+            tc_fence_after();
+            const uint32_t slot = (uint32_t)((it + t) % ST);
+            const uint32_t v_addr = s_ring + slot * X::STAGE + X::KB;
+#pragma unroll
+            for (int kk = 0; kk < kQaTile / 32; ++kk)
+              tc_mma_e4m3(tmem + 2 * N + gp * N, smem_desc(v_addr + kk * 32 * HD, 8 * HD, 8 * HD, X::SWZ),
+                          smem_desc(p_addr + gp * X::PB + kk * 512, 128, 2048, 0), id_o, t > 1 || kk > 0);
+            tc_commit(b_pv + 8u * gp);
+            tc_commit(b_empty + 8u * slot);
+          }
+          if (t + 2 < n) scores(t + 2);
+        }
+        it += n;
+      }
+    }
+  } else {
+    // ---- softmax groups ----
+    const int sw = warp - 2, gp = sw >> 2, gw = sw & 3;  // group, warp in it
+    const int quad = warp & 3;                           // the tensor-memory lanes this warp reads
+    const int stid = tid - 64;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t t_s = tmem + gp * N + lanes, t_o = tmem + 2 * N + gp * N + lanes;
+    unsigned char* pmine = pbuf + gp * X::PB + (quad * 32 + lane) * 16;
+    const int H = a.c.kv * a.g;
+    // tokens that see nothing and share a tile with none that does: zeros
+    for (int t = cta; t < nq; t += gridDim.x) {
+      const QaUnit u = qa_unit(a, t, tpt, nct);
+      if (u.nt == 0 && u.ntok > 0)
+        for (int64_t i = stid; i < (int64_t)u.ntok * H * HD; i += 256) {
+          const int64_t at = (u.qrow + i / (H * HD)) * a.out_stride + i % (H * HD);
+          if constexpr (QT) static_cast<uint16_t*>(a.out)[at] = 0;
+          else static_cast<float*>(a.out)[at] = 0.f;
+        }
+    }
+    uint32_t cs = 0u, cpv = 0u;  // score tiles read, value products waited for
+    long long it = 0;
+    for (; w.there(); w.next(a)) {
+      const int n = w.k1 - w.k0, used = w.u.ntok * a.g;
+      // ---- query pieces: warp = column ----
+      for (int c = sw; c < C; c += 8) {
+        constexpr int E = HD / 32;  // elements per lane
+        const int tok = c / a.g;
+        float x[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = 0.f;
+        if (c < used) {
+          const int64_t at = (w.u.qrow + tok) * a.q_stride + (int64_t)(w.j * a.g + c - tok * a.g) * HD + lane * E;
+          if constexpr (QT == 0) {
+            const float* p = static_cast<const float*>(a.q) + at;
+            if constexpr (E == 4) {
+              const float4 v = *reinterpret_cast<const float4*>(p);
+              x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+            } else {
+              const float2 v = *reinterpret_cast<const float2*>(p);
+              x[0] = v.x; x[1] = v.y;
+            }
+          } else {
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + at);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              const uint32_t v = p[e / 2];
+              x[e] = bf16_lo(v);
+              x[e + 1] = bf16_hi(v);
+            }
+          }
+        }
+        uint32_t top = 0u;
+#pragma unroll
+        for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+        top = __reduce_max_sync(0xffffffffu, top);
+        const bool fine = top < 0x7f800000u;
+        const float s = q_scale(fine ? __uint_as_float(top) : 0.f), r = q_recip(s);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = fine ? x[e] * r : 0.f;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const int row = c * NP + i;
+          uint32_t code = 0u;
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const uint32_t p = e4m3x2(x[e], x[e + 1]);
+            const float2 v = e4m3_pair(p);
+            x[e] = (x[e] - v.x) * 16.f;
+            x[e + 1] = (x[e + 1] - v.y) * 16.f;
+            code |= p << (8 * e);
+          }
+          if constexpr (HD == 128)
+            *reinterpret_cast<uint32_t*>(qbuf + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4) = code;
+          else
+            *reinterpret_cast<uint16_t*>(qbuf + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + (lane & 7) * 2) = (uint16_t)code;
+        }
+        if (lane == 0) {
+          // a query that is not finite makes its scores NaN
+          qsc[c] = c < used ? (fine ? s * (a.scale * 1.4426950408889634f) : __uint_as_float(0x7fc00000u)) : 0.f;
+          cend[c] = c < used ? w.u.end0 + tok : 0;
+        }
+      }
+      fence_proxy_async_smem();
+      named_sync(3, 256);
+      if (stid == 0) mbar_arrive(b_q);
+
+      float ref[C], l[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        ref[c] = c < used ? -INFINITY : INFINITY;  // a column without a token: weights 2^(0 - inf) = 0
+        l[c] = 0.f;
+      }
+      float vref = 0.f, vinv = 0.f;                // the largest value scale seen, and its reciprocal
+      // the scales of this thread's position in tile t (0 and not good where it is not seen)
+      auto scales = [&](int t, float& ks, float& vs) {
+        ks = vs = 0.f;
+        const int pos = (w.u.tile0 + w.k0 + t) * kQaTile + quad * 32 + lane;
+        int row, pp;
+        if (t >= n || pos >= w.u.last || !qa_place(a, w.u.b, pos, row, pp)) return false;
+        const size_t at = ((size_t)row * a.c.kv + w.j) * (a.c.cap / kQBlock) + pp / kQBlock;
+        ks = a.c.ks[at];
+        vs = a.c.vs[at];
+        return true;
+      };
+      float ks, vs;
+      bool good = scales(gp, ks, vs);
+      bool pend = false;                           // a product over the values not waited for yet
+      for (int t = gp; t < n; t += 2) {
+        const int p0 = (w.u.tile0 + w.k0 + t) * kQaTile, pos = p0 + quad * 32 + lane;
+        float ks1, vs1;
+        const bool good1 = scales(t + 2, ks1, vs1);  // the next tile's, in flight behind this one's work
+        wait(b_s + 8u * gp, cs++ & 1u);
+        __syncwarp();
+        tc_fence_after();
+        float s[C];
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch) {
+          float d[16];
+          tc_ld16(t_s + ch * 16, d);
+          tc_wait_ld();
+#pragma unroll
+          for (int c = 0; c < CPC; ++c) {
+            float v = d[c * NP + NP - 1];
+#pragma unroll
+            for (int i = NP - 2; i >= 0; --i) v = fmaf(v, 0.0625f, d[c * NP + i]);
+            s[ch * CPC + c] = v * (ks * qsc[ch * CPC + c]);
+          }
+        }
+        // every column with a token sees the whole tile?
+        const bool whole = __all_sync(0xffffffffu, good) && p0 >= w.u.start && p0 + kQaTile <= w.u.end0;
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+            if (!good || pos >= cend[c] || pos < w.u.start) s[c] = -INFINITY;
+        }
+        bool low = !(vs > vref);
+#pragma unroll
+        for (int c = 0; c < C; ++c) low = low && !(s[c] > ref[c] + kQaLazy);
+        if (!named_sync_and(1 + gp, 128, low)) {
+          // references move (in every thread of the group alike)
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const float m = warp_max(s[c]);
+            if (lane == 0) wmax[(gp * 4 + gw) * C + c] = m;
+          }
+          const float mv = warp_max(vs);
+          if (lane == 0) wvs[gp * 4 + gw] = mv;
+          named_sync(1 + gp, 128);
+          const float v1 = fmaxf(fmaxf(wvs[gp * 4], wvs[gp * 4 + 1]), fmaxf(wvs[gp * 4 + 2], wvs[gp * 4 + 3]));
+          float vcorr = 1.f;
+          if (v1 > vref) {
+            vcorr = vref * q_recip(v1);
+            vref = v1;
+            vinv = q_recip(v1);
+          }
+          float corr[C];
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const float* m = wmax + gp * 4 * C + c;
+            const float top = fmaxf(ref[c], fmaxf(fmaxf(m[0], m[C]), fmaxf(m[2 * C], m[3 * C])));
+            corr[c] = top == ref[c] ? 1.f : qa_exp2(ref[c] - top);
+            ref[c] = top;
+            l[c] *= corr[c];
+            corr[c] *= vcorr;
+          }
+          if (t > gp) {
+            // the accumulators, once the product before is in them
+            if (pend) {
+              wait(b_pv + 8u * gp, cpv++ & 1u);
+              pend = false;
+            }
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int ch = 0; ch < NC; ++ch) {
+              float d[16];
+              tc_ld16(t_o + ch * 16, d);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) d[i] *= corr[ch * CPC + i / NP];
+              tc_st16(t_o + ch * 16, d);
+            }
+            tc_wait_st();
+          }
+        }
+        const float vr = vs * vinv;
+        // weights and their sums; s becomes the weight with the value's scale on it
+        if (whole) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const float p = qa_exp2(s[c] - ref[c]);
+            l[c] += p;
+            s[c] = p * vr;
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const bool seen = good && pos < cend[c] && pos >= w.u.start;
+            const float p = seen ? qa_exp2(s[c] - ref[c]) : 0.f;
+            l[c] += p;
+            s[c] = seen ? p * vr : 0.f;
+          }
+        }
+        if (pend) wait(b_pv + 8u * gp, cpv++ & 1u);  // the weights' buffer is free again
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch) {
+          uint32_t o[4];  // 16 codes: CPC columns of NP pieces
+#pragma unroll
+          for (int c = 0; c < CPC; c += 2) {
+            float x0 = s[ch * CPC + c], x1 = s[ch * CPC + c + 1];
+            uint32_t x[NP];
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+              x[i] = e4m3x2(x0, x1);
+              if (i + 1 < NP) {
+                const float2 v = e4m3_pair(x[i]);
+                x0 = (x0 - v.x) * 16.f;
+                x1 = (x1 - v.y) * 16.f;
+              }
+            }
+            if constexpr (NP == 4) {
+              const uint32_t a01 = x[0] | x[1] << 16, a23 = x[2] | x[3] << 16;
+              o[c] = __byte_perm(a01, a23, 0x6420);
+              o[c + 1] = __byte_perm(a01, a23, 0x7531);
+            } else {
+              o[c / 2] = __byte_perm(x[0], x[1], 0x5140);
+            }
+          }
+          *reinterpret_cast<uint4*>(pmine + ch * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        if (!whole && (!good || pos < w.u.start)) {
+          // rows that no column sees hold dead data (any code, NaN among them): zeros
+          const long long i = it + t;
+          wait(b_full + 8u * (uint32_t)(i % ST), (uint32_t)(i / ST) & 1u);
+          uint4* v = reinterpret_cast<uint4*>(base + (size_t)(i % ST) * X::STAGE + X::KB + (quad * 32 + lane) * HD);
+#pragma unroll
+          for (int e = 0; e < HD / 16; ++e) v[e] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(b_p + 8u * gp);
+        pend = true;
+        good = good1;
+        ks = ks1;
+        vs = vs1;
+      }
+      if (pend) wait(b_pv + 8u * gp, cpv++ & 1u);
+      __syncwarp();
+      tc_fence_after();
+      it += n;
+
+      // ---- the segment's end: the groups' sums meet, group 0 writes ----
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const float sum = warp_sum(l[c]);
+        if (lane == 0) wmax[(gp * 4 + gw) * C + c] = sum;
+        if (lane == 0 && gw == 0) gref[gp * C + c] = ref[c];
+      }
+      if (lane == 0 && gw == 0) gvs[gp] = vref;
+      named_sync(3, 256);  // (both groups' products are done: the weights' buffers are free)
+      const bool both = n > 1;
+      const int d_row = HD == 128 ? quad * 32 + lane : quad * 16 + (lane & 15);  // the dimension of this lane
+      const bool d_on = HD == 128 || lane < 16;
+      float* other = reinterpret_cast<float*>(pbuf);  // [C][HD]: group 1's sums
+      auto column = [&](const float (&d)[16], int c) {
+        float v = d[c * NP + NP - 1];
+#pragma unroll
+        for (int i = NP - 2; i >= 0; --i) v = fmaf(v, 0.0625f, d[c * NP + i]);
+        return v * vref;
+      };
+      if (gp == 1 && both) {
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch) {
+          if (ch * CPC >= used) break;
+          float d[16];
+          tc_ld16(t_o + ch * 16, d);
+          tc_wait_ld();
+#pragma unroll
+          for (int c = 0; c < CPC; ++c)
+            if (d_on && ch * CPC + c < used) other[(ch * CPC + c) * HD + d_row] = column(d, c);
+        }
+      }
+      if (both) named_sync(3, 256);
+      if (gp == 1) continue;
+      const bool alone = w.k0 == 0 && w.k1 == w.u.nt;  // this CTA holds the whole unit
+      float* parts = reinterpret_cast<float*>(a.ws + kQattnTickets);
+      float* mine = parts + ((size_t)cta * 2 + (w.k0 == 0 ? 1 : 0)) * C * (HD + 2);
+      auto out_at = [&](int c) { return (w.u.qrow + c / a.g) * a.out_stride + (int64_t)(w.j * a.g + c % a.g) * HD; };
+      auto put = [&](int c, int e, float v) {
+        if constexpr (QT) static_cast<uint16_t*>(a.out)[out_at(c) + e] = f32_to_bf16(v);
+        else static_cast<float*>(a.out)[out_at(c) + e] = v;
+      };
+#pragma unroll
+      for (int ch = 0; ch < NC; ++ch) {
+        if (ch * CPC >= used) break;
+        float d[16];
+        tc_ld16(t_o + ch * 16, d);
+        tc_wait_ld();
+#pragma unroll
+        for (int cc = 0; cc < CPC; ++cc) {
+          const int c = ch * CPC + cc;
+          if (c >= used) break;
+          const float l0 = wmax[c] + wmax[C + c] + wmax[2 * C + c] + wmax[3 * C + c];
+          const float r0 = gref[c];
+          float M = r0, L = l0, f0 = 1.f, O = column(d, cc);
+          if (both) {
+            const float l1 = wmax[4 * C + c] + wmax[5 * C + c] + wmax[6 * C + c] + wmax[7 * C + c];
+            const float r1 = gref[C + c];
+            M = fmaxf(r0, r1);
+            // (sums without a reference are 0, or NaN, which has to stay)
+            f0 = r0 == -INFINITY ? (l0 == 0.f ? 0.f : 1.f) : qa_exp2(r0 - M);
+            const float f1 = r1 == -INFINITY ? (l1 == 0.f ? 0.f : 1.f) : qa_exp2(r1 - M);
+            L = fmaf(l0, f0, l1 * f1);
+            O = fmaf(O, f0, (d_on ? other[c * HD + d_row] : 0.f) * f1);
+          }
+          if (d_on) {
+            if (alone) {
+              put(c, d_row, L == 0.f ? 0.f : O / L);
+            } else {
+              mine[c * (HD + 2) + d_row] = O;
+              if (d_row == 0) {
+                mine[c * (HD + 2) + HD] = M;
+                mine[c * (HD + 2) + HD + 1] = L;
+              }
+            }
+          }
+        }
+      }
+      if (alone) continue;
+      // ---- a unit of several CTAs: the last of them to get here adds the parts in CTA order ----
+      auto owner = [&](long long i) { return (int)(((i + 1) * G + T - 1) / T - 1); };
+      const int first = owner(w.unit0()), np = owner(w.unit0() + w.u.nt - 1) - first + 1;
+      __threadfence();
+      named_sync(1, 128);
+      if (stid == 0) s_last = atomicInc(reinterpret_cast<uint32_t*>(a.ws) + first, (uint32_t)(np - 1)) == (uint32_t)(np - 1);
+      named_sync(1, 128);
+      if (!s_last) continue;
+      __threadfence();
+      auto part = [&](int i, int c) { return parts + (((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * C + c) * (HD + 2); };
+      float* fac = reinterpret_cast<float*>(pbuf);  // [C][64] factors of 64 parts at a time
+      for (int c = gw; c < used; c += 4) {          // maxima: warp = column, lanes = parts
+        float m = -INFINITY;
+        for (int i = lane; i < np; i += 32) m = fmaxf(m, __ldcg(part(i, c) + HD));
+        m = warp_max(m);
+        if (lane == 0) gref[c] = m;
+      }
+      __syncwarp();
+      // threads own (column, dimension) pairs in strides of 128
+      constexpr int PER = C * HD / 128;
+      float O[PER];
+#pragma unroll
+      for (int q = 0; q < PER; ++q) O[q] = 0.f;
+      float Lw[(C + 3) / 4];                        // this warp's columns' sums, lane by lane
+#pragma unroll
+      for (int q = 0; q < (C + 3) / 4; ++q) Lw[q] = 0.f;
+      for (int i0 = 0; i0 < np; i0 += 64) {
+        const int m = min(64, np - i0);
+        named_sync(1, 128);
+#pragma unroll
+        for (int q = 0; q < (C + 3) / 4; ++q) {
+          const int c = gw + 4 * q;
+          if (c < used)
+            for (int i = lane; i < m; i += 32) {
+              const float mi = __ldcg(part(i0 + i, c) + HD), li = __ldcg(part(i0 + i, c) + HD + 1);
+              const float f = mi == -INFINITY ? (li == 0.f ? 0.f : 1.f) : qa_exp2(mi - gref[c]);
+              fac[c * 64 + i] = f;
+              Lw[q] = fmaf(li, f, Lw[q]);
+            }
+        }
+        named_sync(1, 128);
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+          const int x = q * 128 + stid, c = x / HD, e = x % HD;
+          if (c < used) {
+            int i = 0;
+            for (; i + 8 <= m; i += 8) {
+              float v[8];
+#pragma unroll
+              for (int y = 0; y < 8; ++y) v[y] = __ldcg(part(i0 + i + y, c) + e);
+#pragma unroll
+              for (int y = 0; y < 8; ++y) O[q] = fmaf(fac[c * 64 + i + y], v[y], O[q]);
+            }
+            for (; i < m; ++i) O[q] = fmaf(fac[c * 64 + i], __ldcg(part(i0 + i, c) + e), O[q]);
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < (C + 3) / 4; ++q) {
+        const float L = warp_sum(Lw[q]);
+        if (lane == 0 && gw + 4 * q < C) gref[C + gw + 4 * q] = L;
+      }
+      named_sync(1, 128);
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        const int x = q * 128 + stid, c = x / HD, e = x % HD;
+        if (c < used) put(c, e, gref[C + c] == 0.f ? 0.f : O[q] / gref[C + c]);
+      }
+    }
+  }
+  // ---- everyone leaves together; the products are done, the tensor memory goes back ----
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 4 * N);
+}
+
+// launch for one head size; false results are CUDA errors
+template <int HD>
+cudaError_t launch_qattn_tc_hd(const CUtensorMap& kmap, const CUtensorMap& vmap, const QAttnArgs& a, int qt, int nc,
+                               int grid, cudaStream_t s, bool pdl) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kQaThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto go = [&](auto fn, size_t smem) {
+    // (the limit belongs to the device's context: set on every call, a fraction of a microsecond)
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cfg.dynamicSmemBytes = smem;
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, fn, kmap, vmap, a);
+  };
+  if (qt) {
+    switch (nc) {
+      case 1: return go(qattn_tc_kernel<HD, 2, 1, 1>, QaShape<HD, 2, 1>::SMEM);
+      case 2: return go(qattn_tc_kernel<HD, 2, 2, 1>, QaShape<HD, 2, 2>::SMEM);
+      case 4: return go(qattn_tc_kernel<HD, 2, 4, 1>, QaShape<HD, 2, 4>::SMEM);
+    }
+  } else {
+    switch (nc) {
+      case 1: return go(qattn_tc_kernel<HD, 4, 1, 0>, QaShape<HD, 4, 1>::SMEM);
+      case 2: return go(qattn_tc_kernel<HD, 4, 2, 0>, QaShape<HD, 4, 2>::SMEM);
+      case 4: return go(qattn_tc_kernel<HD, 4, 4, 0>, QaShape<HD, 4, 4>::SMEM);
+      case 8: return go(qattn_tc_kernel<HD, 4, 8, 0>, QaShape<HD, 4, 8>::SMEM);
+    }
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_qattn_tc64(const CUtensorMap& kmap, const CUtensorMap& vmap, const QAttnArgs& a, int qt, int nc,
+                              int grid, cudaStream_t s, bool pdl);
+cudaError_t launch_qattn_tc128(const CUtensorMap& kmap, const CUtensorMap& vmap, const QAttnArgs& a, int qt, int nc,
+                               int grid, cudaStream_t s, bool pdl);
+
+}  // namespace llm

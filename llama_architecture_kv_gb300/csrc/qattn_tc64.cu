@@ -1,0 +1,11 @@
+// The tensor-core attention over an 8-bit cache, head size 64 (qattn_tc.cuh).
+#include "qattn_tc.cuh"
+
+namespace llm {
+
+cudaError_t launch_qattn_tc64(const CUtensorMap& kmap, const CUtensorMap& vmap, const QAttnArgs& a, int qt, int nc,
+                              int grid, cudaStream_t s, bool pdl) {
+  return launch_qattn_tc_hd<64>(kmap, vmap, a, qt, nc, grid, s, pdl);
+}
+
+}  // namespace llm

@@ -128,9 +128,18 @@ struct QAttnArgs {
   int32_t g;
   float scale;
   unsigned char* ws;      // workspace (qattn_workspace bytes): tickets zero between calls, then partials
+  const int32_t* tiles;   // a prefill pass's tiles (attention.cuh), of at most qattn_tile_tokens(g) tokens, or null
+  int32_t krow0;          // row of the cache's position 0 of (row 0, kv head 0) in the tensor maps (step calls)
   int32_t splits;         // set by launch_qattn
 };
+constexpr int kQattnTickets = 4096;  // bytes of tickets (one 32-bit word per CTA) before the partials
 uint64_t qattn_workspace(const QCacheView& c, int g, int B, int S, int num_sms);
-cudaError_t launch_qattn(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s, bool pdl);
+// kmap, vmap: tensor maps of qattn_make_map over the whole caches; null: made for this call
+cudaError_t launch_qattn(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s, bool pdl,
+                         const CUtensorMap* kmap = nullptr, const CUtensorMap* vmap = nullptr);
+bool qattn_uses_tc(int hd);
+bool qattn_make_map(CUtensorMap* map, const void* codes, int hd, uint64_t rows);
+// tokens of one sequence that share a tile of the tensor-core kernel (f32 queries)
+int qattn_tile_tokens(int g);
 
 }  // namespace llm
