@@ -279,7 +279,7 @@ TcPlanQ plan_tc_q(const QCacheView& c, int g, int qt, int64_t rows, int S, int l
   p.tokens = p.cols / g;
   const int64_t units = rows * ((S + p.tokens - 1) / p.tokens) * c.kv;
   const int64_t tiles = units * ((limit + kQaTile - 1) / kQaTile);
-  const int64_t ctas = std::min(num_sms * (p.nc <= 2 ? 2 : 1), kQattnTickets / 4);
+  const int64_t ctas = std::min(num_sms * (p.cols <= 8 ? 2 : 1), kQattnTickets / 4);
   p.grid = (int)std::max<int64_t>(1, std::min(tiles, ctas));
   return p;
 }

@@ -3,11 +3,12 @@
 //
 // The codes go from HBM to shared memory by TMA and from there into e4m3 MMAs as they are: no code
 // is ever widened.  The f32 (bf16) operands that meet them, queries and softmax weights, enter as NP
-// e4m3 pieces, x = 2^e (x_0 + x_1 / 16 + x_2 / 256 + ...), each piece the rounding of what the ones
-// before left over (four bits a piece: four pieces for f32, 2^-19 of a query's largest element and
-// 2^-16 of a weight; two for bf16, which hold a bf16 query's eight bits and a weight to 2^-8).  The
-// pieces are columns of their own, so every accumulator sums like with like in f32 and the powers of 16
-// are applied once, in registers.
+// e4m3 pieces, x = 2^e (x_0 + x_1 / 32 + x_2 / 32^2 + ...) with |x| / 2^e <= 256, each piece the
+// rounding of what the ones before left over (at most half a step, 8 of 256, so 32 times it is in
+// range again).  A piece takes four bits: four pieces leave 2^-16 of an element at worst, or 2^-33 of
+// the largest where it is tiny (f32); two hold a bf16 query's eight bits, and leave 2^-8 of a weight,
+// the rounding that a bf16 output makes itself (bf16).  The pieces are columns of their own, so every
+// accumulator sums like with like in f32 and the powers of 32 are applied once, in registers.
 //
 // A tile is 128 positions of one row and key/value head against up to C = 16 NC / NP columns, the
 // (token, query head) pairs of up to C / g tokens that share the codes:
@@ -17,8 +18,9 @@
 // With the positions on the M side a tile costs 8 MMAs however few columns there are, and a thread
 // writes its position's pieces with one 16-byte store per 16 columns (B's N-major layout).
 //
-// Running maxima are lazy: a column's reference moves only when a score exceeds it by 2^8 (pieces
-// reach 448, weights stay below 2^8), so the accumulators in tensor memory are hardly ever rescaled.
+// Running maxima are lazy: a column's reference is 2^5 below the largest weight it was taken from and
+// moves only when a weight exceeds 2^8, so the accumulators in tensor memory are hardly ever rescaled
+// and the pieces keep both the range above and the precision below.
 // The values' block scales ride on the weights, relative to the largest scale seen (also lazy).
 //
 // One CTA: a producer warp (TMA, a ring of tiles), a warp that issues the MMAs, and two groups of four
@@ -37,7 +39,8 @@ namespace llm {
 constexpr int kQaTile = 128;                       // positions per tile
 constexpr int kQaThreads = 320;                    // producer, MMA issuer, 2 x 4 softmax warps
 constexpr uint64_t kQaWaitCycles = 1000000000ull;  // about 0.5 s
-constexpr float kQaLazy = 8.0f;                    // log2 of how far a weight may exceed the reference
+constexpr float kQaTop = 5.0f;                     // log2 of the largest weight when a reference is taken
+constexpr float kQaMost = 8.0f;                    // log2 of the largest weight that moves no reference
 constexpr size_t kQaSmem = 232448;                 // shared memory a CTA can have
 
 template <int HD, int NP, int NC>
@@ -51,7 +54,7 @@ struct QaShape {
   static constexpr int PB = kQaTile * N;           // weight pieces of one group
   // two CTAs per SM where their tensor memory (4 N columns each) and rings fit: their segment ends
   // and starts overlap (measured: profiles/qcache_attention.md)
-  static constexpr int CTAS = NC <= 2 ? 2 : 1;
+  static constexpr int CTAS = C <= 8 ? 2 : 1;
   static constexpr size_t MISC = 4096;
   static constexpr size_t BUDGET = kQaSmem / CTAS - (CTAS > 1 ? 1024 : 0);
   static constexpr int FIT = (int)((BUDGET - QB - 2 * PB - MISC - 1024) / STAGE);
@@ -387,7 +390,7 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
         for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
         top = __reduce_max_sync(0xffffffffu, top);
         const bool fine = top < 0x7f800000u;
-        const float s = q_scale(fine ? __uint_as_float(top) : 0.f), r = q_recip(s);
+        const float s = q_scale(fine ? __uint_as_float(top) * 1.75f : 0.f), r = q_recip(s);  // |x| r <= 256
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] = fine ? x[e] * r : 0.f;
 #pragma unroll
@@ -398,8 +401,8 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
           for (int e = 0; e < E; e += 2) {
             const uint32_t p = e4m3x2(x[e], x[e + 1]);
             const float2 v = e4m3_pair(p);
-            x[e] = (x[e] - v.x) * 16.f;
-            x[e + 1] = (x[e + 1] - v.y) * 16.f;
+            x[e] = (x[e] - v.x) * 32.f;
+            x[e + 1] = (x[e + 1] - v.y) * 32.f;
             code |= p << (8 * e);
           }
           if constexpr (HD == 128)
@@ -417,12 +420,13 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
       named_sync(3, 256);
       if (stid == 0) mbar_arrive(b_q);
 
-      float ref[C], l[C];
+      // references of the group's columns, alike for all its threads
+      float* ref = gref + gp * C;
+      if ((stid & 127) < C) ref[stid & 127] = (stid & 127) < used ? -INFINITY : INFINITY;  // no token: weights 2^-inf
+      named_sync(1 + gp, 128);
+      float l[C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        ref[c] = c < used ? -INFINITY : INFINITY;  // a column without a token: weights 2^(0 - inf) = 0
-        l[c] = 0.f;
-      }
+      for (int c = 0; c < C; ++c) l[c] = 0.f;
       float vref = 0.f, vinv = 0.f;                // the largest value scale seen, and its reciprocal
       // the scales of this thread's position in tile t (0 and not good where it is not seen)
       auto scales = [&](int t, float& ks, float& vs) {
@@ -455,7 +459,7 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
           for (int c = 0; c < CPC; ++c) {
             float v = d[c * NP + NP - 1];
 #pragma unroll
-            for (int i = NP - 2; i >= 0; --i) v = fmaf(v, 0.0625f, d[c * NP + i]);
+            for (int i = NP - 2; i >= 0; --i) v = fmaf(v, 0.03125f, d[c * NP + i]);
             s[ch * CPC + c] = v * (ks * qsc[ch * CPC + c]);
           }
         }
@@ -468,17 +472,26 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
         }
         bool low = !(vs > vref);
 #pragma unroll
-        for (int c = 0; c < C; ++c) low = low && !(s[c] > ref[c] + kQaLazy);
+        for (int c = 0; c < C; ++c) low = low && !(s[c] > ref[c] + kQaMost);
         if (!named_sync_and(1 + gp, 128, low)) {
-          // references move (in every thread of the group alike)
+          // references move (rare): the group's maxima, then each column's new reference and what the
+          // sums relative to the old one are worth under it
+          float* wm = wmax + gp * 4 * C;
 #pragma unroll
           for (int c = 0; c < C; ++c) {
             const float m = warp_max(s[c]);
-            if (lane == 0) wmax[(gp * 4 + gw) * C + c] = m;
+            if (lane == 0) wm[gw * C + c] = m;
           }
           const float mv = warp_max(vs);
           if (lane == 0) wvs[gp * 4 + gw] = mv;
           named_sync(1 + gp, 128);
+          if ((stid & 127) < C) {
+            const int c = stid & 127;
+            const float old = ref[c];
+            const float top = fmaxf(old, fmaxf(fmaxf(wm[c], wm[C + c]), fmaxf(wm[2 * C + c], wm[3 * C + c])) - kQaTop);
+            ref[c] = top;
+            wm[c] = top == old ? 1.f : qa_exp2(old - top);
+          }
           const float v1 = fmaxf(fmaxf(wvs[gp * 4], wvs[gp * 4 + 1]), fmaxf(wvs[gp * 4 + 2], wvs[gp * 4 + 3]));
           float vcorr = 1.f;
           if (v1 > vref) {
@@ -486,16 +499,9 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
             vref = v1;
             vinv = q_recip(v1);
           }
-          float corr[C];
+          named_sync(1 + gp, 128);
 #pragma unroll
-          for (int c = 0; c < C; ++c) {
-            const float* m = wmax + gp * 4 * C + c;
-            const float top = fmaxf(ref[c], fmaxf(fmaxf(m[0], m[C]), fmaxf(m[2 * C], m[3 * C])));
-            corr[c] = top == ref[c] ? 1.f : qa_exp2(ref[c] - top);
-            ref[c] = top;
-            l[c] *= corr[c];
-            corr[c] *= vcorr;
-          }
+          for (int c = 0; c < C; ++c) l[c] *= wm[c];
           if (t > gp) {
             // the accumulators, once the product before is in them
             if (pend) {
@@ -510,7 +516,7 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
               tc_ld16(t_o + ch * 16, d);
               tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) d[i] *= corr[ch * CPC + i / NP];
+              for (int i = 0; i < 16; ++i) d[i] *= wm[ch * CPC + i / NP] * vcorr;
               tc_st16(t_o + ch * 16, d);
             }
             tc_wait_st();
@@ -547,8 +553,8 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
               x[i] = e4m3x2(x0, x1);
               if (i + 1 < NP) {
                 const float2 v = e4m3_pair(x[i]);
-                x0 = (x0 - v.x) * 16.f;
-                x1 = (x1 - v.y) * 16.f;
+                x0 = (x0 - v.x) * 32.f;
+                x1 = (x1 - v.y) * 32.f;
               }
             }
             if constexpr (NP == 4) {
@@ -587,7 +593,6 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
       for (int c = 0; c < C; ++c) {
         const float sum = warp_sum(l[c]);
         if (lane == 0) wmax[(gp * 4 + gw) * C + c] = sum;
-        if (lane == 0 && gw == 0) gref[gp * C + c] = ref[c];
       }
       if (lane == 0 && gw == 0) gvs[gp] = vref;
       named_sync(3, 256);  // (both groups' products are done: the weights' buffers are free)
@@ -598,7 +603,7 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
       auto column = [&](const float (&d)[16], int c) {
         float v = d[c * NP + NP - 1];
 #pragma unroll
-        for (int i = NP - 2; i >= 0; --i) v = fmaf(v, 0.0625f, d[c * NP + i]);
+        for (int i = NP - 2; i >= 0; --i) v = fmaf(v, 0.03125f, d[c * NP + i]);
         return v * vref;
       };
       if (gp == 1 && both) {
