@@ -323,55 +323,49 @@ def llm_sample_noalloc(logits, B, V, temp, k, p, u, ids, stream=None):
 
 
 # ---- operators on torch CUDA tensors, without a handle (include/llm.h) --------------------
-# Shapes, types, contiguity and the device are checked here; the library checks the rest.
+# Shapes, types, contiguity and the device are checked here; the library checks the rest.  A call on
+# small tensors is bound by this host code, so the checks read plain attributes and build no text.
+
+_torch = None
+
+
+def _need_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
 
 def _refused(name, st):
     why = lib().llm_last_error(None)
     raise LlmError(st, f"{name}: {lib().llm_status_string(st).decode()}: {why.decode() if why else ''}")
 
 
-def _need(ok, what):
-    if not ok:
-        raise LlmError(LLM_ERR_ARG, what)
+def _bad(what):
+    raise LlmError(LLM_ERR_ARG, what)
 
 
-def _int32(t, name, device, shape):
-    """The address of an int32 tensor of the given shape (None: 0)."""
+def _int32(t, name, dev, n):
+    """The address of a contiguous int32 tensor of n elements on CUDA device dev (None: 0)."""
     if t is None:
         return None
-    _need(str(t.dtype) == "torch.int32" and t.device == device and t.is_contiguous() and tuple(t.shape) == shape,
-          f"{name} must be a contiguous int32 tensor {shape} on {device}")
+    if t.dtype is not _torch.int32 or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+        _bad(f"{name} must be a contiguous int32 tensor of {n} elements on cuda:{dev}")
     return t.data_ptr()
 
 
-def _here(device):
-    """Launches go to the current device, which has to be the tensors' own."""
-    import torch
-    _need(device.type == "cuda" and device.index == torch.cuda.current_device(),
-          f"tensors on {device} while the current CUDA device is another")
-
-
-def _rows(t, name, device, dtype, shape):
-    """Token rows [B, S, heads, head] (or [B, S, heads * head]) of one type: the address and the
-    distance between tokens in elements; rows of a wider tensor may be given as a slice."""
-    import torch
-    B, S, width = shape
-    heads = t.dim() == 4
-    _need(t.dim() in (3, 4) and t.device == device and t.dtype in (torch.float32, torch.bfloat16)
-          and (dtype is None or t.dtype == dtype), f"{name} must be f32 or bf16 rows on {device}, all of one type")
-    _need(t.shape[0] == B and t.shape[1] == S and t.numel() == B * S * width,
-          f"{name} must hold {B} x {S} rows of {width} elements, not {tuple(t.shape)}")
-    st = t.stride()
-    _need(st[-1] == 1 and (not heads or st[2] == t.shape[3] or t.shape[2] == 1),
-          f"{name}: the elements of a row must be contiguous")
+def _rows(t, name, dev, B, S, width):
+    """Token rows [B, S, heads, head] (or [B, S, heads * head]): the address and the distance between
+    tokens in elements; rows of a wider tensor may be given as a slice."""
+    shape, st = t.shape, t.stride()
+    if t.get_device() != dev or len(shape) not in (3, 4) or shape[0] != B or shape[1] != S or t.numel() != B * S * width:
+        _bad(f"{name} must hold {B} x {S} rows of {width} elements on cuda:{dev}, not {tuple(shape)}")
     # (the stride of a dimension of size 1 carries no meaning)
     step = st[1] if S > 1 else st[0] if B > 1 else width
-    _need(B == 1 or S == 1 or st[0] == S * step, f"{name}: rows must be evenly spaced")
+    if st[-1] != 1 or (len(shape) == 4 and shape[2] > 1 and st[2] != shape[3]) or (B > 1 and S > 1 and st[0] != S * step):
+        _bad(f"{name}: the elements of a row must be contiguous and the rows evenly spaced")
     return t.data_ptr(), step
-
-
-def _bf16(t):
-    return LLM_DTYPE_BF16 if t.element_size() == 2 else LLM_DTYPE_F32
 
 
 class QCache:
@@ -379,106 +373,141 @@ class QCache:
     (uint8 or float8_e4m3fn) and scales [rows, kv_heads, max_seq // 16] (float32), all zeroed before
     their first use.  The tensors stay the caller's; calls are ordered on `stream` (a cudaStream_t,
     None: the legacy default stream) and return without waiting.  `pos`, `length`, `count` [B] and
-    `table` [B, pages] are int32 CUDA tensors, `status` one int32."""
+    `table` [B, pages] are int32 CUDA tensors, `status` one int32; rows of tokens are f32 or bf16."""
 
     def __init__(self, k, v, k_scale, v_scale):
-        for t, name in ((k, "k"), (v, "v")):
-            _need(t.dim() == 4 and str(t.dtype) in ("torch.uint8", "torch.float8_e4m3fn") and t.is_contiguous()
-                  and t.device == k.device and t.shape == k.shape,
-                  f"{name} must be contiguous codes [rows, kv_heads, max_seq, head] (uint8 or float8_e4m3fn)")
+        torch = _need_torch()
+        if k.dim() != 4 or not k.is_cuda:
+            _bad("k must be codes [rows, kv_heads, max_seq, head] in CUDA memory")
         rows, kv, cap, hd = k.shape
+        for t, name in ((k, "k"), (v, "v")):
+            if t.dtype not in (torch.uint8, torch.float8_e4m3fn) or not t.is_contiguous() or t.device != k.device or t.shape != k.shape:
+                _bad(f"{name} must be contiguous codes [rows, kv_heads, max_seq, head] (uint8 or float8_e4m3fn)")
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            _need(tuple(t.shape) == (rows, kv, cap // 16) and str(t.dtype) == "torch.float32" and t.is_contiguous()
-                  and t.device == k.device, f"{name} must be contiguous float32 [rows, kv_heads, max_seq // 16]")
-        _need(k.is_cuda, "a cache lies in CUDA memory")
+            if tuple(t.shape) != (rows, kv, cap // 16) or t.dtype != torch.float32 or not t.is_contiguous() or t.device != k.device:
+                _bad(f"{name} must be contiguous float32 [rows, kv_heads, max_seq // 16] beside the codes")
         self.tensors = (k, v, k_scale, v_scale)  # kept alive with the addresses below
         self.device, self.kv, self.hd = k.device, kv, hd
+        self._dev, self._scale = k.get_device(), hd ** -0.5
         self.c = LlmQcache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), rows, kv, cap, hd)
-        self._c = ctypes.byref(self.c)
+        self._c, self._lib = ctypes.byref(self.c), lib()
+        self._f32, self._bf16 = torch.float32, torch.bfloat16
 
     @classmethod
     def empty(cls, rows, kv_heads, max_seq, head, device="cuda"):
         """A zeroed cache in new tensors."""
-        import torch
+        torch = _need_torch()
         code = lambda: torch.zeros(rows, kv_heads, max_seq, head, dtype=torch.uint8, device=device)  # noqa: E731
         scale = lambda: torch.zeros(rows, kv_heads, max_seq // 16, device=device)  # noqa: E731
         return cls(code(), code(), scale(), scale())
 
-    def _call_rows(self, B, S, first, name, count, table, status):
-        _here(self.device)
-        _need(first is not None, f"{name} is missing")
-        return (_int32(first, name, self.device, (B,)), _int32(count, "count", self.device, (B,)),
-                _int32(table, "table", self.device, (B, table.shape[1]) if table is not None and table.dim() == 2 else ()),
-                0 if table is None else table.shape[1],
-                None if status is None else _int32(status, "status", self.device, tuple(status.shape)[:1] if status.numel() == 1 else ()))
+    def _dtype(self, a, b):
+        t = a.dtype
+        if b.dtype is not t or (t is not self._f32 and t is not self._bf16):
+            _bad("rows must be f32 or bf16, all of one type")
+        return LLM_DTYPE_F32 if t is self._f32 else LLM_DTYPE_BF16
+
+    def _call_rows(self, B, first, name, count, table, status):
+        """Addresses of positions (or lengths), counts, pages and the status word, and the pages per row."""
+        dev = self._dev
+        if _torch.cuda.current_device() != dev:
+            _bad(f"the cache lies on cuda:{dev} and another CUDA device is current")
+        if first is None:
+            _bad(f"{name} is missing")
+        pages = 0
+        if table is not None:
+            if table.dim() != 2 or table.shape[0] != B:
+                _bad(f"table must be [{B}, pages]")
+            pages = table.shape[1]
+        return (_int32(first, name, dev, B), None if count is None else _int32(count, "count", dev, B),
+                None if table is None else _int32(table, "table", dev, B * pages), pages,
+                None if status is None else _int32(status, "status", dev, 1))
 
     def write(self, k, v, pos, count=None, table=None, status=None, stream=None):
         """Keys and values [B, S, kv_heads, head] at positions pos[b] + i of row b (llm_qcache_write)."""
-        B, S = k.shape[0], k.shape[1]
-        first, count, table, pages, status = self._call_rows(B, S, pos, "pos", count, table, status)
-        kp, step = _rows(k, "k", self.device, None, (B, S, self.kv * self.hd))
-        vp, vstep = _rows(v, "v", self.device, k.dtype, (B, S, self.kv * self.hd))
-        _need(step == vstep, "k and v must have the same row stride")
-        st = lib().llm_qcache_write(self._c, kp, vp, _bf16(k), step, B, S, first, count, table, pages, status, stream)
+        B, S = k.shape[:2]
+        first, count, table, pages, status = self._call_rows(B, pos, "pos", count, table, status)
+        width = self.kv * self.hd
+        kp, step = _rows(k, "k", self._dev, B, S, width)
+        vp, vstep = _rows(v, "v", self._dev, B, S, width)
+        if step != vstep:
+            _bad("k and v must have the same row stride")
+        st = self._lib.llm_qcache_write(self._c, kp, vp, self._dtype(k, v), step, B, S, first, count, table, pages, status,
+                                        stream)
         if st != LLM_OK:
             _refused("llm_qcache_write", st)
 
     def read(self, pos, k, v, count=None, table=None, status=None, stream=None):
         """Positions pos[b] + i of row b into k and v [B, S, kv_heads, head] (llm_qcache_read)."""
-        B, S = k.shape[0], k.shape[1]
-        first, count, table, pages, status = self._call_rows(B, S, pos, "pos", count, table, status)
-        kp, step = _rows(k, "k", self.device, None, (B, S, self.kv * self.hd))
-        vp, vstep = _rows(v, "v", self.device, k.dtype, (B, S, self.kv * self.hd))
-        _need(step == vstep, "k and v must have the same row stride")
-        st = lib().llm_qcache_read(self._c, B, S, first, count, table, pages, kp, vp, _bf16(k), step, status, stream)
+        B, S = k.shape[:2]
+        first, count, table, pages, status = self._call_rows(B, pos, "pos", count, table, status)
+        width = self.kv * self.hd
+        kp, step = _rows(k, "k", self._dev, B, S, width)
+        vp, vstep = _rows(v, "v", self._dev, B, S, width)
+        if step != vstep:
+            _bad("k and v must have the same row stride")
+        st = self._lib.llm_qcache_read(self._c, B, S, first, count, table, pages, kp, vp, self._dtype(k, v), step, status,
+                                       stream)
         if st != LLM_OK:
             _refused("llm_qcache_read", st)
 
     def workspace(self, group, B, S):
         """A zeroed workspace for attend() with this group, rows and tokens per row."""
-        import torch
-        _here(self.device)
+        if _torch.cuda.current_device() != self._dev:
+            _bad(f"the cache lies on cuda:{self._dev} and another CUDA device is current")
         n = ctypes.c_uint64()
-        st = lib().llm_qcache_workspace(self._c, group, B, S, ctypes.byref(n))
+        st = self._lib.llm_qcache_workspace(self._c, group, B, S, ctypes.byref(n))
         if st != LLM_OK:
             _refused("llm_qcache_workspace", st)
-        return torch.zeros(max(16, n.value), dtype=torch.uint8, device=self.device)
+        return _torch.zeros(max(16, n.value), dtype=_torch.uint8, device=self.device)
 
     def attend(self, q, length, out, workspace, count=None, table=None, scale=None, status=None, stream=None):
         """Attention of q [B, S, heads, head] over the first length[b] positions of row b, the tokens
         themselves being the last of them, into out (llm_qcache_attend); scale defaults to
         head ** -0.5."""
-        B, S = q.shape[0], q.shape[1]
-        width = q.numel() // (B * S) if B * S else 0
-        group = width // (self.kv * self.hd)
-        _need(group * self.kv * self.hd == width and width > 0, "q must hold a whole number of heads per key/value head")
-        first, count, table, pages, status = self._call_rows(B, S, length, "length", count, table, status)
-        qp, qstep = _rows(q, "q", self.device, None, (B, S, width))
-        op, ostep = _rows(out, "out", self.device, q.dtype, (B, S, width))
-        _need(workspace.device == self.device and workspace.is_contiguous(), "workspace must be contiguous CUDA memory")
-        st = lib().llm_qcache_attend(self._c, qp, _bf16(q), qstep, group, B, S, first, count, table, pages,
-                                     self.hd ** -0.5 if scale is None else scale, op, ostep, workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), status, stream)
+        B, S = q.shape[:2]
+        per = self.kv * self.hd
+        n = q.numel()
+        group = n // (B * S * per) if B * S else 0
+        if n != B * S * group * per:
+            _bad("q must hold a whole number of heads per key/value head")
+        first, count, table, pages, status = self._call_rows(B, length, "length", count, table, status)
+        qp, qstep = _rows(q, "q", self._dev, B, S, group * per)
+        op, ostep = _rows(out, "out", self._dev, B, S, group * per)
+        if workspace.get_device() != self._dev or not workspace.is_contiguous():
+            _bad("workspace must be contiguous CUDA memory beside the cache")
+        st = self._lib.llm_qcache_attend(self._c, qp, self._dtype(q, out), qstep, group, B, S, first, count, table, pages,
+                                         self._scale if scale is None else scale, op, ostep, workspace.data_ptr(),
+                                         workspace.numel() * workspace.element_size(), status, stream)
         if st != LLM_OK:
             _refused("llm_qcache_attend", st)
+
+
+def _f32s(t, name, dev, n):
+    if t.dtype is not _torch.float32 or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+        _bad(f"{name} must be a contiguous float32 tensor of {n} elements on cuda:{dev}")
+    return t.data_ptr()
 
 
 def llm_verify(p, q, drafts, u, ids, accepted, count=None, stream=None):
     """Verification of drafts [B, S] against the target's probabilities p [B, S + 1, V], the draft
     model's q [B, S, V] (None: deterministic drafts) and draws u [B, S + 1], into ids [B, S + 1] and
     accepted [B] (see include/llm.h); CUDA tensors, f32 and int32."""
-    import torch
-    _need(drafts.dim() == 2 and p.dim() == 3, "drafts must be [B, S] and p [B, S + 1, V]")
-    (B, S), V, dev = drafts.shape, p.shape[2], p.device
-    _here(dev)
-    for t, name, shape in ((p, "p", (B, S + 1, V)), (q, "q", (B, S, V)), (u, "u", (B, S + 1))):
-        _need((t is None and name == "q") or (t is not None and tuple(t.shape) == shape and t.dtype == torch.float32
-                                              and t.is_contiguous() and t.device == dev),
-              f"{name} must be a contiguous float32 tensor {shape} on {dev}")
-    _need(ids is not None and accepted is not None, "ids and accepted are missing")
-    st = lib().llm_verify(p.data_ptr(), None if q is None else q.data_ptr(), _int32(drafts, "drafts", dev, (B, S)),
-                          _int32(count, "count", dev, (B,)), B, S, V, u.data_ptr(), _int32(ids, "ids", dev, (B, S + 1)),
-                          _int32(accepted, "accepted", dev, (B,)), stream)
+    torch = _torch or _need_torch()
+    if drafts.dim() != 2 or p.dim() != 3:
+        _bad("drafts must be [B, S] and p [B, S + 1, V]")
+    B, S = drafts.shape
+    V, dev = p.shape[2], p.get_device()
+    if dev < 0 or torch.cuda.current_device() != dev:
+        _bad("p must lie on the current CUDA device")
+    if p.shape[0] != B or p.shape[1] != S + 1 or (q is not None and tuple(q.shape) != (B, S, V)):
+        _bad("p must be [B, S + 1, V] and q [B, S, V]")
+    if ids is None or accepted is None or drafts is None:
+        _bad("ids and accepted are missing")
+    st = lib().llm_verify(_f32s(p, "p", dev, B * (S + 1) * V), None if q is None else _f32s(q, "q", dev, B * S * V),
+                          _int32(drafts, "drafts", dev, B * S), None if count is None else _int32(count, "count", dev, B),
+                          B, S, V, _f32s(u, "u", dev, B * (S + 1)), _int32(ids, "ids", dev, B * (S + 1)),
+                          _int32(accepted, "accepted", dev, B), stream)
     if st != LLM_OK:
         _refused("llm_verify", st)
 

@@ -12,7 +12,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libllm.so")
 SOURCES = ["llm.cu", "gemv.cu", "gemm.cu", "attention.cu", "sampler.cu", "noalloc.cu", "mega.cu", "qcache.cu",
-           "qattn.cu", "qattn_tc64.cu", "qattn_tc128.cu", "verify.cu", "ops.cu"]
+           "qattn.cu", "verify.cu", "ops.cu"]
+# the longest first
+SOURCES = [f"qattn_tc{hd}_{t}.cu" for t in ("f32", "f32_wide", "bf16") for hd in (128, 64)] + SOURCES
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE]
 

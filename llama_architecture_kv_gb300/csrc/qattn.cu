@@ -323,8 +323,10 @@ cudaError_t launch_qattn(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s
     const int S = a.tiles ? qattn_tile_tokens(a.g) : a.r.S;  // (a tile is a row of its own)
     // (a page table can name a page more than once: rows longer than the pool get no more CTAs)
     const TcPlanQ p = plan_tc_q(a.c, a.g, qt, a.r.B, S, std::min(a.r.limit, a.c.rows * a.c.cap), num_sms);
-    return a.c.hd == 64 ? launch_qattn_tc64(*kmap, *vmap, a, qt, p.nc, p.grid, s, pdl)
-                        : launch_qattn_tc128(*kmap, *vmap, a, qt, p.nc, p.grid, s, pdl);
+    const bool wide = !qt && p.nc == 8;
+    auto fn = a.c.hd == 64 ? (qt ? qattn_tc64_bf16 : wide ? qattn_tc64_f32_wide : qattn_tc64_f32)
+                           : (qt ? qattn_tc128_bf16 : wide ? qattn_tc128_f32_wide : qattn_tc128_f32);
+    return fn(*kmap, *vmap, a, p.nc, p.grid, s, pdl);
   }
   switch (a.c.hd) {
     case 16: return qt ? launch_simple<16, 1>(a, num_sms, s, pdl) : launch_simple<16, 0>(a, num_sms, s, pdl);

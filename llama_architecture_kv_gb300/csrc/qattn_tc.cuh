@@ -619,119 +619,153 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
         }
       }
       if (both) named_sync(3, 256);
-      if (gp == 1) continue;
       const bool alone = w.k0 == 0 && w.k1 == w.u.nt;  // this CTA holds the whole unit
+      // parts of units cut across CTAs: [CTA][the unit's first part?]{[C][HD] sums, [C] (reference, weight)}
       float* parts = reinterpret_cast<float*>(a.ws + kQattnTickets);
-      float* mine = parts + ((size_t)cta * 2 + (w.k0 == 0 ? 1 : 0)) * C * (HD + 2);
       auto out_at = [&](int c) { return (w.u.qrow + c / a.g) * a.out_stride + (int64_t)(w.j * a.g + c % a.g) * HD; };
-      auto put = [&](int c, int e, float v) {
-        if constexpr (QT) static_cast<uint16_t*>(a.out)[out_at(c) + e] = f32_to_bf16(v);
-        else static_cast<float*>(a.out)[out_at(c) + e] = v;
-      };
+      auto owner = [&](long long i) { return (int)(((i + 1) * G + T - 1) / T - 1); };
+      if (gp == 0) {
+        float* mine = parts + ((size_t)cta * 2 + (w.k0 == 0 ? 1 : 0)) * C * (HD + 2);
 #pragma unroll
-      for (int ch = 0; ch < NC; ++ch) {
-        if (ch * CPC >= used) break;
-        float d[16];
-        tc_ld16(t_o + ch * 16, d);
-        tc_wait_ld();
+        for (int ch = 0; ch < NC; ++ch) {
+          if (ch * CPC >= used) break;
+          float d[16];
+          tc_ld16(t_o + ch * 16, d);
+          tc_wait_ld();
 #pragma unroll
-        for (int cc = 0; cc < CPC; ++cc) {
-          const int c = ch * CPC + cc;
-          if (c >= used) break;
-          const float l0 = wmax[c] + wmax[C + c] + wmax[2 * C + c] + wmax[3 * C + c];
-          const float r0 = gref[c];
-          float M = r0, L = l0, f0 = 1.f, O = column(d, cc);
-          if (both) {
-            const float l1 = wmax[4 * C + c] + wmax[5 * C + c] + wmax[6 * C + c] + wmax[7 * C + c];
-            const float r1 = gref[C + c];
-            M = fmaxf(r0, r1);
-            // (sums without a reference are 0, or NaN, which has to stay)
-            f0 = r0 == -INFINITY ? (l0 == 0.f ? 0.f : 1.f) : qa_exp2(r0 - M);
-            const float f1 = r1 == -INFINITY ? (l1 == 0.f ? 0.f : 1.f) : qa_exp2(r1 - M);
-            L = fmaf(l0, f0, l1 * f1);
-            O = fmaf(O, f0, (d_on ? other[c * HD + d_row] : 0.f) * f1);
-          }
-          if (d_on) {
-            if (alone) {
-              put(c, d_row, L == 0.f ? 0.f : O / L);
-            } else {
-              mine[c * (HD + 2) + d_row] = O;
-              if (d_row == 0) {
-                mine[c * (HD + 2) + HD] = M;
-                mine[c * (HD + 2) + HD + 1] = L;
+          for (int cc = 0; cc < CPC; ++cc) {
+            const int c = ch * CPC + cc;
+            if (c >= used) break;
+            const float l0 = wmax[c] + wmax[C + c] + wmax[2 * C + c] + wmax[3 * C + c];
+            const float r0 = gref[c];
+            float M = r0, L = l0, O = column(d, cc);
+            if (both) {
+              const float l1 = wmax[4 * C + c] + wmax[5 * C + c] + wmax[6 * C + c] + wmax[7 * C + c];
+              const float r1 = gref[C + c];
+              M = fmaxf(r0, r1);
+              // (sums without a reference are 0, or NaN, which has to stay)
+              const float f0 = r0 == -INFINITY ? (l0 == 0.f ? 0.f : 1.f) : qa_exp2(r0 - M);
+              const float f1 = r1 == -INFINITY ? (l1 == 0.f ? 0.f : 1.f) : qa_exp2(r1 - M);
+              L = fmaf(l0, f0, l1 * f1);
+              O = fmaf(O, f0, (d_on ? other[c * HD + d_row] : 0.f) * f1);
+            }
+            if (d_on) {
+              if (alone) {
+                O = L == 0.f ? 0.f : O / L;
+                if constexpr (QT) static_cast<uint16_t*>(a.out)[out_at(c) + d_row] = f32_to_bf16(O);
+                else static_cast<float*>(a.out)[out_at(c) + d_row] = O;
+              } else {
+                mine[c * HD + d_row] = O;
+                if (d_row == 0) *reinterpret_cast<float2*>(mine + C * HD + 2 * c) = make_float2(M, L);
               }
             }
+          }
+        }
+        if (!alone) {
+          __threadfence();
+          named_sync(1, 128);
+          if (stid == 0) {
+            const int first = owner(w.unit0()), last = owner(w.unit0() + w.u.nt - 1);
+            s_last = atomicInc(reinterpret_cast<uint32_t*>(a.ws) + first, (uint32_t)(last - first)) == (uint32_t)(last - first);
           }
         }
       }
       if (alone) continue;
       // ---- a unit of several CTAs: the last of them to get here adds the parts in CTA order ----
-      auto owner = [&](long long i) { return (int)(((i + 1) * G + T - 1) / T - 1); };
-      const int first = owner(w.unit0()), np = owner(w.unit0() + w.u.nt - 1) - first + 1;
-      __threadfence();
-      named_sync(1, 128);
-      if (stid == 0) s_last = atomicInc(reinterpret_cast<uint32_t*>(a.ws) + first, (uint32_t)(np - 1)) == (uint32_t)(np - 1);
-      named_sync(1, 128);
+      named_sync(3, 256);
       if (!s_last) continue;
       __threadfence();
-      auto part = [&](int i, int c) { return parts + (((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * C + c) * (HD + 2); };
+      const int first = owner(w.unit0()), np = owner(w.unit0() + w.u.nt - 1) - first + 1;
+      auto part = [&](int i) { return parts + ((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * C * (HD + 2); };
+      auto stat = [&](int i, int c) { return __ldcg(reinterpret_cast<const float2*>(part(i) + C * HD + 2 * c)); };
+      auto factor = [&](float2 ml, float M) { return ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : qa_exp2(ml.x - M); };
       float* fac = reinterpret_cast<float*>(pbuf);  // [C][64] factors of 64 parts at a time
-      for (int c = gw; c < used; c += 4) {          // maxima: warp = column, lanes = parts
-        float m = -INFINITY;
-        for (int i = lane; i < np; i += 32) m = fmaxf(m, __ldcg(part(i, c) + HD));
-        m = warp_max(m);
-        if (lane == 0) gref[c] = m;
+      constexpr int CW = (C + 7) / 8;               // columns of a warp; its lanes take the parts
+      float M[CW], L[CW];
+#pragma unroll
+      for (int q = 0; q < CW; ++q) {
+        const int c = sw + 8 * q;
+        M[q] = -INFINITY;
+        L[q] = 0.f;
+        if (c < used) {
+          const float2 none = make_float2(-INFINITY, 0.f);
+          const float2 x0 = lane < np ? stat(lane, c) : none, x1 = lane + 32 < np ? stat(lane + 32, c) : none;
+          M[q] = fmaxf(x0.x, x1.x);
+          for (int i = lane + 64; i < np; i += 32) M[q] = fmaxf(M[q], stat(i, c).x);
+          M[q] = warp_max(M[q]);
+          const float f0 = factor(x0, M[q]), f1 = factor(x1, M[q]);
+          fac[c * 64 + lane] = f0;
+          fac[c * 64 + lane + 32] = f1;
+          L[q] = fmaf(x0.y, f0, x1.y * f1);
+        }
       }
-      __syncwarp();
-      // threads own (column, dimension) pairs in strides of 128
-      constexpr int PER = C * HD / 128;
-      float O[PER];
+      // threads own groups of four dimensions of a column, in strides of 256
+      constexpr int PER = (C * HD / 4 + 255) / 256, U = PER > 2 ? 4 : 8;  // U parts' loads in flight for each
+      float4 O[PER];
 #pragma unroll
-      for (int q = 0; q < PER; ++q) O[q] = 0.f;
-      float Lw[(C + 3) / 4];                        // this warp's columns' sums, lane by lane
-#pragma unroll
-      for (int q = 0; q < (C + 3) / 4; ++q) Lw[q] = 0.f;
+      for (int q = 0; q < PER; ++q) O[q] = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int i0 = 0; i0 < np; i0 += 64) {
         const int m = min(64, np - i0);
-        named_sync(1, 128);
+        if (i0 > 0) {
+          named_sync(3, 256);
 #pragma unroll
-        for (int q = 0; q < (C + 3) / 4; ++q) {
-          const int c = gw + 4 * q;
-          if (c < used)
-            for (int i = lane; i < m; i += 32) {
-              const float mi = __ldcg(part(i0 + i, c) + HD), li = __ldcg(part(i0 + i, c) + HD + 1);
-              const float f = mi == -INFINITY ? (li == 0.f ? 0.f : 1.f) : qa_exp2(mi - gref[c]);
-              fac[c * 64 + i] = f;
-              Lw[q] = fmaf(li, f, Lw[q]);
-            }
-        }
-        named_sync(1, 128);
-#pragma unroll
-        for (int q = 0; q < PER; ++q) {
-          const int x = q * 128 + stid, c = x / HD, e = x % HD;
-          if (c < used) {
-            int i = 0;
-            for (; i + 8 <= m; i += 8) {
-              float v[8];
-#pragma unroll
-              for (int y = 0; y < 8; ++y) v[y] = __ldcg(part(i0 + i + y, c) + e);
-#pragma unroll
-              for (int y = 0; y < 8; ++y) O[q] = fmaf(fac[c * 64 + i + y], v[y], O[q]);
-            }
-            for (; i < m; ++i) O[q] = fmaf(fac[c * 64 + i], __ldcg(part(i0 + i, c) + e), O[q]);
+          for (int q = 0; q < CW; ++q) {
+            const int c = sw + 8 * q;
+            if (c < used)
+              for (int i = lane; i < m; i += 32) {
+                const float2 x = stat(i0 + i, c);
+                const float f = factor(x, M[q]);
+                fac[c * 64 + i] = f;
+                L[q] = fmaf(x.y, f, L[q]);
+              }
           }
         }
+        named_sync(3, 256);
+        for (int i = 0; i < m; i += U) {
+          float4 v[PER][U];
+#pragma unroll
+          for (int q = 0; q < PER; ++q)
+#pragma unroll
+            for (int y = 0; y < U; ++y) {
+              const int x = q * 256 + stid;
+              v[q][y] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (x < used * (HD / 4) && i + y < m) v[q][y] = __ldcg(reinterpret_cast<const float4*>(part(i0 + i + y)) + x);
+            }
+#pragma unroll
+          for (int q = 0; q < PER; ++q)
+#pragma unroll
+            for (int y = 0; y < U; ++y) {
+              const int x = q * 256 + stid;
+              if (x < used * (HD / 4) && i + y < m) {
+                const float f = fac[x / (HD / 4) * 64 + i + y];
+                O[q].x = fmaf(f, v[q][y].x, O[q].x);
+                O[q].y = fmaf(f, v[q][y].y, O[q].y);
+                O[q].z = fmaf(f, v[q][y].z, O[q].z);
+                O[q].w = fmaf(f, v[q][y].w, O[q].w);
+              }
+            }
+        }
       }
 #pragma unroll
-      for (int q = 0; q < (C + 3) / 4; ++q) {
-        const float L = warp_sum(Lw[q]);
-        if (lane == 0 && gw + 4 * q < C) gref[C + gw + 4 * q] = L;
+      for (int q = 0; q < CW; ++q) {
+        const float sum = warp_sum(L[q]);
+        if (lane == 0 && sw + 8 * q < C) wmax[sw + 8 * q] = sum;
       }
-      named_sync(1, 128);
+      named_sync(3, 256);
 #pragma unroll
       for (int q = 0; q < PER; ++q) {
-        const int x = q * 128 + stid, c = x / HD, e = x % HD;
-        if (c < used) put(c, e, gref[C + c] == 0.f ? 0.f : O[q] / gref[C + c]);
+        const int x = q * 256 + stid, c = x / (HD / 4), e = x % (HD / 4) * 4;
+        if (c < used) {
+          const float r = wmax[c] == 0.f ? 0.f : 1.f / wmax[c];
+          const float4 o = make_float4(O[q].x * r, O[q].y * r, O[q].z * r, O[q].w * r);
+          if constexpr (QT) {
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_at(c) + e) =
+                make_uint2((uint32_t)f32_to_bf16(o.x) | (uint32_t)f32_to_bf16(o.y) << 16,
+                           (uint32_t)f32_to_bf16(o.z) | (uint32_t)f32_to_bf16(o.w) << 16);
+          } else {
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + out_at(c) + e) = o;
+          }
+        }
       }
     }
   }
@@ -742,45 +776,36 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
   if (warp == 1) tmem_dealloc(tmem, 4 * N);
 }
 
-// launch for one head size; false results are CUDA errors
-template <int HD>
-cudaError_t launch_qattn_tc_hd(const CUtensorMap& kmap, const CUtensorMap& vmap, const QAttnArgs& a, int qt, int nc,
-                               int grid, cudaStream_t s, bool pdl) {
+// one instantiation per translation unit (they take half a minute each to compile)
+template <int HD, int NP, int NC, int QT>
+cudaError_t launch_qattn_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const QAttnArgs& a, int grid,
+                            cudaStream_t s, bool pdl) {
+  constexpr size_t smem = QaShape<HD, NP, NC>::SMEM;
+  auto fn = qattn_tc_kernel<HD, NP, NC, QT>;
+  // (the limit belongs to the device's context: set on every call, a fraction of a microsecond)
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kQaThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto go = [&](auto fn, size_t smem) {
-    // (the limit belongs to the device's context: set on every call, a fraction of a microsecond)
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    cfg.dynamicSmemBytes = smem;
-    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, fn, kmap, vmap, a);
-  };
-  if (qt) {
-    switch (nc) {
-      case 1: return go(qattn_tc_kernel<HD, 2, 1, 1>, QaShape<HD, 2, 1>::SMEM);
-      case 2: return go(qattn_tc_kernel<HD, 2, 2, 1>, QaShape<HD, 2, 2>::SMEM);
-      case 4: return go(qattn_tc_kernel<HD, 2, 4, 1>, QaShape<HD, 2, 4>::SMEM);
-    }
-  } else {
-    switch (nc) {
-      case 1: return go(qattn_tc_kernel<HD, 4, 1, 0>, QaShape<HD, 4, 1>::SMEM);
-      case 2: return go(qattn_tc_kernel<HD, 4, 2, 0>, QaShape<HD, 4, 2>::SMEM);
-      case 4: return go(qattn_tc_kernel<HD, 4, 4, 0>, QaShape<HD, 4, 4>::SMEM);
-      case 8: return go(qattn_tc_kernel<HD, 4, 8, 0>, QaShape<HD, 4, 8>::SMEM);
-    }
-  }
-  return cudaErrorInvalidValue;
+  return cudaLaunchKernelEx(&cfg, fn, kmap, vmap, a);
 }
 
-cudaError_t launch_qattn_tc64(const CUtensorMap& kmap, const CUtensorMap& vmap, const QAttnArgs& a, int qt, int nc,
-                              int grid, cudaStream_t s, bool pdl);
-cudaError_t launch_qattn_tc128(const CUtensorMap& kmap, const CUtensorMap& vmap, const QAttnArgs& a, int qt, int nc,
-                               int grid, cudaStream_t s, bool pdl);
+#define LLM_QATTN_TC(NAME) \
+  cudaError_t NAME(const CUtensorMap& kmap, const CUtensorMap& vmap, const QAttnArgs& a, int nc, int grid, \
+                   cudaStream_t s, bool pdl)
+LLM_QATTN_TC(qattn_tc64_f32);
+LLM_QATTN_TC(qattn_tc64_f32_wide);
+LLM_QATTN_TC(qattn_tc64_bf16);
+LLM_QATTN_TC(qattn_tc128_f32);
+LLM_QATTN_TC(qattn_tc128_f32_wide);
+LLM_QATTN_TC(qattn_tc128_bf16);
 
 }  // namespace llm

@@ -1,0 +1,12 @@
+// The tensor-core attention over an 8-bit cache: head size 128, f32 queries, 128 accumulator
+// columns (qattn_tc.cuh).
+#include "qattn_tc.cuh"
+
+namespace llm {
+
+LLM_QATTN_TC(qattn_tc128_f32_wide) {
+  if (nc == 8) return launch_qattn_tc<128, 4, 8, 0>(kmap, vmap, a, grid, s, pdl);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace llm
