@@ -23,12 +23,15 @@
 // and the pieces keep both the range above and the precision below.
 // The values' block scales ride on the weights, relative to the largest scale seen (also lazy).
 //
-// One CTA: a producer warp (TMA, a ring of tiles), a warp that issues the MMAs, and two groups of four
-// softmax warps that take the tiles of a segment in turn, each with its own accumulators, so that one
-// group's softmax overlaps the other's loads and products.  The (row, token tile, kv head, tile)
-// sequence is cut into one equal run per CTA; the parts of a unit cut across CTAs meet in global
-// memory, where the last CTA to arrive (a ticket, nobody waits) adds them in CTA order.  So rows of
-// any lengths fill the SMs evenly and the result does not depend on timing.
+// One CTA: a producer warp (TMA, a ring of tiles), a warp that issues the MMAs, and 16 softmax warps
+// per SM: two groups of four take the tiles of a segment in turn, each with its own accumulators, so
+// that one group's softmax overlaps the other's loads and products; up to 8 columns two CTAs share an
+// SM, beyond that a tile's columns are halved between two groups.  What runs once per segment is kept
+// in short loops: a kernel's cold straight-line code runs at the pace of instruction fetch (unrolled
+// over 32 columns, the end of a segment took 25 us).  The (row, token tile, kv head, tile) sequence is
+// cut into one equal run per CTA; the parts of a unit cut across CTAs meet in global memory, where the
+// last CTA to arrive (a ticket, nobody waits) adds them in CTA order.  So rows of any lengths fill the
+// SMs evenly and the result does not depend on timing.
 #pragma once
 #include "attention.cuh"
 #include "qcache.cuh"
@@ -37,10 +40,10 @@
 namespace llm {
 
 constexpr int kQaTile = 128;                       // positions per tile
-constexpr int kQaThreads = 320;                    // producer, MMA issuer, 2 x 4 softmax warps
 constexpr uint64_t kQaWaitCycles = 1000000000ull;  // about 0.5 s
 constexpr float kQaTop = 5.0f;                     // log2 of the largest weight when a reference is taken
 constexpr float kQaMost = 8.0f;                    // log2 of the largest weight that moves no reference
+constexpr float kQaNone = -3.0e38f;                // a reference before any score
 constexpr size_t kQaSmem = 232448;                 // shared memory a CTA can have
 
 template <int HD, int NP, int NC>
@@ -52,9 +55,11 @@ struct QaShape {
   static constexpr int STAGE = 2 * KB;
   static constexpr int QB = N * HD;                // query pieces
   static constexpr int PB = kQaTile * N;           // weight pieces of one group
-  // two CTAs per SM where their tensor memory (4 N columns each) and rings fit: their segment ends
-  // and starts overlap (measured: profiles/qcache_attention.md)
-  static constexpr int CTAS = C <= 8 ? 2 : 1;
+  static constexpr int CTAS = C <= 8 ? 2 : 1;      // CTAs per SM (4 N columns of tensor memory each)
+  static constexpr int HV = C <= 8 ? 1 : 2;        // groups that share a tile's columns
+  static constexpr int CT = C / HV;                // columns of a thread
+  static constexpr int NCH = NC / HV;              // 16-column chunks of a thread
+  static constexpr int NS = 256 * HV;              // softmax threads
   static constexpr size_t MISC = 4096;
   static constexpr size_t BUDGET = kQaSmem / CTAS - (CTAS > 1 ? 1024 : 0);
   static constexpr int FIT = (int)((BUDGET - QB - 2 * PB - MISC - 1024) / STAGE);
@@ -119,6 +124,22 @@ LLM_D float qa_exp2(float x) {
   return y;
 }
 
+// T tiles cut into G runs, the first T % G of them one longer
+struct QaCut {
+  long long q, r;
+  LLM_D void make(long long T, int G) {
+    q = T < 0x7fffffff ? (long long)((uint32_t)T / (uint32_t)G) : T / G;
+    r = T - q * G;
+  }
+  LLM_D long long begin(int c) const { return c * q + min((long long)c, r); }
+  LLM_D int owner(long long i) const {
+    const long long head = r * (q + 1);
+    const bool in = i < head;
+    const long long n = in ? i : i - head, d = in ? q + 1 : q;
+    return (int)((in ? 0 : r) + (n < 0x7fffffff && d < 0x7fffffff ? (long long)((uint32_t)n / (uint32_t)d) : n / d));
+  }
+};
+
 // the walk of one CTA's run over (token tile, kv head, position tiles)
 struct QaWalk {
   QaUnit u;
@@ -129,8 +150,8 @@ struct QaWalk {
     t = t_; off = off_; st = c0; end = c1; tpt = tpt_; nct = nct_;
     if (st >= end) return;
     u = qa_unit(a, t, tpt, nct);
-    j = (int)((st - off) / u.nt);
-    k0 = (int)(st - off - (long long)j * u.nt);
+    j = (int)((uint32_t)(st - off) / (uint32_t)u.nt);  // (kv heads x tiles of a row: below 2^31)
+    k0 = (int)(st - off) - j * u.nt;
     cut();
   }
   LLM_D void cut() { k1 = (int)min((long long)u.nt, k0 + (end - st)); }
@@ -151,45 +172,47 @@ struct QaWalk {
 };
 
 template <int HD, int NP, int NC, int QT>
-__global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
+__global__ void __launch_bounds__(64 + QaShape<HD, NP, NC>::NS, QaShape<HD, NP, NC>::CTAS)
     qattn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const QAttnArgs a) {
   using X = QaShape<HD, NP, NC>;
-  constexpr int N = X::N, C = X::C, CPC = X::CPC, ST = X::ST;
+  constexpr int N = X::N, C = X::C, CPC = X::CPC, ST = X::ST, CT = X::CT, NCH = X::NCH, HV = X::HV, NS = X::NS;
   extern __shared__ unsigned char qraw[];
   const uint32_t s_raw = smem_u32(qraw);
   unsigned char* base = qraw + (((s_raw + 1023u) & ~1023u) - s_raw);
   const uint32_t s_ring = smem_u32(base);
   unsigned char* qbuf = base + (size_t)ST * X::STAGE;
-  unsigned char* pbuf = qbuf + X::QB;              // [2][PB]
-  float* qsc = reinterpret_cast<float*>(pbuf + 2 * X::PB);  // [C] query scale, in units of log2
-  int* cend = reinterpret_cast<int*>(qsc + C);     // [C] end of the positions a column sees
-  float* wmax = reinterpret_cast<float*>(cend + C);  // [2][4][C] warps' maxima; at a segment's end, sums
-  float* gref = wmax + 8 * C;                      // [2][C] the groups' references
-  float* wvs = gref + 2 * C;                       // [2][4] warps' largest value scales
-  float* gvs = wvs + 8;                            // [2] the groups' value scales
-  const uint32_t bars = (smem_u32(gvs + 2) + 7u) & ~7u;
+  unsigned char* pbuf = qbuf + X::QB;                        // [2][PB]
+  float* qsc = reinterpret_cast<float*>(pbuf + 2 * X::PB);   // [C] query scale, in units of log2
+  int* cend = reinterpret_cast<int*>(qsc + C);               // [C] end of the positions a column sees
+  float* gref = reinterpret_cast<float*>(cend + C);          // [2][C] references, by parity of the tile
+  float* wmax = gref + 2 * C;                                // [2][4][C] warps' maxima; at the end, their sums
+  float* ffac = wmax + 8 * C;                                // [2][C] at the end: factors of the two parities
+  float* wvs = ffac + 2 * C;                                 // [4][4] warps' largest value scales
+  float* gvs = wvs + 16;                                     // [4] the groups' value scales
+  const uint32_t bars = (smem_u32(gvs + 4) + 7u) & ~7u;
   const uint32_t b_full = bars, b_empty = b_full + 8 * ST, b_s = b_empty + 8 * ST, b_p = b_s + 16, b_pv = b_p + 16,
                  b_q = b_pv + 16;
-  static_assert((size_t)C * (4 + 4 + 32 + 8) + 64 + 16 * ST + 64 <= X::MISC, "shared memory");
+  static_assert((size_t)C * 4 * 14 + 80 + 16 * ST + 64 <= X::MISC, "shared memory");
   __shared__ uint32_t s_tmem;
   __shared__ int s_t, s_last;
   __shared__ long long s_off, s_total;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
-  if (tid == 0) {
+  if (tid == 32) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(b_full + 8u * i, 1);
       mbar_init(b_empty + 8u * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_s + 8u * i, 1);
-      mbar_init(b_p + 8u * i, 128);
+      mbar_init(b_p + 8u * i, 128 * HV);
       mbar_init(b_pv + 8u * i, 1);
     }
     mbar_init(b_q, 1);
     mbar_fence_init();
   }
+  __syncwarp();
   if (warp == 1) {
     tmem_alloc(smem_u32(&s_tmem), 4 * N);
     tmem_relinquish();
@@ -205,6 +228,7 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
   if (warp == 0) {
     const int per = (nq + 31) / 32, t0 = min(nq, lane * per), t1 = min(nq, t0 + per);
     long long sum = 0;
+#pragma unroll 1
     for (int t = t0; t < t1; ++t) sum += qa_unit(a, t, tpt, nct).nt;
     long long incl = sum;
 #pragma unroll
@@ -213,18 +237,25 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
       if (lane >= o) incl += v;
     }
     const long long total = __shfl_sync(0xffffffffu, incl, 31) * a.c.kv;
-    const long long ge = min((long long)gridDim.x, total), c0 = cta < ge ? total * cta / ge : total;
-    long long off = (incl - sum) * a.c.kv;
     if (lane == 0) s_total = total;
-    if (sum > 0 && c0 >= off && c0 < incl * a.c.kv) {
-      for (int t = t0; t < t1; ++t) {
-        const long long w = (long long)qa_unit(a, t, tpt, nct).nt * a.c.kv;
-        if (c0 < off + w) {
-          s_t = t;
-          s_off = off;
-          break;
+    // (never more runs than tiles, so that every CTA of a unit's range holds a part of it)
+    const int ge = (int)min((long long)gridDim.x, total);
+    if (cta < ge) {
+      QaCut cut;
+      cut.make(total, ge);
+      const long long c0 = cut.begin(cta);
+      long long off = (incl - sum) * a.c.kv;
+      if (sum > 0 && c0 >= off && c0 < incl * a.c.kv) {
+#pragma unroll 1
+        for (int t = t0; t < t1; ++t) {
+          const long long w = (long long)qa_unit(a, t, tpt, nct).nt * a.c.kv;
+          if (c0 < off + w) {
+            s_t = t;
+            s_off = off;
+            break;
+          }
+          off += w;
         }
-        off += w;
       }
     }
   }
@@ -232,12 +263,14 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  // (never more runs than tiles, so that every CTA of a unit's range holds a part of it)
-  const long long T = s_total;
-  const int G = (int)min((long long)gridDim.x, T);
-  const long long c0 = cta < G ? T * cta / G : T, c1 = cta < G ? T * (cta + 1) / G : T;
   QaWalk w;
-  w.begin(a, s_t, s_off, c0, c1, tpt, nct);
+  QaCut cut = {0, 0};
+  {
+    const long long T = s_total;
+    const int G = (int)min((long long)gridDim.x, T);
+    if (cta < G) cut.make(T, G);
+    w.begin(a, s_t, s_off, cta < G ? cut.begin(cta) : 0, cta < G ? cut.begin(cta + 1) : 0, tpt, nct);
+  }
   bool ok = true;  // a wait that gave up: no further waits, but every loop and barrier is still walked
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (ok && !mbar_wait(bar, parity, kQaWaitCycles)) {
@@ -254,10 +287,9 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
       long long it = 0;
       int slot = 0;
       uint32_t par = 1u;
-      for (; w.there(); w.next(a)) {
+      for (; w.there() && ok; w.next(a)) {
+#pragma unroll 1
         for (int k = w.k0; k < w.k1; ++k, ++it) {
-          wait(b_empty + 8u * slot, par);
-          if (!ok) break;
           const int p0 = (w.u.tile0 + k) * kQaTile;
           int y[2];
           uint32_t bytes = 0;
@@ -270,6 +302,8 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
               bytes += 2 * 64 * HD;
             }
           }
+          wait(b_empty + 8u * slot, par);
+          if (!ok) break;
           const uint32_t dst = s_ring + (uint32_t)slot * X::STAGE;
           const uint32_t bar = b_full + 8u * slot;
           mbar_expect_tx(bar, bytes);
@@ -286,6 +320,7 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
       // no copy may still be writing shared memory when the CTA exits
       ok = true;
       const long long lo = it > ST ? it - ST : 0;
+#pragma unroll 1
       for (long long i = lo; i < it; ++i) wait(b_full + 8u * (uint32_t)(i % ST), (uint32_t)(i / ST) & 1u);
     }
   } else if (warp == 1) {
@@ -293,72 +328,93 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
     if (lane == 0) {
       const uint32_t id_s = idesc_e4m3_f32(kQaTile, N, 0), id_o = idesc_e4m3_f32(HD, N, 1);
       const uint32_t q_addr = smem_u32(qbuf), p_addr = smem_u32(pbuf);
-      uint32_t cnt[2] = {0u, 0u};  // tiles whose weights each group has written
+      uint32_t cnt[2] = {0u, 0u};   // tiles whose weights each parity's groups have written
       uint32_t qpar = 0u;
-      long long it = 0;            // tiles before this segment
-      for (; w.there(); w.next(a)) {
-        const int n = w.k1 - w.k0;
-        auto scores = [&](int t) {
-          const uint32_t slot = (uint32_t)((it + t) % ST);
-          wait(b_full + 8u * slot, (uint32_t)((it + t) / ST) & 1u);
-          if (!ok) return;
+      uint32_t ss = 0u, spar = 0u;  // ring slot and phase of the next tile to score
+      uint32_t vs = 0u;             // ring slot of the next tile to weigh
+      auto scores = [&](int t) {
+        wait(b_full + 8u * ss, spar);
+        if (ok) {
           tc_fence_after();
-          const uint32_t k_addr = s_ring + slot * X::STAGE;
+          const uint32_t k_addr = s_ring + ss * X::STAGE;
 #pragma unroll
           for (int ks = 0; ks < HD / 32; ++ks)
             tc_mma_e4m3(tmem + (t & 1) * N, smem_desc(k_addr + ks * 32, 16, 8 * HD, X::SWZ),
                         smem_desc(q_addr + ks * 32, 16, 8 * HD, X::SWZ), id_s, ks > 0);
           tc_commit(b_s + 8u * (t & 1));
-        };
+        }
+        if (++ss == ST) ss = 0u, spar ^= 1u;
+      };
+      for (; w.there(); w.next(a)) {
+        const int n = w.k1 - w.k0;
         wait(b_q, qpar);
         qpar ^= 1u;
         tc_fence_after();
-        scores(0);
-        if (n > 1) scores(1);
-        for (int t = 0; t < n; ++t) {
-          const int gp = t & 1;
-          wait(b_p + 8u * gp, cnt[gp]++ & 1u);
-          if (ok) {
-            tc_fence_after();
-            const uint32_t slot = (uint32_t)((it + t) % ST);
-            const uint32_t v_addr = s_ring + slot * X::STAGE + X::KB;
+#pragma unroll 1
+        for (int t = -2; t < n; ++t) {
+          if (t >= 0) {
+            const int gp = t & 1;
+            wait(b_p + 8u * gp, cnt[gp]++ & 1u);
+            if (ok) {
+              tc_fence_after();
+              const uint32_t v_addr = s_ring + vs * X::STAGE + X::KB;
 #pragma unroll
-            for (int kk = 0; kk < kQaTile / 32; ++kk)
-              tc_mma_e4m3(tmem + 2 * N + gp * N, smem_desc(v_addr + kk * 32 * HD, 8 * HD, 8 * HD, X::SWZ),
-                          smem_desc(p_addr + gp * X::PB + kk * 512, 128, 2048, 0), id_o, t > 1 || kk > 0);
-            tc_commit(b_pv + 8u * gp);
-            tc_commit(b_empty + 8u * slot);
+              for (int kk = 0; kk < kQaTile / 32; ++kk)
+                tc_mma_e4m3(tmem + 2 * N + gp * N, smem_desc(v_addr + kk * 32 * HD, 8 * HD, 8 * HD, X::SWZ),
+                            smem_desc(p_addr + gp * X::PB + kk * 512, 128, 2048, 0), id_o, t > 1 || kk > 0);
+              tc_commit(b_pv + 8u * gp);
+              tc_commit(b_empty + 8u * vs);
+            }
+            if (++vs == ST) vs = 0u;
           }
           if (t + 2 < n) scores(t + 2);
         }
-        it += n;
       }
     }
   } else {
-    // ---- softmax groups ----
-    const int sw = warp - 2, gp = sw >> 2, gw = sw & 3;  // group, warp in it
-    const int quad = warp & 3;                           // the tensor-memory lanes this warp reads
-    const int stid = tid - 64;
+    // ---- softmax groups: group = (half of the columns, parity of the tiles) ----
+    const int sw = warp - 2, gp = (sw >> 2) & 1, half = sw >> 3, gw = sw & 3, group = sw >> 2;
+    const int quad = warp & 3;              // the tensor-memory lanes this warp reads
+    const int stid = tid - 64, gtid = stid & 127;
+    const int c0 = half * CT;               // this thread's columns
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t t_s = tmem + gp * N + lanes, t_o = tmem + 2 * N + gp * N + lanes;
-    unsigned char* pmine = pbuf + gp * X::PB + (quad * 32 + lane) * 16;
+    const uint32_t t_s = tmem + gp * N + c0 * NP + lanes, t_o = tmem + 2 * N + gp * N + c0 * NP + lanes;
+    unsigned char* pmine = pbuf + gp * X::PB + half * NCH * 2048 + (quad * 32 + lane) * 16;
     const int H = a.c.kv * a.g;
+    auto all_sync = [&]() { named_sync(5, NS); };
+    auto group_sync = [&]() { named_sync(1 + group, 128); };
     // tokens that see nothing and share a tile with none that does: zeros
+#pragma unroll 1
     for (int t = cta; t < nq; t += gridDim.x) {
       const QaUnit u = qa_unit(a, t, tpt, nct);
       if (u.nt == 0 && u.ntok > 0)
-        for (int64_t i = stid; i < (int64_t)u.ntok * H * HD; i += 256) {
+#pragma unroll 1
+        for (int64_t i = stid; i < (int64_t)u.ntok * H * HD; i += NS) {
           const int64_t at = (u.qrow + i / (H * HD)) * a.out_stride + i % (H * HD);
           if constexpr (QT) static_cast<uint16_t*>(a.out)[at] = 0;
           else static_cast<float*>(a.out)[at] = 0.f;
         }
     }
     uint32_t cs = 0u, cpv = 0u;  // score tiles read, value products waited for
-    long long it = 0;
+    uint32_t it = 0u;            // tiles before this segment
     for (; w.there(); w.next(a)) {
       const int n = w.k1 - w.k0, used = w.u.ntok * a.g;
+      // the scales of this thread's position in tile t (0 and not good where nothing sees it)
+      auto scales = [&](int t, float& ks, float& vs) {
+        ks = vs = 0.f;
+        const int pos = (w.u.tile0 + w.k0 + t) * kQaTile + quad * 32 + lane;
+        int row, pp;
+        if (t >= n || pos >= w.u.last || !qa_place(a, w.u.b, pos, row, pp)) return false;
+        const size_t at = ((size_t)row * a.c.kv + w.j) * (a.c.cap / kQBlock) + pp / kQBlock;
+        ks = a.c.ks[at];
+        vs = a.c.vs[at];
+        return true;
+      };
+      float ks, vs;
+      bool good = scales(gp, ks, vs);  // (in flight behind the query pieces)
       // ---- query pieces: warp = column ----
-      for (int c = sw; c < C; c += 8) {
+#pragma unroll 1
+      for (int c = sw; c < C; c += NS / 32) {
         constexpr int E = HD / 32;  // elements per lane
         const int tok = c / a.g;
         float x[E];
@@ -417,91 +473,74 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
         }
       }
       fence_proxy_async_smem();
-      named_sync(3, 256);
+      all_sync();  // (also: the segment before is written, its shared memory is free)
       if (stid == 0) mbar_arrive(b_q);
 
-      // references of the group's columns, alike for all its threads
-      float* ref = gref + gp * C;
-      if ((stid & 127) < C) ref[stid & 127] = (stid & 127) < used ? -INFINITY : INFINITY;  // no token: weights 2^-inf
-      named_sync(1 + gp, 128);
-      float l[C];
+      float* ref = gref + gp * C + c0;      // references of the group's columns, alike for all its threads
+      if (gtid < CT) ref[gtid] = c0 + gtid < used ? kQaNone : INFINITY;  // (no token: weights 2^-inf)
+      group_sync();
+      float l[CT];
 #pragma unroll
-      for (int c = 0; c < C; ++c) l[c] = 0.f;
-      float vref = 0.f, vinv = 0.f;                // the largest value scale seen, and its reciprocal
-      // the scales of this thread's position in tile t (0 and not good where it is not seen)
-      auto scales = [&](int t, float& ks, float& vs) {
-        ks = vs = 0.f;
-        const int pos = (w.u.tile0 + w.k0 + t) * kQaTile + quad * 32 + lane;
-        int row, pp;
-        if (t >= n || pos >= w.u.last || !qa_place(a, w.u.b, pos, row, pp)) return false;
-        const size_t at = ((size_t)row * a.c.kv + w.j) * (a.c.cap / kQBlock) + pp / kQBlock;
-        ks = a.c.ks[at];
-        vs = a.c.vs[at];
-        return true;
-      };
-      float ks, vs;
-      bool good = scales(gp, ks, vs);
-      bool pend = false;                           // a product over the values not waited for yet
+      for (int c = 0; c < CT; ++c) l[c] = 0.f;
+      float vref = 0.f, vinv = 0.f;         // the largest value scale seen, and its reciprocal
+      bool pend = false;                    // a product over the values not waited for yet
+#pragma unroll 1
       for (int t = gp; t < n; t += 2) {
         const int p0 = (w.u.tile0 + w.k0 + t) * kQaTile, pos = p0 + quad * 32 + lane;
         float ks1, vs1;
         const bool good1 = scales(t + 2, ks1, vs1);  // the next tile's, in flight behind this one's work
+        // columns see positions below their cend; where the whole tile is seen by all, every position is
+        const bool whole = __all_sync(0xffffffffu, good) && p0 >= w.u.start && p0 + kQaTile <= w.u.end0;
+        const int mypos = whole ? -0x7fffffff : good && pos >= w.u.start ? pos : 0x7fffffff;
         wait(b_s + 8u * gp, cs++ & 1u);
         __syncwarp();
         tc_fence_after();
-        float s[C];
+        float s[CT];
+        bool low = !(vs > vref);
 #pragma unroll
-        for (int ch = 0; ch < NC; ++ch) {
+        for (int ch = 0; ch < NCH; ++ch) {
           float d[16];
           tc_ld16(t_s + ch * 16, d);
           tc_wait_ld();
 #pragma unroll
-          for (int c = 0; c < CPC; ++c) {
-            float v = d[c * NP + NP - 1];
+          for (int i = 0; i < CPC; ++i) {
+            const int c = ch * CPC + i;
+            float v = d[i * NP + NP - 1];
 #pragma unroll
-            for (int i = NP - 2; i >= 0; --i) v = fmaf(v, 0.03125f, d[c * NP + i]);
-            s[ch * CPC + c] = v * (ks * qsc[ch * CPC + c]);
+            for (int x = NP - 2; x >= 0; --x) v = fmaf(v, 0.03125f, d[i * NP + x]);
+            s[c] = mypos < cend[c0 + c] ? v * (ks * qsc[c0 + c]) : -INFINITY;
+            low = low && !(s[c] > ref[c] + kQaMost);
           }
         }
-        // every column with a token sees the whole tile?
-        const bool whole = __all_sync(0xffffffffu, good) && p0 >= w.u.start && p0 + kQaTile <= w.u.end0;
-        if (!whole) {
-#pragma unroll
-          for (int c = 0; c < C; ++c)
-            if (!good || pos >= cend[c] || pos < w.u.start) s[c] = -INFINITY;
-        }
-        bool low = !(vs > vref);
-#pragma unroll
-        for (int c = 0; c < C; ++c) low = low && !(s[c] > ref[c] + kQaMost);
-        if (!named_sync_and(1 + gp, 128, low)) {
+        if (!named_sync_and(1 + group, 128, low)) {
           // references move (rare): the group's maxima, then each column's new reference and what the
           // sums relative to the old one are worth under it
-          float* wm = wmax + gp * 4 * C;
+          float* wm = wmax + gp * 4 * C + c0;
 #pragma unroll
-          for (int c = 0; c < C; ++c) {
+          for (int c = 0; c < CT; ++c) {
             const float m = warp_max(s[c]);
             if (lane == 0) wm[gw * C + c] = m;
           }
           const float mv = warp_max(vs);
-          if (lane == 0) wvs[gp * 4 + gw] = mv;
-          named_sync(1 + gp, 128);
-          if ((stid & 127) < C) {
-            const int c = stid & 127;
-            const float old = ref[c];
-            const float top = fmaxf(old, fmaxf(fmaxf(wm[c], wm[C + c]), fmaxf(wm[2 * C + c], wm[3 * C + c])) - kQaTop);
-            ref[c] = top;
-            wm[c] = top == old ? 1.f : qa_exp2(old - top);
+          if (lane == 0) wvs[group * 4 + gw] = mv;
+          group_sync();
+          if (gtid < CT) {
+            const float old = ref[gtid];
+            const float top = fmaxf(old, fmaxf(fmaxf(wm[gtid], wm[C + gtid]), fmaxf(wm[2 * C + gtid], wm[3 * C + gtid])) - kQaTop);
+            ref[gtid] = top;
+            wm[gtid] = top == old ? 1.f : qa_exp2(old - top);
           }
-          const float v1 = fmaxf(fmaxf(wvs[gp * 4], wvs[gp * 4 + 1]), fmaxf(wvs[gp * 4 + 2], wvs[gp * 4 + 3]));
+          const float* wv = wvs + group * 4;
+          const float v1 = fmaxf(fmaxf(wv[0], wv[1]), fmaxf(wv[2], wv[3]));
           float vcorr = 1.f;
           if (v1 > vref) {
             vcorr = vref * q_recip(v1);
             vref = v1;
             vinv = q_recip(v1);
           }
-          named_sync(1 + gp, 128);
+          group_sync();
 #pragma unroll
-          for (int c = 0; c < C; ++c) l[c] *= wm[c];
+          for (int c = 0; c < CT; ++c) l[c] *= wm[c];
           if (t > gp) {
             // the accumulators, once the product before is in them
             if (pend) {
@@ -510,8 +549,8 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
             }
             __syncwarp();
             tc_fence_after();
-#pragma unroll
-            for (int ch = 0; ch < NC; ++ch) {
+#pragma unroll 1
+            for (int ch = 0; ch < NCH; ++ch) {
               float d[16];
               tc_ld16(t_o + ch * 16, d);
               tc_wait_ld();
@@ -523,56 +562,46 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
           }
         }
         const float vr = vs * vinv;
-        // weights and their sums; s becomes the weight with the value's scale on it
-        if (whole) {
-#pragma unroll
-          for (int c = 0; c < C; ++c) {
-            const float p = qa_exp2(s[c] - ref[c]);
-            l[c] += p;
-            s[c] = p * vr;
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < C; ++c) {
-            const bool seen = good && pos < cend[c] && pos >= w.u.start;
-            const float p = seen ? qa_exp2(s[c] - ref[c]) : 0.f;
-            l[c] += p;
-            s[c] = seen ? p * vr : 0.f;
-          }
-        }
         if (pend) wait(b_pv + 8u * gp, cpv++ & 1u);  // the weights' buffer is free again
 #pragma unroll
-        for (int ch = 0; ch < NC; ++ch) {
+        for (int ch = 0; ch < NCH; ++ch) {
           uint32_t o[4];  // 16 codes: CPC columns of NP pieces
 #pragma unroll
-          for (int c = 0; c < CPC; c += 2) {
-            float x0 = s[ch * CPC + c], x1 = s[ch * CPC + c + 1];
+          for (int i = 0; i < CPC; i += 2) {
+            const int c = ch * CPC + i;
+            // a weight (0 where the column does not see the position), its sum, and with the value's
+            // scale on it (a scale may be NaN, which reaches only the columns that see it)
+            float x0 = qa_exp2(s[c] - ref[c]), x1 = qa_exp2(s[c + 1] - ref[c + 1]);
+            l[c] += x0;
+            l[c + 1] += x1;
+            x0 = x0 == 0.f ? 0.f : x0 * vr;
+            x1 = x1 == 0.f ? 0.f : x1 * vr;
             uint32_t x[NP];
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-              x[i] = e4m3x2(x0, x1);
-              if (i + 1 < NP) {
-                const float2 v = e4m3_pair(x[i]);
+            for (int y = 0; y < NP; ++y) {
+              x[y] = e4m3x2(x0, x1);
+              if (y + 1 < NP) {
+                const float2 v = e4m3_pair(x[y]);
                 x0 = (x0 - v.x) * 32.f;
                 x1 = (x1 - v.y) * 32.f;
               }
             }
             if constexpr (NP == 4) {
               const uint32_t a01 = x[0] | x[1] << 16, a23 = x[2] | x[3] << 16;
-              o[c] = __byte_perm(a01, a23, 0x6420);
-              o[c + 1] = __byte_perm(a01, a23, 0x7531);
+              o[i] = __byte_perm(a01, a23, 0x6420);
+              o[i + 1] = __byte_perm(a01, a23, 0x7531);
             } else {
-              o[c / 2] = __byte_perm(x[0], x[1], 0x5140);
+              o[i / 2] = __byte_perm(x[0], x[1], 0x5140);
             }
           }
           *reinterpret_cast<uint4*>(pmine + ch * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        if (!whole && (!good || pos < w.u.start)) {
+        if (mypos == 0x7fffffff && half == 0) {
           // rows that no column sees hold dead data (any code, NaN among them): zeros
-          const long long i = it + t;
-          wait(b_full + 8u * (uint32_t)(i % ST), (uint32_t)(i / ST) & 1u);
-          uint4* v = reinterpret_cast<uint4*>(base + (size_t)(i % ST) * X::STAGE + X::KB + (quad * 32 + lane) * HD);
-#pragma unroll
+          const uint32_t i = it + t, slot = i % ST;
+          wait(b_full + 8u * slot, (i / ST) & 1u);
+          uint4* v = reinterpret_cast<uint4*>(base + slot * X::STAGE + X::KB + (quad * 32 + lane) * HD);
+#pragma unroll 1
           for (int e = 0; e < HD / 16; ++e) v[e] = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
@@ -588,146 +617,149 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
       tc_fence_after();
       it += n;
 
-      // ---- the segment's end: the groups' sums meet, group 0 writes ----
+      // ---- the segment's end: the parities' sums meet, parity 0 writes ----
+      {
+        // the lanes' sums of every column at once: each exchange halves the columns a lane holds
+        float x[CT];
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const float sum = warp_sum(l[c]);
-        if (lane == 0) wmax[(gp * 4 + gw) * C + c] = sum;
-      }
-      if (lane == 0 && gw == 0) gvs[gp] = vref;
-      named_sync(3, 256);  // (both groups' products are done: the weights' buffers are free)
-      const bool both = n > 1;
-      const int d_row = HD == 128 ? quad * 32 + lane : quad * 16 + (lane & 15);  // the dimension of this lane
-      const bool d_on = HD == 128 || lane < 16;
-      float* other = reinterpret_cast<float*>(pbuf);  // [C][HD]: group 1's sums
-      auto column = [&](const float (&d)[16], int c) {
-        float v = d[c * NP + NP - 1];
+        for (int c = 0; c < CT; ++c) x[c] = l[c];
+        int col = 0;
 #pragma unroll
-        for (int i = NP - 2; i >= 0; --i) v = fmaf(v, 0.03125f, d[c * NP + i]);
-        return v * vref;
-      };
-      if (gp == 1 && both) {
+        for (int o = 16, m = CT; o > 0; o >>= 1) {
+          if (m > 1) {
+            m >>= 1;
+            const bool up = lane & o;
+            col += up ? m : 0;
 #pragma unroll
-        for (int ch = 0; ch < NC; ++ch) {
-          if (ch * CPC >= used) break;
-          float d[16];
-          tc_ld16(t_o + ch * 16, d);
-          tc_wait_ld();
-#pragma unroll
-          for (int c = 0; c < CPC; ++c)
-            if (d_on && ch * CPC + c < used) other[(ch * CPC + c) * HD + d_row] = column(d, c);
+            for (int c = 0; c < m; ++c) {
+              const float give = up ? x[c] : x[c + m], keep = up ? x[c + m] : x[c];
+              x[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+          } else {
+            x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
+          }
         }
+        wmax[(gp * 4 + gw) * C + c0 + col] = x[0];  // (lanes of one column write the same sum)
+        if (gtid == 0) gvs[group] = vref;
       }
-      if (both) named_sync(3, 256);
-      const bool alone = w.k0 == 0 && w.k1 == w.u.nt;  // this CTA holds the whole unit
+      all_sync();  // (every product is done: the weights' buffers are free)
+      const bool both = n > 1, alone = w.k0 == 0 && w.k1 == w.u.nt;  // alone: this CTA holds the whole unit
       // parts of units cut across CTAs: [CTA][the unit's first part?]{[C][HD] sums, [C] (reference, weight)}
       float* parts = reinterpret_cast<float*>(a.ws + kQattnTickets);
-      auto out_at = [&](int c) { return (w.u.qrow + c / a.g) * a.out_stride + (int64_t)(w.j * a.g + c % a.g) * HD; };
-      auto owner = [&](long long i) { return (int)(((i + 1) * G + T - 1) / T - 1); };
-      if (gp == 0) {
-        float* mine = parts + ((size_t)cta * 2 + (w.k0 == 0 ? 1 : 0)) * C * (HD + 2);
+      float* mine = parts + ((size_t)cta * 2 + (w.k0 == 0 ? 1 : 0)) * C * (HD + 2);
+      if (stid < used) {
+        // column stid: the parities' common reference and what each one's sums are worth under it
+        const int c = stid, hv = c / CT;
+        const float* x = wmax + c;
+        const float r0 = gref[c], r1 = both ? gref[C + c] : kQaNone, M = fmaxf(r0, r1);
+        const float f0 = qa_exp2(r0 - M), f1 = both ? qa_exp2(r1 - M) : 0.f;
+        float L = (x[0] + x[C] + x[2 * C] + x[3 * C]) * f0;
+        if (both) L = fmaf(x[4 * C] + x[5 * C] + x[6 * C] + x[7 * C], f1, L);
+        const float r = alone ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+        ffac[c] = f0 * gvs[2 * hv] * r;
+        ffac[C + c] = f1 * (both ? gvs[2 * hv + 1] : 0.f) * r;
+        if (!alone) *reinterpret_cast<float2*>(mine + C * HD + 2 * c) = make_float2(M, L);
+      }
+      all_sync();
+      const int d_row = HD == 128 ? quad * 32 + lane : quad * 16 + (lane & 15);  // the dimension of this lane
+      const bool d_on = HD == 128 || lane < 16;
+      float* other = reinterpret_cast<float*>(pbuf);  // [C][HD]: parity 1's sums
+#pragma unroll 1
+      for (int pass = 1; pass >= 0; --pass) {
+        if (gp == pass && (both || pass == 0)) {
+#pragma unroll 1
+          for (int ch = 0; ch < NCH && c0 + ch * CPC < used; ++ch) {
+            float d[16];
+            tc_ld16(t_o + ch * 16, d);
+            tc_wait_ld();
 #pragma unroll
-        for (int ch = 0; ch < NC; ++ch) {
-          if (ch * CPC >= used) break;
-          float d[16];
-          tc_ld16(t_o + ch * 16, d);
-          tc_wait_ld();
+            for (int i = 0; i < CPC; ++i) {
+              const int c = c0 + ch * CPC + i;
+              float v = d[i * NP + NP - 1];
 #pragma unroll
-          for (int cc = 0; cc < CPC; ++cc) {
-            const int c = ch * CPC + cc;
-            if (c >= used) break;
-            const float l0 = wmax[c] + wmax[C + c] + wmax[2 * C + c] + wmax[3 * C + c];
-            const float r0 = gref[c];
-            float M = r0, L = l0, O = column(d, cc);
-            if (both) {
-              const float l1 = wmax[4 * C + c] + wmax[5 * C + c] + wmax[6 * C + c] + wmax[7 * C + c];
-              const float r1 = gref[C + c];
-              M = fmaxf(r0, r1);
-              // (sums without a reference are 0, or NaN, which has to stay)
-              const float f0 = r0 == -INFINITY ? (l0 == 0.f ? 0.f : 1.f) : qa_exp2(r0 - M);
-              const float f1 = r1 == -INFINITY ? (l1 == 0.f ? 0.f : 1.f) : qa_exp2(r1 - M);
-              L = fmaf(l0, f0, l1 * f1);
-              O = fmaf(O, f0, (d_on ? other[c * HD + d_row] : 0.f) * f1);
-            }
-            if (d_on) {
-              if (alone) {
-                O = L == 0.f ? 0.f : O / L;
-                if constexpr (QT) static_cast<uint16_t*>(a.out)[out_at(c) + d_row] = f32_to_bf16(O);
-                else static_cast<float*>(a.out)[out_at(c) + d_row] = O;
-              } else {
-                mine[c * HD + d_row] = O;
-                if (d_row == 0) *reinterpret_cast<float2*>(mine + C * HD + 2 * c) = make_float2(M, L);
+              for (int x = NP - 2; x >= 0; --x) v = fmaf(v, 0.03125f, d[i * NP + x]);
+              v *= ffac[pass * C + c];
+              if (d_on && c < used) {
+                if (pass == 0 && both) v += other[c * HD + d_row];
+                float* dst = pass ? other + c * HD : mine + c * HD;
+                if (pass == 0 && alone) {
+                  const int tok = c / a.g;
+                  const int64_t at = (w.u.qrow + tok) * a.out_stride + (int64_t)(w.j * a.g + c - tok * a.g) * HD + d_row;
+                  if constexpr (QT) static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v);
+                  else static_cast<float*>(a.out)[at] = v;
+                } else {
+                  dst[d_row] = v;
+                }
               }
             }
           }
         }
-        if (!alone) {
-          __threadfence();
-          named_sync(1, 128);
-          if (stid == 0) {
-            const int first = owner(w.unit0()), last = owner(w.unit0() + w.u.nt - 1);
-            s_last = atomicInc(reinterpret_cast<uint32_t*>(a.ws) + first, (uint32_t)(last - first)) == (uint32_t)(last - first);
-          }
-        }
+        if (pass == 1 && both) all_sync();
       }
       if (alone) continue;
       // ---- a unit of several CTAs: the last of them to get here adds the parts in CTA order ----
-      named_sync(3, 256);
+      const int first = cut.owner(w.unit0()), np = cut.owner(w.unit0() + w.u.nt - 1) - first + 1;
+      __threadfence();
+      all_sync();
+      if (stid == 0) s_last = atomicInc(reinterpret_cast<uint32_t*>(a.ws) + first, (uint32_t)(np - 1)) == (uint32_t)(np - 1);
+      all_sync();
       if (!s_last) continue;
       __threadfence();
-      const int first = owner(w.unit0()), np = owner(w.unit0() + w.u.nt - 1) - first + 1;
       auto part = [&](int i) { return parts + ((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * C * (HD + 2); };
       auto stat = [&](int i, int c) { return __ldcg(reinterpret_cast<const float2*>(part(i) + C * HD + 2 * c)); };
-      auto factor = [&](float2 ml, float M) { return ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : qa_exp2(ml.x - M); };
       float* fac = reinterpret_cast<float*>(pbuf);  // [C][64] factors of 64 parts at a time
-      constexpr int CW = (C + 7) / 8;               // columns of a warp; its lanes take the parts
+      constexpr int CW = (C + NS / 32 - 1) / (NS / 32);  // columns of a warp; its lanes take the parts
       float M[CW], L[CW];
 #pragma unroll
       for (int q = 0; q < CW; ++q) {
-        const int c = sw + 8 * q;
-        M[q] = -INFINITY;
+        const int c = sw + NS / 32 * q;
+        M[q] = kQaNone;
         L[q] = 0.f;
         if (c < used) {
-          const float2 none = make_float2(-INFINITY, 0.f);
+          const float2 none = make_float2(kQaNone, 0.f);
           const float2 x0 = lane < np ? stat(lane, c) : none, x1 = lane + 32 < np ? stat(lane + 32, c) : none;
           M[q] = fmaxf(x0.x, x1.x);
+#pragma unroll 1
           for (int i = lane + 64; i < np; i += 32) M[q] = fmaxf(M[q], stat(i, c).x);
           M[q] = warp_max(M[q]);
-          const float f0 = factor(x0, M[q]), f1 = factor(x1, M[q]);
+          const float f0 = qa_exp2(x0.x - M[q]), f1 = qa_exp2(x1.x - M[q]);
           fac[c * 64 + lane] = f0;
           fac[c * 64 + lane + 32] = f1;
           L[q] = fmaf(x0.y, f0, x1.y * f1);
         }
       }
-      // threads own groups of four dimensions of a column, in strides of 256
-      constexpr int PER = (C * HD / 4 + 255) / 256, U = PER > 2 ? 4 : 8;  // U parts' loads in flight for each
+      // threads own groups of four dimensions of a column, in strides of NS
+      constexpr int PER = (C * HD / 4 + NS - 1) / NS, U = PER > 1 ? 4 : 8;  // U parts' loads in flight for each
       float4 O[PER];
 #pragma unroll
       for (int q = 0; q < PER; ++q) O[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
       for (int i0 = 0; i0 < np; i0 += 64) {
         const int m = min(64, np - i0);
         if (i0 > 0) {
-          named_sync(3, 256);
+          all_sync();
 #pragma unroll
           for (int q = 0; q < CW; ++q) {
-            const int c = sw + 8 * q;
+            const int c = sw + NS / 32 * q;
             if (c < used)
+#pragma unroll 1
               for (int i = lane; i < m; i += 32) {
                 const float2 x = stat(i0 + i, c);
-                const float f = factor(x, M[q]);
+                const float f = qa_exp2(x.x - M[q]);
                 fac[c * 64 + i] = f;
                 L[q] = fmaf(x.y, f, L[q]);
               }
           }
         }
-        named_sync(3, 256);
+        all_sync();
+#pragma unroll 1
         for (int i = 0; i < m; i += U) {
           float4 v[PER][U];
 #pragma unroll
           for (int q = 0; q < PER; ++q)
 #pragma unroll
             for (int y = 0; y < U; ++y) {
-              const int x = q * 256 + stid;
+              const int x = q * NS + stid;
               v[q][y] = make_float4(0.f, 0.f, 0.f, 0.f);
               if (x < used * (HD / 4) && i + y < m) v[q][y] = __ldcg(reinterpret_cast<const float4*>(part(i0 + i + y)) + x);
             }
@@ -735,7 +767,7 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
           for (int q = 0; q < PER; ++q)
 #pragma unroll
             for (int y = 0; y < U; ++y) {
-              const int x = q * 256 + stid;
+              const int x = q * NS + stid;
               if (x < used * (HD / 4) && i + y < m) {
                 const float f = fac[x / (HD / 4) * 64 + i + y];
                 O[q].x = fmaf(f, v[q][y].x, O[q].x);
@@ -749,21 +781,23 @@ __global__ void __launch_bounds__(kQaThreads, QaShape<HD, NP, NC>::CTAS)
 #pragma unroll
       for (int q = 0; q < CW; ++q) {
         const float sum = warp_sum(L[q]);
-        if (lane == 0 && sw + 8 * q < C) wmax[sw + 8 * q] = sum;
+        if (lane == 0 && sw + NS / 32 * q < C) wmax[sw + NS / 32 * q] = sum;
       }
-      named_sync(3, 256);
+      all_sync();
 #pragma unroll
       for (int q = 0; q < PER; ++q) {
-        const int x = q * 256 + stid, c = x / (HD / 4), e = x % (HD / 4) * 4;
+        const int x = q * NS + stid, c = x / (HD / 4), e = x % (HD / 4) * 4;
         if (c < used) {
           const float r = wmax[c] == 0.f ? 0.f : 1.f / wmax[c];
           const float4 o = make_float4(O[q].x * r, O[q].y * r, O[q].z * r, O[q].w * r);
+          const int tok = c / a.g;
+          const int64_t at = (w.u.qrow + tok) * a.out_stride + (int64_t)(w.j * a.g + c - tok * a.g) * HD + e;
           if constexpr (QT) {
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_at(c) + e) =
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
                 make_uint2((uint32_t)f32_to_bf16(o.x) | (uint32_t)f32_to_bf16(o.y) << 16,
                            (uint32_t)f32_to_bf16(o.z) | (uint32_t)f32_to_bf16(o.w) << 16);
           } else {
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + out_at(c) + e) = o;
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = o;
           }
         }
       }
@@ -787,7 +821,7 @@ cudaError_t launch_qattn_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, co
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kQaThreads);
+  cfg.blockDim = dim3(64 + QaShape<HD, NP, NC>::NS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
