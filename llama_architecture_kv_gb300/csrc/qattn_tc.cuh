@@ -18,20 +18,20 @@
 // With the positions on the M side a tile costs 8 MMAs however few columns there are, and a thread
 // writes its position's pieces with one 16-byte store per 16 columns (B's N-major layout).
 //
-// Running maxima are lazy: a column's reference is 2^5 below the largest weight it was taken from and
-// moves only when a weight exceeds 2^8, so the accumulators in tensor memory are hardly ever rescaled
-// and the pieces keep both the range above and the precision below.
+// Running maxima are lazy: a column's reference makes the first tile's largest weight 2^2 and moves only
+// when a weight exceeds 2^8 (then that one becomes 2^5), so the accumulators in tensor memory are hardly
+// ever rescaled and the pieces keep the range above and the precision below.
 // The values' block scales ride on the weights, relative to the largest scale seen (also lazy).
 //
-// One CTA: a producer warp (TMA, a ring of tiles), a warp that issues the MMAs, and 16 softmax warps
-// per SM: two groups of four take the tiles of a segment in turn, each with its own accumulators, so
+// One CTA: a producer warp (a ring of tiles by TMA, their block scales by 4-byte asynchronous copies), a
+// warp that issues the MMAs, and 16 softmax warps per SM: two groups of four take the tiles of a segment in turn, each with its own accumulators, so
 // that one group's softmax overlaps the other's loads and products; up to 8 columns two CTAs share an
 // SM, beyond that a tile's columns are halved between two groups.  What runs once per segment is kept
-// in short loops: a kernel's cold straight-line code runs at the pace of instruction fetch (unrolled
-// over 32 columns, the end of a segment took 25 us).  The (row, token tile, kv head, tile) sequence is
-// cut into one equal run per CTA; the parts of a unit cut across CTAs meet in global memory, where the
-// last CTA to arrive (a ticket, nobody waits) adds them in CTA order.  So rows of any lengths fill the
-// SMs evenly and the result does not depend on timing.
+// in short loops: cold straight-line code runs at the pace of instruction fetch (unrolled over 32
+// columns, the end of a segment took 25 us).  The (row, token tile, kv head, tile) sequence is cut into
+// one equal run per CTA; the parts of a unit cut across CTAs meet in global memory once a CTA's run is
+// done, where the last CTA to arrive (a ticket, nobody waits) adds them in CTA order.  So rows of any
+// lengths fill the SMs evenly and the result does not depend on timing.
 #pragma once
 #include "attention.cuh"
 #include "qcache.cuh"
@@ -41,8 +41,9 @@ namespace llm {
 
 constexpr int kQaTile = 128;                       // positions per tile
 constexpr uint64_t kQaWaitCycles = 1000000000ull;  // about 0.5 s
-constexpr float kQaTop = 5.0f;                     // log2 of the largest weight when a reference is taken
-constexpr float kQaMost = 8.0f;                    // log2 of the largest weight that moves no reference
+constexpr float kQaFirst = 2.0f;                   // log2 of the largest weight of a segment's first tile
+constexpr float kQaTop = 5.0f;                     // and of a later tile that moved a reference
+constexpr float kQaMost = 8.0f;                    // the largest weight that moves none
 constexpr float kQaNone = -3.0e38f;                // a reference before any score
 constexpr size_t kQaSmem = 232448;                 // shared memory a CTA can have
 
@@ -53,13 +54,14 @@ struct QaShape {
   static constexpr int CPC = 16 / NP;              // of them per 16 accumulator columns
   static constexpr int KB = kQaTile * HD;          // bytes of a tile of keys (or values)
   static constexpr int STAGE = 2 * KB;
-  static constexpr int QB = N * HD;                // query pieces
+  static constexpr int QB = N * HD;                // query pieces of a segment
   static constexpr int PB = kQaTile * N;           // weight pieces of one group
   static constexpr int CTAS = C <= 8 ? 2 : 1;      // CTAs per SM (4 N columns of tensor memory each)
   static constexpr int HV = C <= 8 ? 1 : 2;        // groups that share a tile's columns
   static constexpr int CT = C / HV;                // columns of a thread
   static constexpr int NCH = NC / HV;              // 16-column chunks of a thread
   static constexpr int NS = 256 * HV;              // softmax threads
+  static constexpr int NT = NS + 64;               // all threads
   static constexpr size_t MISC = 4096;
   static constexpr size_t BUDGET = kQaSmem / CTAS - (CTAS > 1 ? 1024 : 0);
   static constexpr int FIT = (int)((BUDGET - QB - 2 * PB - MISC - 1024) / STAGE);
@@ -118,6 +120,22 @@ LLM_D bool qa_place(const QAttnArgs& a, int b, int pos, int& row, int& pp) {
   return true;
 }
 
+// a 4-byte asynchronous copy to shared memory, and this thread's arrival on an mbarrier once its copies
+// are done
+LLM_D void qa_copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+LLM_D void qa_copy_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// f32 maxima by the integer reduction: an order-preserving map of the bits (NaN left out as -inf)
+LLM_D float qa_warp_max(float v) {
+  const uint32_t u = __float_as_uint(v == v ? v : -INFINITY);
+  const uint32_t m = __reduce_max_sync(0xffffffffu, u & 0x80000000u ? ~u : u | 0x80000000u);
+  return __uint_as_float(m & 0x80000000u ? m & 0x7fffffffu : ~m);
+}
+
 LLM_D float qa_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -172,7 +190,7 @@ struct QaWalk {
 };
 
 template <int HD, int NP, int NC, int QT>
-__global__ void __launch_bounds__(64 + QaShape<HD, NP, NC>::NS, QaShape<HD, NP, NC>::CTAS)
+__global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::CTAS)
     qattn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const QAttnArgs a) {
   using X = QaShape<HD, NP, NC>;
   constexpr int N = X::N, C = X::C, CPC = X::CPC, ST = X::ST, CT = X::CT, NCH = X::NCH, HV = X::HV, NS = X::NS;
@@ -187,21 +205,28 @@ __global__ void __launch_bounds__(64 + QaShape<HD, NP, NC>::NS, QaShape<HD, NP, 
   float* gref = reinterpret_cast<float*>(cend + C);          // [2][C] references, by parity of the tile
   float* wmax = gref + 2 * C;                                // [2][4][C] warps' maxima; at the end, their sums
   float* ffac = wmax + 8 * C;                                // [2][C] at the end: factors of the two parities
-  float* wvs = ffac + 2 * C;                                 // [4][4] warps' largest value scales
+  float* ssc = ffac + 2 * C;                                 // [ST][16] a tile's block scales: keys (-1: not seen), values
+  float* wvs = ssc + 16 * ST;                                // [4][4] warps' largest value scales
   float* gvs = wvs + 16;                                     // [4] the groups' value scales
   const uint32_t bars = (smem_u32(gvs + 4) + 7u) & ~7u;
   const uint32_t b_full = bars, b_empty = b_full + 8 * ST, b_s = b_empty + 8 * ST, b_p = b_s + 16, b_pv = b_p + 16,
                  b_q = b_pv + 16;
-  static_assert((size_t)C * 4 * 14 + 80 + 16 * ST + 64 <= X::MISC, "shared memory");
+  static_assert((size_t)C * 4 * 16 + 80 + 80 * ST + 96 <= X::MISC, "shared memory");
   __shared__ uint32_t s_tmem;
-  __shared__ int s_t, s_last;
+  __shared__ int s_t;
   __shared__ long long s_off, s_total;
+  // the units that this CTA holds a part of (the first and the last of its run)
+  struct Pending {
+    int64_t qrow;
+    int j, used, first, np, last;
+  };
+  __shared__ Pending s_pend[2];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
   if (tid == 32) {
     for (int i = 0; i < ST; ++i) {
-      mbar_init(b_full + 8u * i, 1);
+      mbar_init(b_full + 8u * i, 17);
       mbar_init(b_empty + 8u * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -280,49 +305,57 @@ __global__ void __launch_bounds__(64 + QaShape<HD, NP, NC>::NS, QaShape<HD, NP, 
   };
 
   if (warp == 0) {
-    // ---- producer ----
+    // ---- producer: lane 0 the tiles, lanes 0..15 their block scales (keys, then values) ----
     if (lane == 0) {
       tma_prefetch_map(&kmap);
       tma_prefetch_map(&vmap);
-      long long it = 0;
-      int slot = 0;
-      uint32_t par = 1u;
-      for (; w.there() && ok; w.next(a)) {
-#pragma unroll 1
-        for (int k = w.k0; k < w.k1; ++k, ++it) {
-          const int p0 = (w.u.tile0 + k) * kQaTile;
-          int y[2];
-          uint32_t bytes = 0;
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            int row, pp;
-            y[hf] = -1;
-            if (p0 + 64 * hf < w.u.last && qa_place(a, w.u.b, p0 + 64 * hf, row, pp)) {
-              y[hf] = a.krow0 + (row * a.c.kv + w.j) * a.c.cap + pp;
-              bytes += 2 * 64 * HD;
-            }
-          }
-          wait(b_empty + 8u * slot, par);
-          if (!ok) break;
-          const uint32_t dst = s_ring + (uint32_t)slot * X::STAGE;
-          const uint32_t bar = b_full + 8u * slot;
-          mbar_expect_tx(bar, bytes);
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-            if (y[hf] >= 0) {
-              tma_load_2d(dst + hf * 64 * HD, &kmap, bar, 0, y[hf]);
-              tma_load_2d(dst + X::KB + hf * 64 * HD, &vmap, bar, 0, y[hf]);
-            }
-          if (++slot == ST) slot = 0, par ^= 1u;
-        }
-        if (!ok) break;
-      }
-      // no copy may still be writing shared memory when the CTA exits
-      ok = true;
-      const long long lo = it > ST ? it - ST : 0;
-#pragma unroll 1
-      for (long long i = lo; i < it; ++i) wait(b_full + 8u * (uint32_t)(i % ST), (uint32_t)(i / ST) & 1u);
     }
+    uint32_t it = 0u, slot = 0u, par = 1u;
+    const int blk = lane & 7;
+    for (; w.there() && ok; w.next(a)) {
+      const float* sc = lane < 8 ? a.c.ks : a.c.vs;
+#pragma unroll 1
+      for (int k = w.k0; k < w.k1; ++k, ++it) {
+        // the place of this lane's block, and with it of its half of the tile (pages hold 64 positions)
+        const int p0 = (w.u.tile0 + k) * kQaTile, pos = p0 + kQBlock * blk;
+        int row = 0, pp = 0;
+        const bool seen = pos < w.u.last && qa_place(a, w.u.b, pos, row, pp);
+        const int y = a.krow0 + (row * a.c.kv + w.j) * a.c.cap + pp;
+        const int y0 = __shfl_sync(0xffffffffu, y, 0), y1 = __shfl_sync(0xffffffffu, y, 4);
+        const uint32_t have = __ballot_sync(0xffffffffu, seen);
+        wait(b_empty + 8u * slot, par);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t bar = b_full + 8u * slot;
+        if (lane == 0) {
+          const uint32_t dst = s_ring + slot * X::STAGE;
+          mbar_expect_tx(bar, ((have & 1u) + (have >> 4 & 1u)) * 2 * 64 * HD);
+          if (have & 1u) {
+            tma_load_2d(dst, &kmap, bar, 0, y0);
+            tma_load_2d(dst + X::KB, &vmap, bar, 0, y0);
+          }
+          if (have & 16u) {
+            tma_load_2d(dst + 64 * HD, &kmap, bar, 0, y1);
+            tma_load_2d(dst + X::KB + 64 * HD, &vmap, bar, 0, y1);
+          }
+        }
+        if (lane < 16) {
+          float* dst = ssc + slot * 16 + lane;
+          if (seen) {
+            qa_copy4(smem_u32(dst), sc + ((size_t)row * a.c.kv + w.j) * (a.c.cap / kQBlock) + pp / kQBlock);
+            qa_copy_arrive(bar);
+          } else {
+            *dst = lane < 8 ? -1.f : 0.f;
+            mbar_arrive(bar);
+          }
+        }
+        if (++slot == ST) slot = 0u, par ^= 1u;
+      }
+    }
+    // no copy may still be writing shared memory when the CTA exits
+    ok = true;
+#pragma unroll 1
+    for (uint32_t i = it > ST ? it - ST : 0u; i < it; ++i) wait(b_full + 8u * (i % ST), (i / ST) & 1u);
   } else if (warp == 1) {
     // ---- MMA issuer ----
     if (lane == 0) {
@@ -395,23 +428,11 @@ __global__ void __launch_bounds__(64 + QaShape<HD, NP, NC>::NS, QaShape<HD, NP, 
           else static_cast<float*>(a.out)[at] = 0.f;
         }
     }
-    uint32_t cs = 0u, cpv = 0u;  // score tiles read, value products waited for
-    uint32_t it = 0u;            // tiles before this segment
+    uint32_t cs = 0u, cpv = 0u;             // score tiles read, value products waited for
+    uint32_t sb = 0u, spar = 0u;            // ring slot and phase of the segment's first tile
+    int pending = 0;
     for (; w.there(); w.next(a)) {
       const int n = w.k1 - w.k0, used = w.u.ntok * a.g;
-      // the scales of this thread's position in tile t (0 and not good where nothing sees it)
-      auto scales = [&](int t, float& ks, float& vs) {
-        ks = vs = 0.f;
-        const int pos = (w.u.tile0 + w.k0 + t) * kQaTile + quad * 32 + lane;
-        int row, pp;
-        if (t >= n || pos >= w.u.last || !qa_place(a, w.u.b, pos, row, pp)) return false;
-        const size_t at = ((size_t)row * a.c.kv + w.j) * (a.c.cap / kQBlock) + pp / kQBlock;
-        ks = a.c.ks[at];
-        vs = a.c.vs[at];
-        return true;
-      };
-      float ks, vs;
-      bool good = scales(gp, ks, vs);  // (in flight behind the query pieces)
       // ---- query pieces: warp = column ----
 #pragma unroll 1
       for (int c = sw; c < C; c += NS / 32) {
@@ -450,8 +471,8 @@ __global__ void __launch_bounds__(64 + QaShape<HD, NP, NC>::NS, QaShape<HD, NP, 
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] = fine ? x[e] * r : 0.f;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const int row = c * NP + i;
+        for (int y = 0; y < NP; ++y) {
+          const int row = c * NP + y;
           uint32_t code = 0u;
 #pragma unroll
           for (int e = 0; e < E; e += 2) {
@@ -475,10 +496,13 @@ __global__ void __launch_bounds__(64 + QaShape<HD, NP, NC>::NS, QaShape<HD, NP, 
       fence_proxy_async_smem();
       all_sync();  // (also: the segment before is written, its shared memory is free)
       if (stid == 0) mbar_arrive(b_q);
-
       float* ref = gref + gp * C + c0;      // references of the group's columns, alike for all its threads
       if (gtid < CT) ref[gtid] = c0 + gtid < used ? kQaNone : INFINITY;  // (no token: weights 2^-inf)
       group_sync();
+      const float* qsg = qsc + c0;
+      const int* ceg = cend + c0;
+      uint32_t slot = sb + gp, fpar = spar;  // ring slot and phase of this group's next tile
+      if (slot >= ST) slot -= ST, fpar ^= 1u;
       float l[CT];
 #pragma unroll
       for (int c = 0; c < CT; ++c) l[c] = 0.f;
@@ -487,46 +511,55 @@ __global__ void __launch_bounds__(64 + QaShape<HD, NP, NC>::NS, QaShape<HD, NP, 
 #pragma unroll 1
       for (int t = gp; t < n; t += 2) {
         const int p0 = (w.u.tile0 + w.k0 + t) * kQaTile, pos = p0 + quad * 32 + lane;
-        float ks1, vs1;
-        const bool good1 = scales(t + 2, ks1, vs1);  // the next tile's, in flight behind this one's work
+        wait(b_full + 8u * slot, fpar);
+        const float ks = ssc[slot * 16 + quad * 2 + (lane >> 4)], vs = ssc[slot * 16 + 8 + quad * 2 + (lane >> 4)];
         // columns see positions below their cend; where the whole tile is seen by all, every position is
-        const bool whole = __all_sync(0xffffffffu, good) && p0 >= w.u.start && p0 + kQaTile <= w.u.end0;
-        const int mypos = whole ? -0x7fffffff : good && pos >= w.u.start ? pos : 0x7fffffff;
+        const bool good = !(ks < 0.f) && pos < w.u.last && pos >= w.u.start;
+        const bool whole = __all_sync(0xffffffffu, good) && p0 + kQaTile <= w.u.end0;
+        const int mypos = whole ? -0x7fffffff : good ? pos : 0x7fffffff;
         wait(b_s + 8u * gp, cs++ & 1u);
         __syncwarp();
         tc_fence_after();
-        float s[CT];
-        bool low = !(vs > vref);
+        float s[CT], above = -INFINITY;  // scores, and the most by which one is above its reference
 #pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
           float d[16];
           tc_ld16(t_s + ch * 16, d);
           tc_wait_ld();
 #pragma unroll
-          for (int i = 0; i < CPC; ++i) {
-            const int c = ch * CPC + i;
-            float v = d[i * NP + NP - 1];
+          for (int i = 0; i < CPC; i += 4) {
+            const float4 qv = *reinterpret_cast<const float4*>(qsg + ch * CPC + i);
+            const float4 rv = *reinterpret_cast<const float4*>(ref + ch * CPC + i);
+            const int4 ev = *reinterpret_cast<const int4*>(ceg + ch * CPC + i);
+            const float q4[4] = {qv.x, qv.y, qv.z, qv.w}, r4[4] = {rv.x, rv.y, rv.z, rv.w};
+            const int e4[4] = {ev.x, ev.y, ev.z, ev.w};
 #pragma unroll
-            for (int x = NP - 2; x >= 0; --x) v = fmaf(v, 0.03125f, d[i * NP + x]);
-            s[c] = mypos < cend[c0 + c] ? v * (ks * qsc[c0 + c]) : -INFINITY;
-            low = low && !(s[c] > ref[c] + kQaMost);
+            for (int y = 0; y < 4; ++y) {
+              float v = d[(i + y) * NP + NP - 1];
+#pragma unroll
+              for (int x = NP - 2; x >= 0; --x) v = fmaf(v, 0.03125f, d[(i + y) * NP + x]);
+              v = mypos < e4[y] ? v * (ks * q4[y]) : -INFINITY;
+              s[ch * CPC + i + y] = v;
+              above = fmaxf(above, v - r4[y]);
+            }
           }
         }
+        const bool low = !(above > kQaMost) && !(good && vs > vref);
         if (!named_sync_and(1 + group, 128, low)) {
           // references move (rare): the group's maxima, then each column's new reference and what the
           // sums relative to the old one are worth under it
           float* wm = wmax + gp * 4 * C + c0;
 #pragma unroll
           for (int c = 0; c < CT; ++c) {
-            const float m = warp_max(s[c]);
+            const float m = qa_warp_max(s[c]);
             if (lane == 0) wm[gw * C + c] = m;
           }
-          const float mv = warp_max(vs);
+          const float mv = qa_warp_max(good ? vs : 0.f);
           if (lane == 0) wvs[group * 4 + gw] = mv;
           group_sync();
           if (gtid < CT) {
             const float old = ref[gtid];
-            const float top = fmaxf(old, fmaxf(fmaxf(wm[gtid], wm[C + gtid]), fmaxf(wm[2 * C + gtid], wm[3 * C + gtid])) - kQaTop);
+            const float top = fmaxf(old, fmaxf(fmaxf(wm[gtid], wm[C + gtid]), fmaxf(wm[2 * C + gtid], wm[3 * C + gtid])) - (t > gp ? kQaTop : kQaFirst));
             ref[gtid] = top;
             wm[gtid] = top == old ? 1.f : qa_exp2(old - top);
           }
@@ -561,7 +594,7 @@ __global__ void __launch_bounds__(64 + QaShape<HD, NP, NC>::NS, QaShape<HD, NP, 
             tc_wait_st();
           }
         }
-        const float vr = vs * vinv;
+        const float vr = good ? vs * vinv : 0.f;
         if (pend) wait(b_pv + 8u * gp, cpv++ & 1u);  // the weights' buffer is free again
 #pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
@@ -569,9 +602,10 @@ __global__ void __launch_bounds__(64 + QaShape<HD, NP, NC>::NS, QaShape<HD, NP, 
 #pragma unroll
           for (int i = 0; i < CPC; i += 2) {
             const int c = ch * CPC + i;
+            const float2 rv = *reinterpret_cast<const float2*>(ref + c);
             // a weight (0 where the column does not see the position), its sum, and with the value's
             // scale on it (a scale may be NaN, which reaches only the columns that see it)
-            float x0 = qa_exp2(s[c] - ref[c]), x1 = qa_exp2(s[c + 1] - ref[c + 1]);
+            float x0 = qa_exp2(s[c] - rv.x), x1 = qa_exp2(s[c + 1] - rv.y);
             l[c] += x0;
             l[c + 1] += x1;
             x0 = x0 == 0.f ? 0.f : x0 * vr;
@@ -598,8 +632,6 @@ __global__ void __launch_bounds__(64 + QaShape<HD, NP, NC>::NS, QaShape<HD, NP, 
         }
         if (mypos == 0x7fffffff && half == 0) {
           // rows that no column sees hold dead data (any code, NaN among them): zeros
-          const uint32_t i = it + t, slot = i % ST;
-          wait(b_full + 8u * slot, (i / ST) & 1u);
           uint4* v = reinterpret_cast<uint4*>(base + slot * X::STAGE + X::KB + (quad * 32 + lane) * HD);
 #pragma unroll 1
           for (int e = 0; e < HD / 16; ++e) v[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -608,14 +640,14 @@ __global__ void __launch_bounds__(64 + QaShape<HD, NP, NC>::NS, QaShape<HD, NP, 
         tc_fence_before();
         mbar_arrive(b_p + 8u * gp);
         pend = true;
-        good = good1;
-        ks = ks1;
-        vs = vs1;
+        slot += 2;
+        if (slot >= ST) slot -= ST, fpar ^= 1u;
       }
       if (pend) wait(b_pv + 8u * gp, cpv++ & 1u);
       __syncwarp();
       tc_fence_after();
-      it += n;
+      spar ^= ((sb + n) / ST) & 1u;
+      sb = (sb + n) % ST;
 
       // ---- the segment's end: the parities' sums meet, parity 0 writes ----
       {
@@ -696,15 +728,32 @@ __global__ void __launch_bounds__(64 + QaShape<HD, NP, NC>::NS, QaShape<HD, NP, 
         }
         if (pass == 1 && both) all_sync();
       }
-      if (alone) continue;
-      // ---- a unit of several CTAs: the last of them to get here adds the parts in CTA order ----
-      const int first = cut.owner(w.unit0()), np = cut.owner(w.unit0() + w.u.nt - 1) - first + 1;
+      if (!alone) {
+        if (stid == 0) {
+          const int first = cut.owner(w.unit0());
+          s_pend[pending] = Pending{w.u.qrow, w.j, used, first, cut.owner(w.unit0() + w.u.nt - 1) - first + 1, 0};
+        }
+        ++pending;
+      }
+    }
+    // ---- units of several CTAs: the last of them to get here adds the parts in CTA order ----
+    if (pending > 0) {
       __threadfence();
       all_sync();
-      if (stid == 0) s_last = atomicInc(reinterpret_cast<uint32_t*>(a.ws) + first, (uint32_t)(np - 1)) == (uint32_t)(np - 1);
+      if (stid < pending) {
+        Pending& u = s_pend[stid];
+        u.last = atomicInc(reinterpret_cast<uint32_t*>(a.ws) + u.first, (uint32_t)(u.np - 1)) == (uint32_t)(u.np - 1);
+      }
       all_sync();
-      if (!s_last) continue;
       __threadfence();
+    }
+#pragma unroll 1
+    for (int pi = 0; pi < pending; ++pi) {
+      const Pending u = s_pend[pi];
+      if (!u.last) continue;
+      all_sync();  // (the unit before is written)
+      const int np = u.np, first = u.first, used = u.used;
+      const float* parts = reinterpret_cast<const float*>(a.ws + kQattnTickets);
       auto part = [&](int i) { return parts + ((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * C * (HD + 2); };
       auto stat = [&](int i, int c) { return __ldcg(reinterpret_cast<const float2*>(part(i) + C * HD + 2 * c)); };
       float* fac = reinterpret_cast<float*>(pbuf);  // [C][64] factors of 64 parts at a time
@@ -791,7 +840,7 @@ __global__ void __launch_bounds__(64 + QaShape<HD, NP, NC>::NS, QaShape<HD, NP, 
           const float r = wmax[c] == 0.f ? 0.f : 1.f / wmax[c];
           const float4 o = make_float4(O[q].x * r, O[q].y * r, O[q].z * r, O[q].w * r);
           const int tok = c / a.g;
-          const int64_t at = (w.u.qrow + tok) * a.out_stride + (int64_t)(w.j * a.g + c - tok * a.g) * HD + e;
+          const int64_t at = (u.qrow + tok) * a.out_stride + (int64_t)(u.j * a.g + c - tok * a.g) * HD + e;
           if constexpr (QT) {
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
                 make_uint2((uint32_t)f32_to_bf16(o.x) | (uint32_t)f32_to_bf16(o.y) << 16,
@@ -821,7 +870,7 @@ cudaError_t launch_qattn_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, co
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(64 + QaShape<HD, NP, NC>::NS);
+  cfg.blockDim = dim3(QaShape<HD, NP, NC>::NT);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
