@@ -53,6 +53,7 @@ enum {
 };
 
 enum { LLM_DTYPE_F32 = 0, LLM_DTYPE_BF16 = 1 };
+enum { LLM_CACHE_MODEL = 0, LLM_CACHE_E4M3 = 1 };
 
 /*
  * Model shape and capacity (P1 Cfg; P3 nest.toml generics and rope.linnet constants).
@@ -87,6 +88,14 @@ typedef struct llm_config {
                            heads per kv head): 1 run all layers and the head as one persistent
                            kernel where the device allows it; 0 one kernel per operation (the
                            default: faster at the 8B shape so far) */
+  int32_t cache_type;   /* LLM_CACHE_MODEL (0): the cache holds dtype; LLM_CACHE_E4M3: 8-bit codes with
+                           block scales (see llm_qcache), in about half the bytes of a bf16 cache.
+                           Keys and values are rounded to dtype, then quantised as llm_qcache_write
+                           does; every entry works on it (step_kernel is ignored).  A step at a
+                           position that is not a multiple of 16 ends what its block of 16 held after
+                           it: with llm_decode_paged, write a page's positions in order; llm_kv_import
+                           and llm_prefill_packed refuse to end inside a block whose later positions
+                           are filled and not written by the call (LLM_ERR_POS_RANGE) */
 } llm_config;
 
 typedef struct llm_handle llm_handle;
@@ -269,6 +278,25 @@ llm_status llm_generate_dev(llm_handle* h, const int32_t* tokens_dev, int32_t B,
                             int32_t n_steps, float temp, int32_t k, float p, const float* u_dev,
                             int32_t* ids_dev);
 
+/*
+ * Drafted tokens, verified in one pass (speculative sampling; the pages have no counterpart): row b
+ * takes the S + 1 tokens tokens_host [B][S + 1] -- its last token, then S drafts -- at positions
+ * positions_host[b] .. + S, as a prefill pass would.  p_dev [B][S + 1][V] receives the target's
+ * probabilities after each of them: softmax(logits / temp), or for temp == 0 a 1 at the first index of
+ * the largest logit.  Then llm_verify runs on them with q_dev [B][S][V] (the draft model's
+ * probabilities at the same temperature, or NULL), the drafts and u_dev [B][S + 1], into ids_dev
+ * [B][S + 1] and accepted_dev [B]: ids_dev[b][0 .. accepted] are the row's next tokens.  tokens and
+ * positions are host memory, the rest device memory; ordered on the handle's stream, returns without
+ * waiting.  Checks: 1 <= B <= max_batch and B * (S + 1) <= max(max_batch, max_tokens) (LLM_ERR_BATCH);
+ * S >= 1, temp finite and >= 0, no debug_trace handle (LLM_ERR_ARG); 0 <= positions_host[b] <= filled
+ * length of row b and positions_host[b] + S < max_seq (LLM_ERR_POS_RANGE); tokens in [0, vocab)
+ * (LLM_ERR_TOKEN_RANGE).  After success the filled length of row b is positions_host[b] + S + 1; its
+ * next step starts at positions_host[b] + accepted + 1, which rewinds over the drafts not kept.
+ */
+llm_status llm_verify_step(llm_handle* h, const int32_t* tokens_host, int32_t B, int32_t S,
+                           const int32_t* positions_host, float temp, const float* q_dev,
+                           const float* u_dev, float* p_dev, int32_t* ids_dev, int32_t* accepted_dev);
+
 /* Wait for the handle's stream; return the first error recorded on the device since the last
  * call (LLM_ERR_TOKEN_RANGE, LLM_ERR_DEVICE_TIMEOUT) and clear it. */
 llm_status llm_synchronize(llm_handle* h);
@@ -289,8 +317,8 @@ const char* llm_status_string(llm_status s);
 
 /*
  * Test hooks.  kv_import / kv_export copy n positions starting at pos0 of one layer and cache
- * row, for every key/value head, from / to host memory laid out [kv][n][hd] in the cache element
- * type (bf16 bits or f32).  kv_import raises the row's filled length to at least pos0 + n.
+ * row, for every key/value head, from / to host memory laid out [kv][n][hd] in dtype (bf16 bits or
+ * f32; an 8-bit cache is quantised and read back as llm_qcache_write and _read do).  kv_import raises the row's filled length to at least pos0 + n.
  * Positions must satisfy 0 <= pos0, pos0 + n <= max_seq (else LLM_ERR_POS_RANGE).
  */
 llm_status llm_kv_import(llm_handle* h, int32_t layer, int32_t row, int32_t pos0, int32_t n,

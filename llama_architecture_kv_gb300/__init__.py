@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(_HERE, "libllm.so")
 LLM_OK, LLM_ERR_CONFIG, LLM_ERR_WEIGHTS_SIZE, LLM_ERR_OOM, LLM_ERR_POS_RANGE = 0, 1, 2, 3, 4
 LLM_ERR_TOKEN_RANGE, LLM_ERR_BATCH, LLM_ERR_ARG, LLM_ERR_CUDA, LLM_ERR_DEVICE_TIMEOUT = 5, 6, 7, 8, 9
 LLM_DTYPE_F32, LLM_DTYPE_BF16 = 0, 1
+LLM_CACHE_MODEL, LLM_CACHE_E4M3 = 0, 1
 
 # every extern "C" symbol include/llm.h declares
 EXPORTS = ("llm_weight_count", "llm_create", "llm_destroy", "llm_reset", "llm_prefill", "llm_decode",
@@ -26,7 +27,7 @@ EXPORTS = ("llm_weight_count", "llm_create", "llm_destroy", "llm_reset", "llm_pr
            "llm_step_rows_dev", "llm_generate", "llm_generate_dev", "llm_decode_paged",
            "llm_decode_paged_dev", "llm_step_paged", "llm_step_paged_dev", "llm_check_wait_timeout",
            "llm_prefill_packed", "llm_qcache_write", "llm_qcache_read", "llm_qcache_workspace",
-           "llm_qcache_attend", "llm_verify")
+           "llm_qcache_attend", "llm_verify", "llm_verify_step")
 
 
 class LlmConfig(ctypes.Structure):
@@ -38,7 +39,8 @@ class LlmConfig(ctypes.Structure):
                 ("rope_orig_max_pos", ctypes.c_float), ("max_batch", ctypes.c_int32),
                 ("max_seq", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("debug_trace", ctypes.c_int32), ("tc_min_batch", ctypes.c_int32),
-                ("max_tokens", ctypes.c_int32), ("step_kernel", ctypes.c_int32)]
+                ("max_tokens", ctypes.c_int32), ("step_kernel", ctypes.c_int32),
+                ("cache_type", ctypes.c_int32)]
 
 
 class LlmQcache(ctypes.Structure):
@@ -99,6 +101,7 @@ SIGNATURES = {
     "llm_qcache_workspace": ([_pqc, _i32, _i32, _i32, ctypes.POINTER(_u64)], _i32),
     "llm_qcache_attend": ([_pqc, _vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _f32, _vp, _i64, _vp, _u64,
                            _vp, _vp], _i32),
+    "llm_verify_step": ([_vp, _vp, _i32, _i32, _vp, _f32, _vp, _vp, _vp, _vp, _vp], _i32),
     "llm_verify": ([_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp], _i32),
     }
 
@@ -122,14 +125,14 @@ def lib():
 
 
 def config(shape, max_batch, max_seq, debug_trace=False, tc_min_batch=0, max_tokens=0,
-           step_kernel=0) -> LlmConfig:
+           step_kernel=0, cache_type=LLM_CACHE_MODEL) -> LlmConfig:
     """An llm_config from a shape description (fields kv, g, half, ffn, layers, vocab, eps,
     theta, tied, llama3, factor, low_freq, high_freq, orig_max, bf16)."""
     return LlmConfig(shape.kv, shape.g, shape.half, shape.ffn, shape.layers, shape.vocab,
                      shape.eps, shape.theta, int(shape.tied), int(shape.llama3), shape.factor,
                      shape.low_freq, shape.high_freq, shape.orig_max, max_batch, max_seq,
                      LLM_DTYPE_BF16 if shape.bf16 else LLM_DTYPE_F32, int(debug_trace),
-                     int(tc_min_batch), int(max_tokens), int(step_kernel))
+                     int(tc_min_batch), int(max_tokens), int(step_kernel), int(cache_type))
 
 
 def _ptr(a):
@@ -260,6 +263,11 @@ def llm_step_paged_dev(h, tokens, B, positions, table, pages_per_row, temp, k, p
 def llm_prefill_packed(h, tokens, rows, positions, segments, P, last, nlast, logits):
     _check(h, lib().llm_prefill_packed(h, _ptr(tokens), _ptr(rows), _ptr(positions), _ptr(segments), P,
                                        _ptr(last), nlast, _ptr(logits)))
+
+
+def llm_verify_step(h, tokens, B, S, positions, temp, q, u, p, ids, accepted):
+    _check(h, lib().llm_verify_step(h, _ptr(tokens), B, S, _ptr(positions), temp, _ptr(q), _ptr(u), _ptr(p),
+                                    _ptr(ids), _ptr(accepted)))
 
 
 def llm_synchronize(h):
@@ -518,9 +526,9 @@ class Model:
     """One handle: host-memory entry points with numpy arrays."""
 
     def __init__(self, shape, weights, max_batch, max_seq, stream=None, debug_trace=False,
-                 weights_on_device=False, tc_min_batch=0, max_tokens=0, step_kernel=0):
+                 weights_on_device=False, tc_min_batch=0, max_tokens=0, step_kernel=0, cache_type=LLM_CACHE_MODEL):
         self.shape = shape
-        self.cfg = config(shape, max_batch, max_seq, debug_trace, tc_min_batch, max_tokens, step_kernel)
+        self.cfg = config(shape, max_batch, max_seq, debug_trace, tc_min_batch, max_tokens, step_kernel, cache_type)
         self.h = llm_create(self.cfg, weights, weights_on_device, stream)
         self.V = shape.vocab
         self.cache_dtype = np.uint16 if shape.bf16 else np.float32
@@ -609,6 +617,25 @@ class Model:
         out = np.empty((last.size, self.V), np.float32) if logits else None
         llm_prefill_packed(self.h, tokens, rows, positions, segments, P, last, last.size, out)
         return out
+
+    def verify_step(self, tokens, positions, u, temp=0.0, q=None):
+        """The last token and S drafts of each row (tokens [B][S + 1]) at positions[b] .. + S in one pass,
+        verified against the model: the row's next tokens ids [B][S + 1] (the kept drafts, one drawn
+        token, then -1), the drafts kept [B], and the probabilities p [B][S + 1][V].  q [B][S][V]: the
+        draft model's probabilities (None: deterministic drafts); u [B][S + 1] draws."""
+        import torch
+        tokens = np.ascontiguousarray(tokens, np.int32)
+        B, S = tokens.shape[0], tokens.shape[1] - 1
+        positions = np.ascontiguousarray(positions, np.int32).reshape(-1)
+        u = np.ascontiguousarray(u, np.float32)
+        assert positions.size == B and u.shape == (B, S + 1) and (q is None or q.shape == (B, S, self.V))
+        dev = lambda a: None if a is None else torch.from_numpy(np.ascontiguousarray(a, np.float32)).cuda()  # noqa: E731
+        ud, qd, p = dev(u), dev(q), torch.empty(B, S + 1, self.V, device="cuda")
+        ids, acc = torch.empty(B, S + 1, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()  # (the copies ran on torch's stream)
+        llm_verify_step(self.h, tokens, B, S, positions, temp, qd, ud, p, ids, acc)
+        self.synchronize()
+        return ids.cpu().numpy(), acc.cpu().numpy(), p.cpu().numpy()
 
     def sample(self, logits, temp, k, p, u):
         logits = np.ascontiguousarray(logits, np.float32)

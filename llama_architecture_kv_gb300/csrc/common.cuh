@@ -142,6 +142,16 @@ LLM_D void cache_slot(const StepState* s, int cap, int b, int pos, int& r, int& 
   r = page / per_row;
   pp = (page - r * per_row) * kPage + (pos & (kPage - 1));
 }
+// The slot that the Q/K/V kernels store row b's new key and value in: its cache slot, or with an 8-bit
+// cache row b of a staging buffer [rows][kv][hd], from which they are quantised into the cache.
+LLM_D void store_slot(const StepState* s, int cap, int staged, int b, int pos, int& r, int& pp) {
+  if (staged) {
+    r = b;
+    pp = 0;
+    return;
+  }
+  cache_slot(s, cap, b, pos, r, pp);
+}
 LLM_HD size_t step_state_bytes(int max_rows) { return sizeof(StepState) + (size_t)max_rows * 4 * 4; }
 
 // device error codes (same values as llm.h)

@@ -57,6 +57,7 @@ struct TcQkvArgs {
   void* kc;
   void* vc;
   int32_t H, kv, hd, cap;
+  int32_t staged;         // 1: kc, vc are staging buffers [rows][kv][hd] and cap is 1
   const float* rope_cos;
   const float* rope_sin;
   const StepState* step;

@@ -302,14 +302,14 @@ __global__ void __launch_bounds__(kGemvThreads, 2) gemv_kernel(const GemvArgs a)
               a.tr_rot[row * a.tr_stride + (size_t)(head - a.H) * a.hd + e + half] = hi;
             }
             int r, pp;
-            cache_slot(a.step, a.cap, (int)row, pos, r, pp);
+            store_slot(a.step, a.cap, a.staged, (int)row, pos, r, pp);
             const size_t ci = (((size_t)r * a.kv + (size_t)(head - a.H)) * a.cap + pp) * a.hd;
             store_elem<WT>(a.kc, ci + e, lo);
             store_elem<WT>(a.kc, ci + e + half, hi);
           }
         } else {
           int r, pp;
-          cache_slot(a.step, a.cap, (int)row, pos, r, pp);
+          store_slot(a.step, a.cap, a.staged, (int)row, pos, r, pp);
           const size_t ci = (((size_t)r * a.kv + (size_t)(head - a.H - a.kv)) * a.cap + pp) * a.hd;
           store_elem<WT>(a.vc, ci + e, x0);
           store_elem<WT>(a.vc, ci + e + half, x1);
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kTmaWarps * 32, 1) gemv_tma_kernel(const GemvA
         in.c = __ldg(a.rope_cos + (size_t)in.pos * half + e);
         in.s = __ldg(a.rope_sin + (size_t)in.pos * half + e);
       }
-      if (head >= a.H) cache_slot(a.step, a.cap, 0, in.pos, in.r, in.pp);
+      if (head >= a.H) store_slot(a.step, a.cap, a.staged, 0, in.pos, in.r, in.pp);
     }
     return in;
   };

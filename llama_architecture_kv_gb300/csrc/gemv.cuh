@@ -36,7 +36,8 @@ struct GemvArgs {
   void* kc;             // this layer's key cache [max_batch][kv][cap][hd]
   void* vc;             // this layer's value cache
   int32_t H, kv, hd, cap;
-  const float* rope_cos;  // [cap][hd/2]
+  int32_t staged;       // 1: kc, vc are staging buffers [rows][kv][hd] and cap is 1
+  const float* rope_cos;  // [positions][hd/2]
   const float* rope_sin;
   int32_t* status;      // device error flag (a bounded wait that ran out)
   // intermediates for a traced step (null otherwise; set, the launch runs gemv_kernel):

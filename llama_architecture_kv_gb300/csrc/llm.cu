@@ -23,8 +23,10 @@
 #include "mega.cuh"
 #include "gemv.cuh"
 #include "llm.h"
+#include "qcache.cuh"
 #include "sampler.cuh"
 #include "tc.cuh"
+#include "verify.cuh"
 
 using namespace llm;
 
@@ -278,6 +280,14 @@ struct llm_handle {
   void* kc = nullptr;  // [L][max_batch][kv][cap][hd]
   void* vc = nullptr;
   size_t layer_cache_elems = 0;
+  // 8-bit cache (LLM_CACHE_E4M3; kc and vc are not allocated)
+  bool q8 = false;
+  int qcap = 0;                                   // max_seq rounded up to whole pages
+  uint8_t *qk = nullptr, *qv = nullptr;           // codes [L][max_batch][kv][qcap][hd]
+  float *qks = nullptr, *qvs = nullptr;           // scales [L][max_batch][kv][qcap / kQBlock]
+  void *stage_k = nullptr, *stage_v = nullptr;    // [NT][kv][hd] keys and values of a step, in dtype
+  unsigned char* qws = nullptr;                   // attention workspace
+  bool q_tiles = false;                           // prefill passes list tiles for the 8-bit attention
   float *rope_cos = nullptr, *rope_sin = nullptr;
   float *xa = nullptr, *xb = nullptr, *q = nullptr, *attn = nullptr, *m = nullptr, *logits = nullptr;
   float* part = nullptr;
@@ -374,6 +384,8 @@ const char* check_config(const llm_config* c) {
   const int64_t d = (int64_t)c->kv_heads * c->group * hd;
   if (d % per16 || c->ffn % per16) return "hidden and ffn widths must fill whole 16-byte chunks";
   if ((int64_t)c->max_seq * c->max_batch > (int64_t)1 << 40) return "cache too large";
+  if (c->cache_type != LLM_CACHE_MODEL && c->cache_type != LLM_CACHE_E4M3)
+    return "cache_type must be LLM_CACHE_MODEL or LLM_CACHE_E4M3";
   return nullptr;
 }
 
@@ -549,6 +561,24 @@ float* tr_slot(llm_handle* h, int l, int slot) {
   return h->trace + ((size_t)l * kTraceSlots + slot) * h->cfg.max_batch * h->trace_w;
 }
 
+// layer l of the 8-bit cache, and the rows of a step (their places: cache_slot)
+QCacheView q8_view(const llm_handle* h, int l) {
+  const size_t rows = (size_t)h->cfg.max_batch * h->cfg.kv_heads, codes = rows * h->qcap * h->hd,
+               blocks = rows * (h->qcap / kQBlock);
+  return QCacheView{h->qk + l * codes, h->qv + l * codes, h->qks + l * blocks, h->qvs + l * blocks,
+                    h->cfg.max_batch, h->cfg.kv_heads, h->qcap, h->hd};
+}
+QRows q8_rows(const llm_handle* h, int B) {
+  QRows r = {};
+  r.B = B; r.S = 1; r.limit = h->qcap; r.step = h->st; r.status = h->status;
+  return r;
+}
+// the staged keys and values of a step into layer l
+llm_status q8_store(llm_handle* h, int l, int B, bool pdl) {
+  CUDA_TRY(h, launch_qcache_write_step(q8_view(h, l), q8_rows(h, B), h->stage_k, h->stage_v, h->wt, h->stream, pdl));
+  return LLM_OK;
+}
+
 // launch one kernel of the decode step (layer l where it applies); on the tensor-core path a
 // projection is two kernels (activation split, then the GEMM)
 llm_status launch_one(llm_handle* h, int which, int l, int B, bool pdl) {
@@ -594,8 +624,8 @@ llm_status launch_one(llm_handle* h, int which, int l, int B, bool pdl) {
     return LLM_OK;
   }
   const LayerW& w = h->lw[l];
-  char* kcl = (char*)h->kc + (size_t)l * h->layer_cache_elems * h->es;
-  char* vcl = (char*)h->vc + (size_t)l * h->layer_cache_elems * h->es;
+  char* kcl = h->q8 ? (char*)h->stage_k : (char*)h->kc + (size_t)l * h->layer_cache_elems * h->es;
+  char* vcl = h->q8 ? (char*)h->stage_v : (char*)h->vc + (size_t)l * h->layer_cache_elems * h->es;
   if (tc && which != K_ATTN) {
     const TcMaps& tm = h->tmaps[l];
     const int qkv_rows = (h->H + 2 * c.kv_heads) * h->hd;
@@ -613,10 +643,10 @@ llm_status launch_one(llm_handle* h, int which, int l, int B, bool pdl) {
       TcQkvArgs qa = {};
       qa.part = h->tc_part; qa.S = plan_tc(qkv_rows, h->d, B, h->num_sms).S; qa.rows = qkv_rows; qa.B = B;
       qa.q_out = h->q; qa.q_stride = h->d; qa.kc = kcl; qa.vc = vcl;
-      qa.H = h->H; qa.kv = c.kv_heads; qa.hd = h->hd; qa.cap = c.max_seq;
+      qa.H = h->H; qa.kv = c.kv_heads; qa.hd = h->hd; qa.cap = h->q8 ? 1 : c.max_seq; qa.staged = h->q8;
       qa.rope_cos = h->rope_cos; qa.rope_sin = h->rope_sin; qa.step = h->st;
       CUDA_TRY(h, launch_tc_qkv(qa, h->stream, pdl));
-      return LLM_OK;
+      return h->q8 ? q8_store(h, l, B, pdl) : LLM_OK;
     }
     if (which == K_O) {
       in.x = h->attn; in.x_stride = h->d;
@@ -645,12 +675,21 @@ llm_status launch_one(llm_handle* h, int which, int l, int B, bool pdl) {
     a.x = h->xa; a.x_stride = h->d; a.gain = w.ln1;
     a.lpr = p.lpr; a.seg_ch = p.seg_ch; a.nseg = p.nseg; a.rows_cap = p.rows_cap; a.ws = p.ws;
     a.q_out = h->q; a.q_stride = h->d; a.kc = kcl; a.vc = vcl;
-    a.H = h->H; a.kv = c.kv_heads; a.hd = h->hd; a.cap = c.max_seq;
+    a.H = h->H; a.kv = c.kv_heads; a.hd = h->hd; a.cap = h->q8 ? 1 : c.max_seq; a.staged = h->q8;
     a.rope_cos = h->rope_cos; a.rope_sin = h->rope_sin;
     a.status = h->status;
     a.tr_in = tr_slot(h, l, TR_N1); a.tr_pre = tr_slot(h, l, TR_QKV); a.tr_rot = tr_slot(h, l, TR_KR);
     a.tr_stride = (int32_t)h->trace_w;
     CUDA_TRY(h, launch_gemv(a, p, wt, EPI_QKV, true, h->stream, pdl));
+    if (h->q8) return q8_store(h, l, B, pdl);
+  } else if (which == K_ATTN && h->q8) {
+    QAttnArgs qa = {};
+    qa.c = q8_view(h, l); qa.r = q8_rows(h, B);
+    qa.q = h->q; qa.out = h->attn; qa.q_stride = qa.out_stride = h->d; qa.g = c.group;
+    qa.scale = 1.0f / sqrtf((float)h->hd); qa.ws = h->qws;
+    qa.tiles = h->capturing_pass && h->q_tiles ? h->tile_buf : nullptr;
+    qa.krow0 = (int32_t)((size_t)l * c.max_batch * c.kv_heads * h->qcap);
+    CUDA_TRY(h, launch_qattn(qa, 0, h->num_sms, h->stream, pdl, &h->kmap, &h->vmap));
   } else if (which == K_ATTN && h->capturing_pass && h->pf_attn) {
     // a prefill pass: tiles of consecutive prompt tokens share each key/value stream
     AttnPrefillArgs pa = {};
@@ -1013,7 +1052,10 @@ llm_status llm_create(const llm_config* cfg, const void* weights, uint64_t nbyte
     h->tc_min = tc_min;
   }
   if ((ce = attn_prepare(h->smem_optin)) != cudaSuccess) return cuda_bail("attention kernel attributes", ce);
-  h->pf_attn = attn_prefill_supported(h->wt, 2 * c.half, c.group);
+  h->q8 = c.cache_type == LLM_CACHE_E4M3;
+  h->qcap = (c.max_seq + kPage - 1) / kPage * kPage;
+  h->q_tiles = h->q8 && qattn_uses_tc(h->hd);
+  h->pf_attn = !h->q8 && attn_prefill_supported(h->wt, 2 * c.half, c.group);
   if (h->pf_attn && (ce = attn_prefill_prepare(h->smem_optin)) != cudaSuccess)
     return cuda_bail("prefill attention kernel attributes", ce);
   // the allocation-free sampler's array is reserved here, where allocating is allowed
@@ -1039,11 +1081,32 @@ llm_status llm_create(const llm_config* cfg, const void* weights, uint64_t nbyte
   // KV cache, RoPE table, activations, scratch
   h->layer_cache_elems = (size_t)c.max_batch * c.kv_heads * c.max_seq * h->hd;
   const size_t cache_bytes = (size_t)h->L * h->layer_cache_elems * es;
-  if ((st = dalloc(h, &h->kc, cache_bytes)) || (st = dalloc(h, &h->vc, cache_bytes))) return bail(st);
-  if ((uint64_t)h->L * c.max_batch * c.kv_heads * c.max_seq >= (1ull << 31) ||
-      !attn_make_kmap(&h->kmap, h->kc, h->wt, h->hd, (uint64_t)h->L * c.max_batch * c.kv_heads * c.max_seq) ||
-      !attn_make_kmap(&h->vmap, h->vc, h->wt, h->hd, (uint64_t)h->L * c.max_batch * c.kv_heads * c.max_seq)) {
-    fail(h, LLM_ERR_CONFIG, "the key cache does not fit a tensor map (layers x rows x kv heads x positions < 2^31)");
+  const uint64_t cache_rows = (uint64_t)h->L * c.max_batch * c.kv_heads * (h->q8 ? h->qcap : c.max_seq);
+  const size_t scale_bytes = cache_rows / kQBlock * 4;
+  if (cache_rows >= (1ull << 31)) {
+    fail(h, LLM_ERR_CONFIG, "the cache does not fit a tensor map (layers x rows x kv heads x positions < 2^31)");
+    return bail(LLM_ERR_CONFIG);
+  }
+  if (h->q8) {
+    const size_t stage = (size_t)h->NT * h->kvw * es;
+    if ((st = dalloc(h, &h->qk, cache_rows * h->hd)) || (st = dalloc(h, &h->qv, cache_rows * h->hd)) ||
+        (st = dalloc(h, &h->qks, scale_bytes)) || (st = dalloc(h, &h->qvs, scale_bytes)) ||
+        (st = dalloc(h, &h->stage_k, stage)) || (st = dalloc(h, &h->stage_v, stage)))
+      return bail(st);
+    const size_t ws = qattn_step_workspace(q8_view(h, 0), c.group, h->NT, h->num_sms);
+    if ((st = dalloc(h, &h->qws, ws))) return bail(st);
+    if (cudaMemsetAsync(h->qk, 0, cache_rows * h->hd, h->stream) != cudaSuccess ||
+        cudaMemsetAsync(h->qv, 0, cache_rows * h->hd, h->stream) != cudaSuccess ||
+        cudaMemsetAsync(h->qks, 0, scale_bytes, h->stream) != cudaSuccess ||
+        cudaMemsetAsync(h->qvs, 0, scale_bytes, h->stream) != cudaSuccess ||
+        cudaMemsetAsync(h->qws, 0, ws, h->stream) != cudaSuccess)
+      return cuda_bail("clearing the cache", cudaGetLastError());
+  } else if ((st = dalloc(h, &h->kc, cache_bytes)) || (st = dalloc(h, &h->vc, cache_bytes))) {
+    return bail(st);
+  }
+  if (h->q8 ? h->q_tiles && (!qattn_make_map(&h->kmap, h->qk, h->hd, cache_rows) || !qattn_make_map(&h->vmap, h->qv, h->hd, cache_rows))
+            : !attn_make_kmap(&h->kmap, h->kc, h->wt, h->hd, cache_rows) || !attn_make_kmap(&h->vmap, h->vc, h->wt, h->hd, cache_rows)) {
+    fail(h, LLM_ERR_CONFIG, "the cache does not fit a tensor map");
     return bail(LLM_ERR_CONFIG);
   }
   if ((st = dalloc(h, &h->rope_cos, (size_t)c.max_seq * c.half * 4)) ||
@@ -1065,7 +1128,7 @@ llm_status llm_create(const llm_config* cfg, const void* weights, uint64_t nbyte
   h->part_ns = maxns;
   h->ticket_count = (int)(NT * c.kv_heads);
   const int slots = attn_part_slots(h->wt, h->hd, maxns);
-  if ((st = dalloc(h, &h->part, NT * h->H * slots * (h->hd + 2) * 4)) ||
+  if ((!h->q8 && (st = dalloc(h, &h->part, NT * h->H * slots * (h->hd + 2) * 4))) ||
       (st = dalloc(h, &h->ticket, NT * c.kv_heads * 4)) || (st = dalloc(h, &h->st, step_state_bytes((int)NT))) ||
       (st = dalloc(h, &h->pos_buf, NT * 4)) || (st = dalloc(h, &h->gen, sizeof(GenState))) ||
       (st = dalloc(h, &h->u_gen, (size_t)kGenChunk * B * 4)) || (st = dalloc(h, &h->ids_gen, (size_t)kGenChunk * B * 4)) ||
@@ -1115,7 +1178,7 @@ llm_status llm_create(const llm_config* cfg, const void* weights, uint64_t nbyte
     // batch-1 steps as one persistent kernel where the shape allows it and every CTA can be resident
     int coop = 0;
     cudaDeviceGetAttribute(&coop, cudaDevAttrCooperativeLaunch, h->dev);
-    if (coop && !c.debug_trace && c.step_kernel == 1 && h->num_sms >= c.kv_heads &&
+    if (coop && !c.debug_trace && c.step_kernel == 1 && !h->q8 && h->num_sms >= c.kv_heads &&
         mega_supported(h->wt, h->hd, c.group, h->d, h->f) &&
         mega_smem(h->d, h->f) + 1024 <= (size_t)h->smem_optin && mega_prepare(h->smem_optin) == cudaSuccess) {
       if ((st = dalloc(h, &h->mega_layers, sizeof(MegaLayer) * (size_t)h->L)) ||
@@ -1137,8 +1200,8 @@ llm_status llm_create(const llm_config* cfg, const void* weights, uint64_t nbyte
   }
   if (cudaMemsetAsync(h->ticket, 0, NT * c.kv_heads * 4, h->stream) != cudaSuccess ||
       cudaMemsetAsync(h->status, 0, 16, h->stream) != cudaSuccess ||
-      cudaMemsetAsync(h->kc, 0, cache_bytes, h->stream) != cudaSuccess ||
-      cudaMemsetAsync(h->vc, 0, cache_bytes, h->stream) != cudaSuccess)
+      (!h->q8 && (cudaMemsetAsync(h->kc, 0, cache_bytes, h->stream) != cudaSuccess ||
+                  cudaMemsetAsync(h->vc, 0, cache_bytes, h->stream) != cudaSuccess)))
     return cuda_bail("clearing the cache", cudaGetLastError());
   RopeArgs ra = {c.theta, h->hd, c.half, c.max_seq, c.rope_llama3, c.rope_factor, c.rope_low_freq, c.rope_high_freq,
                  c.rope_orig_max_pos, h->rope_cos, h->rope_sin};
@@ -1171,6 +1234,7 @@ llm_status llm_synchronize(llm_handle* h) {
     // a kernel that gave up may have left the attention's merge tickets short of their count
     if (s == LLM_ERR_DEVICE_TIMEOUT) {
       CUDA_TRY(h, cudaMemset(h->ticket, 0, (size_t)h->ticket_count * 4));
+      if (h->qws) CUDA_TRY(h, cudaMemset(h->qws, 0, kQattnTickets));
       if (h->mega_ticket) CUDA_TRY(h, cudaMemset(h->mega_ticket, 0, ((size_t)h->cfg.kv_heads + 1) * 4));
     }
     return fail(h, s, "device reported: %s", llm_status_string(s));
@@ -1204,23 +1268,32 @@ __global__ void gather_rows_f32_kernel(float* dst, const float* src, const int32
   for (int i = threadIdx.x; i < width; i += blockDim.x) o[i] = s[i];
 }
 
-// final norm + LM head over rows 0..m-1 of xh into the logits buffer
-static llm_status head_rows(llm_handle* h, int m) {
+// final norm + LM head over m rows of x ([m][d]) into out ([m][V])
+static llm_status head_rows(llm_handle* h, const float* x, int m, float* out) {
   if (h->tc_min > 0 && m >= h->tc_min) {
     PrepIn in;
-    in.x = h->xh; in.x_stride = h->d; in.gain = h->lnf;
+    in.x = x; in.x_stride = h->d; in.gain = h->lnf;
     TRY(launch_prep(h, in, h->d, m, false));
-    return launch_gemm(h, h->tmap_head, h->V, h->d, m, h->logits, false, true);
+    return launch_gemm(h, h->tmap_head, h->V, h->d, m, out, false, true);
   }
   const GemvPlan p = plan_gemv(h->V, h->d, 1, h->wt, m, h->num_sms, 2);
   GemvArgs a = {};
   a.step = h->st; a.B = m; a.eps = h->cfg.eps; a.W = h->head; a.rows = h->V; a.cols = h->d; a.rg = 1;
-  a.x = h->xh; a.x_stride = h->d; a.gain = h->lnf;
+  a.x = x; a.x_stride = h->d; a.gain = h->lnf;
   a.lpr = p.lpr; a.seg_ch = p.seg_ch; a.nseg = p.nseg; a.rows_cap = p.rows_cap; a.ws = p.ws;
-  a.out = h->logits; a.out_stride = h->V;
+  a.out = out; a.out_stride = h->V;
   a.status = h->status;
   CUDA_TRY(h, launch_gemv(a, p, h->wt, EPI_STORE, true, h->stream, false));
   return LLM_OK;
+}
+
+// the residual stream after the last layer of the pass of n entries just run, whole in xa
+static llm_status pass_residual(llm_handle* h, int n) {
+  if (h->tc_min == 0 || n < h->tc_min) return LLM_OK;
+  // its down projection's split sums + x1
+  PrepIn in;
+  in.src_rows = h->d; in.src_K = h->f; in.resid = h->xb; in.xout = h->xa;
+  return launch_prep(h, in, h->d, n, false);
 }
 
 // logits after entries ents[i] of the pass of n entries just run, into dst rows dst_row[i]
@@ -1228,19 +1301,14 @@ static llm_status head_rows(llm_handle* h, int m) {
 static llm_status pass_logits(llm_handle* h, int n, const std::vector<int32_t>& ents, const std::vector<int>& dst_row,
                               float* dst, bool host) {
   if (ents.empty()) return LLM_OK;
-  if (h->tc_min > 0 && n >= h->tc_min) {
-    // the residual stream after the last layer: its down projection's split sums + x1
-    PrepIn in;
-    in.src_rows = h->d; in.src_K = h->f; in.resid = h->xb; in.xout = h->xa;
-    TRY(launch_prep(h, in, h->d, n, false));
-  }
+  TRY(pass_residual(h, n));
   const int mb = h->cfg.max_batch;
   for (size_t c0 = 0; c0 < ents.size(); c0 += mb) {
     const int m = (int)std::min<size_t>(mb, ents.size() - c0);
     CUDA_TRY(h, cudaMemcpyAsync(h->head_map, ents.data() + c0, (size_t)m * 4, cudaMemcpyHostToDevice, h->stream));
     gather_rows_f32_kernel<<<m, 256, 0, h->stream>>>(h->xh, h->xa, h->head_map, h->d);
     CUDA_TRY(h, cudaGetLastError());
-    TRY(head_rows(h, m));
+    TRY(head_rows(h, h->xh, m, h->logits));
     for (int i = 0; i < m; ++i)
       CUDA_TRY(h, cudaMemcpyAsync(dst + (size_t)dst_row[c0 + i] * h->V, h->logits + (size_t)i * h->V, (size_t)h->V * 4,
                                   host ? cudaMemcpyDeviceToHost : cudaMemcpyDeviceToDevice, h->stream));
@@ -1254,10 +1322,10 @@ static llm_status pass_logits(llm_handle* h, int n, const std::vector<int32_t>& 
 static llm_status run_pass(llm_handle* h, int n, const int32_t* tok_host, const int32_t* tok_dev, int tok_stride,
                            int tok_col, int tok_np, const int32_t* pos_host, const int32_t* ranges_host) {
   CUDA_TRY(h, cudaMemcpyAsync(h->range_buf, ranges_host, (size_t)3 * n * 4, cudaMemcpyHostToDevice, h->stream));
-  if (h->pf_attn) {
+  if (h->pf_attn || h->q_tiles) {
     // tiles: runs of at most qt entries of one cache row with one attention start at consecutive
     // positions; units (tile, kv head), longest key range first
-    const int qt = attn_prefill_tile_tokens(h->cfg.group), kv = h->cfg.kv_heads, NT = h->NT;
+    const int qt = h->q_tiles ? qattn_tile_tokens(h->cfg.group) : attn_prefill_tile_tokens(h->cfg.group), kv = h->cfg.kv_heads, NT = h->NT;
     const int32_t* start = ranges_host;
     const int32_t* row = ranges_host + 2 * (size_t)n;
     std::vector<int32_t> tb(4 + 4 * (size_t)NT + 2 * (size_t)NT * kv, 0);
@@ -1518,6 +1586,18 @@ static llm_status packed_impl(llm_handle* h, const int32_t* toks, const int32_t*
         if (a.first < b.first && a.second.row == b.second.row && a.second.lo <= b.second.hi && b.second.lo <= a.second.hi)
           return fail(h, LLM_ERR_ARG, "prompts %d and %d overlap in row %d", a.first, b.first, a.second.row);
   }
+  if (h->q8) {
+    // a block's scale is set by what is written: filled positions behind a prompt's end in its last
+    // block, which this call does not write, would lose their contents
+    for (auto& a : span)
+      for (int p = a.second.hi + 1; p % kQBlock != 0 && p < h->filled[a.second.row]; ++p) {
+        bool written = false;
+        for (auto& b : span) written = written || (b.second.row == a.second.row && b.second.lo <= p && p <= b.second.hi);
+        if (!written)
+          return fail(h, LLM_ERR_POS_RANGE, "prompt %d ends inside a block of an 8-bit cache: position %d of row %d is filled",
+                      a.first, p, a.second.row);
+      }
+  }
   // position order, then passes of at most NT entries
   std::vector<int> order(P);
   for (int i = 0; i < P; ++i) order[i] = i;
@@ -1570,6 +1650,46 @@ llm_status llm_prefill_packed(llm_handle* h, const int32_t* tokens_host, const i
   if (!h || !tokens_host || !rows_host || !positions_host || !segments_host || (nlast > 0 && !last_host))
     return LLM_ERR_ARG;
   return packed_impl(h, tokens_host, rows_host, positions_host, segments_host, P, last_host, nlast, logits_host);
+}
+
+// S + 1 tokens per row as one prefill pass, the target's probabilities after each of them, and the
+// verification of the S drafts among them (verify.cu)
+llm_status llm_verify_step(llm_handle* h, const int32_t* tokens_host, int32_t B, int32_t S, const int32_t* positions_host,
+                           float temp, const float* q_dev, const float* u_dev, float* p_dev, int32_t* ids_dev,
+                           int32_t* accepted_dev) {
+  if (!h || !tokens_host || !positions_host || !u_dev || !p_dev || !ids_dev || !accepted_dev) return LLM_ERR_ARG;
+  if (B < 1 || B > h->cfg.max_batch) return fail(h, LLM_ERR_BATCH, "batch %d outside 1..%d", B, h->cfg.max_batch);
+  if (S < 1) return fail(h, LLM_ERR_ARG, "drafts per row %d < 1", S);
+  if ((int64_t)B * ((int64_t)S + 1) > h->NT)
+    return fail(h, LLM_ERR_BATCH, "%d rows of %d tokens exceed one pass of %d", B, S + 1, h->NT);
+  if (!(temp >= 0.0f) || temp == INFINITY) return fail(h, LLM_ERR_ARG, "temperature must be finite and >= 0");
+  if (h->cfg.debug_trace) return fail(h, LLM_ERR_ARG, "debug_trace handles run without graphs");
+  TRY(check_row_positions(h, B, positions_host));
+  for (int b = 0; b < B; ++b)
+    if ((int64_t)positions_host[b] + S >= h->cfg.max_seq)
+      return fail(h, LLM_ERR_POS_RANGE, "row %d: position %lld outside the cache of %d", b, (long long)positions_host[b] + S, h->cfg.max_seq);
+  const int T = S + 1, n = B * T;
+  TRY(check_tokens(h, tokens_host, (size_t)n));
+  std::vector<int32_t> epos(n), ranges(3 * (size_t)n), drafts((size_t)B * S);
+  for (int b = 0; b < B; ++b)
+    for (int i = 0; i < T; ++i) {
+      const int e = b * T + i;
+      epos[e] = positions_host[b] + i;
+      ranges[e] = 0;
+      ranges[n + e] = positions_host[b];
+      ranges[2 * (size_t)n + e] = b;
+      if (i > 0) drafts[(size_t)b * S + i - 1] = tokens_host[e];
+    }
+  TRY(run_pass(h, n, tokens_host, nullptr, 1, 0, 1, epos.data(), ranges.data()));
+  TRY(pass_residual(h, n));
+  TRY(head_rows(h, h->xa, n, p_dev));  // (every entry's logits are wanted: no gather, the head is read once)
+  CUDA_TRY(h, launch_probs(p_dev, n, h->V, temp, h->stream));
+  // (the pass has read its tokens: their buffer takes the drafts)
+  CUDA_TRY(h, cudaMemcpyAsync(h->tok_buf, drafts.data(), drafts.size() * 4, cudaMemcpyHostToDevice, h->stream));
+  const VerifyArgs va = {p_dev, q_dev, h->tok_buf, nullptr, u_dev, B, S, h->V, ids_dev, accepted_dev};
+  CUDA_TRY(h, launch_verify(va, h->stream));
+  for (int b = 0; b < B; ++b) h->filled[b] = positions_host[b] + T;
+  return LLM_OK;
 }
 
 // n decode steps, each feeding its draws to the next as tokens, as CUDA graphs of kGenChunk
@@ -1739,6 +1859,39 @@ static llm_status kv_copy(llm_handle* h, int32_t layer, int32_t row, int32_t pos
     return fail(h, LLM_ERR_POS_RANGE, "positions %d..+%d outside the cache of %d", pos0, n, h->cfg.max_seq);
   const size_t es = h->es, hd = h->hd, kv = h->cfg.kv_heads, cap = h->cfg.max_seq;
   const size_t bytes = (size_t)n * hd * es;
+  if (h->q8) {
+    if (import && (pos0 + n) % kQBlock != 0 && h->filled[row] > pos0 + n)
+      return fail(h, LLM_ERR_POS_RANGE, "import ends at %d, inside a filled block of an 8-bit cache (row %d holds %d)", pos0 + n,
+                  row, h->filled[row]);
+    // through the staging buffers, whole blocks at a time: the cache row as a cache of one row
+    QCacheView c = q8_view(h, layer);
+    c.k += (size_t)row * kv * h->qcap * hd; c.v += (size_t)row * kv * h->qcap * hd;
+    c.ks += (size_t)row * kv * (h->qcap / kQBlock); c.vs += (size_t)row * kv * (h->qcap / kQBlock);
+    c.rows = 1;
+    QRows r = {};
+    r.first = h->pos_buf; r.B = 1; r.limit = h->qcap; r.status = h->status;
+    const int64_t stride = (int64_t)kv * hd;
+    for (int32_t i = 0; i < n;) {
+      const int32_t p = pos0 + i, room = std::max(1, h->NT / kQBlock * kQBlock - p % kQBlock);
+      r.S = std::min(std::min(n - i, room), h->NT);
+      CUDA_TRY(h, cudaMemcpyAsync(h->pos_buf, &p, 4, cudaMemcpyHostToDevice, h->stream));
+      if (!import) CUDA_TRY(h, launch_qcache_read(c, r, h->stage_k, h->stage_v, h->wt, stride, h->stream));
+      for (size_t j = 0; j < kv; ++j)
+        for (int side = 0; side < 2; ++side) {
+          char* host = (char*)(side ? v : k) + j * bytes + (size_t)i * hd * es;
+          char* dev = (char*)(side ? h->stage_v : h->stage_k) + j * hd * es;
+          if (import)
+            CUDA_TRY(h, cudaMemcpy2DAsync(dev, stride * es, host, hd * es, hd * es, r.S, cudaMemcpyHostToDevice, h->stream));
+          else
+            CUDA_TRY(h, cudaMemcpy2DAsync(host, hd * es, dev, stride * es, hd * es, r.S, cudaMemcpyDeviceToHost, h->stream));
+        }
+      if (import) CUDA_TRY(h, launch_qcache_write(c, r, h->stage_k, h->stage_v, h->wt, stride, h->stream));
+      CUDA_TRY(h, cudaStreamSynchronize(h->stream));
+      i += r.S;
+    }
+    if (import && h->filled[row] < pos0 + n) h->filled[row] = pos0 + n;
+    return LLM_OK;
+  }
   for (size_t j = 0; j < kv; ++j) {
     const size_t elem = (size_t)layer * h->layer_cache_elems + (((size_t)row * kv + j) * cap + pos0) * hd;
     char* dk = (char*)h->kc + elem * es;

@@ -309,6 +309,13 @@ uint64_t qattn_workspace(const QCacheView& c, int g, int B, int S, int num_sms) 
   return splits == 1 ? 0 : kQattnTickets + (uint64_t)tokens * c.kv * g * splits * (c.hd + 2) * 4;
 }
 
+uint64_t qattn_step_workspace(const QCacheView& c, int g, int NT, int num_sms) {
+  uint64_t most = 0;
+  for (int b = 1; b <= NT; ++b) most = std::max(most, qattn_workspace(c, g, b, 1, num_sms));
+  if (qattn_uses_tc(c.hd)) most = std::max(most, qattn_workspace(c, g, NT, qattn_tile_tokens(g), num_sms));
+  return most;
+}
+
 cudaError_t launch_qattn(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s, bool pdl, const CUtensorMap* kmap,
                          const CUtensorMap* vmap) {
   if (qattn_uses_tc(a.c.hd)) {

@@ -134,6 +134,8 @@ struct QAttnArgs {
 };
 constexpr int kQattnTickets = 4096;  // bytes of tickets (one 32-bit word per CTA) before the partials
 uint64_t qattn_workspace(const QCacheView& c, int g, int B, int S, int num_sms);
+// the same for the steps and passes of at most NT rows of a handle (f32 queries)
+uint64_t qattn_step_workspace(const QCacheView& c, int g, int NT, int num_sms);
 // kmap, vmap: tensor maps of qattn_make_map over the whole caches; null: made for this call
 cudaError_t launch_qattn(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s, bool pdl,
                          const CUtensorMap* kmap = nullptr, const CUtensorMap* vmap = nullptr);

@@ -172,12 +172,80 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
   }
 }
 
-}  // namespace
+// Logits to probabilities, a cluster of 8 CTAs per row: each CTA's slice is read once (the exponentials
+// are taken in place and scaled when the row's sum is known), the maxima and sums meet through
+// distributed shared memory in CTA order.  Two passes over a slice of V / 8 floats, which stays in L2.
+__global__ void __launch_bounds__(kVerThreads) probs_kernel(float* x, int V, float temp) {
+  __shared__ float s_v[kVerWarps];
+  __shared__ int s_i[kVerWarps];
+  __shared__ uint64_t s_cta, s_all[kVerCluster];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = ver_rank();
+  float* row = x + (size_t)(blockIdx.x / kVerCluster) * V;
+  const int per = (V + kVerCluster - 1) / kVerCluster;
+  const int i0 = min(V, (int)rank * per), i1 = min(V, i0 + per);
+  // every CTA's value through the cluster: bits of a float, and an index
+  auto share = [&](float v, int i) {
+    if (tid == 0) s_cta = (uint64_t)__float_as_uint(v) << 32 | (uint32_t)i;
+    ver_cluster_sync();
+    if (tid < kVerCluster) s_all[tid] = ver_remote(&s_cta, (uint32_t)tid);
+    ver_cluster_sync();  // (also: nobody leaves or writes its value again before all have read it)
+  };
+  float top = -INFINITY;
+  int at = 0x7fffffff;
+  for (int i = i0 + tid; i < i1; i += kVerThreads) {
+    const float v = row[i];
+    if (v > top) {
+      top = v;
+      at = i;
+    }
+  }
+  auto better = [&](float v, int i) {
+    if (v > top || (v == top && i < at)) {
+      top = v;
+      at = i;
+    }
+  };
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float v = __shfl_xor_sync(0xffffffffu, top, o);
+    better(v, __shfl_xor_sync(0xffffffffu, at, o));
+  }
+  if (lane == 0) {
+    s_v[warp] = top;
+    s_i[warp] = at;
+  }
+  __syncthreads();
+  for (int w = 0; w < kVerWarps; ++w) better(s_v[w], s_i[w]);
+  share(top, at);
+  for (int c = 0; c < kVerCluster; ++c) better(__uint_as_float((uint32_t)(s_all[c] >> 32)), (int)(uint32_t)s_all[c]);
+  if (temp == 0.0f) {
+    if (at == 0x7fffffff) at = 0;  // (no logit above -inf)
+    for (int i = i0 + tid; i < i1; i += kVerThreads) row[i] = i == at ? 1.0f : 0.0f;
+    return;
+  }
+  float sum = 0.0f;
+  for (int i = i0 + tid; i < i1; i += kVerThreads) {
+    const float e = expf((row[i] - top) / temp);
+    row[i] = e;
+    sum += e;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) s_v[warp] = sum;
+  __syncthreads();
+  sum = 0.0f;
+  for (int w = 0; w < kVerWarps; ++w) sum += s_v[w];
+  share(sum, 0);
+  sum = 0.0f;
+  for (int c = 0; c < kVerCluster; ++c) sum += __uint_as_float((uint32_t)(s_all[c] >> 32));
+  for (int i = i0 + tid; i < i1; i += kVerThreads) row[i] /= sum;
+}
 
-cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
-  const bool vec = a.V % 4 == 0 && (reinterpret_cast<uintptr_t>(a.p) & 15) == 0 && (reinterpret_cast<uintptr_t>(a.q) & 15) == 0;
+template <class... P, class... A>
+cudaError_t launch_cluster(void (*fn)(P...), int rows, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.B * kVerCluster);
+  cfg.gridDim = dim3((unsigned)rows * kVerCluster);
   cfg.blockDim = dim3(kVerThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -187,7 +255,18 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, vec ? verify_kernel<true> : verify_kernel<false>, a);
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+}  // namespace
+
+cudaError_t launch_probs(float* x, int rows, int V, float temp, cudaStream_t s) {
+  return launch_cluster(probs_kernel, rows, s, x, V, temp);
+}
+
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
+  const bool vec = a.V % 4 == 0 && (reinterpret_cast<uintptr_t>(a.p) & 15) == 0 && (reinterpret_cast<uintptr_t>(a.q) & 15) == 0;
+  return launch_cluster(vec ? verify_kernel<true> : verify_kernel<false>, a.B, s, a);
 }
 
 }  // namespace llm

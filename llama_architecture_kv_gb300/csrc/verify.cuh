@@ -14,6 +14,8 @@ struct VerifyArgs {
   int32_t* ids;           // [B][S + 1]: the kept drafts, the drawn token, then -1
   int32_t* accepted;      // [B]
 };
+// rows of V logits to softmax(logits / temp), in place; temp == 0: a 1 at the first largest logit
+cudaError_t launch_probs(float* x, int rows, int V, float temp, cudaStream_t s);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
 
 }  // namespace llm

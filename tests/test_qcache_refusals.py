@@ -82,6 +82,19 @@ def test_verification_refuses_bad_arguments(lib):
         assert verify(**kw) == code, kw
 
 
+def test_create_refuses_an_unknown_cache_type(lib):
+    from synth.configs import TINY
+    c = pkg.config(TINY, 1, 16, cache_type=2)
+    h = ctypes.c_void_p()
+    buf = np.zeros(4, np.uint8)
+    n = pkg.llm_weight_count(c) * 4
+    assert lib.llm_create(ctypes.byref(c), buf.ctypes.data, n, 0, None, ctypes.byref(h)) == CONFIG
+    # the types that exist pass this check (and fail on the blob's size, before any GPU work)
+    for t in (pkg.LLM_CACHE_MODEL, pkg.LLM_CACHE_E4M3):
+        c = pkg.config(TINY, 1, 16, cache_type=t)
+        assert lib.llm_create(ctypes.byref(c), buf.ctypes.data, n + 4, 0, None, ctypes.byref(h)) == pkg.LLM_ERR_WEIGHTS_SIZE
+
+
 def test_python_wrappers_refuse_tensors_of_the_cpu():
     torch = pytest.importorskip("torch")
     with pytest.raises(pkg.LlmError):
