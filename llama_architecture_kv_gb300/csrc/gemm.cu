@@ -491,9 +491,10 @@ TcPlan plan_tc(int rows, int K, int B, int num_sms, bool whole) {
   };
   if (whole) {
     // no K split (the reader takes the output as it is): 256- or 128-row tiles, whichever fills
-    // the SMs more evenly
+    // the SMs more evenly with one activation tile (the head's tensor map has one tile height for
+    // every batch)
     const int m256 = (rows + 255) / 256, m128 = (rows + 127) / 128;
-    p.n_tile = eff((long long)m128 * p.ntiles) > eff((long long)m256 * p.ntiles) + 1e-9 ? 128 : 256;
+    p.n_tile = eff(m128) > eff(m256) + 1e-9 ? 128 : 256;
     p.S = 1;
   } else {
     // splits: the most even fill of the SMs (units / (waves * SMs)), at least 4 K blocks a split.

@@ -222,6 +222,24 @@ def test_verification_steps_follow_the_model(name, shape, B, tc, cache):
     g.close()
 
 
+def test_more_rows_than_one_activation_tile_through_the_head():
+    # 70 rows are two tiles of the tensor-core head; on this vocabulary (as on the 8B shape's) the tile
+    # height that fills the SMs best differs between one tile and two, and the head's map has one height
+    shape = shrink(LLAMA8, layers=1, kv=1, g=2, ffn=256, vocab=128256)
+    B, S, n = 14, 4, 9
+    g = make(shape, 781, 80, 64, wstd=0.06)
+    toks = synth.tokens(782, 0, 80 * n, shape.vocab).reshape(80, n)
+    g.prefill(toks[:, :n - 1], 0, logits=False)
+    chain = g.generate(toks[:, n - 1], n - 1, S + 1).T.copy()           # 80 rows in one step
+    g.prefill(toks[:B, :n - 1], 0, logits=False)
+    assert np.array_equal(g.generate(toks[:B, n - 1], n - 1, S + 1).T, chain[:B])
+    g.prefill(toks[:B, :n - 1], 0, logits=False)
+    ids, acc, p = g.verify_step(np.concatenate([toks[:B, n - 1:], chain[:B, :S]], 1), np.full(B, n - 1),
+                                np.full((B, S + 1), 0.5, np.float32))
+    assert (acc == S).all() and np.array_equal(ids, chain[:B])
+    g.close()
+
+
 def test_verification_step_refusals():
     shape = SHAPES[0][1]
     g = make(shape, 771, 2, 64, max_tokens=8)
