@@ -32,40 +32,47 @@ namespace {
 
 constexpr int kQThreads = 128;
 
-// four consecutive elements of a row of type ST (0 f32, 1 bf16) as f32
+// 16 bytes of a row of type ST (0 f32, 1 bf16): E elements
+template <int ST> constexpr int kE = ST ? 8 : 4;
 template <int ST>
-LLM_D float4 load_quad(const void* p, int64_t i) {
-  if constexpr (ST == 0) {
-    return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-  } else {
-    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-    return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+LLM_D uint4 load16(const void* p, int64_t i) {
+  return ST ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i)
+            : *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+}
+// the largest |element| of 16 bytes, as the bits of an f32 (ordered; not finite: >= 0x7f800000)
+template <int ST>
+LLM_D uint32_t top16(const uint4& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t t = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t = max(t, w[i] & (ST ? 0x7fff0000u : 0x7fffffffu));
+    if constexpr (ST) t = max(t, w[i] << 16 & 0x7fff0000u);
   }
+  return t;
 }
 
 // One warp: n tokens (1 <= t0 + n <= kQBlock) at positions t0 .. t0 + n - 1 of a block, whose codes
-// start at `codes` and whose scale is *scale; token i's values are the HD elements at src + i * stride
+// start at `codes` and whose scale is *scale; token i's values are the HD elements at src + i * stride.
+// The values stay packed as they were read (bf16: half the registers, twice the warps in flight).
 template <int HD, int ST>
 LLM_D void quantise_run(uint8_t* codes, float* scale, int t0, int n, const void* src, int64_t base, int64_t stride) {
-  constexpr int QR = HD / 4;                  // groups of four values per token
-  constexpr int NQ = kQBlock * QR / 32;       // groups per lane
+  constexpr int E = kE<ST>;
+  constexpr int QR = HD / E;                  // 16-byte pieces per token
+  constexpr int NQ = (kQBlock * QR + 31) / 32;  // pieces per lane
   const int lane = threadIdx.x & 31;
   const int nq = n * QR;
   const float s_old = t0 > 0 ? *scale : 0.0f;
-  float4 x[NQ];
-  uint32_t top = 0u;                          // largest |x| as bits (ordered; not finite: >= 0x7f800000)
+  uint4 x[NQ];
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
     const int q = lane + 32 * i;
-    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (q < nq) x[i] = load_quad<ST>(src, base + (int64_t)(q / QR) * stride + (q % QR) * 4);
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (q < nq) x[i] = load16<ST>(src, base + (int64_t)(q / QR) * stride + (q % QR) * E);
   }
+  uint32_t top = 0u;
 #pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    const uint32_t a = max(__float_as_uint(x[i].x) & 0x7fffffffu, __float_as_uint(x[i].y) & 0x7fffffffu);
-    const uint32_t b = max(__float_as_uint(x[i].z) & 0x7fffffffu, __float_as_uint(x[i].w) & 0x7fffffffu);
-    top = max(top, max(a, b));
-  }
+  for (int i = 0; i < NQ; ++i) top = max(top, top16<ST>(x[i]));
   top = __reduce_max_sync(0xffffffffu, top);
   const bool fine = top < 0x7f800000u && s_old == s_old;
   float s = fine ? q_scale(__uint_as_float(top)) : __uint_as_float(0x7fc00000u);
@@ -74,7 +81,7 @@ LLM_D void quantise_run(uint8_t* codes, float* scale, int t0, int n, const void*
     // the tokens before, from s_old to s: their values times s_old / s < 1 (both powers of two)
     const float f = s_old * q_recip(s);
     uint32_t* c4 = reinterpret_cast<uint32_t*>(codes);
-    for (int q = lane; q < t0 * QR; q += 32) {
+    for (int q = lane; q < t0 * (HD / 4); q += 32) {
       const float4 v = e4m3_quad(c4[q]);
       c4[q] = e4m3x2(v.x * f, v.y * f) | e4m3x2(v.z * f, v.w * f) << 16;
     }
@@ -84,8 +91,19 @@ LLM_D void quantise_run(uint8_t* codes, float* scale, int t0, int n, const void*
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
     const int q = lane + 32 * i;
-    if (q < nq)
-      dst[q] = fine ? e4m3x2(x[i].x * r, x[i].y * r) | e4m3x2(x[i].z * r, x[i].w * r) << 16 : 0u;
+    if (q < nq) {
+      if constexpr (ST) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t c[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) c[y] = fine ? e4m3x2(bf16_lo(w[y]) * r, bf16_hi(w[y]) * r) : 0u;
+        reinterpret_cast<uint2*>(dst)[q] = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+      } else {
+        const float4 f = make_float4(__uint_as_float(x[i].x), __uint_as_float(x[i].y), __uint_as_float(x[i].z),
+                                     __uint_as_float(x[i].w));
+        dst[q] = fine ? e4m3x2(f.x * r, f.y * r) | e4m3x2(f.z * r, f.w * r) << 16 : 0u;
+      }
+    }
   }
   __syncwarp();  // every lane has read the old scale
   if (lane == 0) *scale = s;
@@ -172,46 +190,61 @@ __global__ void __launch_bounds__(kQThreads)
   }
 }
 
-// thread: 16 consecutive dimensions of one (row, token, kv head), keys and values
+// warp (row, touched block, kv head, keys or values): E codes a lane and store of 16 bytes, so that
+// every store of the warp is one contiguous run
 template <int HD, int ST>
-__global__ void __launch_bounds__(256) qcache_read_kernel(const QCacheView c, const QRows r, void* k, void* v, int64_t stride) {
-  constexpr int PR = HD / 16;
-  const int64_t total = (int64_t)r.B * r.S * c.kv * PR;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-    const int e = (int)(i % PR);
-    const int h = (int)(i / PR % c.kv);
-    const int64_t bt = i / PR / c.kv;
-    const int b = (int)(bt / r.S), t = (int)(bt - (int64_t)b * r.S);
-    const int p0 = r.first[b], n = q_count(r, b);
-    if (t >= n) continue;
-    if (p0 < 0 || p0 > r.limit - n) {
-      q_report(r.status, kErrPosRange);
-      continue;
+__global__ void __launch_bounds__(kQThreads)
+    qcache_read_kernel(const QCacheView c, const QRows r, void* k, void* v, int64_t stride, int span) {
+  constexpr int E = kE<ST>, QR = HD / E, NQ = (kQBlock * QR + 31) / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
+  const int side = (int)(w & 1);
+  const int h = (int)((w >> 1) % c.kv);
+  const int64_t bj = (w >> 1) / c.kv;
+  const int b = (int)(bj / span), j = (int)(bj - (int64_t)b * span);
+  if (b >= r.B) return;
+  const int p0 = r.first[b], n = q_count(r, b);
+  if (n == 0) return;
+  if (p0 < 0 || p0 > r.limit - n) {
+    q_report(r.status, kErrPosRange);
+    return;
+  }
+  const int blk = p0 / kQBlock + j;
+  const int lo = max(p0, blk * kQBlock), hi = min(p0 + n, (blk + 1) * kQBlock);
+  if (lo >= hi) return;
+  int row, pp;
+  if (!q_place(r, c, b, blk * kQBlock, row, pp)) return;
+  const size_t head = (size_t)row * c.kv + h;
+  const uint8_t* codes = (side ? c.v : c.k) + (head * c.cap + pp + lo - blk * kQBlock) * HD;
+  const float s = (side ? c.vs : c.ks)[head * (c.cap / kQBlock) + pp / kQBlock];
+  const int64_t base = ((int64_t)b * r.S + (lo - p0)) * stride + (int64_t)h * HD;
+  const int nq = (hi - lo) * QR;
+  uint2 x[NQ];
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    const int q = lane + 32 * i;
+    x[i] = make_uint2(0u, 0u);
+    if (q < nq) {
+      if constexpr (ST) x[i] = reinterpret_cast<const uint2*>(codes)[q];
+      else x[i].x = reinterpret_cast<const uint32_t*>(codes)[q];
     }
-    int row, pp;
-    if (!q_place(r, c, b, p0 + t, row, pp)) continue;
-    const size_t head = (size_t)row * c.kv + h;
-    const size_t at = (head * c.cap + pp) * HD + e * 16, sc = head * (c.cap / kQBlock) + pp / kQBlock;
-    const uint4 u[2] = {*reinterpret_cast<const uint4*>(c.k + at), *reinterpret_cast<const uint4*>(c.v + at)};
-    const float s[2] = {c.ks[sc], c.vs[sc]};
-    const int64_t o = bt * stride + (int64_t)h * HD + e * 16;
+  }
+  void* dst = side ? v : k;
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const uint32_t w[4] = {u[side].x, u[side].y, u[side].z, u[side].w};
-      void* dst = side ? v : k;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float4 f = e4m3_quad(w[q]);
-        f.x *= s[side]; f.y *= s[side]; f.z *= s[side]; f.w *= s[side];
-        if constexpr (ST == 0) {
-          *reinterpret_cast<float4*>(static_cast<float*>(dst) + o + 4 * q) = f;
-        } else {
-          // (codes hold four significant bits: rounding to bf16 changes only values below 2^-126)
-          const uint2 p = make_uint2((uint32_t)f32_to_bf16(f.x) | (uint32_t)f32_to_bf16(f.y) << 16,
-                                     (uint32_t)f32_to_bf16(f.z) | (uint32_t)f32_to_bf16(f.w) << 16);
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dst) + o + 4 * q) = p;
-        }
-      }
+  for (int i = 0; i < NQ; ++i) {
+    const int q = lane + 32 * i;
+    if (q >= nq) break;
+    const int64_t o = base + (int64_t)(q / QR) * stride + (q % QR) * E;
+    float4 f = e4m3_quad(x[i].x);
+    f.x *= s; f.y *= s; f.z *= s; f.w *= s;
+    if constexpr (ST == 0) {
+      *reinterpret_cast<float4*>(static_cast<float*>(dst) + o) = f;
+    } else {
+      float4 g = e4m3_quad(x[i].y);
+      g.x *= s; g.y *= s; g.z *= s; g.w *= s;
+      // (codes hold four significant bits: rounding to bf16 changes only values below 2^-126)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + o) =
+          make_uint4(bf16x2(f.x, f.y), bf16x2(f.z, f.w), bf16x2(g.x, g.y), bf16x2(g.z, g.w));
     }
   }
 }
@@ -267,9 +300,11 @@ cudaError_t launch_qcache_write_step(const QCacheView& c, const QRows& r, const 
 
 cudaError_t launch_qcache_read(const QCacheView& c, const QRows& r, void* k, void* v, int st, int64_t stride,
                                cudaStream_t s) {
-  const int64_t threads = (int64_t)r.B * r.S * c.kv * (c.hd / 16), grid = std::min<int64_t>((threads + 255) / 256, 1 << 20);
+  const int span = (r.S + kQBlock - 2) / kQBlock + 1;
+  const int64_t warps = (int64_t)r.B * span * c.kv * 2, grid = (warps + kQThreads / 32 - 1) / (kQThreads / 32);
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   return with_shape(c.hd, st, [&](auto hd, auto t) {
-    qcache_read_kernel<hd.value, t.value><<<(unsigned)grid, 256, 0, s>>>(c, r, k, v, stride);
+    qcache_read_kernel<hd.value, t.value><<<(unsigned)grid, kQThreads, 0, s>>>(c, r, k, v, stride, span);
     return cudaGetLastError();
   });
 }

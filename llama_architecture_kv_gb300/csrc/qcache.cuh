@@ -96,6 +96,13 @@ LLM_D float4 e4m3_quad(uint32_t x) {
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
+// two f32 rounded to bf16 (x0 in the low half)
+LLM_D uint32_t bf16x2(float x0, float x1) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x1), "f"(x0));
+  return r;
+}
+
 // the least power of two s >= 2^-126 with amax / s <= 448 = 1.75 * 2^8 (amax finite, >= 0)
 LLM_D float q_scale(float amax) {
   const uint32_t u = __float_as_uint(amax);

@@ -12,9 +12,11 @@
 // whatever its order: the drawn token is that of a sequential walk over the row, on any split.
 //
 // Bound: the two rows of V floats that the last token is drawn from (everything else is a few
-// scalars).  A cluster of 8 CTAs shares a row, since one SM's loads would need about 10 us for 1 MB:
-// each warp sums one contiguous stretch with coalesced loads, the stretches' sums meet through
-// distributed shared memory, and only the warp whose stretch holds the draw reads it again (from L2).
+// scalars), and for a few rows the chain of dependent loads: drafts, their probabilities, the rows.  A
+// cluster of 8 CTAs shares a row, since one SM's loads would need about 10 us for 1 MB: each warp sums
+// one contiguous stretch with coalesced loads and keeps its weights in registers, the stretches' sums
+// meet through distributed shared memory behind one cluster barrier, and the warp whose stretch holds
+// the draw walks its registers (reading the stretch again in steps of 32 ids cost 11 us).
 #include <algorithm>
 
 #include "verify.cuh"
@@ -45,8 +47,11 @@ LLM_D uint64_t ver_remote(const uint64_t* p, uint32_t rank) {
 
 // a weight in units of 2^-61 (NaN and negative values weigh nothing)
 LLM_D uint64_t ver_units(float w) {
-  w = w > 0.0f ? fminf(w, 1.0f) : 0.0f;
-  return (uint64_t)__float2ull_rz(w * 2305843009213693952.0f);
+  // w 2^61 = its 24-bit significand shifted: w = s 2^(e - 150)
+  const uint32_t u = __float_as_uint(w > 0.0f ? fminf(w, 1.0f) : 0.0f);
+  const int up = (int)(u >> 23) - (150 - 61);
+  const uint64_t s = (u & 0x7fffffu) | 0x800000u;
+  return up >= 0 ? s << up : up > -24 ? s >> -up : 0ull;  // (f32 subnormals are far below 2^-61)
 }
 
 struct VerRow {
@@ -60,28 +65,50 @@ LLM_D uint64_t ver_weight(const VerRow& r, int v) {
   return v == r.skip ? 0ull : ver_units(w);
 }
 
-// cluster = row; VEC: rows start on 16-byte boundaries
-template <bool VEC>
-__global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a) {
+// a store to the same variable of another CTA of the cluster
+LLM_D void ver_put(uint64_t* p, uint32_t rank, uint64_t v) {
+  uint32_t local = (uint32_t)__cvta_generic_to_shared(p), remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote), "l"(v) : "memory");
+}
+// a running sum over the lanes
+LLM_D uint64_t ver_scan(uint64_t x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+constexpr int kVerKeep = 1024;  // longest stretch kept in registers: vocabularies up to 131072
+
+// cluster = row; W: ids per lane and load (4 where rows start on 16-byte boundaries, else 1)
+template <int W>
+__global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs a) {
+  constexpr int NL = kVerKeep / (32 * W);  // loads of a kept stretch: id i0 + 32 W i + W lane + c
   __shared__ int s_r;
   __shared__ uint64_t s_warp[kVerWarps];   // sums of this CTA's stretches
-  __shared__ uint64_t s_cta;               // their sum
-  __shared__ uint64_t s_all[kVerCluster];
+  __shared__ uint64_t s_all[2][kVerCluster];  // the CTAs' sums, by attempt
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = ver_rank();
   const int b = blockIdx.x / kVerCluster;
   const int S = a.S, V = a.V;
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (waited for before the first store to another CTA)
+  if (tid == 0) s_r = S;
+  __syncthreads();
   int n = a.count ? a.count[b] : S;
   n = n < 0 ? 0 : n > S ? S : n;
-  if (tid == 0) s_r = n;
-  __syncthreads();
-  for (int i = tid; i < n; i += kVerThreads) {
+  if (tid == 0) atomicMin(&s_r, n);
+  for (int i = tid; i < S; i += kVerThreads) {
     const int x = a.drafts[(size_t)b * S + i];
+    const float u = a.u[(size_t)b * (S + 1) + i];
     bool kept = false;
     if (x >= 0 && x < V) {
       const float p = a.p[((size_t)b * (S + 1) + i) * V + x];
       const float q = a.q ? a.q[((size_t)b * S + i) * V + x] : 1.0f;
-      kept = (double)a.u[(size_t)b * (S + 1) + i] * (double)q < (double)p;
+      kept = (double)u * (double)q < (double)p;
     }
     if (!kept) atomicMin(&s_r, i);
   }
@@ -94,48 +121,77 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
   }
   // stretches of whole groups of 4 ids, warp by warp over the cluster
   const int per = ((V + kVerCluster * kVerWarps - 1) / (kVerCluster * kVerWarps) + 3) & ~3;
+  const bool keep = per <= kVerKeep;
   const int64_t i0_ = (int64_t)((int)rank * kVerWarps + warp) * per;
   const int i0 = (int)min((int64_t)V, i0_), i1 = (int)min((int64_t)V, i0_ + per);
   int32_t* ids = a.ids + (size_t)b * (S + 1);
   // no weight at all (not a row of probabilities): id 0; the draw's owner writes over it after the
-  // cluster barriers
+  // cluster barrier
   if (rank == 0 && tid == 0) ids[r] = 0;
-  uint64_t total = 0;
+  float w[NL][W];
+  uint64_t total = 0, before = 0;
   for (int attempt = 0; attempt < 2; ++attempt) {
     uint64_t sum = 0;
-    if (VEC) {
-      const int v4 = i1 & ~3;  // (i0 is a multiple of 4; only the last stretch can end off one)
-#pragma unroll 4
-      for (int v = i0 + 4 * lane; v < v4; v += 128) {
-        const float4 p = *reinterpret_cast<const float4*>(row.p + v);
-        float w[4] = {p.x, p.y, p.z, p.w};
-        if (row.q) {
-          const float4 q = *reinterpret_cast<const float4*>(row.q + v);
-          w[0] = __fsub_rn(w[0], q.x); w[1] = __fsub_rn(w[1], q.y);
-          w[2] = __fsub_rn(w[2], q.z); w[3] = __fsub_rn(w[3], q.w);
-        }
+    if (keep) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum += v + i == row.skip ? 0ull : ver_units(w[i]);
+      for (int i = 0; i < NL; ++i) {
+        const int v = i0 + 32 * W * i + W * lane;
+#pragma unroll
+        for (int c = 0; c < W; ++c) w[i][c] = 0.f;
+        if (v < i1) {
+          if constexpr (W == 4) {  // (V, and so every stretch, is a multiple of 4)
+            const float4 x = *reinterpret_cast<const float4*>(row.p + v);
+            w[i][0] = x.x; w[i][1] = x.y; w[i][2] = x.z; w[i][3] = x.w;
+          } else {
+            w[i][0] = row.p[v];
+          }
+        }
       }
-      for (int v = max(i0, v4) + lane; v < i1; v += 32) sum += ver_weight(row, v);
+      if (row.q) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+          const int v = i0 + 32 * W * i + W * lane;
+          if (v < i1) {
+            if constexpr (W == 4) {
+              const float4 x = *reinterpret_cast<const float4*>(row.q + v);
+              w[i][0] = __fsub_rn(w[i][0], x.x); w[i][1] = __fsub_rn(w[i][1], x.y);
+              w[i][2] = __fsub_rn(w[i][2], x.z); w[i][3] = __fsub_rn(w[i][3], x.w);
+            } else {
+              w[i][0] = __fsub_rn(w[i][0], row.q[v]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        if (i0 + 32 * W * i >= i1) break;
+#pragma unroll
+        for (int c = 0; c < W; ++c) {
+          if (i0 + 32 * W * i + W * lane + c == row.skip) w[i][c] = 0.f;
+          sum += ver_units(w[i][c]);
+        }
+      }
     } else {
-#pragma unroll 4
+#pragma unroll 8
       for (int v = i0 + lane; v < i1; v += 32) sum += ver_weight(row, v);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) s_warp[warp] = sum;
     __syncthreads();
-    if (tid == 0) {
-      uint64_t t = 0;
-      for (int w = 0; w < kVerWarps; ++w) t += s_warp[w];
-      s_cta = t;
+    if (attempt == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA has started
+    if (warp == 0) {
+      uint64_t t = lane < kVerWarps ? s_warp[lane] : 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if (lane < kVerCluster) ver_put(&s_all[attempt][rank], (uint32_t)lane, t);
     }
-    ver_cluster_sync();
-    if (tid < kVerCluster) s_all[tid] = ver_remote(&s_cta, (uint32_t)tid);
-    ver_cluster_sync();  // (also: nobody leaves or overwrites its sum before all have read it)
-    total = 0;
-    for (int c = 0; c < kVerCluster; ++c) total += s_all[c];
+    ver_cluster_sync();  // every sum is here; nothing is stored to another CTA after the last of these
+    total = before = 0;
+    for (int c = 0; c < kVerCluster; ++c) {
+      if (c == (int)rank) before = total;
+      total += s_all[attempt][c];
+    }
     if (total > 0 || (!row.q && row.skip < 0)) break;
     // nothing left over (p <= q everywhere): the target's own probabilities
     row.q = nullptr;
@@ -145,30 +201,45 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const VerifyArgs a)
   const float u = a.u[(size_t)b * (S + 1) + S];
   const uint64_t d = u > 0.0f ? (uint64_t)(min(u, 0.99999994f) * 16777216.0f) : 0ull;
   const uint64_t goal = d * (total >> 24) + ((d * (total & 0xffffffull)) >> 24);
-  uint64_t before = 0;
-  for (uint32_t c = 0; c < rank; ++c) before += s_all[c];
   if (rank == 0) {
     for (int i = tid; i <= S; i += kVerThreads)
       if (i != r) ids[i] = i < r ? a.drafts[(size_t)b * S + i] : -1;
     if (tid == 0) a.accepted[b] = r;
   }
-  for (int w = 0; w < warp; ++w) before += s_warp[w];
+  for (int x = 0; x < warp; ++x) before += s_warp[x];
   if (goal < before || goal - before >= s_warp[warp]) return;
-  // this warp's stretch holds the draw: 32 ids at a time, a running sum over the lanes
-  for (int v0 = i0; v0 < i1; v0 += 32) {
-    const int v = v0 + lane;
-    uint64_t incl = v < i1 ? ver_weight(row, v) : 0ull;
+  // this warp's stretch holds the draw: a running sum over its ids, a load's worth at a time
+  auto walk = [&](uint64_t mine, auto weight, int v0) {  // v0: this lane's first id, mine: its weights' sum
+    const uint64_t upto = ver_scan(mine);
+    const uint32_t above = __ballot_sync(0xffffffffu, before + upto > goal);
+    if (!above) {
+      before += __shfl_sync(0xffffffffu, upto, 31);
+      return false;
+    }
+    if (lane == __ffs(above) - 1) {
+      uint64_t run = before + upto - mine;
+      int c = 0;
+      while ((run += weight(c)) <= goal) ++c;
+      ids[r] = v0 + c;
+    }
+    return true;
+  };
+  if (keep) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
+    for (int i = 0; i < NL; ++i) {
+      if (i0 + 32 * W * i >= i1) break;
+      uint64_t mine = 0;
+#pragma unroll
+      for (int c = 0; c < W; ++c) mine += ver_units(w[i][c]);
+      const float(&x)[W] = w[i];
+      auto weight = [&](int c) { return ver_units(W == 4 ? (c == 0 ? x[0] : c == 1 ? x[W / 4] : c == 2 ? x[W / 2] : x[W - 1]) : x[0]); };
+      if (walk(mine, weight, i0 + 32 * W * i + W * lane)) return;
     }
-    const uint32_t above = __ballot_sync(0xffffffffu, before + incl > goal);
-    if (above) {
-      if (lane == 0) ids[r] = v0 + __ffs(above) - 1;
-      return;
+  } else {
+    for (int v = i0; v < i1; v += 32) {
+      const uint64_t mine = v + lane < i1 ? ver_weight(row, v + lane) : 0ull;
+      if (walk(mine, [&](int) { return mine; }, v + lane)) return;
     }
-    before += __shfl_sync(0xffffffffu, incl, 31);
   }
 }
 
@@ -266,7 +337,7 @@ cudaError_t launch_probs(float* x, int rows, int V, float temp, cudaStream_t s) 
 
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
   const bool vec = a.V % 4 == 0 && (reinterpret_cast<uintptr_t>(a.p) & 15) == 0 && (reinterpret_cast<uintptr_t>(a.q) & 15) == 0;
-  return launch_cluster(vec ? verify_kernel<true> : verify_kernel<false>, a.B, s, a);
+  return launch_cluster(vec ? verify_kernel<4> : verify_kernel<1>, a.B, s, a);
 }
 
 }  // namespace llm
