@@ -158,6 +158,15 @@ struct QaCut {
   }
 };
 
+// four elements of the output
+template <int QT>
+LLM_D void qa_put4(void* out, int64_t at, float4 o) {
+  if constexpr (QT)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = o;
+}
+
 // the walk of one CTA's run over (token tile, kv head, position tiles)
 struct QaWalk {
   QaUnit u;
@@ -208,10 +217,11 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   float* ssc = ffac + 2 * C;                                 // [ST][16] a tile's block scales: keys (-1: not seen), values
   float* wvs = ssc + 16 * ST;                                // [4][4] warps' largest value scales
   float* gvs = wvs + 16;                                     // [4] the groups' value scales
-  const uint32_t bars = (smem_u32(gvs + 4) + 7u) & ~7u;
+  int64_t* coff = reinterpret_cast<int64_t*>(gvs + 4);       // [C] a column's place in the unit's output
+  const uint32_t bars = (smem_u32(coff + C) + 7u) & ~7u;
   const uint32_t b_full = bars, b_empty = b_full + 8 * ST, b_s = b_empty + 8 * ST, b_p = b_s + 16, b_pv = b_p + 16,
                  b_q = b_pv + 16;
-  static_assert((size_t)C * 4 * 16 + 80 + 80 * ST + 96 <= X::MISC, "shared memory");
+  static_assert((size_t)C * 4 * 16 + 80 + 80 * ST + 8 * C + 96 <= X::MISC, "shared memory");
   __shared__ uint32_t s_tmem;
   __shared__ int s_t;
   __shared__ long long s_off, s_total;
@@ -690,12 +700,15 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         const float r = alone ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
         ffac[c] = f0 * gvs[2 * hv] * r;
         ffac[C + c] = f1 * (both ? gvs[2 * hv + 1] : 0.f) * r;
+        const int tok = c / a.g;
+        coff[c] = tok * a.out_stride + (c - tok * a.g) * HD;
         if (!alone) *reinterpret_cast<float2*>(mine + C * HD + 2 * c) = make_float2(M, L);
       }
       all_sync();
       const int d_row = HD == 128 ? quad * 32 + lane : quad * 16 + (lane & 15);  // the dimension of this lane
       const bool d_on = HD == 128 || lane < 16;
       float* other = reinterpret_cast<float*>(pbuf);  // [C][HD]: parity 1's sums
+      const int64_t obase = w.u.qrow * a.out_stride + (int64_t)w.j * a.g * HD;
 #pragma unroll 1
       for (int pass = 1; pass >= 0; --pass) {
         if (gp == pass && (both || pass == 0)) {
@@ -713,14 +726,12 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
               v *= ffac[pass * C + c];
               if (d_on && c < used) {
                 if (pass == 0 && both) v += other[c * HD + d_row];
-                float* dst = pass ? other + c * HD : mine + c * HD;
                 if (pass == 0 && alone) {
-                  const int tok = c / a.g;
-                  const int64_t at = (w.u.qrow + tok) * a.out_stride + (int64_t)(w.j * a.g + c - tok * a.g) * HD + d_row;
+                  const int64_t at = obase + coff[c] + d_row;
                   if constexpr (QT) static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v);
                   else static_cast<float*>(a.out)[at] = v;
                 } else {
-                  dst[d_row] = v;
+                  (pass ? other : mine)[c * HD + d_row] = v;
                 }
               }
             }
@@ -756,98 +767,70 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
       const float* parts = reinterpret_cast<const float*>(a.ws + kQattnTickets);
       auto part = [&](int i) { return parts + ((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * C * (HD + 2); };
       auto stat = [&](int i, int c) { return __ldcg(reinterpret_cast<const float2*>(part(i) + C * HD + 2 * c)); };
-      float* fac = reinterpret_cast<float*>(pbuf);  // [C][64] factors of 64 parts at a time
-      constexpr int CW = (C + NS / 32 - 1) / (NS / 32);  // columns of a warp; its lanes take the parts
-      float M[CW], L[CW];
-#pragma unroll
-      for (int q = 0; q < CW; ++q) {
-        const int c = sw + NS / 32 * q;
-        M[q] = kQaNone;
-        L[q] = 0.f;
-        if (c < used) {
-          const float2 none = make_float2(kQaNone, 0.f);
-          const float2 x0 = lane < np ? stat(lane, c) : none, x1 = lane + 32 < np ? stat(lane + 32, c) : none;
-          M[q] = fmaxf(x0.x, x1.x);
+      // (the ring is idle: factors [used][np], then the slices' sums; short loops, see above)
+      float* fac = reinterpret_cast<float*>(base);
 #pragma unroll 1
-          for (int i = lane + 64; i < np; i += 32) M[q] = fmaxf(M[q], stat(i, c).x);
-          M[q] = warp_max(M[q]);
-          const float f0 = qa_exp2(x0.x - M[q]), f1 = qa_exp2(x1.x - M[q]);
-          fac[c * 64 + lane] = f0;
-          fac[c * 64 + lane + 32] = f1;
-          L[q] = fmaf(x0.y, f0, x1.y * f1);
+      for (int c = sw; c < used; c += NS / 32) {  // warp = column, lanes = parts
+        float M = kQaNone, L = 0.f;
+#pragma unroll 1
+        for (int i = lane; i < np; i += 32) M = fmaxf(M, stat(i, c).x);
+        M = qa_warp_max(M);
+#pragma unroll 1
+        for (int i = lane; i < np; i += 32) {
+          const float2 x = stat(i, c);
+          const float f = qa_exp2(x.x - M);
+          fac[c * np + i] = f;
+          L = fmaf(x.y, f, L);
         }
-      }
-      // threads own groups of four dimensions of a column, in strides of NS
-      constexpr int PER = (C * HD / 4 + NS - 1) / NS, U = PER > 1 ? 4 : 8;  // U parts' loads in flight for each
-      float4 O[PER];
-#pragma unroll
-      for (int q = 0; q < PER; ++q) O[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-      for (int i0 = 0; i0 < np; i0 += 64) {
-        const int m = min(64, np - i0);
-        if (i0 > 0) {
-          all_sync();
-#pragma unroll
-          for (int q = 0; q < CW; ++q) {
-            const int c = sw + NS / 32 * q;
-            if (c < used)
-#pragma unroll 1
-              for (int i = lane; i < m; i += 32) {
-                const float2 x = stat(i0 + i, c);
-                const float f = qa_exp2(x.x - M[q]);
-                fac[c * 64 + i] = f;
-                L[q] = fmaf(x.y, f, L[q]);
-              }
-          }
+        L = warp_sum(L);
+        const int tok = c / a.g;
+        if (lane == 0) {
+          wmax[c] = L;
+          coff[c] = tok * a.out_stride + (c - tok * a.g) * HD;
         }
-        all_sync();
-#pragma unroll 1
-        for (int i = 0; i < m; i += U) {
-          float4 v[PER][U];
-#pragma unroll
-          for (int q = 0; q < PER; ++q)
-#pragma unroll
-            for (int y = 0; y < U; ++y) {
-              const int x = q * NS + stid;
-              v[q][y] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (x < used * (HD / 4) && i + y < m) v[q][y] = __ldcg(reinterpret_cast<const float4*>(part(i0 + i + y)) + x);
-            }
-#pragma unroll
-          for (int q = 0; q < PER; ++q)
-#pragma unroll
-            for (int y = 0; y < U; ++y) {
-              const int x = q * NS + stid;
-              if (x < used * (HD / 4) && i + y < m) {
-                const float f = fac[x / (HD / 4) * 64 + i + y];
-                O[q].x = fmaf(f, v[q][y].x, O[q].x);
-                O[q].y = fmaf(f, v[q][y].y, O[q].y);
-                O[q].z = fmaf(f, v[q][y].z, O[q].z);
-                O[q].w = fmaf(f, v[q][y].w, O[q].w);
-              }
-            }
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < CW; ++q) {
-        const float sum = warp_sum(L[q]);
-        if (lane == 0 && sw + NS / 32 * q < C) wmax[sw + NS / 32 * q] = sum;
       }
       all_sync();
+      // thread = four dimensions of a column, and every SL-th part where there are fewer of these than threads
+      constexpr int X4 = C * HD / 4, SL = NS > X4 ? NS / X4 : 1, U = 8;
+      static_assert((size_t)C * kQattnTickets <= (size_t)ST * X::STAGE, "factors of as many parts as there can be CTAs");
+      const int64_t obase = u.qrow * a.out_stride + (int64_t)u.j * a.g * HD;
+      float4* sums = reinterpret_cast<float4*>(pbuf);  // [SL][X4]
+#pragma unroll 1
+      for (int x = stid % X4; x < used * (HD / 4); x += NS) {
+        const int c = x / (HD / 4), sl = stid / X4 % SL;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int i = sl; i < np; i += SL * U) {
+          float4 v[U];
 #pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        const int x = q * NS + stid, c = x / (HD / 4), e = x % (HD / 4) * 4;
-        if (c < used) {
-          const float r = wmax[c] == 0.f ? 0.f : 1.f / wmax[c];
-          const float4 o = make_float4(O[q].x * r, O[q].y * r, O[q].z * r, O[q].w * r);
-          const int tok = c / a.g;
-          const int64_t at = (u.qrow + tok) * a.out_stride + (int64_t)(u.j * a.g + c - tok * a.g) * HD + e;
-          if constexpr (QT) {
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-                make_uint2((uint32_t)f32_to_bf16(o.x) | (uint32_t)f32_to_bf16(o.y) << 16,
-                           (uint32_t)f32_to_bf16(o.z) | (uint32_t)f32_to_bf16(o.w) << 16);
-          } else {
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = o;
+          for (int y = 0; y < U; ++y) v[y] = __ldcg(reinterpret_cast<const float4*>(part(min(i + y * SL, np - 1))) + x);
+#pragma unroll
+          for (int y = 0; y < U; ++y) {
+            const float f = i + y * SL < np ? fac[c * np + i + y * SL] : 0.f;
+            o.x = fmaf(f, v[y].x, o.x);
+            o.y = fmaf(f, v[y].y, o.y);
+            o.z = fmaf(f, v[y].z, o.z);
+            o.w = fmaf(f, v[y].w, o.w);
           }
+        }
+        const float r = wmax[c] == 0.f ? 0.f : 1.f / wmax[c];
+        o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
+        if constexpr (SL > 1) {
+          sums[sl * X4 + x] = o;  // (one turn of this loop: X4 < NS)
+        } else {
+          qa_put4<QT>(a.out, obase + coff[c] + x % (HD / 4) * 4, o);
+        }
+      }
+      if constexpr (SL > 1) {
+        all_sync();
+        if (stid < used * (HD / 4)) {
+          float4 o = sums[stid];
+#pragma unroll
+          for (int i = 1; i < SL; ++i) {
+            const float4 v = sums[i * X4 + stid];
+            o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+          }
+          qa_put4<QT>(a.out, obase + coff[stid / (HD / 4)] + stid % (HD / 4) * 4, o);
         }
       }
     }
