@@ -274,7 +274,8 @@ TcPlanQ plan_tc_q(const QCacheView& c, int g, int qt, int64_t rows, int S, int l
   const int np = qt ? 2 : 4, most = qt ? 4 : 8;
   TcPlanQ p;
   p.nc = 1;
-  while (p.nc < most && (int64_t)p.nc * 16 / np < (int64_t)S * g) p.nc *= 2;
+  // (f32: 1, 2, 4, 6 or 8; bf16: 1, 2 or 4)
+  while (p.nc < most && (int64_t)p.nc * 16 / np < (int64_t)S * g) p.nc = p.nc < 4 ? p.nc * 2 : p.nc + 2;
   p.cols = p.nc * 16 / np;
   p.tokens = p.cols / g;
   const int64_t units = rows * ((S + p.tokens - 1) / p.tokens) * c.kv;
@@ -330,7 +331,7 @@ cudaError_t launch_qattn(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s
     const int S = a.tiles ? qattn_tile_tokens(a.g) : a.r.S;  // (a tile is a row of its own)
     // (a page table can name a page more than once: rows longer than the pool get no more CTAs)
     const TcPlanQ p = plan_tc_q(a.c, a.g, qt, a.r.B, S, std::min(a.r.limit, a.c.rows * a.c.cap), num_sms);
-    const bool wide = !qt && p.nc == 8;
+    const bool wide = p.nc > 4;
     auto fn = a.c.hd == 64 ? (qt ? qattn_tc64_bf16 : wide ? qattn_tc64_f32_wide : qattn_tc64_f32)
                            : (qt ? qattn_tc128_bf16 : wide ? qattn_tc128_f32_wide : qattn_tc128_f32);
     return fn(*kmap, *vmap, a, p.nc, p.grid, s, pdl);

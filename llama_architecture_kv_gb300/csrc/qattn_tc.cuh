@@ -56,6 +56,7 @@ struct QaShape {
   static constexpr int STAGE = 2 * KB;
   static constexpr int QB = N * HD;                // query pieces of a segment
   static constexpr int PB = kQaTile * N;           // weight pieces of one group
+  static constexpr int TMEM = 4 * N <= 64 ? 64 : 4 * N <= 128 ? 128 : 4 * N <= 256 ? 256 : 512;  // columns
   static constexpr int CTAS = C <= 8 ? 2 : 1;      // CTAs per SM (4 N columns of tensor memory each)
   static constexpr int HV = C <= 8 ? 1 : 2;        // groups that share a tile's columns
   static constexpr int CT = C / HV;                // columns of a thread
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   const uint32_t bars = (smem_u32(coff + C) + 7u) & ~7u;
   const uint32_t b_full = bars, b_empty = b_full + 8 * ST, b_s = b_empty + 8 * ST, b_p = b_s + 16, b_pv = b_p + 16,
                  b_q = b_pv + 16;
-  static_assert((size_t)C * 4 * 16 + 80 + 80 * ST + 8 * C + 96 <= X::MISC, "shared memory");
+  static_assert((size_t)C * 4 * 16 + 80 + 80 * ST + 8 * C + 112 <= X::MISC, "shared memory");
   __shared__ uint32_t s_tmem;
   __shared__ int s_t;
   __shared__ long long s_off, s_total;
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   }
   __syncwarp();
   if (warp == 1) {
-    tmem_alloc(smem_u32(&s_tmem), 4 * N);
+    tmem_alloc(smem_u32(&s_tmem), X::TMEM);
     tmem_relinquish();
   }
   grid_dep_wait();
@@ -393,23 +394,23 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         wait(b_q, qpar);
         qpar ^= 1u;
         tc_fence_after();
+        scores(0);
+        if (n > 1) scores(1);
 #pragma unroll 1
-        for (int t = -2; t < n; ++t) {
-          if (t >= 0) {
-            const int gp = t & 1;
-            wait(b_p + 8u * gp, cnt[gp]++ & 1u);
-            if (ok) {
-              tc_fence_after();
-              const uint32_t v_addr = s_ring + vs * X::STAGE + X::KB;
+        for (int t = 0; t < n; ++t) {
+          const int gp = t & 1;
+          wait(b_p + 8u * gp, cnt[gp]++ & 1u);
+          if (ok) {
+            tc_fence_after();
+            const uint32_t v_addr = s_ring + vs * X::STAGE + X::KB;
 #pragma unroll
-              for (int kk = 0; kk < kQaTile / 32; ++kk)
-                tc_mma_e4m3(tmem + 2 * N + gp * N, smem_desc(v_addr + kk * 32 * HD, 8 * HD, 8 * HD, X::SWZ),
-                            smem_desc(p_addr + gp * X::PB + kk * 512, 128, 2048, 0), id_o, t > 1 || kk > 0);
-              tc_commit(b_pv + 8u * gp);
-              tc_commit(b_empty + 8u * vs);
-            }
-            if (++vs == ST) vs = 0u;
+            for (int kk = 0; kk < kQaTile / 32; ++kk)
+              tc_mma_e4m3(tmem + 2 * N + gp * N, smem_desc(v_addr + kk * 32 * HD, 8 * HD, 8 * HD, X::SWZ),
+                          smem_desc(p_addr + gp * X::PB + kk * 512, 128, 2048, 0), id_o, t > 1 || kk > 0);
+            tc_commit(b_pv + 8u * gp);
+            tc_commit(b_empty + 8u * vs);
           }
+          if (++vs == ST) vs = 0u;
           if (t + 2 < n) scores(t + 2);
         }
       }
@@ -662,12 +663,13 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
       // ---- the segment's end: the parities' sums meet, parity 0 writes ----
       {
         // the lanes' sums of every column at once: each exchange halves the columns a lane holds
-        float x[CT];
+        constexpr int CP = CT <= 4 ? 4 : CT <= 8 ? 8 : 16;  // (a power of two)
+        float x[CP];
 #pragma unroll
-        for (int c = 0; c < CT; ++c) x[c] = l[c];
+        for (int c = 0; c < CP; ++c) x[c] = c < CT ? l[c < CT ? c : 0] : 0.f;
         int col = 0;
 #pragma unroll
-        for (int o = 16, m = CT; o > 0; o >>= 1) {
+        for (int o = 16, m = CP; o > 0; o >>= 1) {
           if (m > 1) {
             m >>= 1;
             const bool up = lane & o;
@@ -681,7 +683,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
             x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
           }
         }
-        wmax[(gp * 4 + gw) * C + c0 + col] = x[0];  // (lanes of one column write the same sum)
+        if (col < CT) wmax[(gp * 4 + gw) * C + c0 + col] = x[0];  // (lanes of one column write the same sum)
         if (gtid == 0) gvs[group] = vref;
       }
       all_sync();  // (every product is done: the weights' buffers are free)
@@ -839,7 +841,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 4 * N);
+  if (warp == 1) tmem_dealloc(tmem, X::TMEM);
 }
 
 // one instantiation per translation unit (they take half a minute each to compile)
