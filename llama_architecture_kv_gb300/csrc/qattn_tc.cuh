@@ -44,6 +44,7 @@ constexpr uint64_t kQaWaitCycles = 1000000000ull;  // about 0.5 s
 constexpr float kQaFirst = 2.0f;                   // log2 of the largest weight of a segment's first tile
 constexpr float kQaTop = 5.0f;                     // and of a later tile that moved a reference
 constexpr float kQaMost = 8.0f;                    // the largest weight that moves none
+constexpr int kQaNear = 4, kQaNearRun = 16;        // cuts move by up to so many tiles in runs of up to so many
 constexpr float kQaNone = -3.0e38f;                // a reference before any score
 constexpr size_t kQaSmem = 232448;                 // shared memory a CTA can have
 
@@ -143,20 +144,34 @@ LLM_D float qa_exp2(float x) {
   return y;
 }
 
-// T tiles cut into G runs, the first T % G of them one longer
+// T tiles cut into G runs, the first T % G of them one longer; a cut within `near` tiles of a unit's
+// start or end moves there.  A segment costs about as much as four tiles besides its tiles, and a cut
+// unit its join, so short runs gain more from whole units than they lose by their unevenness; long ones
+// do not (kQaNearRun).
 struct QaCut {
   long long q, r;
+  int near;
   LLM_D void make(long long T, int G) {
     q = T < 0x7fffffff ? (long long)((uint32_t)T / (uint32_t)G) : T / G;
     r = T - q * G;
+    near = q <= kQaNearRun ? min(kQaNear, (int)q * 3 / 8) : 0;
   }
   LLM_D long long begin(int c) const { return c * q + min((long long)c, r); }
+  // the run that holds tile i, before cuts move
   LLM_D int owner(long long i) const {
     const long long head = r * (q + 1);
     const bool in = i < head;
     const long long n = in ? i : i - head, d = in ? q + 1 : q;
     return (int)((in ? 0 : r) + (n < 0x7fffffff && d < 0x7fffffff ? (long long)((uint32_t)n / (uint32_t)d) : n / d));
   }
+  // a cut at x inside the unit of nt tiles from u0
+  LLM_D long long moved(long long x, long long u0, int nt) const {
+    const long long d0 = x - u0, d1 = nt - d0;
+    return d0 <= d1 ? (d0 <= near ? u0 : x) : d1 <= near ? u0 + nt : x;
+  }
+  // the first and last run of a unit that is cut: its cuts lie more than `near` from both ends
+  LLM_D int first(long long u0) const { return owner(u0 + near); }
+  LLM_D int last(long long u0, int nt) const { return owner(u0 + nt - 1 - near); }
 };
 
 // four elements of the output
@@ -178,6 +193,11 @@ struct QaWalk {
     t = t_; off = off_; st = c0; end = c1; tpt = tpt_; nct = nct_;
     if (st >= end) return;
     u = qa_unit(a, t, tpt, nct);
+    if (st - off == (long long)a.c.kv * u.nt) {  // (a cut moved to the end of its token tile)
+      off = st;
+      do u = qa_unit(a, ++t, tpt, nct);
+      while (u.nt == 0);
+    }
     j = (int)((uint32_t)(st - off) / (uint32_t)u.nt);  // (kv heads x tiles of a row: below 2^31)
     k0 = (int)(st - off) - j * u.nt;
     cut();
@@ -225,7 +245,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   static_assert((size_t)C * 4 * 16 + 80 + 80 * ST + 8 * C + 112 <= X::MISC, "shared memory");
   __shared__ uint32_t s_tmem;
   __shared__ int s_t;
-  __shared__ long long s_off, s_total;
+  __shared__ long long s_off, s_total, s_begin, s_end;
   // the units that this CTA holds a part of (the first and the last of its run)
   struct Pending {
     int64_t qrow;
@@ -276,18 +296,30 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
     if (lane == 0) s_total = total;
     // (never more runs than tiles, so that every CTA of a unit's range holds a part of it)
     const int ge = (int)min((long long)gridDim.x, total);
+    if (lane == 0) s_begin = s_end = total;
+    __syncwarp();
     if (cta < ge) {
       QaCut cut;
       cut.make(total, ge);
-      const long long c0 = cut.begin(cta);
-      long long off = (incl - sum) * a.c.kv;
-      if (sum > 0 && c0 >= off && c0 < incl * a.c.kv) {
+      const long long lo = (incl - sum) * a.c.kv, hi = incl * a.c.kv;  // this lane's stretch
+#pragma unroll 1
+      for (int side = 0; side < 2; ++side) {  // the run's start, then its end
+        const long long x = cut.begin(cta + side);
+        if (sum == 0 || x < lo || x >= hi) continue;
+        long long off = lo;
 #pragma unroll 1
         for (int t = t0; t < t1; ++t) {
-          const long long w = (long long)qa_unit(a, t, tpt, nct).nt * a.c.kv;
-          if (c0 < off + w) {
-            s_t = t;
-            s_off = off;
+          const int nt = qa_unit(a, t, tpt, nct).nt;
+          const long long w = (long long)nt * a.c.kv;
+          if (x < off + w) {
+            const long long u0 = x - (uint32_t)(x - off) % (uint32_t)nt, to = cut.moved(x, u0, nt);
+            if (side) {
+              s_end = to;
+            } else {
+              s_t = t;
+              s_off = off;
+              s_begin = to;
+            }
             break;
           }
           off += w;
@@ -300,13 +332,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   QaWalk w;
-  QaCut cut = {0, 0};
-  {
-    const long long T = s_total;
-    const int G = (int)min((long long)gridDim.x, T);
-    if (cta < G) cut.make(T, G);
-    w.begin(a, s_t, s_off, cta < G ? cut.begin(cta) : 0, cta < G ? cut.begin(cta + 1) : 0, tpt, nct);
-  }
+  w.begin(a, s_t, s_off, s_begin, s_end, tpt, nct);
   bool ok = true;  // a wait that gave up: no further waits, but every loop and barrier is still walked
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (ok && !mbar_wait(bar, parity, kQaWaitCycles)) {
@@ -743,8 +769,10 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
       }
       if (!alone) {
         if (stid == 0) {
-          const int first = cut.owner(w.unit0());
-          s_pend[pending] = Pending{w.u.qrow, w.j, used, first, cut.owner(w.unit0() + w.u.nt - 1) - first + 1, 0};
+          QaCut cut;
+          cut.make(s_total, (int)min((long long)gridDim.x, s_total));
+          const int first = cut.first(w.unit0());
+          s_pend[pending] = Pending{w.u.qrow, w.j, used, first, cut.last(w.unit0(), w.u.nt) - first + 1, 0};
         }
         ++pending;
       }
