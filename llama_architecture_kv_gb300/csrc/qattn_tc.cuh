@@ -183,6 +183,26 @@ LLM_D void qa_put4(void* out, int64_t at, float4 o) {
     *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = o;
 }
 
+// pairs of f16: from f32, their e4m3 codes, and 32 times what the codes leave over (exact)
+LLM_D uint32_t qa_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+LLM_D uint32_t qa_e4m3_half2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+LLM_D uint32_t qa_rest32(uint32_t h, uint32_t code) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 d, k;\n\tcvt.rn.f16x2.e4m3x2 d, %2;\n\tsub.rn.f16x2 d, %1, d;\n\tmov.b32 k, 0x50005000;\n\t"
+      "mul.rn.f16x2 %0, d, k;\n\t}"
+      : "=r"(r)
+      : "r"(h), "h"((uint16_t)code));
+  return r;
+}
+
 // the walk of one CTA's run over (token tile, kv head, position tiles)
 struct QaWalk {
   QaUnit u;
@@ -550,10 +570,9 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         const int p0 = (w.u.tile0 + w.k0 + t) * kQaTile, pos = p0 + quad * 32 + lane;
         wait(b_full + 8u * slot, fpar);
         const float ks = ssc[slot * 16 + quad * 2 + (lane >> 4)], vs = ssc[slot * 16 + 8 + quad * 2 + (lane >> 4)];
-        // columns see positions below their cend; where the whole tile is seen by all, every position is
         const bool good = !(ks < 0.f) && pos < w.u.last && pos >= w.u.start;
         const bool whole = __all_sync(0xffffffffu, good) && p0 + kQaTile <= w.u.end0;
-        const int mypos = whole ? -0x7fffffff : good ? pos : 0x7fffffff;
+        const int mypos = good ? pos : 0x7fffffff;
         wait(b_s + 8u * gp, cs++ & 1u);
         __syncwarp();
         tc_fence_after();
@@ -567,18 +586,26 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
           for (int i = 0; i < CPC; i += 4) {
             const float4 qv = *reinterpret_cast<const float4*>(qsg + ch * CPC + i);
             const float4 rv = *reinterpret_cast<const float4*>(ref + ch * CPC + i);
-            const int4 ev = *reinterpret_cast<const int4*>(ceg + ch * CPC + i);
             const float q4[4] = {qv.x, qv.y, qv.z, qv.w}, r4[4] = {rv.x, rv.y, rv.z, rv.w};
-            const int e4[4] = {ev.x, ev.y, ev.z, ev.w};
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               float v = d[(i + y) * NP + NP - 1];
 #pragma unroll
               for (int x = NP - 2; x >= 0; --x) v = fmaf(v, 0.03125f, d[(i + y) * NP + x]);
-              v = mypos < e4[y] ? v * (ks * q4[y]) : -INFINITY;
+              v *= ks * q4[y];
               s[ch * CPC + i + y] = v;
               above = fmaxf(above, v - r4[y]);
             }
+          }
+        }
+        float vr = good ? vs * vinv : 0.f;
+        if (!whole) {
+          // columns see positions below their cend
+          above = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            if (mypos >= ceg[c]) s[c] = -INFINITY;
+            above = fmaxf(above, s[c] - ref[c]);
           }
         }
         const bool low = !(above > kQaMost) && !(good && vs > vref);
@@ -607,6 +634,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
             vcorr = vref * q_recip(v1);
             vref = v1;
             vinv = q_recip(v1);
+            vr = good ? vs * vinv : 0.f;
           }
           group_sync();
 #pragma unroll
@@ -631,7 +659,15 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
             tc_wait_st();
           }
         }
-        const float vr = good ? vs * vinv : 0.f;
+        if (__any_sync(0xffffffffu, vr != vr)) {
+          // a block of values that are NaN: so are the weights of the columns that see it, and no others
+          if (vr != vr) {
+            vr = 0.f;
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+              if (s[c] > -INFINITY) s[c] = __uint_as_float(0x7fc00000u);
+          }
+        }
         if (pend) wait(b_pv + 8u * gp, cpv++ & 1u);  // the weights' buffer is free again
 #pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
@@ -641,20 +677,27 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
             const int c = ch * CPC + i;
             const float2 rv = *reinterpret_cast<const float2*>(ref + c);
             // a weight (0 where the column does not see the position), its sum, and with the value's
-            // scale on it (a scale may be NaN, which reaches only the columns that see it)
+            // scale on it
             float x0 = qa_exp2(s[c] - rv.x), x1 = qa_exp2(s[c + 1] - rv.y);
             l[c] += x0;
             l[c + 1] += x1;
-            x0 = x0 == 0.f ? 0.f : x0 * vr;
-            x1 = x1 == 0.f ? 0.f : x1 * vr;
+            x0 *= vr;
+            x1 *= vr;
             uint32_t x[NP];
+            if constexpr (NP == 2) {
+              // (two pieces hold eight bits: the eleven of f16 are enough to take them from, in packed pairs)
+              const uint32_t h = qa_half2(x0, x1);
+              x[0] = qa_e4m3_half2(h);
+              x[1] = qa_e4m3_half2(qa_rest32(h, x[0]));
+            } else {
 #pragma unroll
-            for (int y = 0; y < NP; ++y) {
-              x[y] = e4m3x2(x0, x1);
-              if (y + 1 < NP) {
-                const float2 v = e4m3_pair(x[y]);
-                x0 = (x0 - v.x) * 32.f;
-                x1 = (x1 - v.y) * 32.f;
+              for (int y = 0; y < NP; ++y) {
+                x[y] = e4m3x2(x0, x1);
+                if (y + 1 < NP) {
+                  const float2 v = e4m3_pair(x[y]);
+                  x0 = (x0 - v.x) * 32.f;
+                  x1 = (x1 - v.y) * 32.f;
+                }
               }
             }
             if constexpr (NP == 4) {
