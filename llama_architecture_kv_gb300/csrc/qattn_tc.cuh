@@ -32,6 +32,14 @@
 // one equal run per CTA; the parts of a unit cut across CTAs meet in global memory once a CTA's run is
 // done, where the last CTA to arrive (a ticket, nobody waits) adds them in CTA order.  So rows of any
 // lengths fill the SMs evenly and the result does not depend on timing.
+//
+// Bound by HBM where a tile's columns are few and rows long, by the softmax warps' instructions from
+// about 16 columns on, by latencies where a CTA has only a few tiles (a segment costs about 4 us besides
+// its tiles: first loads, the groups' sums, the join).  GB300, f32 queries, heads of 128, groups of 4, 8
+// key/value heads: 8 rows of 32768 positions 88 us (538 MB: 6.1 TB/s, 90% of the copy rate); one row of
+// 131072 53 us (5.1 TB/s); 32 rows of up to 2100 31 us (108 MB: 3.5 TB/s); one row of 2048 10 us; five
+// tokens in each of 32 rows of 2048 60 us (20 columns).  bf16 queries, 8 tokens at 131072 positions (32
+// columns): 79 us (269 MB: 3.4 TB/s).
 #pragma once
 #include "attention.cuh"
 #include "qcache.cuh"
@@ -44,7 +52,7 @@ constexpr uint64_t kQaWaitCycles = 1000000000ull;  // about 0.5 s
 constexpr float kQaFirst = 2.0f;                   // log2 of the largest weight of a segment's first tile
 constexpr float kQaTop = 5.0f;                     // and of a later tile that moved a reference
 constexpr float kQaMost = 8.0f;                    // the largest weight that moves none
-constexpr int kQaNear = 4, kQaNearRun = 16;        // cuts move by up to so many tiles in runs of up to so many
+constexpr int kQaNear = 4;                         // most tiles by which a cut moves to a unit's end
 constexpr float kQaNone = -3.0e38f;                // a reference before any score
 constexpr size_t kQaSmem = 232448;                 // shared memory a CTA can have
 
@@ -58,7 +66,10 @@ struct QaShape {
   static constexpr int QB = N * HD;                // query pieces of a segment
   static constexpr int PB = kQaTile * N;           // weight pieces of one group
   static constexpr int TMEM = 4 * N <= 64 ? 64 : 4 * N <= 128 ? 128 : 4 * N <= 256 ? 256 : 512;  // columns
-  static constexpr int CTAS = C <= 8 ? 2 : 1;      // CTAs per SM (4 N columns of tensor memory each)
+  // Up to 8 columns two CTAs per SM (16 rows of 5 tokens of one head of 64: 26 us against 39 us with
+  // one; 32 rows of one token of 4 heads of 128: 31 against 34), more in one CTA whose groups halve them
+  // (16 rows of 16 columns at 2048 positions: 30 us against 39 us as two CTAs of whole columns)
+  static constexpr int CTAS = C <= 8 ? 2 : 1;
   static constexpr int HV = C <= 8 ? 1 : 2;        // groups that share a tile's columns
   static constexpr int CT = C / HV;                // columns of a thread
   static constexpr int NCH = NC / HV;              // 16-column chunks of a thread
@@ -145,16 +156,16 @@ LLM_D float qa_exp2(float x) {
 }
 
 // T tiles cut into G runs, the first T % G of them one longer; a cut within `near` tiles of a unit's
-// start or end moves there.  A segment costs about as much as four tiles besides its tiles, and a cut
-// unit its join, so short runs gain more from whole units than they lose by their unevenness; long ones
-// do not (kQaNearRun).
+// start or end moves there: a segment costs about as much as four tiles besides its tiles, and a cut unit
+// its join, which whole units save at the price of runs that are uneven by as much (16 rows of 5 tokens,
+// 32 heads of 64, about 900 positions: 31 us without, 26 us with; 8 positions instead of 4: the same).
 struct QaCut {
   long long q, r;
   int near;
   LLM_D void make(long long T, int G) {
     q = T < 0x7fffffff ? (long long)((uint32_t)T / (uint32_t)G) : T / G;
     r = T - q * G;
-    near = q <= kQaNearRun ? min(kQaNear, (int)q * 3 / 8) : 0;
+    near = (int)min((long long)kQaNear, q * 3 / 8);
   }
   LLM_D long long begin(int c) const { return c * q + min((long long)c, r); }
   // the run that holds tile i, before cuts move

@@ -20,7 +20,12 @@
 // Bounds: both directions are HBM-bound for long inputs and launch-latency-bound for one token per
 // row.  One warp owns a (block, head, keys or values): its 16 tokens' rows are all loaded at once
 // (16 independent 16-byte loads a lane at hd 128, f32), reduced in registers and stored as codes, so
-// each value is read once and the maximum costs no second pass.
+// each value is read once and the maximum costs no second pass.  Reading mirrors it, every store of a
+// warp one contiguous run.  GB300, copy rate 6.79 TB/s: 32 rows of one token (8 heads of 128) written in
+// 2.7 us; 16 rows of up to 2048 bf16 tokens (174 MB in and out) in 30.7 us, 84% of the copy rate, with the
+// values packed as read (widened to f32 in registers: 46 us, half the warps in flight); 32 such rows read
+// back (315 MB) in 48.5 us, 96% (rounding to bf16 in integer steps instead of one conversion per pair:
+// 77 us).
 #include <algorithm>
 #include <type_traits>
 

@@ -14,11 +14,12 @@
 // Bound: the two rows of V floats that the last token is drawn from (everything else is a few
 // scalars), and for a few rows the chain of dependent loads: drafts, their probabilities, the rows.  A
 // cluster of 8 CTAs shares a row, since one SM's loads would need about 10 us for 1 MB: each warp sums
-// one contiguous stretch with coalesced loads and keeps its weights in registers, the stretches' sums
-// meet through distributed shared memory behind one cluster barrier, and the warp whose stretch holds
-// the draw walks its registers (reading the stretch again in steps of 32 ids cost 11 us).
-#include <algorithm>
-
+// one contiguous stretch with coalesced loads, the stretches' sums meet through distributed shared
+// memory behind one cluster barrier, and the warp whose stretch holds the draw reads it again from L2 in
+// two rounds (in rounds of 32 ids it took 11 us).  Loads of one id per lane do for rows of any alignment
+// (16-byte loads of aligned rows measured the same), and short loops: unrolled 16 times the sum was
+// slower, waiting for its own instructions.  GB300: 5.7 us for one row of 49152 ids, 14.8 us for 32 rows
+// of 128256 with q (33 MB: 2.2 TB/s; the chain and the launch are 6 us of it).
 #include "verify.cuh"
 
 namespace llm {
@@ -82,12 +83,8 @@ LLM_D uint64_t ver_scan(uint64_t x) {
   return x;
 }
 
-constexpr int kVerKeep = 1024;  // longest stretch kept in registers: vocabularies up to 131072
-
-// cluster = row; W: ids per lane and load (4 where rows start on 16-byte boundaries, else 1)
-template <int W>
+// cluster = row
 __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs a) {
-  constexpr int NL = kVerKeep / (32 * W);  // loads of a kept stretch: id i0 + 32 W i + W lane + c
   __shared__ int s_r;
   __shared__ uint64_t s_warp[kVerWarps];   // sums of this CTA's stretches
   __shared__ uint64_t s_all[2][kVerCluster];  // the CTAs' sums, by attempt
@@ -119,62 +116,19 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
     if (a.q) row.q = a.q + ((size_t)b * S + r) * V;
     else row.skip = a.drafts[(size_t)b * S + r];
   }
-  // stretches of whole groups of 4 ids, warp by warp over the cluster
-  const int per = ((V + kVerCluster * kVerWarps - 1) / (kVerCluster * kVerWarps) + 3) & ~3;
-  const bool keep = per <= kVerKeep;
+  // stretches of ids, warp by warp over the cluster
+  const int per = (V + kVerCluster * kVerWarps - 1) / (kVerCluster * kVerWarps);
   const int64_t i0_ = (int64_t)((int)rank * kVerWarps + warp) * per;
   const int i0 = (int)min((int64_t)V, i0_), i1 = (int)min((int64_t)V, i0_ + per);
   int32_t* ids = a.ids + (size_t)b * (S + 1);
   // no weight at all (not a row of probabilities): id 0; the draw's owner writes over it after the
   // cluster barrier
   if (rank == 0 && tid == 0) ids[r] = 0;
-  float w[NL][W];
   uint64_t total = 0, before = 0;
   for (int attempt = 0; attempt < 2; ++attempt) {
     uint64_t sum = 0;
-    if (keep) {
-#pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const int v = i0 + 32 * W * i + W * lane;
-#pragma unroll
-        for (int c = 0; c < W; ++c) w[i][c] = 0.f;
-        if (v < i1) {
-          if constexpr (W == 4) {  // (V, and so every stretch, is a multiple of 4)
-            const float4 x = *reinterpret_cast<const float4*>(row.p + v);
-            w[i][0] = x.x; w[i][1] = x.y; w[i][2] = x.z; w[i][3] = x.w;
-          } else {
-            w[i][0] = row.p[v];
-          }
-        }
-      }
-      if (row.q) {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-          const int v = i0 + 32 * W * i + W * lane;
-          if (v < i1) {
-            if constexpr (W == 4) {
-              const float4 x = *reinterpret_cast<const float4*>(row.q + v);
-              w[i][0] = __fsub_rn(w[i][0], x.x); w[i][1] = __fsub_rn(w[i][1], x.y);
-              w[i][2] = __fsub_rn(w[i][2], x.z); w[i][3] = __fsub_rn(w[i][3], x.w);
-            } else {
-              w[i][0] = __fsub_rn(w[i][0], row.q[v]);
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        if (i0 + 32 * W * i >= i1) break;
-#pragma unroll
-        for (int c = 0; c < W; ++c) {
-          if (i0 + 32 * W * i + W * lane + c == row.skip) w[i][c] = 0.f;
-          sum += ver_units(w[i][c]);
-        }
-      }
-    } else {
-#pragma unroll 8
-      for (int v = i0 + lane; v < i1; v += 32) sum += ver_weight(row, v);
-    }
+#pragma unroll 4
+    for (int v = i0 + lane; v < i1; v += 32) sum += ver_weight(row, v);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) s_warp[warp] = sum;
@@ -208,38 +162,24 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const VerifyArgs
   }
   for (int x = 0; x < warp; ++x) before += s_warp[x];
   if (goal < before || goal - before >= s_warp[warp]) return;
-  // this warp's stretch holds the draw: a running sum over its ids, a load's worth at a time
-  auto walk = [&](uint64_t mine, auto weight, int v0) {  // v0: this lane's first id, mine: its weights' sum
-    const uint64_t upto = ver_scan(mine);
-    const uint32_t above = __ballot_sync(0xffffffffu, before + upto > goal);
-    if (!above) {
-      before += __shfl_sync(0xffffffffu, upto, 31);
-      return false;
+  // this warp's stretch holds the draw: lanes sum equal pieces of it, then the piece that holds the draw is
+  // walked 32 ids at a time
+  const int piece = (i1 - i0 + 31) / 32, l0 = min(i1, i0 + lane * piece), l1 = min(i1, l0 + piece);
+  uint64_t part = 0;
+#pragma unroll 8
+  for (int v = l0; v < l1; ++v) part += ver_weight(row, v);
+  const uint64_t upto = ver_scan(part);
+  const int who = __ffs(__ballot_sync(0xffffffffu, before + upto > goal)) - 1;  // (one does: goal is in this stretch)
+  before += __shfl_sync(0xffffffffu, upto - part, who);
+  const int v0 = __shfl_sync(0xffffffffu, l0, who), v1 = __shfl_sync(0xffffffffu, l1, who);
+  for (int v = v0; v < v1; v += 32) {
+    const uint64_t incl = ver_scan(v + lane < v1 ? ver_weight(row, v + lane) : 0ull);
+    const uint32_t above = __ballot_sync(0xffffffffu, before + incl > goal);
+    if (above) {
+      if (lane == 0) ids[r] = v + __ffs(above) - 1;
+      return;
     }
-    if (lane == __ffs(above) - 1) {
-      uint64_t run = before + upto - mine;
-      int c = 0;
-      while ((run += weight(c)) <= goal) ++c;
-      ids[r] = v0 + c;
-    }
-    return true;
-  };
-  if (keep) {
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      if (i0 + 32 * W * i >= i1) break;
-      uint64_t mine = 0;
-#pragma unroll
-      for (int c = 0; c < W; ++c) mine += ver_units(w[i][c]);
-      const float(&x)[W] = w[i];
-      auto weight = [&](int c) { return ver_units(W == 4 ? (c == 0 ? x[0] : c == 1 ? x[W / 4] : c == 2 ? x[W / 2] : x[W - 1]) : x[0]); };
-      if (walk(mine, weight, i0 + 32 * W * i + W * lane)) return;
-    }
-  } else {
-    for (int v = i0; v < i1; v += 32) {
-      const uint64_t mine = v + lane < i1 ? ver_weight(row, v + lane) : 0ull;
-      if (walk(mine, [&](int) { return mine; }, v + lane)) return;
-    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
   }
 }
 
@@ -336,8 +276,7 @@ cudaError_t launch_probs(float* x, int rows, int V, float temp, cudaStream_t s) 
 }
 
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
-  const bool vec = a.V % 4 == 0 && (reinterpret_cast<uintptr_t>(a.p) & 15) == 0 && (reinterpret_cast<uintptr_t>(a.q) & 15) == 0;
-  return launch_cluster(vec ? verify_kernel<4> : verify_kernel<1>, a.B, s, a);
+  return launch_cluster(verify_kernel, a.B, s, a);
 }
 
 }  // namespace llm
