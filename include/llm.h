@@ -288,7 +288,7 @@ llm_status llm_generate_dev(llm_handle* h, const int32_t* tokens_dev, int32_t B,
  * [B][S + 1] and accepted_dev [B]: ids_dev[b][0 .. accepted] are the row's next tokens.  tokens and
  * positions are host memory, the rest device memory; ordered on the handle's stream, returns without
  * waiting.  Checks: 1 <= B <= max_batch and B * (S + 1) <= max(max_batch, max_tokens) (LLM_ERR_BATCH);
- * S >= 1, temp finite and >= 0, no debug_trace handle (LLM_ERR_ARG); 0 <= positions_host[b] <= filled
+ * S >= 1, temp finite and >= 0, p_dev 16-byte aligned, no debug_trace handle (LLM_ERR_ARG); 0 <= positions_host[b] <= filled
  * length of row b and positions_host[b] + S < max_seq (LLM_ERR_POS_RANGE); tokens in [0, vocab)
  * (LLM_ERR_TOKEN_RANGE).  After success the filled length of row b is positions_host[b] + S + 1; its
  * next step starts at positions_host[b] + accepted + 1, which rewinds over the drafts not kept.
@@ -414,7 +414,7 @@ llm_status llm_sample_noalloc(const float* logits_dev, int32_t B, int32_t V, flo
  *                 written.
  *   table_dev     [B][pages_per_row] pages as for llm_decode_paged, over a pool of rows * (max_seq / 64)
  *                 pages (NULL: row b of the call is cache row b, and B <= rows).  Rows may share pages
- *                 that none of them writes.
+ *                 that none of them writes.  pages_per_row * 64 * kv_heads stays below 2^31 - 1024.
  *   status_dev    one int32 (may be NULL): where a position, length or count is out of range, or a
  *                 page outside the pool, the first such error is stored there if it holds 0
  *                 (LLM_ERR_POS_RANGE, LLM_ERR_ARG), and a wait that gave up (LLM_ERR_DEVICE_TIMEOUT).
@@ -477,8 +477,8 @@ llm_status llm_qcache_attend(const llm_qcache* cache, const void* q_dev, int32_t
 
 /*
  * Verify drafted tokens, without a handle (speculative sampling: the tokens that come out are
- * distributed as if the target model had drawn them one by one).  Row b has n = count_dev[b] drafts
- * (NULL: S; clamped to 0..S) drafts_dev [B][S], the target's probabilities p_dev [B][S + 1][V] (row
+ * distributed as if the target model had drawn them one by one).  S is 1..65535, V at most 2^30.  Row
+ * b has n = count_dev[b] drafts (NULL: S; clamped to 0..S) drafts_dev [B][S], the target's probabilities p_dev [B][S + 1][V] (row
  * i: after the first i drafts), the draft model's q_dev [B][S][V] or NULL (deterministic drafts:
  * q_i(x_i) = 1), and draws u_dev [B][S + 1] in [0, 1).  Draft i is kept while
  * u[i] * q_i(x_i) < p_i(x_i) (an exact comparison; an id outside 0..V-1 is never kept).  After the r

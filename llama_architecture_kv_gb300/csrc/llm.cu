@@ -1664,6 +1664,9 @@ llm_status llm_verify_step(llm_handle* h, const int32_t* tokens_host, int32_t B,
     return fail(h, LLM_ERR_BATCH, "%d rows of %d tokens exceed one pass of %d", B, S + 1, h->NT);
   if (!(temp >= 0.0f) || temp == INFINITY) return fail(h, LLM_ERR_ARG, "temperature must be finite and >= 0");
   if (h->cfg.debug_trace) return fail(h, LLM_ERR_ARG, "debug_trace handles run without graphs");
+  if ((reinterpret_cast<uintptr_t>(p_dev) & 15u) || ((reinterpret_cast<uintptr_t>(q_dev) | reinterpret_cast<uintptr_t>(u_dev) |
+       reinterpret_cast<uintptr_t>(ids_dev) | reinterpret_cast<uintptr_t>(accepted_dev)) & 3u))
+    return fail(h, LLM_ERR_ARG, "p_dev must be aligned to 16 bytes, the other arrays to 4");
   TRY(check_row_positions(h, B, positions_host));
   for (int b = 0; b < B; ++b)
     if ((int64_t)positions_host[b] + S >= h->cfg.max_seq)
@@ -1860,7 +1863,7 @@ static llm_status kv_copy(llm_handle* h, int32_t layer, int32_t row, int32_t pos
   const size_t es = h->es, hd = h->hd, kv = h->cfg.kv_heads, cap = h->cfg.max_seq;
   const size_t bytes = (size_t)n * hd * es;
   if (h->q8) {
-    if (import && (pos0 + n) % kQBlock != 0 && h->filled[row] > pos0 + n)
+    if (import && n > 0 && (pos0 + n) % kQBlock != 0 && h->filled[row] > pos0 + n)
       return fail(h, LLM_ERR_POS_RANGE, "import ends at %d, inside a filled block of an 8-bit cache (row %d holds %d)", pos0 + n,
                   row, h->filled[row]);
     // through the staging buffers, whole blocks at a time: the cache row as a cache of one row

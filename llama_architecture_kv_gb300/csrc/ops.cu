@@ -44,7 +44,8 @@ llm_status check_rows(const llm_qcache* c, int32_t B, int32_t S, const int32_t* 
   REFUSE((int64_t)B * S >= (int64_t)1 << 31, LLM_ERR_ARG, "rows x tokens must be below 2^31");
   if (table) {
     REFUSE(c->max_seq % kPage, LLM_ERR_CONFIG, "pages need max_seq to be a multiple of 64");
-    REFUSE(pages_per_row < 1 || (int64_t)pages_per_row * kPage > 0x7fffffff - 1024, LLM_ERR_ARG, "pages per row out of range");
+    REFUSE(pages_per_row < 1 || (int64_t)pages_per_row * kPage * c->kv_heads > 0x7fffffff - 1024, LLM_ERR_ARG,
+           "pages per row must be at least 1, and their positions x kv heads below 2^31 - 1024");
   }
   REFUSE(!aligned4(first) || !aligned4(count) || !aligned4(table) || !aligned4(status), LLM_ERR_ARG, "int32 arrays must be aligned");
   *view = QCacheView{(uint8_t*)c->k, (uint8_t*)c->v, c->k_scale, c->v_scale, c->rows, c->kv_heads, c->max_seq, c->head};
@@ -155,7 +156,8 @@ llm_status llm_verify(const float* p_dev, const float* q_dev, const int32_t* dra
                       void* cuda_stream) {
   REFUSE(!p_dev || !drafts_dev || !u_dev || !ids_dev || !accepted_dev, LLM_ERR_ARG, "NULL argument");
   REFUSE(B < 1 || B > 1 << 24, LLM_ERR_BATCH, "batch out of range");
-  REFUSE(S < 1 || S > 65535 || V < 1, LLM_ERR_ARG, "drafts per row must be in 1..65535 and the vocabulary at least 1");
+  REFUSE(S < 1 || S > 65535 || V < 1 || V > 1 << 30, LLM_ERR_ARG,
+         "drafts per row must be in 1..65535 and the vocabulary in 1..2^30");
   REFUSE(!aligned4(p_dev) || !aligned4(q_dev) || !aligned4(drafts_dev) || !aligned4(count_dev) || !aligned4(u_dev) ||
              !aligned4(ids_dev) || !aligned4(accepted_dev),
          LLM_ERR_ARG, "arrays must be aligned to 4 bytes");

@@ -1,5 +1,5 @@
 // Attention over an 8-bit cache on the 5th-generation tensor cores, head sizes 64 and 128: the
-// kernel template (instantiated in qattn_tc64.cu and qattn_tc128.cu).
+// kernel template (its instantiations, a translation unit each: qattn_tc<head size>_<type>.cu).
 //
 // The codes go from HBM to shared memory by TMA and from there into e4m3 MMAs as they are: no code
 // is ever widened.  The f32 (bf16) operands that meet them, queries and softmax weights, enter as NP
@@ -20,13 +20,14 @@
 //
 // Running maxima are lazy: a column's reference makes the first tile's largest weight 2^2 and moves only
 // when a weight exceeds 2^8 (then that one becomes 2^5), so the accumulators in tensor memory are hardly
-// ever rescaled and the pieces keep the range above and the precision below.
-// The values' block scales ride on the weights, relative to the largest scale seen (also lazy).
+// ever rescaled and the pieces keep the range above and the precision below.  The values' block scales
+// ride on the weights, relative to the largest scale seen (also lazy).
 //
 // One CTA: a producer warp (a ring of tiles by TMA, their block scales by 4-byte asynchronous copies), a
-// warp that issues the MMAs, and 16 softmax warps per SM: two groups of four take the tiles of a segment in turn, each with its own accumulators, so
-// that one group's softmax overlaps the other's loads and products; up to 8 columns two CTAs share an
-// SM, beyond that a tile's columns are halved between two groups.  What runs once per segment is kept
+// warp that issues the MMAs, and 16 softmax warps per SM: two groups of four take the tiles of a segment
+// in turn, each with its own accumulators, so that one group's softmax overlaps the other's loads and
+// products; up to 8 columns two CTAs share an SM, beyond that a tile's columns are halved between two
+// groups.  What runs once per segment is kept
 // in short loops: cold straight-line code runs at the pace of instruction fetch (unrolled over 32
 // columns, the end of a segment took 25 us).  The (row, token tile, kv head, tile) sequence is cut into
 // one equal run per CTA; the parts of a unit cut across CTAs meet in global memory once a CTA's run is

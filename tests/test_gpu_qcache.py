@@ -280,6 +280,35 @@ def test_attend_long_rows_many_parts(dtype):
         check_attend(c, r, rng, 2, 2, 4, dtype, length, ws=ws)
 
 
+@pytest.mark.parametrize("hd", [16, 64, 128])
+@pytest.mark.parametrize("rows,kv,cap", [(1, 1, 16), (1, 1, 48), (3, 1, 80), (1, 2, 112)])
+def test_caches_smaller_than_a_tile_and_with_ragged_ends(hd, rows, kv, cap):
+    # tiles of 128 positions reach past the row, the head and the whole cache
+    rng = np.random.default_rng(hd + cap)
+    c, r = make(rows, kv, cap, hd, garbage=5)
+    fill(c, r, rng, cap)
+    for dtype in ("f32", "bf16"):
+        check_attend(c, r, rng, rows, 1, 2, dtype, [cap - b for b in range(rows)])
+        check_attend(c, r, rng, rows, 3, 2, dtype, [1 + b for b in range(rows)])
+
+
+def test_attend_takes_slices_of_wider_rows_and_many_rows():
+    # queries as slices of fused rows; more rows than lanes of the warp that shares the work out
+    rng = np.random.default_rng(21)
+    B, kv, g, hd, cap = 70, 2, 3, 64, 144
+    c, r = make(B, kv, cap, hd, garbage=6)
+    fill(c, r, rng, 140)
+    wide, wn = rows_of(rng, (B, 2, (kv * g + 2 * kv) * hd), "f32")
+    n = kv * g * hd
+    out = torch.full((B, 2, n + 8), 9.0, device="cuda")
+    length = [(b * 29) % 141 for b in range(B)]
+    c.attend(wide[..., :n], i32(length), out[..., 8:], c.workspace(g, B, 2), stream=stream())
+    want, mag, sens, flat = r.attend(wn[..., :n].reshape(B, 2, kv * g, hd), length)
+    got = out[..., 8:].reshape(B, 2, kv * g, hd).double().cpu().numpy()
+    assert (np.abs(got - want) <= attend_tolerance("f32", hd, want, mag, sens, flat)).all()
+    assert (out[..., :8] == 9.0).all()
+
+
 def test_attend_scores_that_rise_along_the_row_and_other_scales():
     # running maxima move at every tile; the scale argument is used as given (zero and negative too)
     rng = np.random.default_rng(12)

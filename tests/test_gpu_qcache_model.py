@@ -260,6 +260,13 @@ def test_verification_step_refusals():
         g.verify_step(np.zeros((2, 1), np.int32), np.array([10, 10]), np.zeros((2, 1), np.float32))
     assert e.value.status == pkg.LLM_ERR_ARG
     assert g.filled(0) == 10
+    # probabilities at an address that the head's 16-byte stores could not use
+    import torch
+    p = torch.zeros(2 * 4 * shape.vocab + 4, device="cuda")
+    i4, f4 = torch.zeros(16, dtype=torch.int32, device="cuda"), torch.zeros(16, device="cuda")
+    with pytest.raises(pkg.LlmError) as e:
+        pkg.llm_verify_step(g.h, ok, 2, 3, np.array([10, 10], np.int32), 0.0, None, f4, p[1:], i4, i4[8:])
+    assert e.value.status == pkg.LLM_ERR_ARG
     g.close()
     h = make(shape, 771, 2, 12)
     h.prefill(synth.tokens(772, 0, 20, shape.vocab).reshape(2, 10), 0, logits=False)

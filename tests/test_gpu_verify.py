@@ -36,7 +36,7 @@ def softmax(x):
 
 @pytest.mark.parametrize("drawn", [True, False])
 @pytest.mark.parametrize("B,S,V", [(1, 1, 1), (2, 1, 3), (5, 4, 7), (3, 2, 130), (4, 3, 1000), (2, 5, 49152), (1, 7, 50001),
-                                   (2, 2, 128256), (9, 13, 2048)])
+                                   (2, 2, 128256), (9, 13, 2048), (1, 1, 262147)])
 def test_ids_equal_the_definition(B, S, V, drawn):
     rng = np.random.default_rng(B * 1000 + V)
     logits = rng.standard_normal((B, S + 1, V)) * 3
@@ -89,6 +89,25 @@ def test_edges():
     assert ((ids[:, 0] >= 0) & (ids[:, 0] < V)).all()
     ids, acc = run(p, q, d, np.full((6, S + 1), np.nan, np.float32), count=[-3, 0, 9, 1, 2, 3])
     assert ((ids[:, 0] >= 0) & (ids[:, 0] < V)).all()
+
+
+def test_rows_that_start_off_16_byte_boundaries():
+    # contiguous tensors at odd offsets of their storage
+    rng = np.random.default_rng(6)
+    B, S, V = 3, 2, 1003
+    p, q = softmax(rng.standard_normal((B, S + 1, V)) * 3), softmax(rng.standard_normal((B, S, V)) * 3)
+    d = rng.integers(0, V, (B, S)).astype(np.int32)
+    u = (rng.integers(0, 1 << 24, (B, S + 1)) / (1 << 24)).astype(np.float32)
+
+    def off(a, by):
+        flat = torch.zeros(a.size + by, dtype=torch.from_numpy(a).dtype, device="cuda")
+        flat[by:] = torch.from_numpy(a).cuda().reshape(-1)
+        return flat[by:].view(a.shape)
+
+    ids, acc = off(np.full((B, S + 1), -7, np.int32), 1), off(np.full(B, -7, np.int32), 3)
+    pkg.llm_verify(off(p, 1), off(q, 3), off(d, 1), off(u, 2), ids, acc, stream=torch.cuda.current_stream().cuda_stream)
+    for b in range(B):
+        assert (ids[b].tolist(), int(acc[b])) == ref.verify(p[b], q[b], d[b], None, u[b])
 
 
 def test_tokens_are_distributed_like_the_target():

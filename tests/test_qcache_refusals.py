@@ -39,7 +39,8 @@ CACHES = [(dict(k=None), ARG), (dict(v_scale=None), ARG), (dict(k=P + 8), ARG), 
 ROWS = [(dict(B=0), BATCH), (dict(B=3), BATCH), (dict(S=0), ARG), (dict(pos=None), ARG), (dict(pos=P + 1), ARG),
         (dict(S=1 << 30), ARG), (dict(dtype=2), ARG),
         (dict(k=None), ARG), (dict(v=P + 4), ARG), (dict(stride=120), ARG), (dict(stride=132), ARG),
-        (dict(table=P, pages=0), ARG), (dict(table=P, pages=1 << 30), ARG), (dict(status=P + 2), ARG)]
+        (dict(table=P, pages=0), ARG), (dict(table=P, pages=1 << 30), ARG), (dict(status=P + 2), ARG),
+        (dict(table=P, pages=1 << 24), ARG), (dict(table=P, pages=-1), ARG)]
 
 
 @pytest.mark.parametrize("call", [write, read])
@@ -78,7 +79,7 @@ def test_verification_refuses_bad_arguments(lib):
         return lib.llm_verify(p, q, drafts, count, B, S, V, u, ids, accepted, None)
     for kw, code in [(dict(p=None), ARG), (dict(drafts=None), ARG), (dict(u=None), ARG), (dict(ids=None), ARG),
                      (dict(accepted=None), ARG), (dict(B=0), BATCH), (dict(S=0), ARG), (dict(S=65536), ARG),
-                     (dict(V=0), ARG), (dict(p=P + 2), ARG), (dict(ids=P + 1), ARG)]:
+                     (dict(V=0), ARG), (dict(V=(1 << 30) + 1), ARG), (dict(B=(1 << 24) + 1), BATCH), (dict(p=P + 2), ARG), (dict(ids=P + 1), ARG)]:
         assert verify(**kw) == code, kw
 
 
