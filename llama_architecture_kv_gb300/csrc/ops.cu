@@ -141,6 +141,8 @@ llm_status llm_qcache_attend(const llm_qcache* cache, const void* q_dev, int32_t
   REFUSE(!isfinite(scale), LLM_ERR_ARG, "scale must be finite");
   int sms = 0;
   TRY(device_sms(&sms));
+  REFUSE(!qattn_fits(a.c, group, dtype, B, S, a.r.limit, sms), LLM_ERR_ARG,
+         "too large for one call: rows x tokens x kv heads x 128-position tiles must stay below 2^31");
   const uint64_t need = qattn_workspace(a.c, group, B, S, sms);
   if (need > 0) {
     REFUSE(!workspace_dev || workspace_bytes < need, LLM_ERR_ARG, "workspace smaller than llm_qcache_workspace says");

@@ -299,6 +299,12 @@ bool qattn_make_map(CUtensorMap* map, const void* codes, int hd, uint64_t rows) 
                      hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+bool qattn_fits(const QCacheView& c, int g, int qt, int B, int S, int limit, int num_sms) {
+  if (!qattn_uses_tc(c.hd)) return true;
+  const TcPlanQ p = plan_tc_q(c, g, qt, B, S, limit, num_sms);
+  return (double)B * ((S + p.tokens - 1) / p.tokens) * c.kv * ((limit + kQaTile - 1) / kQaTile) < 2147483648.0;
+}
+
 uint64_t qattn_workspace(const QCacheView& c, int g, int B, int S, int num_sms) {
   const int64_t tokens = (int64_t)B * S;
   const int limit = c.rows * c.cap;
@@ -321,8 +327,9 @@ uint64_t qattn_step_workspace(const QCacheView& c, int g, int NT, int num_sms) {
   return most;
 }
 
-cudaError_t launch_qattn(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s, bool pdl, const CUtensorMap* kmap,
+cudaError_t launch_qattn(const QAttnArgs& a0, int qt, int num_sms, cudaStream_t s, bool pdl, const CUtensorMap* kmap,
                          const CUtensorMap* vmap) {
+  QAttnArgs a = a0;
   if (qattn_uses_tc(a.c.hd)) {
     CUtensorMap maps[2];
     if (!kmap) {
@@ -335,6 +342,8 @@ cudaError_t launch_qattn(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s
     const int S = a.tiles ? qattn_tile_tokens(a.g) : a.r.S;  // (a tile is a row of its own)
     // (a page table can name a page more than once: rows longer than the pool get no more CTAs)
     const TcPlanQ p = plan_tc_q(a.c, a.g, qt, a.r.B, S, std::min(a.r.limit, a.c.rows * a.c.cap), num_sms);
+    a.tpt = p.tokens;
+    a.nct = a.r.step ? 1 : (a.r.S + p.tokens - 1) / p.tokens;
     const bool wide = p.nc > 4;
     auto fn = a.c.hd == 64 ? (qt ? qattn_tc64_bf16 : wide ? qattn_tc64_f32_wide : qattn_tc64_f32)
                            : (qt ? qattn_tc128_bf16 : wide ? qattn_tc128_f32_wide : qattn_tc128_f32);

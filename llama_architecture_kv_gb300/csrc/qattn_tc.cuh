@@ -94,7 +94,7 @@ struct QaUnit {
   int tile0, nt;  // its position tiles
 };
 
-LLM_D QaUnit qa_unit(const QAttnArgs& a, int t, int tpt, int nct) {
+LLM_D QaUnit qa_unit(const QAttnArgs& a, int t) {
   QaUnit u;
   if (a.r.step) {
     if (a.tiles) {
@@ -110,14 +110,14 @@ LLM_D QaUnit qa_unit(const QAttnArgs& a, int t, int tpt, int nct) {
     u.qrow = u.b;
     u.end0 = row_pos(a.r.step, u.b) + 1;
   } else {
-    u.b = t / nct;
-    const int n = q_count(a.r, u.b), i0 = (t - u.b * nct) * tpt;
+    u.b = a.nct == 1 ? t : (int)((uint32_t)t / (uint32_t)a.nct);
+    const int n = q_count(a.r, u.b), i0 = (t - u.b * a.nct) * a.tpt;
     int len = a.r.first[u.b];
     if (len < 0 || len > a.r.limit) {
       q_report(a.r.status, kErrPosRange);
       len = 0;
     }
-    u.ntok = max(0, min(tpt, n - i0));
+    u.ntok = max(0, min(a.tpt, n - i0));
     u.qrow = (int64_t)u.b * a.r.S + i0;
     u.start = 0;
     u.end0 = len - n + i0 + 1;
@@ -161,29 +161,27 @@ LLM_D float qa_exp2(float x) {
 // its join, which whole units save at the price of runs that are uneven by as much (16 rows of 5 tokens,
 // 32 heads of 64, about 900 positions: 31 us without, 26 us with; 8 positions instead of 4: the same).
 struct QaCut {
-  long long q, r;
-  int near;
-  LLM_D void make(long long T, int G) {
-    q = T < 0x7fffffff ? (long long)((uint32_t)T / (uint32_t)G) : T / G;
+  int q, r, near;
+  LLM_D void make(int T, int G) {
+    q = (int)((uint32_t)T / (uint32_t)G);
     r = T - q * G;
-    near = (int)min((long long)kQaNear, q * 3 / 8);
+    near = min(kQaNear, q * 3 / 8);
   }
-  LLM_D long long begin(int c) const { return c * q + min((long long)c, r); }
+  LLM_D int begin(int c) const { return c * q + min(c, r); }
   // the run that holds tile i, before cuts move
-  LLM_D int owner(long long i) const {
-    const long long head = r * (q + 1);
+  LLM_D int owner(int i) const {
+    const int head = r * (q + 1);
     const bool in = i < head;
-    const long long n = in ? i : i - head, d = in ? q + 1 : q;
-    return (int)((in ? 0 : r) + (n < 0x7fffffff && d < 0x7fffffff ? (long long)((uint32_t)n / (uint32_t)d) : n / d));
+    return (in ? 0 : r) + (int)((uint32_t)(in ? i : i - head) / (uint32_t)(in ? q + 1 : q));
   }
   // a cut at x inside the unit of nt tiles from u0
-  LLM_D long long moved(long long x, long long u0, int nt) const {
-    const long long d0 = x - u0, d1 = nt - d0;
+  LLM_D int moved(int x, int u0, int nt) const {
+    const int d0 = x - u0, d1 = nt - d0;
     return d0 <= d1 ? (d0 <= near ? u0 : x) : d1 <= near ? u0 + nt : x;
   }
   // the first and last run of a unit that is cut: its cuts lie more than `near` from both ends
-  LLM_D int first(long long u0) const { return owner(u0 + near); }
-  LLM_D int last(long long u0, int nt) const { return owner(u0 + nt - 1 - near); }
+  LLM_D int first(int u0) const { return owner(u0 + near); }
+  LLM_D int last(int u0, int nt) const { return owner(u0 + nt - 1 - near); }
 };
 
 // four elements of the output
@@ -219,32 +217,31 @@ LLM_D uint32_t qa_rest32(uint32_t h, uint32_t code) {
 struct QaWalk {
   QaUnit u;
   int t, j, k0, k1;
-  long long st, end, off;  // off: place of (t, head 0) in the sequence
-  int tpt, nct;
-  LLM_D void begin(const QAttnArgs& a, int t_, long long off_, long long c0, long long c1, int tpt_, int nct_) {
-    t = t_; off = off_; st = c0; end = c1; tpt = tpt_; nct = nct_;
+  int st, end, off;  // off: place of (t, head 0) in the sequence
+  LLM_D void begin(const QAttnArgs& a, int t_, int off_, int c0, int c1) {
+    t = t_; off = off_; st = c0; end = c1;
     if (st >= end) return;
-    u = qa_unit(a, t, tpt, nct);
-    if (st - off == (long long)a.c.kv * u.nt) {  // (a cut moved to the end of its token tile)
+    u = qa_unit(a, t);
+    if (st - off == a.c.kv * u.nt) {  // (a cut moved to the end of its token tile)
       off = st;
-      do u = qa_unit(a, ++t, tpt, nct);
+      do u = qa_unit(a, ++t);
       while (u.nt == 0);
     }
-    j = (int)((uint32_t)(st - off) / (uint32_t)u.nt);  // (kv heads x tiles of a row: below 2^31)
-    k0 = (int)(st - off) - j * u.nt;
+    j = (int)((uint32_t)(st - off) / (uint32_t)u.nt);
+    k0 = st - off - j * u.nt;
     cut();
   }
-  LLM_D void cut() { k1 = (int)min((long long)u.nt, k0 + (end - st)); }
+  LLM_D void cut() { k1 = min(u.nt, k0 + (end - st)); }
   LLM_D bool there() const { return st < end; }
-  LLM_D long long unit0() const { return off + (long long)j * u.nt; }
+  LLM_D int unit0() const { return off + j * u.nt; }
   LLM_D void next(const QAttnArgs& a) {
     st += k1 - k0;
     if (st >= end) return;  // (a unit that goes on belongs to the next CTA)
     k0 = 0;
     if (++j == a.c.kv) {
       j = 0;
-      off += (long long)a.c.kv * u.nt;
-      do u = qa_unit(a, ++t, tpt, nct);
+      off += a.c.kv * u.nt;
+      do u = qa_unit(a, ++t);
       while (u.nt == 0);
     }
     cut();
@@ -276,8 +273,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
                  b_q = b_pv + 16;
   static_assert((size_t)C * 4 * 16 + 80 + 80 * ST + 8 * C + 112 <= X::MISC, "shared memory");
   __shared__ uint32_t s_tmem;
-  __shared__ int s_t;
-  __shared__ long long s_off, s_total, s_begin, s_end;
+  __shared__ int s_t, s_off, s_total, s_begin, s_end;
   // the units that this CTA holds a part of (the first and the last of its run)
   struct Pending {
     int64_t qrow;
@@ -310,51 +306,45 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
 
   // this CTA's run: the token tiles' position tiles are counted lane by lane (contiguous stretches),
   // and the lane whose stretch holds the run's start finds its token tile
-  const int tpt = C / a.g;
-  const int nct = a.r.step ? 1 : (a.r.S + tpt - 1) / tpt;
-  const int nq = a.r.step ? (a.tiles ? a.tiles[1] : a.r.B) : a.r.B * nct;
+  const int nq = a.r.step ? (a.tiles ? a.tiles[1] : a.r.B) : a.r.B * a.nct;
   if (warp == 0) {
     const int per = (nq + 31) / 32, t0 = min(nq, lane * per), t1 = min(nq, t0 + per);
-    long long sum = 0;
+    int sum = 0;
 #pragma unroll 1
-    for (int t = t0; t < t1; ++t) sum += qa_unit(a, t, tpt, nct).nt;
-    long long incl = sum;
+    for (int t = t0; t < t1; ++t) sum += qa_unit(a, t).nt;
+    int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    const long long total = __shfl_sync(0xffffffffu, incl, 31) * a.c.kv;
-    if (lane == 0) s_total = total;
+    const int total = __shfl_sync(0xffffffffu, incl, 31) * a.c.kv;
     // (never more runs than tiles, so that every CTA of a unit's range holds a part of it)
-    const int ge = (int)min((long long)gridDim.x, total);
-    if (lane == 0) s_begin = s_end = total;
+    const int ge = min((int)gridDim.x, total);
+    if (lane == 0) s_total = s_begin = s_end = total;
     __syncwarp();
     if (cta < ge) {
       QaCut cut;
       cut.make(total, ge);
-      const long long lo = (incl - sum) * a.c.kv, hi = incl * a.c.kv;  // this lane's stretch
+      const int lo = (incl - sum) * a.c.kv, hi = incl * a.c.kv;  // this lane's stretch
 #pragma unroll 1
       for (int side = 0; side < 2; ++side) {  // the run's start, then its end
-        const long long x = cut.begin(cta + side);
+        const int x = cut.begin(cta + side);
         if (sum == 0 || x < lo || x >= hi) continue;
-        long long off = lo;
+        int off = lo, t = t0, nt = sum;  // (one token tile per lane: it is the one)
 #pragma unroll 1
-        for (int t = t0; t < t1; ++t) {
-          const int nt = qa_unit(a, t, tpt, nct).nt;
-          const long long w = (long long)nt * a.c.kv;
-          if (x < off + w) {
-            const long long u0 = x - (uint32_t)(x - off) % (uint32_t)nt, to = cut.moved(x, u0, nt);
-            if (side) {
-              s_end = to;
-            } else {
-              s_t = t;
-              s_off = off;
-              s_begin = to;
-            }
-            break;
-          }
-          off += w;
+        for (; per > 1; ++t) {
+          nt = qa_unit(a, t).nt;
+          if (x < off + nt * a.c.kv) break;
+          off += nt * a.c.kv;
+        }
+        const int to = cut.moved(x, x - (int)((uint32_t)(x - off) % (uint32_t)nt), nt);
+        if (side) {
+          s_end = to;
+        } else {
+          s_t = t;
+          s_off = off;
+          s_begin = to;
         }
       }
     }
@@ -364,7 +354,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   QaWalk w;
-  w.begin(a, s_t, s_off, s_begin, s_end, tpt, nct);
+  w.begin(a, s_t, s_off, s_begin, s_end);
   bool ok = true;  // a wait that gave up: no further waits, but every loop and barrier is still walked
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (ok && !mbar_wait(bar, parity, kQaWaitCycles)) {
@@ -488,7 +478,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
     // tokens that see nothing and share a tile with none that does: zeros
 #pragma unroll 1
     for (int t = cta; t < nq; t += gridDim.x) {
-      const QaUnit u = qa_unit(a, t, tpt, nct);
+      const QaUnit u = qa_unit(a, t);
       if (u.nt == 0 && u.ntok > 0)
 #pragma unroll 1
         for (int64_t i = stid; i < (int64_t)u.ntok * H * HD; i += NS) {
@@ -825,7 +815,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
       if (!alone) {
         if (stid == 0) {
           QaCut cut;
-          cut.make(s_total, (int)min((long long)gridDim.x, s_total));
+          cut.make(s_total, min((int)gridDim.x, s_total));
           const int first = cut.first(w.unit0());
           s_pend[pending] = Pending{w.u.qrow, w.j, used, first, cut.last(w.unit0(), w.u.nt) - first + 1, 0};
         }

@@ -137,9 +137,12 @@ struct QAttnArgs {
   unsigned char* ws;      // workspace (qattn_workspace bytes): tickets zero between calls, then partials
   const int32_t* tiles;   // a prefill pass's tiles (attention.cuh), of at most qattn_tile_tokens(g) tokens, or null
   int32_t krow0;          // row of the cache's position 0 of (row 0, kv head 0) in the tensor maps (step calls)
-  int32_t splits;         // set by launch_qattn
+  // set by launch_qattn: parts of a token's positions (CUDA cores), or tokens per tile and tiles per row
+  int32_t splits, tpt, nct;
 };
 constexpr int kQattnTickets = 4096;  // bytes of tickets (one 32-bit word per CTA) before the partials
+// whether the tiles of a call can be counted in 31 bits
+bool qattn_fits(const QCacheView& c, int g, int qt, int B, int S, int limit, int num_sms);
 uint64_t qattn_workspace(const QCacheView& c, int g, int B, int S, int num_sms);
 // the same for the steps and passes of at most NT rows of a handle (f32 queries)
 uint64_t qattn_step_workspace(const QCacheView& c, int g, int NT, int num_sms);
