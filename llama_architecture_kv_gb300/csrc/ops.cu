@@ -53,6 +53,13 @@ llm_status check_rows(const llm_qcache* c, int32_t B, int32_t S, const int32_t* 
   return LLM_OK;
 }
 
+// writes and reads take a warp per block, head and side
+llm_status check_warps(const QCacheView& c, const QRows& r) {
+  REFUSE((int64_t)r.B * q_span(r.S) >= ((int64_t)1 << 30) / c.kv, LLM_ERR_ARG,
+         "too large for one call: rows x blocks of 16 tokens x kv heads must stay below 2^30");
+  return LLM_OK;
+}
+
 // rows of `width` elements, `stride` elements apart, of a 16-byte aligned buffer
 llm_status check_buffer(const void* p, int32_t dtype, int64_t stride, int64_t width) {
   REFUSE(!p, LLM_ERR_ARG, "NULL buffer");
@@ -94,6 +101,7 @@ llm_status llm_qcache_write(const llm_qcache* cache, const void* k_dev, const vo
   QRows r;
   TRY(check_cache(cache));
   TRY(check_rows(cache, B, S, pos_dev, count_dev, table_dev, pages_per_row, status_dev, &c, &r));
+  TRY(check_warps(c, r));
   TRY(check_buffer(k_dev, dtype, stride, (int64_t)c.kv * c.hd));
   TRY(check_buffer(v_dev, dtype, stride, (int64_t)c.kv * c.hd));
   return launched(launch_qcache_write(c, r, k_dev, v_dev, dtype, stride, (cudaStream_t)cuda_stream));
@@ -107,6 +115,7 @@ llm_status llm_qcache_read(const llm_qcache* cache, int32_t B, int32_t S, const 
   QRows r;
   TRY(check_cache(cache));
   TRY(check_rows(cache, B, S, pos_dev, count_dev, table_dev, pages_per_row, status_dev, &c, &r));
+  TRY(check_warps(c, r));
   TRY(check_buffer(k_dev, dtype, stride, (int64_t)c.kv * c.hd));
   TRY(check_buffer(v_dev, dtype, stride, (int64_t)c.kv * c.hd));
   return launched(launch_qcache_read(c, r, k_dev, v_dev, dtype, stride, (cudaStream_t)cuda_stream));

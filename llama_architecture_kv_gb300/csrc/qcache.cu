@@ -118,11 +118,10 @@ LLM_D void quantise_run(uint8_t* codes, float* scale, int t0, int n, const void*
 template <int HD, int ST>
 __global__ void __launch_bounds__(kQThreads)
     qcache_write_kernel(const QCacheView c, const QRows r, const void* k, const void* v, int64_t stride, int span) {
-  const int64_t w = (int64_t)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t w = blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);  // (below 2^31: the host refuses more)
   const int side = (int)(w & 1);
-  const int h = (int)((w >> 1) % c.kv);
-  const int64_t bj = (w >> 1) / c.kv;
-  const int b = (int)(bj / span), j = (int)(bj - (int64_t)b * span);
+  const uint32_t bj = (w >> 1) / (uint32_t)c.kv;
+  const int h = (int)((w >> 1) - bj * (uint32_t)c.kv), b = (int)(bj / (uint32_t)span), j = (int)bj - b * span;
   if (b >= r.B) return;
   const int p0 = r.first[b], n = q_count(r, b);
   if (n == 0) return;
@@ -151,12 +150,10 @@ __global__ void __launch_bounds__(kQThreads)
     qcache_write_step_kernel(const QCacheView c, const QRows r, const void* k, const void* v) {
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t w = (int64_t)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t w = blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
   const int side = (int)(w & 1);
-  const int h = (int)((w >> 1) % c.kv);
-  const int64_t e64 = (w >> 1) / c.kv;
-  if (e64 >= r.B) return;
-  const int e = (int)e64;
+  const int e = (int)((w >> 1) / (uint32_t)c.kv), h = (int)((w >> 1) - (uint32_t)e * (uint32_t)c.kv);
+  if (e >= r.B) return;
   auto slot = [&](int i, int& row, int& pp) { cache_slot(r.step, c.cap, i, row_pos(r.step, i), row, pp); };
   int row, pp;
   slot(e, row, pp);
@@ -202,11 +199,10 @@ __global__ void __launch_bounds__(kQThreads)
     qcache_read_kernel(const QCacheView c, const QRows r, void* k, void* v, int64_t stride, int span) {
   constexpr int E = kE<ST>, QR = HD / E, NQ = (kQBlock * QR + 31) / 32;
   const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t w = blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);  // (below 2^31: the host refuses more)
   const int side = (int)(w & 1);
-  const int h = (int)((w >> 1) % c.kv);
-  const int64_t bj = (w >> 1) / c.kv;
-  const int b = (int)(bj / span), j = (int)(bj - (int64_t)b * span);
+  const uint32_t bj = (w >> 1) / (uint32_t)c.kv;
+  const int h = (int)((w >> 1) - bj * (uint32_t)c.kv), b = (int)(bj / (uint32_t)span), j = (int)bj - b * span;
   if (b >= r.B) return;
   const int p0 = r.first[b], n = q_count(r, b);
   if (n == 0) return;
@@ -277,9 +273,8 @@ bool qcache_head_supported(int hd) { return hd == 16 || hd == 32 || hd == 64 || 
 
 cudaError_t launch_qcache_write(const QCacheView& c, const QRows& r, const void* k, const void* v, int st,
                                 int64_t stride, cudaStream_t s) {
-  const int span = (r.S + kQBlock - 2) / kQBlock + 1;  // blocks that S tokens can touch
-  const int64_t warps = (int64_t)r.B * span * c.kv * 2, grid = (warps + kQThreads / 32 - 1) / (kQThreads / 32);
-  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  const int span = q_span(r.S);
+  const int64_t grid = ((int64_t)r.B * span * c.kv * 2 + kQThreads / 32 - 1) / (kQThreads / 32);
   return with_shape(c.hd, st, [&](auto hd, auto t) {
     qcache_write_kernel<hd.value, t.value><<<(unsigned)grid, kQThreads, 0, s>>>(c, r, k, v, stride, span);
     return cudaGetLastError();
@@ -288,7 +283,7 @@ cudaError_t launch_qcache_write(const QCacheView& c, const QRows& r, const void*
 
 cudaError_t launch_qcache_write_step(const QCacheView& c, const QRows& r, const void* k, const void* v, int st,
                                      cudaStream_t s, bool pdl) {
-  const int64_t warps = (int64_t)r.B * c.kv * 2, grid = (warps + kQThreads / 32 - 1) / (kQThreads / 32);
+  const int64_t grid = ((int64_t)r.B * c.kv * 2 + kQThreads / 32 - 1) / (kQThreads / 32);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kQThreads);
@@ -305,9 +300,8 @@ cudaError_t launch_qcache_write_step(const QCacheView& c, const QRows& r, const 
 
 cudaError_t launch_qcache_read(const QCacheView& c, const QRows& r, void* k, void* v, int st, int64_t stride,
                                cudaStream_t s) {
-  const int span = (r.S + kQBlock - 2) / kQBlock + 1;
-  const int64_t warps = (int64_t)r.B * span * c.kv * 2, grid = (warps + kQThreads / 32 - 1) / (kQThreads / 32);
-  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  const int span = q_span(r.S);
+  const int64_t grid = ((int64_t)r.B * span * c.kv * 2 + kQThreads / 32 - 1) / (kQThreads / 32);
   return with_shape(c.hd, st, [&](auto hd, auto t) {
     qcache_read_kernel<hd.value, t.value><<<(unsigned)grid, kQThreads, 0, s>>>(c, r, k, v, stride, span);
     return cudaGetLastError();

@@ -113,8 +113,12 @@ LLM_D float q_scale(float amax) {
 // 1 / s for a power of two s in 2^-126 .. 2^120
 LLM_D float q_recip(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
+// blocks that S tokens can touch
+LLM_HD int q_span(int S) { return (S - 1 + kQBlock - 1) / kQBlock + 1; }
+
 // ---- launches -----------------------------------------------------------------------------
 bool qcache_head_supported(int hd);
+// (B * q_span(S) * kv * 2, the warps of a write or read, below 2^31: the callers check)
 // keys and values of a call's tokens into the cache: rows of `stride` elements, bf16 (st 1) or f32
 cudaError_t launch_qcache_write(const QCacheView& c, const QRows& r, const void* k, const void* v, int st,
                                 int64_t stride, cudaStream_t s);
