@@ -301,9 +301,10 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
     tmem_alloc(smem_u32(&s_tmem), X::TMEM);
     tmem_relinquish();
   }
-  grid_dep_wait();
   grid_dep_launch();
 
+  // (a step's state and tiles were written before its kernels: only queries and cache wait for the
+  // previous kernel, below)
   // this CTA's run: the token tiles' position tiles are counted lane by lane (contiguous stretches),
   // and the lane whose stretch holds the run's start finds its token tile
   const int nq = a.r.step ? (a.tiles ? a.tiles[1] : a.r.B) : a.r.B * a.nct;
@@ -355,6 +356,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   const uint32_t tmem = s_tmem;
   QaWalk w;
   w.begin(a, s_t, s_off, s_begin, s_end);
+  grid_dep_wait();
   bool ok = true;  // a wait that gave up: no further waits, but every loop and barrier is still walked
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (ok && !mbar_wait(bar, parity, kQaWaitCycles)) {

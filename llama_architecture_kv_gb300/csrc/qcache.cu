@@ -148,7 +148,6 @@ __global__ void __launch_bounds__(kQThreads)
 template <int HD, int ST>
 __global__ void __launch_bounds__(kQThreads)
     qcache_write_step_kernel(const QCacheView c, const QRows r, const void* k, const void* v) {
-  grid_dep_wait();
   grid_dep_launch();
   const uint32_t w = blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
   const int side = (int)(w & 1);
@@ -176,6 +175,7 @@ __global__ void __launch_bounds__(kQThreads)
   uint8_t* codes = (side ? c.v : c.k) + (head * c.cap + (size_t)blk * kQBlock) * HD;
   float* scale = (side ? c.vs : c.ks) + head * (c.cap / kQBlock) + blk;
   const int64_t stride = (int64_t)c.kv * HD;
+  grid_dep_wait();  // (the step's state was written before its kernels; the staged values were not)
   for (int i = 0; i < n;) {
     int r0, q0, len = 1;
     slot(e + i, r0, q0);
