@@ -37,9 +37,9 @@
 // Bound by HBM where a tile's columns are few and rows long, by the softmax warps' instructions from
 // about 16 columns on, by latencies where a CTA has only a few tiles (a segment costs about 4 us besides
 // its tiles: first loads, the groups' sums, the join).  GB300, f32 queries, heads of 128, groups of 4, 8
-// key/value heads: 8 rows of 32768 positions 88 us (538 MB: 6.1 TB/s, 90% of the copy rate); one row of
-// 131072 53 us (5.1 TB/s); 32 rows of up to 2100 31 us (108 MB: 3.5 TB/s); one row of 2048 10 us; five
-// tokens in each of 32 rows of 2048 60 us (20 columns).  bf16 queries, 8 tokens at 131072 positions (32
+// key/value heads: 8 rows of 32768 positions 86 us (538 MB: 6.2 TB/s, 92% of the copy rate); one row of
+// 131072 51 us (5.3 TB/s); 32 rows of up to 2100 30 us (108 MB: 3.6 TB/s); one row of 2048 9.3 us; five
+// tokens in each of 32 rows of 2048 59 us (20 columns).  bf16 queries, 8 tokens at 131072 positions (32
 // columns): 79 us (269 MB: 3.4 TB/s).
 #pragma once
 #include "attention.cuh"
@@ -68,8 +68,9 @@ struct QaShape {
   static constexpr int PB = kQaTile * N;           // weight pieces of one group
   static constexpr int TMEM = 4 * N <= 64 ? 64 : 4 * N <= 128 ? 128 : 4 * N <= 256 ? 256 : 512;  // columns
   // Up to 8 columns two CTAs per SM (16 rows of 5 tokens of one head of 64: 26 us against 39 us with
-  // one; 32 rows of one token of 4 heads of 128: 31 against 34), more in one CTA whose groups halve them
-  // (16 rows of 16 columns at 2048 positions: 30 us against 39 us as two CTAs of whole columns)
+  // one; 32 rows of one token of 4 heads of 128: 31 against 34; but one row of 131072: 55 against 54), more
+  // in one CTA whose groups halve them (16 rows of 16 columns at 2048 positions: 30 us against 39 us as two
+  // CTAs of whole columns)
   static constexpr int CTAS = C <= 8 ? 2 : 1;
   static constexpr int HV = C <= 8 ? 1 : 2;        // groups that share a tile's columns
   static constexpr int CT = C / HV;                // columns of a thread
