@@ -18,10 +18,10 @@
 // With the positions on the M side a tile costs 8 MMAs however few columns there are, and a thread
 // writes its position's pieces with one 16-byte store per 16 columns (B's N-major layout).
 //
-// Running maxima are lazy: a column's reference makes the first tile's largest weight 2^2 and moves only
-// when a weight exceeds 2^8 (then that one becomes 2^5), so the accumulators in tensor memory are hardly
-// ever rescaled and the pieces keep the range above and the precision below.  The values' block scales
-// ride on the weights, relative to the largest scale seen (also lazy).
+// Running maxima are lazy: a column's reference makes the first tile's largest weight 2^2 (bf16: 2^5) and
+// moves only when a weight exceeds 2^8 (then that one becomes 2^5), so the accumulators in tensor memory
+// are hardly ever rescaled and the pieces keep the range above and the precision below.  The values' block
+// scales ride on the weights, relative to the largest scale seen (also lazy).
 //
 // One CTA: a producer warp (a ring of tiles by TMA, their block scales by 4-byte asynchronous copies), a
 // warp that issues the MMAs, and 16 softmax warps per SM: two groups of four take the tiles of a segment
@@ -40,7 +40,7 @@
 // key/value heads: 8 rows of 32768 positions 86 us (538 MB: 6.2 TB/s, 92% of the copy rate); one row of
 // 131072 51 us (5.3 TB/s); 32 rows of up to 2100 30 us (108 MB: 3.6 TB/s); one row of 2048 9.3 us; five
 // tokens in each of 32 rows of 2048 59 us (20 columns).  bf16 queries, 8 tokens at 131072 positions (32
-// columns): 79 us (269 MB: 3.4 TB/s).
+// columns): 82 us (269 MB: 3.3 TB/s).
 #pragma once
 #include "attention.cuh"
 #include "qcache.cuh"
@@ -50,8 +50,12 @@ namespace llm {
 
 constexpr int kQaTile = 128;                       // positions per tile
 constexpr uint64_t kQaWaitCycles = 1000000000ull;  // about 0.5 s
-constexpr float kQaFirst = 2.0f;                   // log2 of the largest weight of a segment's first tile
-constexpr float kQaTop = 5.0f;                     // and of a later tile that moved a reference
+constexpr float kQaTop = 5.0f;                     // log2 of the largest weight of a tile that moved a reference
+// and of a segment's first tile.  The last digit of a weight's pieces is 2^-24 (f32) or 2^-14 (bf16), so
+// where one position outweighs a long tail f32 can start low, and its references hardly ever move (32
+// columns, f32: 60 us against 62 us with 2^5); bf16 starts high, at 2^-20 of the largest weight instead of
+// 2^-17 (one row, 8 tokens, 131072 positions: 82 us against 79).
+template <int QT> constexpr float kQaFirst = QT ? 5.0f : 2.0f;
 constexpr float kQaMost = 8.0f;                    // the largest weight that moves none
 constexpr int kQaNear = 4;                         // most tiles by which a cut moves to a unit's end
 constexpr float kQaNone = -3.0e38f;                // a reference before any score
@@ -628,7 +632,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
           group_sync();
           if (gtid < CT) {
             const float old = ref[gtid];
-            const float top = fmaxf(old, fmaxf(fmaxf(wm[gtid], wm[C + gtid]), fmaxf(wm[2 * C + gtid], wm[3 * C + gtid])) - (t > gp ? kQaTop : kQaFirst));
+            const float top = fmaxf(old, fmaxf(fmaxf(wm[gtid], wm[C + gtid]), fmaxf(wm[2 * C + gtid], wm[3 * C + gtid])) - (t > gp ? kQaTop : kQaFirst<QT>));
             ref[gtid] = top;
             wm[gtid] = top == old ? 1.f : qa_exp2(old - top);
           }

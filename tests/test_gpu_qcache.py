@@ -1,6 +1,8 @@
 """The 8-bit key/value cache on the GPU (llm_qcache_write / read / attend) against the 64-bit definitions
 of tests/qcache_ref.py.  Codes, scales and read values must be equal; attention is held to a bound
 derived from its roundings (attend_tolerance)."""
+import math
+
 import numpy as np
 import pytest
 
@@ -337,6 +339,41 @@ def test_attend_value_scales_far_apart():
     r.write(kn, vn, [0])
     for length in ([n], [48], [177]):
         check_attend(c, r, rng, 1, 3, 4, "f32", length)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_heavy_position_and_a_long_flat_tail(dtype):
+    # position 0 weighs 2^15 to 2^19 times one of the 4095 others, which share a score and have values of
+    # one sign: whatever is lost of their weights adds up.  320 (row, kv head) pairs of 32 tiles keep a
+    # CTA on one of them for most of its tiles.
+    B, kv, g, hd, n = 40, 8, 4, 64, 4096
+    c = pkg.QCache.empty(B, kv, n, hd)
+    gen = torch.Generator(device="cuda").manual_seed(15)
+    k = torch.zeros(B, n, kv, hd, device="cuda")
+    k[..., 0] = 1.0
+    k[:, 0, :, 0] = 2.0
+    v = 0.5 + 0.5 * torch.rand(B, n, kv, hd, device="cuda", generator=gen)
+    c.write(k, v, i32([0] * B), stream=stream())
+    q = torch.zeros(B, 1, kv * g, hd, device="cuda")
+    q[..., 0] = 15.0 + 4.0 * torch.rand(B, 1, kv * g, device="cuda", generator=gen)
+    q = (q * math.log(2.0) * hd ** 0.5).to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    out = torch.empty_like(q)
+    c.attend(q, i32([n] * B), out, c.workspace(g, B, 1), stream=stream())
+    c.read(i32([0] * B), k, v, stream=stream())
+    for b in range(0, B, 13):
+        x = q[b, 0].double().reshape(kv, g, hd)
+        kd, vd = k[b].double().transpose(0, 1), v[b].double().transpose(0, 1)   # [kv][n][hd]
+        w = torch.softmax(hd ** -0.5 * x @ kd.transpose(1, 2), -1)
+        want = (w @ vd).cpu().numpy()
+        top = w.amax(-1, keepdim=True).cpu().numpy()
+        sens = (hd ** -0.5 * x.abs().amax(-1, keepdim=True) * kd.abs().sum(-1).max()).cpu().numpy()
+        # as attend_tolerance (all values are positive: mag is the result), but for the weights' last
+        # digit: 2^-27 (bf16 2^-20) of the largest weight, times values of up to 2 under their scale, n times
+        ds = sens * (2.0 ** -19 + (hd + 32) * 2.0 ** -24)
+        last, digits, half = (2.0 ** -27, 2.0 ** -16, 0.0) if dtype == "f32" else (2.0 ** -20, 2.0 ** -8, 2.0 ** -8)
+        tol = want * (2.2 * ds + digits + 2.0 ** -20 + half) + 2 * n * top * last
+        err = np.abs(out[b, 0].double().reshape(kv, g, hd).cpu().numpy() - want)
+        assert (err <= tol).all(), f"worst {float((err / tol).max()):.3g} of the tolerance"
 
 
 def test_nan_reaches_only_the_tokens_that_see_it():
