@@ -376,6 +376,73 @@ def test_a_heavy_position_and_a_long_flat_tail(dtype):
         assert (err <= tol).all(), f"worst {float((err / tol).max()):.3g} of the tolerance"
 
 
+@pytest.mark.parametrize("hd,kv,g", [(128, 2, 4), (256, 2, 2)])
+def test_pages_beyond_32_bit_offsets(hd, kv, g):
+    # codes of 8.6 GB each, written and attended to through pages at both ends; the reference holds those alone
+    rng = np.random.default_rng(22)
+    per = (1 << 33) // (kv * hd * 64) + 1
+    c = pkg.QCache.empty(1, kv, per * 64, hd)
+    r = ref.RefCache(1, kv, 6 * 64, hd)
+    far = np.array([[per - 1, 0, per - 2], [1, per - 3, per // 2 + 1]], np.int32)
+    near = np.arange(6, dtype=np.int32).reshape(2, 3)
+    k, kn = rows_of(rng, (2, 150, kv, hd), "f32")
+    v, vn = rows_of(rng, (2, 150, kv, hd), "f32")
+    c.write(k, v, i32([0, 7]), table=i32(far), stream=stream())
+    r.write(kn, vn, [0, 7], None, near)
+    kb, vb = torch.empty_like(k), torch.empty_like(v)
+    c.read(i32([0, 7]), kb, vb, table=i32(far), stream=stream())
+    for b, n in ((0, 0), (1, 7)):
+        kk, vv = r.values(near, b, 150, n)
+        assert np.array_equal(kb[b].double().cpu().numpy(), kk.transpose(1, 0, 2))
+        assert np.array_equal(vb[b].double().cpu().numpy(), vv.transpose(1, 0, 2))
+    for dtype in ("f32", "bf16"):
+        q, qn = rows_of(rng, (2, 3, kv * g, hd), dtype)
+        out = torch.empty_like(q)
+        c.attend(q, i32([150, 157]), out, c.workspace(g, 2, 3), table=i32(far), stream=stream())
+        want, mag, sens, flat = r.attend(qn, [150, 157], table=near)
+        assert (np.abs(out.double().cpu().numpy() - want) <= attend_tolerance(dtype, hd, want, mag, sens, flat)).all()
+
+
+def test_one_row_of_more_than_2_to_the_25_positions():
+    # zeros but for the last 16 positions, which weigh about as much as all the others together
+    rng = np.random.default_rng(23)
+    hd, g, n = 128, 4, (1 << 25) + 1000
+    c = pkg.QCache.empty(1, 1, (n + 15) // 16 * 16, hd)
+    v, vn = rows_of(rng, (1, 16, 1, hd), "f32")
+    k = torch.ones(1, 16, 1, hd, device="cuda")
+    c.write(k, v, i32([n - 16]), stream=stream())
+    c.read(i32([n - 16]), k, v, stream=stream())
+    q = torch.full((1, 1, g, hd), 15.0 / hd ** 0.5, device="cuda")
+    out = torch.empty_like(q)
+    c.attend(q, i32([n]), out, c.workspace(g, 1, 1), stream=stream())
+    s = hd ** -0.5 * float(q[0, 0, 0].double().sum())
+    vd = v[0, :, 0].double().cpu().numpy()
+    total = n - 16 + 16 * math.exp(s)
+    want, mag = math.exp(s) * vd.sum(0) / total, math.exp(s) * np.abs(vd).sum(0) / total
+    # zero values lose nothing with their weights, so 16 positions count for flat; a lane adds up at most
+    # 2^9 weights of a CTA's tiles in f32, each addition off by half a step
+    tol = attend_tolerance("f32", hd, want, mag, s, np.abs(vd).max() * 16 * math.exp(s) / total) + mag * 2.0 ** -15
+    assert (np.abs(out[0, 0].double().cpu().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("hd", [32, 64, 128])
+def test_calls_without_any_visible_position(hd):
+    kv, g, B = 2, 4, 3
+    c, r = make(B, kv, 64, hd, garbage=2)
+    ws = c.workspace(g, B, 2)
+    q = torch.ones(B, 2, kv * g, hd, device="cuda")
+    for length, count, want in (([0] * B, None, 0.0), ([0] * B, [0] * B, 9.0), ([40, 64, 1], [0] * B, 9.0)):
+        out = torch.full_like(q, 9.0)
+        c.attend(q, i32(length), out, ws, count=None if count is None else i32(count), stream=stream())
+        assert (out == want).all()
+    x = torch.ones(B, 2, kv, hd, device="cuda")
+    c.write(x, x, i32([0, 63, 64]), count=i32([0] * B), stream=stream())   # nothing to write, anywhere
+    same(c, r)
+    rng = np.random.default_rng(24)                                        # the workspace is as it was
+    fill(c, r, rng, 64)
+    check_attend(c, r, rng, B, 2, g, "f32", [64, 1, 33], ws=ws)
+
+
 def test_nan_reaches_only_the_tokens_that_see_it():
     rng = np.random.default_rng(14)
     for hd, g in ((128, 4), (64, 1), (32, 2)):
