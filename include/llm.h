@@ -341,7 +341,8 @@ llm_status llm_debug_trace(llm_handle* h, int32_t layer, const char* name, float
 /*
  * Measurement hook: the mean duration of `reps` back-to-back launches of one kernel of the
  * decode step, timed alone with CUDA events on the handle's stream.  which: 0 Q/K/V projection
- * (with norm, RoPE and cache write), 1 attention, 2 o_proj + residual, 3 norm + gate/up +
+ * (with norm, RoPE and cache write), 1 attention (heads of 64 and 128 over an 8-bit cache: with
+ * the cache write), 2 o_proj + residual, 3 norm + gate/up +
  * SwiGLU, 4 down + residual, 5 final norm + LM head, 6 sampler.  Launch r uses layer r % layers,
  * so consecutive launches stream different weights from HBM.  B rows at position pos (pos <=
  * filled length; the cache entry at pos is rewritten).  *ms_per_launch receives the mean.

@@ -573,6 +573,9 @@ QRows q8_rows(const llm_handle* h, int B) {
   r.B = B; r.S = 1; r.limit = h->qcap; r.step = h->st; r.status = h->status;
   return r;
 }
+// whether a step's attention stores the staged keys and values itself: a prefill pass, whose tokens share
+// blocks, and the other head sizes take a kernel for it
+bool q8_fused(const llm_handle* h) { return qattn_uses_tc(h->hd) && !h->capturing_pass; }
 // the staged keys and values of a step into layer l
 llm_status q8_store(llm_handle* h, int l, int B, bool pdl) {
   CUDA_TRY(h, launch_qcache_write_step(q8_view(h, l), q8_rows(h, B), h->stage_k, h->stage_v, h->wt, h->stream, pdl));
@@ -646,7 +649,7 @@ llm_status launch_one(llm_handle* h, int which, int l, int B, bool pdl) {
       qa.H = h->H; qa.kv = c.kv_heads; qa.hd = h->hd; qa.cap = h->q8 ? 1 : c.max_seq; qa.staged = h->q8;
       qa.rope_cos = h->rope_cos; qa.rope_sin = h->rope_sin; qa.step = h->st;
       CUDA_TRY(h, launch_tc_qkv(qa, h->stream, pdl));
-      return h->q8 ? q8_store(h, l, B, pdl) : LLM_OK;
+      return h->q8 && !q8_fused(h) ? q8_store(h, l, B, pdl) : LLM_OK;
     }
     if (which == K_O) {
       in.x = h->attn; in.x_stride = h->d;
@@ -681,13 +684,16 @@ llm_status launch_one(llm_handle* h, int which, int l, int B, bool pdl) {
     a.tr_in = tr_slot(h, l, TR_N1); a.tr_pre = tr_slot(h, l, TR_QKV); a.tr_rot = tr_slot(h, l, TR_KR);
     a.tr_stride = (int32_t)h->trace_w;
     CUDA_TRY(h, launch_gemv(a, p, wt, EPI_QKV, true, h->stream, pdl));
-    if (h->q8) return q8_store(h, l, B, pdl);
+    if (h->q8 && !q8_fused(h)) return q8_store(h, l, B, pdl);
   } else if (which == K_ATTN && h->q8) {
     QAttnArgs qa = {};
     qa.c = q8_view(h, l); qa.r = q8_rows(h, B);
     qa.q = h->q; qa.out = h->attn; qa.q_stride = qa.out_stride = h->d; qa.g = c.group;
     qa.scale = 1.0f / sqrtf((float)h->hd); qa.ws = h->qws;
     qa.tiles = h->capturing_pass && h->q_tiles ? h->tile_buf : nullptr;
+    if (q8_fused(h)) {
+      qa.new_k = h->stage_k; qa.new_v = h->stage_v; qa.new_t = h->wt;
+    }
     qa.krow0 = (int32_t)((size_t)l * c.max_batch * c.kv_heads * h->qcap);
     CUDA_TRY(h, launch_qattn(qa, 0, h->num_sms, h->stream, pdl, &h->kmap, &h->vmap));
   } else if (which == K_ATTN && h->capturing_pass && h->pf_attn) {
@@ -1099,6 +1105,8 @@ llm_status llm_create(const llm_config* cfg, const void* weights, uint64_t nbyte
         cudaMemsetAsync(h->qv, 0, cache_rows * h->hd, h->stream) != cudaSuccess ||
         cudaMemsetAsync(h->qks, 0, scale_bytes, h->stream) != cudaSuccess ||
         cudaMemsetAsync(h->qvs, 0, scale_bytes, h->stream) != cudaSuccess ||
+        cudaMemsetAsync(h->stage_k, 0, stage, h->stream) != cudaSuccess ||
+        cudaMemsetAsync(h->stage_v, 0, stage, h->stream) != cudaSuccess ||
         cudaMemsetAsync(h->qws, 0, ws, h->stream) != cudaSuccess)
       return cuda_bail("clearing the cache", cudaGetLastError());
   } else if ((st = dalloc(h, &h->kc, cache_bytes)) || (st = dalloc(h, &h->vc, cache_bytes))) {

@@ -1,4 +1,4 @@
-// Writing into and reading from an 8-bit key/value cache, and its attention on CUDA cores.
+// Writing into and reading from an 8-bit key/value cache.
 //
 // A block is kQBlock consecutive positions of one cache row and key/value head.  Its scale s is a
 // power of two, so dividing by it, multiplying by it and moving a code from one scale to another
@@ -22,9 +22,9 @@
 // (16 independent 16-byte loads a lane at hd 128, f32), reduced in registers and stored as codes, so
 // each value is read once and the maximum costs no second pass.  Reading mirrors it, every store of a
 // warp one contiguous run.  GB300, copy rate 6.79 TB/s: 32 rows of one token (8 heads of 128) written in
-// 2.7 us; 16 rows of up to 2048 bf16 tokens (174 MB in and out) in 30.7 us, 84% of the copy rate, with the
+// 2.6 us; 16 rows of up to 2048 bf16 tokens (174 MB in and out) in 30.3 us, 85% of the copy rate, with the
 // values packed as read (widened to f32 in registers: 46 us, half the warps in flight); 32 such rows read
-// back (315 MB) in 48.5 us, 96% (rounding to bf16 in integer steps instead of one conversion per pair:
+// back (315 MB) in 48.8 us, 95% (rounding to bf16 in integer steps instead of one conversion per pair:
 // 77 us).
 #include <algorithm>
 #include <type_traits>
@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(kQThreads)
                        ((int64_t)b * r.S + (lo - p0)) * stride + (int64_t)h * HD, stride);
 }
 
-// Rows of a handle's step: warp (entry, kv head, keys or values); staged values [B][kv][HD].  A
+// Rows of a handle's step (heads of 64 and 128: only a prefill pass's entries; their decode steps store
+// within the attention): warp (entry, kv head, keys or values); staged values [B][kv][HD].  A
 // prefill pass lists the entries of a cache row in position order, so the entries of one block
 // follow one another: the first of them (the leader) writes all, run by run of consecutive
 // positions, and the others' warps leave.

@@ -141,6 +141,10 @@ struct QAttnArgs {
   unsigned char* ws;      // workspace (qattn_workspace bytes): tickets zero between calls, then partials
   const int32_t* tiles;   // a prefill pass's tiles (attention.cuh), of at most qattn_tile_tokens(g) tokens, or null
   int32_t krow0;          // row of the cache's position 0 of (row 0, kv head 0) in the tensor maps (step calls)
+  // a decode step's keys and values [B][kv][hd] of type new_t (0 f32, 1 bf16), which the attention itself
+  // quantises into the cache (tensor cores only); null where they are there already
+  const void *new_k, *new_v;
+  int32_t new_t;
   // set by launch_qattn: parts of a token's positions (CUDA cores), or tokens per tile and tiles per row
   int32_t splits, tpt, nct;
 };

@@ -18,7 +18,7 @@
 // memory behind one cluster barrier, and the warp whose stretch holds the draw reads it again from L2 in
 // two rounds (in rounds of 32 ids it took 11 us).  Loads of one id per lane do for rows of any alignment
 // (16-byte loads of aligned rows measured the same), and short loops: unrolled 16 times the sum was
-// slower, waiting for its own instructions.  GB300: 5.7 us for one row of 49152 ids, 14.8 us for 32 rows
+// slower, waiting for its own instructions.  GB300: 5.9 us for one row of 49152 ids, 15.1 us for 32 rows
 // of 128256 with q (33 MB: 2.2 TB/s; the chain and the launch are 6 us of it).
 #include "verify.cuh"
 

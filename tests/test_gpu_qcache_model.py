@@ -71,6 +71,38 @@ def test_steps_store_the_quantised_keys_and_values(name, shape, B, tc):
 
 
 @pytest.mark.parametrize("name,shape,B,tc", SHAPES, ids=[s[0] for s in SHAPES])
+def test_steps_of_rows_at_their_own_positions_store_across_block_and_tile_edges(name, shape, B, tc):
+    # rows around position 128, the first of a block and of a tile among theirs
+    P, steps, cap = 131, 14, 192
+    toks = synth.tokens(712, 0, B * (P + steps), shape.vocab).reshape(B, P + steps)
+    first = np.array([P - 5 * (b % 3) for b in range(B)])
+    plain, q8 = make(shape, 711, B, cap, tc_min_batch=tc), make(shape, 711, B, cap, tc_min_batch=tc, cache_type=E4M3)
+    logits, prompt = [], {}
+    for g in (plain, q8):
+        g.prefill(toks[:, :P], 0, logits=False)
+        prompt = prompt or {b: g.kv_export(0, b, 0, P) for b in {0, 1, B - 1}}
+        for s in range(steps):
+            lg = g.decode_rows(np.ascontiguousarray(toks[np.arange(B), first + s]), first + s)
+        logits.append(lg)
+    for b, (k0, v0) in prompt.items():
+        n = int(first[b]) + steps
+        k, v = plain.kv_export(0, b, 0, n)
+        k0, v0, kk, vv = (wide(x).swapaxes(0, 1)[None] for x in (k0, v0, k, v))
+        want = ref.RefCache(1, shape.kv, cap, shape.hd)
+        want.write(k0, v0, [0])               # (the steps rewrite its tokens from first[b] on)
+        for p in range(int(first[b]), n):
+            want.write(kk[:, p:p + 1], vv[:, p:p + 1], [p])
+        wk, wv = want.values(None, 0, n)
+        gk, gv = q8.kv_export(0, b, 0, n)
+        assert np.array_equal(wide(gk), wk) and np.array_equal(wide(gv), wv)
+    # a step's graph replayed: the same bits
+    again = q8.decode_rows(np.ascontiguousarray(toks[np.arange(B), first + steps - 1]), first + steps - 1)
+    assert np.array_equal(again, logits[1])
+    plain.close()
+    q8.close()
+
+
+@pytest.mark.parametrize("name,shape,B,tc", SHAPES, ids=[s[0] for s in SHAPES])
 def test_attention_of_every_layer_is_that_over_the_values_read_back(name, shape, B, tc):
     n, cap = 150, 192
     toks = synth.tokens(712, 0, B * n, shape.vocab).reshape(B, n)
