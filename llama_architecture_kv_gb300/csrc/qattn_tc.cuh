@@ -437,7 +437,9 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
       const float* sc = lane < 8 ? a.c.ks : a.c.vs;
 #pragma unroll 1
       for (int k = w.k0; k < w.k1; ++k, ++it) {
-        if (a.new_k && k == w.u.nt - 1) qa_store_new<HD>(a, w.u.b, w.j);
+        if constexpr (QT == 0) {  // (a handle's queries are f32)
+          if (a.new_k && k == w.u.nt - 1) qa_store_new<HD>(a, w.u.b, w.j);
+        }
         // the place of this lane's block, and with it of its half of the tile (pages hold 64 positions)
         const int p0 = (w.u.tile0 + k) * kQaTile, pos = p0 + kQBlock * blk;
         int row = 0, pp = 0;
