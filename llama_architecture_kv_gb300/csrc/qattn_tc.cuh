@@ -40,7 +40,7 @@
 // key/value heads: 8 rows of 32768 positions 86 us (538 MB: 6.2 TB/s, 92% of the copy rate); one row of
 // 131072 51 us (5.3 TB/s); 32 rows of up to 2100 30 us (108 MB: 3.6 TB/s); one row of 2048 9.3 us; five
 // tokens in each of 32 rows of 2048 59 us (20 columns).  bf16 queries, 8 tokens at 131072 positions (32
-// columns): 82 us (269 MB: 3.3 TB/s).
+// columns): 81 us (269 MB: 3.3 TB/s).
 #pragma once
 #include "attention.cuh"
 #include "qcache.cuh"
