@@ -1100,14 +1100,14 @@ llm_status llm_create(const llm_config* cfg, const void* weights, uint64_t nbyte
         (st = dalloc(h, &h->stage_k, stage)) || (st = dalloc(h, &h->stage_v, stage)))
       return bail(st);
     const size_t ws = qattn_step_workspace(q8_view(h, 0), c.group, h->NT, h->num_sms);
-    if ((st = dalloc(h, &h->qws, ws))) return bail(st);
+    if (ws > 0 && (st = dalloc(h, &h->qws, ws))) return bail(st);
     if (cudaMemsetAsync(h->qk, 0, cache_rows * h->hd, h->stream) != cudaSuccess ||
         cudaMemsetAsync(h->qv, 0, cache_rows * h->hd, h->stream) != cudaSuccess ||
         cudaMemsetAsync(h->qks, 0, scale_bytes, h->stream) != cudaSuccess ||
         cudaMemsetAsync(h->qvs, 0, scale_bytes, h->stream) != cudaSuccess ||
         cudaMemsetAsync(h->stage_k, 0, stage, h->stream) != cudaSuccess ||
         cudaMemsetAsync(h->stage_v, 0, stage, h->stream) != cudaSuccess ||
-        cudaMemsetAsync(h->qws, 0, ws, h->stream) != cudaSuccess)
+        (ws > 0 && cudaMemsetAsync(h->qws, 0, ws, h->stream) != cudaSuccess))
       return cuda_bail("clearing the cache", cudaGetLastError());
   } else if ((st = dalloc(h, &h->kc, cache_bytes)) || (st = dalloc(h, &h->vc, cache_bytes))) {
     return bail(st);
@@ -1242,7 +1242,8 @@ llm_status llm_synchronize(llm_handle* h) {
     // a kernel that gave up may have left the attention's merge tickets short of their count
     if (s == LLM_ERR_DEVICE_TIMEOUT) {
       CUDA_TRY(h, cudaMemset(h->ticket, 0, (size_t)h->ticket_count * 4));
-      if (h->qws) CUDA_TRY(h, cudaMemset(h->qws, 0, kQattnTickets));
+      // (only the tensor-core kernel has tickets: the others' workspace may be smaller than they are)
+      if (h->q_tiles) CUDA_TRY(h, cudaMemset(h->qws, 0, kQattnTickets));
       if (h->mega_ticket) CUDA_TRY(h, cudaMemset(h->mega_ticket, 0, ((size_t)h->cfg.kv_heads + 1) * 4));
     }
     return fail(h, s, "device reported: %s", llm_status_string(s));
