@@ -361,7 +361,6 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
     tmem_alloc(smem_u32(&s_tmem), X::TMEM);
     tmem_relinquish();
   }
-  grid_dep_launch();
 
   // (a step's state and tiles were written before its kernels: only queries and cache wait for the
   // previous kernel, below)
@@ -413,6 +412,9 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // (only now: a later kernel's CTA on this SM could take the tensor memory first, and wait for this kernel
+  // while this kernel waits for the tensor memory)
+  grid_dep_launch();
   const uint32_t tmem = s_tmem;
   QaWalk w;
   w.begin(a, s_t, s_off, s_begin, s_end);
