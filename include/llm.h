@@ -95,7 +95,11 @@ typedef struct llm_config {
                            position that is not a multiple of 16 ends what its block of 16 held after
                            it: with llm_decode_paged, write a page's positions in order; llm_kv_import
                            and llm_prefill_packed refuse to end inside a block whose later positions
-                           are filled and not written by the call (LLM_ERR_POS_RANGE) */
+                           are filled and not written by the call (LLM_ERR_POS_RANGE), and where they
+                           start inside a block whose earlier positions are neither filled nor written
+                           by the call, the block counts as empty.  A rewind into a block keeps the
+                           scale that the dropped positions gave it until its first position is
+                           written again */
 } llm_config;
 
 typedef struct llm_handle llm_handle;

@@ -573,6 +573,12 @@ QRows q8_rows(const llm_handle* h, int B) {
   r.B = B; r.S = 1; r.limit = h->qcap; r.step = h->st; r.status = h->status;
   return r;
 }
+// a call starts to write behind the first position of a block of `row` that holds nothing live: what the
+// block held in an earlier sequence must not count (its scale would stay, or its NaN)
+llm_status q8_open_block(llm_handle* h, int row, int pos) {
+  CUDA_TRY(h, launch_qcache_clear(q8_view(h, 0), h->L, row, pos / kQBlock, h->stream));
+  return LLM_OK;
+}
 // whether a step's attention stores the staged keys and values itself: a prefill pass, whose tokens share
 // blocks, and the other head sizes take a kernel for it
 bool q8_fused(const llm_handle* h) { return qattn_uses_tc(h->hd) && !h->capturing_pass; }
@@ -1606,6 +1612,16 @@ static llm_status packed_impl(llm_handle* h, const int32_t* toks, const int32_t*
           return fail(h, LLM_ERR_POS_RANGE, "prompt %d ends inside a block of an 8-bit cache: position %d of row %d is filled",
                       a.first, p, a.second.row);
       }
+    // a prompt that starts inside a block whose earlier positions are neither filled nor written by this
+    // call finds the block empty
+    for (auto& a : span) {
+      bool live = a.second.lo % kQBlock == 0;
+      for (int p = a.second.lo / kQBlock * kQBlock; p < a.second.lo && !live; ++p) {
+        live = p < h->filled[a.second.row];
+        for (auto& b : span) live = live || (b.second.row == a.second.row && b.second.lo <= p && p <= b.second.hi);
+      }
+      if (!live) TRY(q8_open_block(h, a.second.row, a.second.lo));
+    }
   }
   // position order, then passes of at most NT entries
   std::vector<int> order(P);
@@ -1875,6 +1891,8 @@ static llm_status kv_copy(llm_handle* h, int32_t layer, int32_t row, int32_t pos
     if (import && n > 0 && (pos0 + n) % kQBlock != 0 && h->filled[row] > pos0 + n)
       return fail(h, LLM_ERR_POS_RANGE, "import ends at %d, inside a filled block of an 8-bit cache (row %d holds %d)", pos0 + n,
                   row, h->filled[row]);
+    if (import && n > 0 && pos0 % kQBlock != 0 && h->filled[row] <= pos0 / kQBlock * kQBlock)
+      TRY(q8_open_block(h, row, pos0));  // (in every layer: those imported next find the row filled)
     // through the staging buffers, whole blocks at a time: the cache row as a cache of one row
     QCacheView c = q8_view(h, layer);
     c.k += (size_t)row * kv * h->qcap * hd; c.v += (size_t)row * kv * h->qcap * hd;

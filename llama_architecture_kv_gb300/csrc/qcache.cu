@@ -251,6 +251,18 @@ __global__ void __launch_bounds__(kQThreads)
   }
 }
 
+// a thread per (layer, kv head): the scales of one block of a cache row to 0, so that nothing of what the
+// block held counts for a write that starts behind its first position
+__global__ void __launch_bounds__(kQThreads)
+    qcache_clear_kernel(float* ks, float* vs, int n, int rows, int kv, int blocks, int row, int blk) {
+  const int i = blockIdx.x * kQThreads + threadIdx.x;
+  if (i >= n) return;
+  const int l = i / kv, j = i - l * kv;
+  const size_t at = (((size_t)l * rows + row) * kv + j) * blocks + blk;
+  ks[at] = 0.f;
+  vs[at] = 0.f;
+}
+
 // calls f with the head size and the element type as compile-time numbers
 template <class F>
 cudaError_t with_shape(int hd, int st, F f) {
@@ -280,6 +292,13 @@ cudaError_t launch_qcache_write(const QCacheView& c, const QRows& r, const void*
     qcache_write_kernel<hd.value, t.value><<<(unsigned)grid, kQThreads, 0, s>>>(c, r, k, v, stride, span);
     return cudaGetLastError();
   });
+}
+
+cudaError_t launch_qcache_clear(const QCacheView& c, int layers, int row, int blk, cudaStream_t s) {
+  const int n = layers * c.kv;
+  qcache_clear_kernel<<<(n + kQThreads - 1) / kQThreads, kQThreads, 0, s>>>(c.ks, c.vs, n, c.rows, c.kv,
+                                                                            c.cap / kQBlock, row, blk);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_qcache_write_step(const QCacheView& c, const QRows& r, const void* k, const void* v, int st,

@@ -125,6 +125,8 @@ cudaError_t launch_qcache_write(const QCacheView& c, const QRows& r, const void*
 // the same for the rows of a handle's step, or the entries of a prefill pass: staged [B][kv][hd]
 cudaError_t launch_qcache_write_step(const QCacheView& c, const QRows& r, const void* k, const void* v, int st,
                                      cudaStream_t s, bool pdl);
+// the scales of block blk of cache row `row` to 0 in `layers` caches that follow one another, c the first
+cudaError_t launch_qcache_clear(const QCacheView& c, int layers, int row, int blk, cudaStream_t s);
 cudaError_t launch_qcache_read(const QCacheView& c, const QRows& r, void* k, void* v, int st, int64_t stride,
                                cudaStream_t s);
 

@@ -7,7 +7,7 @@ import llama_architecture_kv_gb300 as pkg
 import synth
 from synth import shrink
 from synth.configs import TINY
-from tests.test_gpu_qcache_model import E4M3, make
+from tests.test_gpu_qcache_model import E4M3, SHAPES, make
 
 pytestmark = pytest.mark.gpu
 
@@ -31,4 +31,62 @@ def test_a_wait_that_ran_out_leaves_the_handle_as_it_was(half, cap):
     g.synchronize()                            # reported once, then cleared
     assert np.array_equal(bits(g.decode(toks[9:10], 9)), bits(step))
     assert np.array_equal(bits(g.prefill(toks[None, :9], 0)), bits(first))
+    g.close()
+
+
+def sick(rng, shape, n, how):
+    """Cache elements [kv][n][hd] of an earlier sequence: large, or not finite."""
+    x = (rng.standard_normal((shape.kv, n, shape.hd)) * 2.0 ** 12).astype(np.float32)
+    if how == "nan":
+        x[:, ::3, 1] = np.nan
+    return (x.view(np.uint32) >> 16).astype(np.uint16) if shape.bf16 else x
+
+
+@pytest.mark.parametrize("how", ["large", "nan"])
+@pytest.mark.parametrize("reset", [True, False], ids=["reset", "rewound"])
+@pytest.mark.parametrize("name,shape,B,tc", SHAPES, ids=[s[0] for s in SHAPES])
+def test_dead_data_decides_nothing_for_prompts_and_imports_that_start_inside_blocks(name, shape, B, tc, reset, how):
+    cap, rng = 192, np.random.default_rng(812)
+    t0, t1, t2, t3 = (synth.tokens(813 + i, 0, m, shape.vocab) for i, m in enumerate((10, 13, 20, 3)))
+    got = []
+    for old in (True, False):
+        g = make(shape, 811, 2, cap, tc_min_batch=tc, cache_type=E4M3)
+        if old:
+            for layer in range(shape.layers):
+                for row in range(2):
+                    g.kv_import(layer, row, 0, sick(rng, shape, 150, how), sick(rng, shape, 150, how))
+        if reset:
+            pkg.llm_reset(g.h)
+        # (without a reset: row 0 rewound to nothing kept but its first 10 positions, row 1 too)
+        g.prefill(np.stack([t0, t0]), 0, logits=False)
+        # row 0: 37..49 in a block of dead positions; row 1: 52..54, then 55..74 of another prompt in the same block
+        lg = g.prefill_packed(np.concatenate([t1, t3, t2]), [0] * 13 + [1] * 23, list(range(37, 50)) + list(range(52, 75)),
+                              [1] * 13 + [2] * 3 + [3] * 20, [12, 15, 35])
+        out = [bits(lg)]
+        k, v = sick(np.random.default_rng(5), shape, 9, "large"), sick(np.random.default_rng(6), shape, 9, "large")
+        for layer in range(shape.layers):
+            out += [g.kv_export(layer, 0, 37, 13), g.kv_export(layer, 1, 52, 23)]
+        for layer in range(shape.layers):
+            g.kv_import(layer, 0, 133, k, v)   # positions 128 .. 132 are dead
+            out.append(g.kv_export(layer, 0, 133, 9))
+        got.append(out)
+        g.close()
+    for a, b in zip(*got):
+        assert all(np.array_equal(x, y, equal_nan=np.asarray(x).dtype == np.float32) for x, y in zip(a, b))
+
+
+def test_dead_data_of_the_block_is_kept_where_it_is_live():
+    # a prompt that starts right behind filled positions keeps what they hold
+    name, shape, B, tc = SHAPES[2]
+    g = make(shape, 821, 2, 128, tc_min_batch=tc, cache_type=E4M3)
+    t = synth.tokens(822, 0, 60, shape.vocab)
+    g.prefill(np.stack([t[:37], t[:37]]), 0, logits=False)
+    k0, v0 = g.kv_export(0, 0, 0, 37)
+    g.prefill_packed(t[37:40], [0] * 3, [37, 38, 39], [1] * 3, [2])
+    k1, v1 = g.kv_export(0, 0, 0, 37)
+    # codes are rounded again at most where the scale grew: by 2^-4 of a value at most, or a step of the block
+    for a, b in ((k0, k1), (v0, v1)):
+        a, b = ((x.astype(np.uint32) << 16).view(np.float32) for x in (a, b))
+        assert np.array_equal(a[:, :32], b[:, :32])
+        assert (np.abs(a - b) <= np.abs(a) * 2.0 ** -4 + np.abs(b).max() * 2.0 ** -14).all() and np.abs(b[:, 32:]).max() > 0
     g.close()
