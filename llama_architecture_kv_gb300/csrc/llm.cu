@@ -249,7 +249,8 @@ struct TcMaps {
 
 struct GraphKey {
   int B, mode, gen;  // gen: steps of a generation graph (0: one step after a host prologue)
-  int pass;          // 1: a prefill pass (its rows are prompt tokens with attention ranges)
+  int pass;          // 1: a prefill pass (its rows are prompt tokens with attention ranges); 1 + T: a
+                     // verification pass of T tokens per row on an 8-bit cache
   bool operator<(const GraphKey& o) const {
     return B != o.B ? B < o.B : mode != o.mode ? mode < o.mode : gen != o.gen ? gen < o.gen : pass < o.pass;
   }
@@ -287,6 +288,12 @@ struct llm_handle {
   float *qks = nullptr, *qvs = nullptr;           // scales [L][max_batch][kv][qcap / kQBlock]
   void *stage_k = nullptr, *stage_v = nullptr;    // [NT][kv][hd] keys and values of a step, in dtype
   unsigned char* qws = nullptr;                   // attention workspace
+  // verification passes (allocated by the first): the tokens' keys and values of every layer
+  // [L][NT][kv][hd], and the blocks that the rows' first tokens go into [L][max_batch][kv][kQBlock][hd]
+  void *vstage_k = nullptr, *vstage_v = nullptr;
+  uint8_t *kept_k = nullptr, *kept_v = nullptr;
+  float *kept_ks = nullptr, *kept_vs = nullptr;   // [L][max_batch][kv]
+  int capturing_verify = 0;                       // tokens per row of the verification pass being captured
   bool q_tiles = false;                           // prefill passes list tiles for the 8-bit attention
   float *rope_cos = nullptr, *rope_sin = nullptr;
   float *xa = nullptr, *xb = nullptr, *q = nullptr, *attn = nullptr, *m = nullptr, *logits = nullptr;
@@ -570,8 +577,21 @@ QCacheView q8_view(const llm_handle* h, int l) {
 }
 QRows q8_rows(const llm_handle* h, int B) {
   QRows r = {};
-  r.B = B; r.S = 1; r.limit = h->qcap; r.step = h->st; r.status = h->status;
+  r.B = B; r.S = 1; r.limit = h->qcap; r.step = h->st; r.status = h->status; r.entry_step = 1;
   return r;
+}
+// the rows of a verification pass of n entries, T tokens per row
+QVerify q8_verify(const llm_handle* h, int n, int T, const int32_t* accepted) {
+  QVerify v = {};
+  v.c = q8_view(h, 0); v.layers = h->L; v.T = T; v.r = q8_rows(h, n / T); v.r.entry_step = T;
+  v.kept_k = h->kept_k; v.kept_v = h->kept_v; v.kept_ks = h->kept_ks; v.kept_vs = h->kept_vs;
+  v.stage_k = h->vstage_k; v.stage_v = h->vstage_v; v.stage_rows = h->NT; v.accepted = accepted;
+  return v;
+}
+// where the Q/K/V kernels of layer l put a step's keys and values
+char* q8_stage(const llm_handle* h, int l, bool value) {
+  if (!h->capturing_verify) return (char*)(value ? h->stage_v : h->stage_k);
+  return (char*)(value ? h->vstage_v : h->vstage_k) + (size_t)l * h->NT * h->kvw * h->es;
 }
 // a call starts to write behind the first position of a block of `row` that holds nothing live: what the
 // block held in an earlier sequence must not count (its scale would stay, or its NaN)
@@ -581,10 +601,28 @@ llm_status q8_open_block(llm_handle* h, int row, int pos) {
 }
 // whether a step's attention stores the staged keys and values itself: a prefill pass, whose tokens share
 // blocks, and the other head sizes take a kernel for it
-bool q8_fused(const llm_handle* h) { return qattn_uses_tc(h->hd) && !h->capturing_pass; }
-// the staged keys and values of a step into layer l
-llm_status q8_store(llm_handle* h, int l, int B, bool pdl) {
-  CUDA_TRY(h, launch_qcache_write_step(q8_view(h, l), q8_rows(h, B), h->stage_k, h->stage_v, h->wt, h->stream, pdl));
+bool q8_fused(const llm_handle* h) { return qattn_uses_tc(h->hd) && (!h->capturing_pass || h->capturing_verify); }
+// the staged keys and values of a step's rows into layer l
+llm_status q8_store(llm_handle* h, int l, const QRows& r, bool pdl) {
+  CUDA_TRY(h, launch_qcache_write_step(q8_view(h, l), r, q8_stage(h, l, false), q8_stage(h, l, true), h->wt, h->stream, pdl));
+  return LLM_OK;
+}
+// whether the projection of a step's keys and values is followed by their write: the others write with, or (a
+// verification pass) between, their attention
+bool q8_stores_first(const llm_handle* h) { return h->q8 && !q8_fused(h) && !h->capturing_verify; }
+// the attention of a step's rows over layer l, storing their keys and values where it does
+llm_status q8_attend(llm_handle* h, int l, const QRows& r, bool pdl) {
+  const llm_config& c = h->cfg;
+  QAttnArgs qa = {};
+  qa.c = q8_view(h, l); qa.r = r;
+  qa.q = h->q; qa.out = h->attn; qa.q_stride = qa.out_stride = h->d; qa.g = c.group;
+  qa.scale = 1.0f / sqrtf((float)h->hd); qa.ws = h->qws;
+  qa.tiles = h->capturing_pass && h->q_tiles && !h->capturing_verify ? h->tile_buf : nullptr;
+  if (q8_fused(h)) {
+    qa.new_k = q8_stage(h, l, false); qa.new_v = q8_stage(h, l, true); qa.new_t = h->wt;
+  }
+  qa.krow0 = (int32_t)((size_t)l * c.max_batch * c.kv_heads * h->qcap);
+  CUDA_TRY(h, launch_qattn(qa, 0, h->num_sms, h->stream, pdl, &h->kmap, &h->vmap));
   return LLM_OK;
 }
 
@@ -633,8 +671,8 @@ llm_status launch_one(llm_handle* h, int which, int l, int B, bool pdl) {
     return LLM_OK;
   }
   const LayerW& w = h->lw[l];
-  char* kcl = h->q8 ? (char*)h->stage_k : (char*)h->kc + (size_t)l * h->layer_cache_elems * h->es;
-  char* vcl = h->q8 ? (char*)h->stage_v : (char*)h->vc + (size_t)l * h->layer_cache_elems * h->es;
+  char* kcl = h->q8 ? q8_stage(h, l, false) : (char*)h->kc + (size_t)l * h->layer_cache_elems * h->es;
+  char* vcl = h->q8 ? q8_stage(h, l, true) : (char*)h->vc + (size_t)l * h->layer_cache_elems * h->es;
   if (tc && which != K_ATTN) {
     const TcMaps& tm = h->tmaps[l];
     const int qkv_rows = (h->H + 2 * c.kv_heads) * h->hd;
@@ -655,7 +693,7 @@ llm_status launch_one(llm_handle* h, int which, int l, int B, bool pdl) {
       qa.H = h->H; qa.kv = c.kv_heads; qa.hd = h->hd; qa.cap = h->q8 ? 1 : c.max_seq; qa.staged = h->q8;
       qa.rope_cos = h->rope_cos; qa.rope_sin = h->rope_sin; qa.step = h->st;
       CUDA_TRY(h, launch_tc_qkv(qa, h->stream, pdl));
-      return h->q8 && !q8_fused(h) ? q8_store(h, l, B, pdl) : LLM_OK;
+      return q8_stores_first(h) ? q8_store(h, l, q8_rows(h, B), pdl) : LLM_OK;
     }
     if (which == K_O) {
       in.x = h->attn; in.x_stride = h->d;
@@ -690,18 +728,17 @@ llm_status launch_one(llm_handle* h, int which, int l, int B, bool pdl) {
     a.tr_in = tr_slot(h, l, TR_N1); a.tr_pre = tr_slot(h, l, TR_QKV); a.tr_rot = tr_slot(h, l, TR_KR);
     a.tr_stride = (int32_t)h->trace_w;
     CUDA_TRY(h, launch_gemv(a, p, wt, EPI_QKV, true, h->stream, pdl));
-    if (h->q8 && !q8_fused(h)) return q8_store(h, l, B, pdl);
+    if (q8_stores_first(h)) return q8_store(h, l, q8_rows(h, B), pdl);
   } else if (which == K_ATTN && h->q8) {
-    QAttnArgs qa = {};
-    qa.c = q8_view(h, l); qa.r = q8_rows(h, B);
-    qa.q = h->q; qa.out = h->attn; qa.q_stride = qa.out_stride = h->d; qa.g = c.group;
-    qa.scale = 1.0f / sqrtf((float)h->hd); qa.ws = h->qws;
-    qa.tiles = h->capturing_pass && h->q_tiles ? h->tile_buf : nullptr;
-    if (q8_fused(h)) {
-      qa.new_k = h->stage_k; qa.new_v = h->stage_v; qa.new_t = h->wt;
+    if (!h->capturing_verify) return q8_attend(h, l, q8_rows(h, B), pdl);
+    // a verification pass: token by token, as single steps would.  A block's scale is that of all it holds, so
+    // with all tokens written at once what a token sees would depend on the drafts after it.
+    for (int i = 0; i < h->capturing_verify; ++i) {
+      QRows r = q8_rows(h, B / h->capturing_verify);
+      r.entry0 = i; r.entry_step = h->capturing_verify;
+      if (!q8_fused(h)) TRY(q8_store(h, l, r, pdl));
+      TRY(q8_attend(h, l, r, pdl));
     }
-    qa.krow0 = (int32_t)((size_t)l * c.max_batch * c.kv_heads * h->qcap);
-    CUDA_TRY(h, launch_qattn(qa, 0, h->num_sms, h->stream, pdl, &h->kmap, &h->vmap));
   } else if (which == K_ATTN && h->capturing_pass && h->pf_attn) {
     // a prefill pass: tiles of consecutive prompt tokens share each key/value stream
     AttnPrefillArgs pa = {};
@@ -761,6 +798,7 @@ llm_status launch_one(llm_handle* h, int which, int l, int B, bool pdl) {
 
 llm_status launch_layer_kernels(llm_handle* h, int B, int mode, bool pdl, bool trace) {
   const llm_config& c = h->cfg;
+  if (h->capturing_verify) CUDA_TRY(h, launch_qcache_keep(q8_verify(h, B, h->capturing_verify, nullptr), h->stream));
   TRY(launch_one(h, K_EMBED, 0, B, false));
   if (h->mega && B == 1 && !trace && !h->capturing_pass) {
     // every layer, the head and a greedy draw in one persistent kernel; a top-k top-p draw after
@@ -808,8 +846,8 @@ llm_status launch_layer_kernels(llm_handle* h, int B, int mode, bool pdl, bool t
 // the step graph of (B, mode), captured on first use; with gen > 0, a generation graph of gen
 // steps, each its own prologue (gen_begin_kernel), the step's kernels and gen_end_kernel
 llm_status step_graph(llm_handle* h, int B, int mode, std::pair<cudaGraphExec_t, int>** out, int gen = 0,
-                      bool pass = false) {
-  GraphKey key{B, mode, gen, pass ? 1 : 0};
+                      bool pass = false, int verify = 0) {
+  GraphKey key{B, mode, gen, pass ? 1 + verify : 0};
   auto it = h->graphs.find(key);
   if (it == h->graphs.end()) {
     // capture on a private stream, then replay on the handle's stream
@@ -818,6 +856,7 @@ llm_status step_graph(llm_handle* h, int B, int mode, std::pair<cudaGraphExec_t,
     CUDA_TRY(h, cudaStreamBeginCapture(h->stream, cudaStreamCaptureModeThreadLocal));
     llm_status s = LLM_OK;
     h->capturing_pass = pass;
+    h->capturing_verify = verify;
     if (gen == 0) {
       s = launch_layer_kernels(h, B, mode, true, false);
     } else {
@@ -828,6 +867,7 @@ llm_status step_graph(llm_handle* h, int B, int mode, std::pair<cudaGraphExec_t,
       }
     }
     h->capturing_pass = false;
+    h->capturing_verify = 0;
     cudaGraph_t graph = nullptr;
     cudaError_t e = cudaStreamEndCapture(h->stream, &graph);
     h->stream = saved;
@@ -848,10 +888,10 @@ llm_status step_graph(llm_handle* h, int B, int mode, std::pair<cudaGraphExec_t,
   return LLM_OK;
 }
 
-llm_status run_step(llm_handle* h, int B, int mode, bool pass = false) {
+llm_status run_step(llm_handle* h, int B, int mode, bool pass = false, int verify = 0) {
   if (h->cfg.debug_trace) return launch_layer_kernels(h, B, mode, false, true);
   std::pair<cudaGraphExec_t, int>* g = nullptr;
-  TRY(step_graph(h, B, mode, &g, 0, pass));
+  TRY(step_graph(h, B, mode, &g, 0, pass, verify));
   CUDA_TRY(h, cudaGraphLaunch(g->first, h->stream));
   return LLM_OK;
 }
@@ -1333,11 +1373,12 @@ static llm_status pass_logits(llm_handle* h, int n, const std::vector<int32_t>& 
 
 // one pass of n entries; ranges [3][n]: attention starts, first written positions, cache rows;
 // tokens as for begin (host array, or device array read at (e / tok_np) * tok_stride + e % tok_np
-// + tok_col)
+// + tok_col); verify: tokens per row of a verification pass on an 8-bit cache
 static llm_status run_pass(llm_handle* h, int n, const int32_t* tok_host, const int32_t* tok_dev, int tok_stride,
-                           int tok_col, int tok_np, const int32_t* pos_host, const int32_t* ranges_host) {
+                           int tok_col, int tok_np, const int32_t* pos_host, const int32_t* ranges_host,
+                           int verify = 0) {
   CUDA_TRY(h, cudaMemcpyAsync(h->range_buf, ranges_host, (size_t)3 * n * 4, cudaMemcpyHostToDevice, h->stream));
-  if (h->pf_attn || h->q_tiles) {
+  if (h->pf_attn || (h->q_tiles && !verify)) {
     // tiles: runs of at most qt entries of one cache row with one attention start at consecutive
     // positions; units (tile, kv head), longest key range first
     const int qt = h->q_tiles ? qattn_tile_tokens(h->cfg.group) : attn_prefill_tile_tokens(h->cfg.group), kv = h->cfg.kv_heads, NT = h->NT;
@@ -1377,7 +1418,7 @@ static llm_status run_pass(llm_handle* h, int n, const int32_t* tok_host, const 
   }
   TRY(begin(h, 0, n, tok_host, tok_dev, tok_stride, tok_col, 0.0f, 1, 1.0f, nullptr, nullptr, pos_host, nullptr, 0,
             h->range_buf, tok_np));
-  return run_step(h, n, MODE_NOHEAD, true);
+  return run_step(h, n, MODE_NOHEAD, true, verify);
 }
 
 static llm_status prefill_impl(llm_handle* h, const int32_t* tok_host, const int32_t* tok_dev, int32_t B, int32_t S,
@@ -1708,7 +1749,16 @@ llm_status llm_verify_step(llm_handle* h, const int32_t* tokens_host, int32_t B,
       ranges[2 * (size_t)n + e] = b;
       if (i > 0) drafts[(size_t)b * S + i - 1] = tokens_host[e];
     }
-  TRY(run_pass(h, n, tokens_host, nullptr, 1, 0, 1, epos.data(), ranges.data()));
+  if (h->q8 && !h->vstage_k) {
+    const size_t stage = (size_t)h->L * h->NT * h->kvw * h->es, blocks = (size_t)h->L * h->cfg.max_batch * h->cfg.kv_heads;
+    if (!h->vstage_v) TRY(dalloc(h, &h->vstage_v, stage));
+    if (!h->kept_k) TRY(dalloc(h, &h->kept_k, blocks * kQBlock * h->hd));
+    if (!h->kept_v) TRY(dalloc(h, &h->kept_v, blocks * kQBlock * h->hd));
+    if (!h->kept_ks) TRY(dalloc(h, &h->kept_ks, blocks * 4));
+    if (!h->kept_vs) TRY(dalloc(h, &h->kept_vs, blocks * 4));
+    TRY(dalloc(h, &h->vstage_k, stage));
+  }
+  TRY(run_pass(h, n, tokens_host, nullptr, 1, 0, 1, epos.data(), ranges.data(), h->q8 ? T : 0));
   TRY(pass_residual(h, n));
   TRY(head_rows(h, h->xa, n, p_dev));  // (every entry's logits are wanted: no gather, the head is read once)
   CUDA_TRY(h, launch_probs(p_dev, n, h->V, temp, h->stream));
@@ -1716,6 +1766,7 @@ llm_status llm_verify_step(llm_handle* h, const int32_t* tokens_host, int32_t B,
   CUDA_TRY(h, cudaMemcpyAsync(h->tok_buf, drafts.data(), drafts.size() * 4, cudaMemcpyHostToDevice, h->stream));
   const VerifyArgs va = {p_dev, q_dev, h->tok_buf, nullptr, u_dev, B, S, h->V, ids_dev, accepted_dev};
   CUDA_TRY(h, launch_verify(va, h->stream));
+  if (h->q8) CUDA_TRY(h, launch_qcache_settle(q8_verify(h, n, T, accepted_dev), h->wt, h->stream));
   for (int b = 0; b < B; ++b) h->filled[b] = positions_host[b] + T;
   return LLM_OK;
 }

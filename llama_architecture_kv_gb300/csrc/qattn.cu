@@ -40,13 +40,14 @@ LLM_D void store_o(void* o, int64_t i, float v) {
   else static_cast<float*>(o)[i] = v;
 }
 
-// positions [start, end) of the token in row t of a call (t = b * S + i); false: the token is not there
+// positions [start, end) of token t of a call (t = b * S + i; of a step: of its row b, the entry whose place the
+// token's positions and rows of q and out have); false: the token is not there
 LLM_D bool token_range(const QRows& r, int t, int& b, int& start, int& end) {
   start = 0;
   if (r.step) {
-    b = t;
-    start = row_start(r.step, t);
-    end = row_pos(r.step, t) + 1;
+    b = q_entry(r, t);
+    start = row_start(r.step, b);
+    end = row_pos(r.step, b) + 1;
     return true;
   }
   b = t / r.S;
@@ -83,13 +84,14 @@ __global__ void __launch_bounds__(kSimpleThreads) qattn_simple_kernel(const QAtt
     const int t = (int)t64;
     int b, start, end;
     if (!token_range(a.r, t, b, start, end)) continue;
+    const int64_t qrow = a.r.step ? b : t64;
     // this part's positions: a whole number of 32-position chunks, aligned so that none crosses a page
     const int base = start & ~31;
     const int nch = end > start ? (end - base + 31) / 32 : 0;
     const int c0 = (int)((int64_t)nch * split / a.splits), c1 = (int)((int64_t)nch * (split + 1) / a.splits);
     __syncthreads();  // the previous token's shared memory is free
     for (int i = tid; i < g * HD; i += kSimpleThreads)
-      qs[i] = load_q<QT>(a.q, t64 * a.q_stride + (int64_t)j * g * HD + i) ;
+      qs[i] = load_q<QT>(a.q, qrow * a.q_stride + (int64_t)j * g * HD + i);
     __syncthreads();
     float m[GM], l[GM], o[GM][DPL];
 #pragma unroll
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(kSimpleThreads) qattn_simple_kernel(const QAtt
       }
       const int head = j * g + h;
       if (a.splits == 1) {
-        store_o<QT>(a.out, t64 * a.out_stride + (int64_t)head * HD + e, L == 0.f ? 0.f : O / L);
+        store_o<QT>(a.out, qrow * a.out_stride + (int64_t)head * HD + e, L == 0.f ? 0.f : O / L);
       } else {
         float* dst = reinterpret_cast<float*>(a.ws + kQattnTickets) + ((t64 * a.c.kv * g + head) * a.splits + split) * (HD + 2);
         dst[e] = O;
@@ -227,7 +229,7 @@ __global__ void qattn_merge_kernel(const QAttnArgs a) {
       O = fmaf(f, src[s * (HD + 2) + e], O);
       L = fmaf(f, ls, L);
     }
-    store_o<QT>(a.out, t * a.out_stride + (int64_t)head * HD + e, L == 0.f ? 0.f : O / L);
+    store_o<QT>(a.out, (a.r.step ? b : t) * a.out_stride + (int64_t)head * HD + e, L == 0.f ? 0.f : O / L);
   }
 }
 

@@ -108,9 +108,9 @@ LLM_D QaUnit qa_unit(const QAttnArgs& a, int t) {
       u.ntok = e[1];
       u.start = e[3];
     } else {
-      u.b = t;
+      u.b = q_entry(a.r, t);
       u.ntok = 1;
-      u.start = row_start(a.r.step, t);
+      u.start = row_start(a.r.step, u.b);
     }
     u.qrow = u.b;
     u.end0 = row_pos(a.r.step, u.b) + 1;

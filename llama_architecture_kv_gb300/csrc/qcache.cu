@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(kQThreads)
 }
 
 // Rows of a handle's step (heads of 64 and 128: only a prefill pass's entries; their decode steps store
-// within the attention): warp (entry, kv head, keys or values); staged values [B][kv][HD].  A
-// prefill pass lists the entries of a cache row in position order, so the entries of one block
+// within the attention): warp (entry, kv head, keys or values); staged values [entries][kv][HD].  A
+// prefill pass (all of its entries at once: entry_step 1) lists the entries of a cache row in position order, so the entries of one block
 // follow one another: the first of them (the leader) writes all, run by run of consecutive
 // positions, and the others' warps leave.
 template <int HD, int ST>
@@ -152,13 +152,14 @@ __global__ void __launch_bounds__(kQThreads)
   grid_dep_launch();
   const uint32_t w = blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
   const int side = (int)(w & 1);
-  const int e = (int)((w >> 1) / (uint32_t)c.kv), h = (int)((w >> 1) - (uint32_t)e * (uint32_t)c.kv);
-  if (e >= r.B) return;
+  const int b = (int)((w >> 1) / (uint32_t)c.kv), h = (int)((w >> 1) - (uint32_t)b * (uint32_t)c.kv);
+  if (b >= r.B) return;
+  const int e = q_entry(r, b);
   auto slot = [&](int i, int& row, int& pp) { cache_slot(r.step, c.cap, i, row_pos(r.step, i), row, pp); };
   int row, pp;
   slot(e, row, pp);
   int n = 1;
-  if (r.step->rowmap) {
+  if (r.step->rowmap && r.entry_step == 1) {
     int pr, pq;
     if (e > 0) {
       slot(e - 1, pr, pq);
@@ -190,6 +191,61 @@ __global__ void __launch_bounds__(kQThreads)
                          stride);
     __syncwarp();
     i += len;
+  }
+}
+
+// CTA (layer and kv head, row)
+__global__ void __launch_bounds__(kQThreads) qcache_keep_kernel(const QVerify v) {
+  const int l = blockIdx.x / v.c.kv, h = blockIdx.x - l * v.c.kv, b = blockIdx.y;
+  const int e = q_entry(v.r, b), hd = v.c.hd;
+  int row, pp;
+  cache_slot(v.r.step, v.c.cap, e, row_pos(v.r.step, e), row, pp);
+  const int t0 = pp % kQBlock;
+  if (t0 == 0) return;
+  const size_t head = ((size_t)l * v.c.rows + row) * v.c.kv + h, kept = ((size_t)l * v.c.rows + b) * v.c.kv + h;
+  const size_t from = (head * v.c.cap + (pp - t0)) * hd, to = kept * kQBlock * hd;
+  for (int i = threadIdx.x; i < t0 * hd / 16; i += kQThreads) {
+    reinterpret_cast<uint4*>(v.kept_k + to)[i] = reinterpret_cast<const uint4*>(v.c.k + from)[i];
+    reinterpret_cast<uint4*>(v.kept_v + to)[i] = reinterpret_cast<const uint4*>(v.c.v + from)[i];
+  }
+  if (threadIdx.x == 0) {
+    const size_t sc = head * (v.c.cap / kQBlock) + pp / kQBlock;
+    v.kept_ks[kept] = v.c.ks[sc];
+    v.kept_vs[kept] = v.c.vs[sc];
+  }
+}
+
+// warp (layer, row, kv head, keys or values)
+template <int HD, int ST>
+__global__ void __launch_bounds__(kQThreads) qcache_settle_kernel(const QVerify v) {
+  const int64_t w = (int64_t)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
+  const int side = (int)(w & 1), lane = threadIdx.x & 31;
+  const int64_t u = w >> 1;
+  const int h = (int)(u % v.c.kv), b = (int)(u / v.c.kv % v.r.B), l = (int)(u / v.c.kv / v.r.B);
+  if (l >= v.layers) return;
+  const int e = q_entry(v.r, b), kept_drafts = v.accepted[b];
+  if (kept_drafts >= v.T - 1) return;         // nothing else was written
+  const int p0 = row_pos(v.r.step, e), last = p0 + kept_drafts;
+  const int t1 = last % kQBlock + 1;          // tokens of the block up to the last that was kept
+  if (t1 == kQBlock) return;                  // the others are in blocks of their own
+  int row, pp;
+  cache_slot(v.r.step, v.c.cap, e, last, row, pp);
+  const size_t head = ((size_t)l * v.c.rows + row) * v.c.kv + h;
+  uint8_t* codes = (side ? v.c.v : v.c.k) + (head * v.c.cap + (pp + 1 - t1)) * HD;
+  float* scale = (side ? v.c.vs : v.c.ks) + head * (v.c.cap / kQBlock) + pp / kQBlock;
+  const int t0 = max(0, p0 - (last + 1 - t1));  // tokens of the block before this call's
+  if (t0 > 0) {
+    const size_t kept = ((size_t)l * v.c.rows + b) * v.c.kv + h;
+    const uint4* from = reinterpret_cast<const uint4*>((side ? v.kept_v : v.kept_k) + kept * kQBlock * HD);
+    for (int i = lane; i < t0 * HD / 16; i += 32) reinterpret_cast<uint4*>(codes)[i] = from[i];
+    if (lane == 0) *scale = (side ? v.kept_vs : v.kept_ks)[kept];
+    __syncwarp();
+  }
+  const int64_t stride = (int64_t)v.c.kv * HD;
+  const int64_t base = ((int64_t)l * v.stage_rows + e + (last + 1 - t1 + t0 - p0)) * stride + (int64_t)h * HD;
+  for (int t = t0; t < t1; ++t) {
+    quantise_run<HD, ST>(codes, scale, t, 1, side ? v.stage_v : v.stage_k, base + (t - t0) * stride, stride);
+    __syncwarp();
   }
 }
 
@@ -299,6 +355,19 @@ cudaError_t launch_qcache_clear(const QCacheView& c, int layers, int row, int bl
   qcache_clear_kernel<<<(n + kQThreads - 1) / kQThreads, kQThreads, 0, s>>>(c.ks, c.vs, n, c.rows, c.kv,
                                                                             c.cap / kQBlock, row, blk);
   return cudaGetLastError();
+}
+
+cudaError_t launch_qcache_keep(const QVerify& v, cudaStream_t s) {
+  qcache_keep_kernel<<<dim3((unsigned)(v.layers * v.c.kv), (unsigned)v.r.B), kQThreads, 0, s>>>(v);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_qcache_settle(const QVerify& v, int st, cudaStream_t s) {
+  const int64_t grid = ((int64_t)v.layers * v.r.B * v.c.kv * 2 + kQThreads / 32 - 1) / (kQThreads / 32);
+  return with_shape(v.c.hd, st, [&](auto hd, auto t) {
+    qcache_settle_kernel<hd.value, t.value><<<(unsigned)grid, kQThreads, 0, s>>>(v);
+    return cudaGetLastError();
+  });
 }
 
 cudaError_t launch_qcache_write_step(const QCacheView& c, const QRows& r, const void* k, const void* v, int st,

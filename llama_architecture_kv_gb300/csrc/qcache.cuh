@@ -22,8 +22,8 @@ struct QCacheView {
 // The rows of a call.  Without a step: row b holds `first[b]` (a first position, or a length) and
 // `count[b]` tokens (S where count is null), its positions found through table [B][stride] or, with
 // no table, in cache row b; everything read from device memory is checked against these bounds and
-// an error is recorded in *status (where given).  With a step: row b is row b of a decode step, or
-// entry b of a prefill pass, of a handle (common.cuh), which the host has validated.
+// an error is recorded in *status (where given).  With a step: row b is row entry0 + b * entry_step of a
+// decode step, or that entry of a prefill pass, of a handle (common.cuh), which the host has validated.
 struct QRows {
   const int32_t* first;
   const int32_t* count;
@@ -33,7 +33,10 @@ struct QRows {
   int32_t limit;         // positions a row can hold
   const StepState* step;
   int32_t* status;
+  int32_t entry0, entry_step;  // with a step (0 and 1 but for a verification pass, which takes one token
+                               // of every row at a time)
 };
+LLM_D int q_entry(const QRows& r, int b) { return r.entry0 + b * r.entry_step; }
 
 // device error codes (same values as llm.h)
 constexpr int32_t kErrPosRange = 4;
@@ -125,6 +128,22 @@ cudaError_t launch_qcache_write(const QCacheView& c, const QRows& r, const void*
 // the same for the rows of a handle's step, or the entries of a prefill pass: staged [B][kv][hd]
 cudaError_t launch_qcache_write_step(const QCacheView& c, const QRows& r, const void* k, const void* v, int st,
                                      cudaStream_t s, bool pdl);
+// Verification passes: entry b * T + i of the step is token i of row b.  keep: the codes and scales of the
+// blocks that the rows' first tokens go into (where their positions before hold something) to the kept_*
+// arrays; settle: after accepted[b] of the T - 1 drafts were kept, the block that ends with the last of the kept
+// tokens as if no other had been written, from what was kept and the tokens' staged values.
+struct QVerify {
+  QCacheView c;                // layer 0; the others follow
+  int32_t layers, T;
+  QRows r;                     // with a step; entry_step = T
+  uint8_t *kept_k, *kept_v;    // [layers][rows][kv][kQBlock][hd]
+  float *kept_ks, *kept_vs;    // [layers][rows][kv]
+  const void *stage_k, *stage_v;  // [layers][stage_rows][kv][hd], bf16 (st 1) or f32
+  int64_t stage_rows;
+  const int32_t* accepted;
+};
+cudaError_t launch_qcache_keep(const QVerify& v, cudaStream_t s);
+cudaError_t launch_qcache_settle(const QVerify& v, int st, cudaStream_t s);
 // the scales of block blk of cache row `row` to 0 in `layers` caches that follow one another, c the first
 cudaError_t launch_qcache_clear(const QCacheView& c, int layers, int row, int blk, cudaStream_t s);
 cudaError_t launch_qcache_read(const QCacheView& c, const QRows& r, void* k, void* v, int st, int64_t stride,

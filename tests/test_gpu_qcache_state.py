@@ -90,3 +90,96 @@ def test_dead_data_of_the_block_is_kept_where_it_is_live():
         assert np.array_equal(a[:, :32], b[:, :32])
         assert (np.abs(a - b) <= np.abs(a) * 2.0 ** -4 + np.abs(b).max() * 2.0 ** -14).all() and np.abs(b[:, 32:]).max() > 0
     g.close()
+
+
+# ---- drafts ----
+
+def chain_of(g, start, pos, n):
+    out = np.empty((len(start), n), np.int32)
+    cur = start
+    for s in range(n):
+        cur = g.step_rows(cur, pos + s)
+        out[:, s] = cur
+    return out
+
+
+@pytest.mark.parametrize("cache", [pkg.LLM_CACHE_MODEL, E4M3], ids=["model", "e4m3"])
+@pytest.mark.parametrize("name,shape,B,tc", SHAPES, ids=[s[0] for s in SHAPES])
+def test_probabilities_do_not_depend_on_later_drafts(name, shape, B, tc, cache):
+    n, S, cap = 24, 5, 128
+    g = make(shape, 841, B, cap, tc_min_batch=tc, cache_type=cache, wstd=0.2 if not shape.bf16 else 0.06)
+    toks = synth.tokens(842, 0, B * n, shape.vocab).reshape(B, n)
+    pos = np.array([n - 1 - 3 * (b % 4) for b in range(B)])
+    start = toks[np.arange(B), pos]
+    rng = np.random.default_rng(843)
+    u = rng.random((B, S + 1)).astype(np.float32)
+    base = rng.integers(0, shape.vocab, (B, S)).astype(np.int32)
+    first = None
+    for at in (S - 1, S - 1, S - 1, 2, 0):     # the draft from which on this list differs from the first
+        drafts = base.copy()
+        if first is not None:
+            drafts[:, at:] = rng.integers(0, shape.vocab, (B, S - at))
+        g.prefill(toks[:, :n - 1], 0, logits=False)
+        _, _, p = g.verify_step(np.concatenate([start[:, None], drafts], 1), pos, u, temp=0.8)
+        if first is None:
+            first = p
+        else:
+            assert np.array_equal(bits(p[:, :at + 1]), bits(first[:, :at + 1])), at
+    g.close()
+
+
+@pytest.mark.parametrize("name,shape,B,tc", SHAPES, ids=[s[0] for s in SHAPES])
+def test_drafts_that_are_not_kept_leave_nothing_behind(name, shape, B, tc):
+    from tests import qcache_ref as ref
+    from tests.test_gpu_qcache_model import wide
+    n, S, cap = 40, 9, 128
+    kw = dict(tc_min_batch=tc, wstd=0.2 if not shape.bf16 else 0.06)
+    g = make(shape, 851, B, cap, cache_type=E4M3, **kw)
+    toks = synth.tokens(852, 0, B * n, shape.vocab).reshape(B, n)
+    pos = np.array([n - 1 - 3 * (b % 5) for b in range(B)])   # some rows cross from one block into the next
+    start = toks[np.arange(B), pos]
+    g.prefill(toks[:, :n - 1], 0, logits=False)
+    chain = chain_of(g, start, pos, S + 2)
+    kept = (np.arange(B) * 2 + 1) % (S + 1)
+    u = np.full((B, S + 1), 0.5, np.float32)
+    rng = np.random.default_rng(853)
+    seen, lists = [], []
+    for trial in range(3):
+        drafts = chain[:, :S].copy()
+        for b in range(B):
+            tail = rng.integers(0, shape.vocab, S - kept[b])
+            if kept[b] < S:
+                tail[0] = (chain[b, kept[b]] + 1 + trial) % shape.vocab
+            drafts[b, kept[b]:] = tail
+        lists.append(drafts)
+        g.prefill(toks[:, :n - 1], 0, logits=False)
+        ids, acc, p = g.verify_step(np.concatenate([start[:, None], drafts], 1), pos, u)
+        if trial == 0:
+            # (a draft may be lost to a near tie between the steps' logits and the pass's: the lists agree up to it)
+            assert (acc <= kept).all() and 2 * (acc == kept).sum() > B and (acc < S).any()
+            kept = acc.copy()
+        assert np.array_equal(acc, kept)
+        out = [g.kv_export(layer, b, 0, int(pos[b] + kept[b]) + 1) for layer in range(shape.layers) for b in range(B)]
+        nxt = g.decode_rows(ids[np.arange(B), kept], pos + kept + 1)
+        seen.append((out, bits(nxt)))
+    for out, nxt in seen[1:]:
+        assert np.array_equal(nxt, seen[0][1])
+        for (k, v), (k0, v0) in zip(out, seen[0][0]):
+            assert np.array_equal(k, k0) and np.array_equal(v, v0)
+    # what layer 0 holds: the kept tokens written one by one (its keys and values depend on no cache)
+    plain = make(shape, 851, B, cap, **kw)
+    plain.prefill(toks[:, :n - 1], 0, logits=False)
+    prompt = {b: plain.kv_export(0, b, 0, n - 1) for b in range(B)}
+    plain.verify_step(np.concatenate([start[:, None], lists[0]], 1), pos, u)
+    for b in range(B):
+        end = int(pos[b] + kept[b]) + 1
+        k0, v0, kk, vv = (wide(x).swapaxes(0, 1)[None] for x in (*prompt[b], *plain.kv_export(0, b, 0, end)))
+        want = ref.RefCache(1, shape.kv, cap, shape.hd)
+        want.write(k0, v0, [0])
+        for q in range(int(pos[b]), end):
+            want.write(kk[:, q:q + 1], vv[:, q:q + 1], [q])
+        wk, wv = want.values(None, 0, end)
+        gk, gv = seen[0][0][b]
+        assert np.array_equal(wide(gk), wk) and np.array_equal(wide(gv), wv), b
+    plain.close()
+    g.close()
