@@ -286,7 +286,8 @@ struct llm_handle {
   int qcap = 0;                                   // max_seq rounded up to whole pages
   uint8_t *qk = nullptr, *qv = nullptr;           // codes [L][max_batch][kv][qcap][hd]
   float *qks = nullptr, *qvs = nullptr;           // scales [L][max_batch][kv][qcap / kQBlock]
-  void *stage_k = nullptr, *stage_v = nullptr;    // [NT][kv][hd] keys and values of a step, in dtype
+  void *stage_k = nullptr, *stage_v = nullptr;    // [stage_rows][kv][hd] keys and values of a step, in dtype
+  int stage_rows = 0;                             // NT, at least a block (kv_import writes whole blocks from them)
   unsigned char* qws = nullptr;                   // attention workspace
   // verification passes (allocated by the first): the tokens' keys and values of every layer
   // [L][NT][kv][hd], and the blocks that the rows' first tokens go into [L][max_batch][kv][kQBlock][hd]
@@ -1140,7 +1141,8 @@ llm_status llm_create(const llm_config* cfg, const void* weights, uint64_t nbyte
     return bail(LLM_ERR_CONFIG);
   }
   if (h->q8) {
-    const size_t stage = (size_t)h->NT * h->kvw * es;
+    h->stage_rows = std::max(h->NT, kQBlock);
+    const size_t stage = (size_t)h->stage_rows * h->kvw * es;
     if ((st = dalloc(h, &h->qk, cache_rows * h->hd)) || (st = dalloc(h, &h->qv, cache_rows * h->hd)) ||
         (st = dalloc(h, &h->qks, scale_bytes)) || (st = dalloc(h, &h->qvs, scale_bytes)) ||
         (st = dalloc(h, &h->stage_k, stage)) || (st = dalloc(h, &h->stage_v, stage)))
@@ -1953,8 +1955,8 @@ static llm_status kv_copy(llm_handle* h, int32_t layer, int32_t row, int32_t pos
     r.first = h->pos_buf; r.B = 1; r.limit = h->qcap; r.status = h->status;
     const int64_t stride = (int64_t)kv * hd;
     for (int32_t i = 0; i < n;) {
-      const int32_t p = pos0 + i, room = std::max(1, h->NT / kQBlock * kQBlock - p % kQBlock);
-      r.S = std::min(std::min(n - i, room), h->NT);
+      const int32_t p = pos0 + i;
+      r.S = std::min(n - i, h->stage_rows / kQBlock * kQBlock - p % kQBlock);
       CUDA_TRY(h, cudaMemcpyAsync(h->pos_buf, &p, 4, cudaMemcpyHostToDevice, h->stream));
       if (!import) CUDA_TRY(h, launch_qcache_read(c, r, h->stage_k, h->stage_v, h->wt, stride, h->stream));
       for (size_t j = 0; j < kv; ++j)

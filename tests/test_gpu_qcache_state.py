@@ -92,6 +92,30 @@ def test_dead_data_of_the_block_is_kept_where_it_is_live():
     g.close()
 
 
+@pytest.mark.parametrize("tokens", [8, 16, 20, 0])
+@pytest.mark.parametrize("name,shape,B,tc", SHAPES[:3], ids=[s[0] for s in SHAPES[:3]])
+def test_imports_are_one_write_whatever_a_pass_holds(name, shape, B, tc, tokens):
+    # values that grow inside blocks: a write of the whole range rounds each of them once
+    from tests import qcache_ref as ref
+    from tests.test_gpu_qcache_model import wide
+    g = make(shape, 831, 2, 128, max_tokens=tokens, cache_type=E4M3)
+    rng = np.random.default_rng(832)
+    n, at = 75, 5
+    grow = 2.0 ** (np.arange(n) * 0.7 % 9)[None, :, None]
+    k, v = ((rng.standard_normal((shape.kv, n, shape.hd)) * grow).astype(np.float32) for _ in range(2))
+    if shape.bf16:
+        k, v = ((x.view(np.uint32) >> 16).astype(np.uint16) for x in (k, v))
+    want = ref.RefCache(1, shape.kv, 128, shape.hd)
+    kk, vv = (wide(x).swapaxes(0, 1)[None] for x in (k, v))
+    want.write(kk, vv, [at])
+    wk, wv = want.values(None, 0, n, at)
+    for layer in range(shape.layers):
+        g.kv_import(layer, 1, at, k, v)
+        gk, gv = g.kv_export(layer, 1, at, n)
+        assert np.array_equal(wide(gk), wk) and np.array_equal(wide(gv), wv)
+    g.close()
+
+
 # ---- drafts ----
 
 def chain_of(g, start, pos, n):
