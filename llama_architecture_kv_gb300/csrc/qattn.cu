@@ -6,7 +6,7 @@
 // A token that no position is visible to gets zeros.
 //
 // Head sizes 64 and 128 run on the tensor cores (qattn_tc.cuh: 32 rows of up to 2100 positions, 8 heads
-// of 128, groups of 4, in 30 us, against 170 us with the kernel here).  qattn_simple_kernel takes the
+// of 128, groups of 4, in 34 us, against 170 us with the kernel here).  qattn_simple_kernel takes the
 // others (16, 32, 256), whose rows are no 64- or 128-byte swizzle row: a CTA of four warps takes one
 // token, one key/value head and one contiguous part of the positions.  Each warp takes 32 positions at a
 // time: lane = position for the scores of the group's heads (the codes widened to f32, the scale applied
@@ -273,7 +273,7 @@ namespace {
 
 // the tensor-core kernel's tiles: 16 nc accumulator columns of np pieces, the smallest that holds all
 // of a row's (token, head) columns, else the largest: a tile's cost grows with its columns (five tokens of
-// a group of four in each of 32 rows of 2048 positions: 64 us with 24 columns, 73 us with 32), and every
+// a group of four in each of 32 rows of 2048 positions: 66 us with 24 columns, 70 us with 32), and every
 // further tile reads the codes again
 struct TcPlanQ {
   int nc, cols, tokens, grid;

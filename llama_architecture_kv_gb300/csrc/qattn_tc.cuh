@@ -1,27 +1,29 @@
 // Attention over an 8-bit cache on the 5th-generation tensor cores, head sizes 64 and 128: the
 // kernel template (its instantiations, a translation unit each: qattn_tc<head size>_<type>.cu).
 //
-// The codes go from HBM to shared memory by TMA and from there into e4m3 MMAs as they are: no code
-// is ever widened.  The f32 (bf16) operands that meet them, queries and softmax weights, enter as NP
-// e4m3 pieces, x = 2^e (x_0 + x_1 / 32 + x_2 / 32^2 + ...) with |x| / 2^e <= 256, each piece the
-// rounding of what the ones before left over (at most half a step, 8 of 256, so 32 times it is in
-// range again).  A piece takes four bits: four pieces leave 2^-16 of an element at worst, or 2^-33 of
-// the largest where it is tiny (f32); two hold a bf16 query's eight bits, and leave 2^-8 of a weight,
-// the rounding that a bf16 output makes itself (bf16).  The pieces are columns of their own, so every
-// accumulator sums like with like in f32 and the powers of 32 are applied once, in registers.
+// The codes go from HBM to shared memory by TMA, the keys' from there into e4m3 MMAs as they are.  The
+// f32 (bf16) queries that meet them enter as NP e4m3 pieces, x = 2^e (x_0 + x_1 / 32 + x_2 / 32^2 + ...)
+// with |x| / 2^e <= 256, each piece the rounding of what the ones before left over (at most half a step, 8
+// of 256, so 32 times it is in range again).  A piece takes four bits: four pieces leave 2^-16 of an element
+// at worst, or 2^-33 of the largest where it is tiny (f32); two hold a bf16 query's eight bits.  The pieces
+// are columns of their own, so every accumulator sums like with like in f32 and the powers of 32 are applied
+// once, in registers.  The values are widened to bf16 (exact) in shared memory, in the place of the tile's
+// keys and values: their softmax weights, as bf16 pieces, have the exponents of f32, so that a weight keeps its
+// digits however small it is beside the largest.  (As e4m3 pieces, codes as they lie, tiles took 5 to 15% less
+// time -- 32 rows of up to 2100: 30 us, 131072 positions with 8 tokens: 81 -- but weights below 2^-20 (f32:
+// 2^-27) of the largest were lost, and where the heavy positions' values are small those are the result.)
 //
 // A tile is 128 positions of one row and key/value head against up to C = 16 NC / NP columns, the
 // (token, query head) pairs of up to C / g tokens that share the codes:
 //   S [128 positions][16 NC]  = K [128][HD] Q^T      A = keys, K-major as stored; B = query pieces
 //   softmax                     thread = position: pieces summed, block scales applied, weights split
-//   O [HD][16 NC]            += V^T [HD][128] P^T     A = values, M-major as stored; B = weight pieces
-// With the positions on the M side a tile costs 8 MMAs however few columns there are, and a thread
-// writes its position's pieces with one 16-byte store per 16 columns (B's N-major layout).
+//   O [HD][NW]               += V^T [HD][128] P^T     A = widened values, M-major; B = weight pieces
+// With the positions on the M side a tile costs HD / 32 + 8 MMAs however few columns there are, and a thread
+// writes its position's pieces with 16-byte stores, one per 8 pieces (B's N-major layout).
 //
-// Running maxima are lazy: a column's reference makes the first tile's largest weight 2^2 (bf16: 2^5) and
-// moves only when a weight exceeds 2^8 (then that one becomes 2^5), so the accumulators in tensor memory
-// are hardly ever rescaled and the pieces keep the range above and the precision below.  The values' block
-// scales ride on the weights, relative to the largest scale seen (also lazy).
+// Running maxima are lazy: a column's reference makes the first tile's largest weight 1 and moves only when
+// a weight exceeds 2^32 (then that one becomes 1), so the accumulators in tensor memory are hardly ever
+// rescaled.  The values' block scales ride on the weights, relative to the largest scale seen (also lazy).
 //
 // One CTA: a producer warp (a ring of tiles by TMA, their block scales by 4-byte asynchronous copies), a
 // warp that issues the MMAs, and 16 softmax warps per SM: two groups of four take the tiles of a segment
@@ -34,13 +36,15 @@
 // done, where the last CTA to arrive (a ticket, nobody waits) adds them in CTA order.  So rows of any
 // lengths fill the SMs evenly and the result does not depend on timing.
 //
-// Bound by HBM where a tile's columns are few and rows long, by the softmax warps' instructions from
-// about 16 columns on, by latencies where a CTA has only a few tiles (a segment costs about 4 us besides
-// its tiles: first loads, the groups' sums, the join).  GB300, f32 queries, heads of 128, groups of 4, 8
-// key/value heads: 8 rows of 32768 positions 86 us (538 MB: 6.2 TB/s, 92% of the copy rate); one row of
-// 131072 51 us (5.3 TB/s); 32 rows of up to 2100 30 us (108 MB: 3.6 TB/s); one row of 2048 9.3 us; five
-// tokens in each of 32 rows of 2048 59 us (20 columns).  bf16 queries, 8 tokens at 131072 positions (32
-// columns): 81 us (269 MB: 3.3 TB/s).
+// Bound by HBM where a tile's columns are few and rows long (shared memory is next: the loads, the widening
+// and both products move 128 KB per tile of 128 x 128, three quarters of what it can at that rate), by the
+// latency of a tile's chain (scores, widening, weights, products) from about 16 columns on, and by latencies
+// where a CTA has only a few tiles (a segment costs about 4 us besides its tiles: first loads, the groups'
+// sums, the join).  Widening by integer steps instead of conversions, rolled or before the scores are there,
+// measured the same.  GB300, f32 queries, heads of 128, groups of 4, 8 key/value heads: 8 rows of 32768
+// positions 91 us (538 MB: 5.9 TB/s, 87% of the copy rate); one row of 131072 56 us (4.8 TB/s); 32 rows of up
+// to 2100 34 us (108 MB: 3.2 TB/s); one row of 2048 10.0 us; five tokens in each of 32 rows of 2048 66 us (20
+// columns).  bf16 queries, 8 tokens at 131072 positions (32 columns): 87 us (269 MB: 3.1 TB/s).
 #pragma once
 #include "attention.cuh"
 #include "qcache.cuh"
@@ -50,35 +54,37 @@ namespace llm {
 
 constexpr int kQaTile = 128;                       // positions per tile
 constexpr uint64_t kQaWaitCycles = 1000000000ull;  // about 0.5 s
-constexpr float kQaTop = 5.0f;                     // log2 of the largest weight of a tile that moved a reference
-// and of a segment's first tile.  The last digit of a weight's pieces is 2^-24 (f32) or 2^-14 (bf16), so
-// where one position outweighs a long tail f32 can start low, and its references hardly ever move (32
-// columns, f32: 60 us against 62 us with 2^5); bf16 starts high, at 2^-20 of the largest weight instead of
-// 2^-17 (one row, 8 tokens, 131072 positions: 82 us against 79).
-template <int QT> constexpr float kQaFirst = QT ? 5.0f : 2.0f;
-constexpr float kQaMost = 8.0f;                    // the largest weight that moves none
+constexpr float kQaMost = 32.0f;                   // log2 of the largest weight that moves no reference
 constexpr int kQaNear = 4;                         // most tiles by which a cut moves to a unit's end
 constexpr float kQaNone = -3.0e38f;                // a reference before any score
 constexpr size_t kQaSmem = 232448;                 // shared memory a CTA can have
 
 template <int HD, int NP, int NC>
 struct QaShape {
-  static constexpr int N = 16 * NC;                // accumulator columns
+  static constexpr int N = 16 * NC;                // score columns
   static constexpr int C = N / NP;                 // (token, head) columns
-  static constexpr int CPC = 16 / NP;              // of them per 16 accumulator columns
+  static constexpr int CPC = 16 / NP;              // of them per 16 score columns
+  // A weight's bf16 pieces, and the columns that they take (at least 16 in all, an MMA's least): one piece for
+  // bf16 queries, whose rounding (2^-8 of the weight) is the output's own, two for f32 (2^-17); where they would
+  // not fill the 16 columns, as many as do (two more and a column of zeros: 2^-26)
+  static constexpr int WS = C * (NP == 4 ? 2 : 1) >= 16 ? (NP == 4 ? 2 : 1) : 16 / C;
+  static constexpr int WP = WS < 4 ? WS : 3;
+  static constexpr int NW = C * WS;                // accumulator columns of the product over the values
   static constexpr int KB = kQaTile * HD;          // bytes of a tile of keys (or values)
   static constexpr int STAGE = 2 * KB;
   static constexpr int QB = N * HD;                // query pieces of a segment
-  static constexpr int PB = kQaTile * N;           // weight pieces of one group
-  static constexpr int TMEM = 4 * N <= 64 ? 64 : 4 * N <= 128 ? 128 : 4 * N <= 256 ? 256 : 512;  // columns
-  // Up to 8 columns two CTAs per SM (16 rows of 5 tokens of one head of 64: 26 us against 39 us with
-  // one; 32 rows of one token of 4 heads of 128: 31 against 34; but one row of 131072: 55 against 54), more
-  // in one CTA whose groups halve them (16 rows of 16 columns at 2048 positions: 30 us against 39 us as two
-  // CTAs of whole columns)
+  static constexpr int PB = 2 * kQaTile * NW;      // weight pieces of one parity's groups
+  static constexpr int COLS = 2 * (N + NW);
+  static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;  // columns
+  // Up to 8 columns two CTAs per SM (16 rows of 5 tokens of 32 heads of 64: 29 us against 42 us with one; 32 rows
+  // of one token of groups of 4: 34 against 41; one row of 131072: 56 against 64), more in one CTA whose groups
+  // halve them (16 rows of 16 columns at 2048 positions: 32 us against 39 us as two CTAs of whole columns)
   static constexpr int CTAS = C <= 8 ? 2 : 1;
   static constexpr int HV = C <= 8 ? 1 : 2;        // groups that share a tile's columns
   static constexpr int CT = C / HV;                // columns of a thread
-  static constexpr int NCH = NC / HV;              // 16-column chunks of a thread
+  static constexpr int NCH = NC / HV;              // 16-column chunks of scores of a thread
+  static constexpr int CPW = 8 / WS;               // columns per 8 weight pieces (16 bytes)
+  static constexpr int NCW = CT / CPW;             // such chunks of a thread
   static constexpr int NS = 256 * HV;              // softmax threads
   static constexpr int NT = NS + 64;               // all threads
   static constexpr size_t MISC = 4096;
@@ -88,6 +94,9 @@ struct QaShape {
   static constexpr size_t SMEM = 1024 + (size_t)ST * STAGE + QB + 2 * PB + MISC;
   static constexpr uint32_t SWZ = HD == 128 ? 2 : 4;  // 128- or 64-byte swizzle
   static_assert(ST >= 2, "ring");
+  static_assert(NCW * CPW == CT && CPW % 2 == 0 && NW % 16 == 0, "weight chunks");
+  // (the weights' buffers hold a segment's sums at its end)
+  static_assert(2 * PB >= C * HD * 4 && 2 * PB >= (NS > C * HD / 4 ? NS * 16 : 0), "sums");
 };
 
 // one tile of tokens: ntok tokens whose queries are rows qrow .. of q; token i sees start <= t < end0 + i
@@ -219,7 +228,8 @@ LLM_D float qa_exp2(float x) {
 // T tiles cut into G runs, the first T % G of them one longer; a cut within `near` tiles of a unit's
 // start or end moves there: a segment costs about as much as four tiles besides its tiles, and a cut unit
 // its join, which whole units save at the price of runs that are uneven by as much (16 rows of 5 tokens,
-// 32 heads of 64, about 900 positions: 31 us without, 26 us with; 8 positions instead of 4: the same).
+// 32 heads of 64, about 900 positions: 34 us without, 29 us with; 32 rows of up to 2100 positions, 8 heads of
+// 128: 33 without, 34 with).
 struct QaCut {
   int q, r, near;
   LLM_D void make(int T, int G) {
@@ -253,24 +263,34 @@ LLM_D void qa_put4(void* out, int64_t at, float4 o) {
     *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = o;
 }
 
-// pairs of f16: from f32, their e4m3 codes, and 32 times what the codes leave over (exact)
-LLM_D uint32_t qa_half2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
+// sixteen e4m3 codes to bf16 (exact)
+LLM_D void qa_widen16(const uint4& u, uint4& lo, uint4& hi) {
+  const float4 a = e4m3_quad(u.x), b = e4m3_quad(u.y), c = e4m3_quad(u.z), d = e4m3_quad(u.w);
+  lo = make_uint4(bf16x2(a.x, a.y), bf16x2(a.z, a.w), bf16x2(b.x, b.y), bf16x2(b.z, b.w));
+  hi = make_uint4(bf16x2(c.x, c.y), bf16x2(c.z, c.w), bf16x2(d.x, d.y), bf16x2(d.z, d.w));
 }
-LLM_D uint32_t qa_e4m3_half2(uint32_t h) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-  return r;
-}
-LLM_D uint32_t qa_rest32(uint32_t h, uint32_t code) {
-  uint32_t r;
-  asm("{\n\t.reg .b32 d, k;\n\tcvt.rn.f16x2.e4m3x2 d, %2;\n\tsub.rn.f16x2 d, %1, d;\n\tmov.b32 k, 0x50005000;\n\t"
-      "mul.rn.f16x2 %0, d, k;\n\t}"
-      : "=r"(r)
-      : "r"(h), "h"((uint16_t)code));
-  return r;
+
+// The values of a tile in bf16, in the place of its keys and values (`stage`), whose scores are done: the row of
+// a position has HD bytes in either half of the stage; the first HD / 2 dimensions go where its key was, the
+// others where its codes were, swizzled as the codes were.  HV lanes of one warp share a row (r; sub: the lane's
+// place), so that no other warp touches what this one reads or writes, and a step overwrites only codes that
+// have been read.  Rows that no column sees (live false: dead data, any code, NaN's among them) become zeros.
+template <int HD, int HV>
+LLM_D void qa_widen_row(unsigned char* stage, int r, int sub, bool live) {
+  constexpr int HB = HD / 32;  // 16-byte chunks of codes of half a row
+  const int swz = HD == 128 ? r & 7 : r >> 1 & 3;
+  unsigned char* codes = stage + kQaTile * HD + r * HD;
+#pragma unroll 4
+  for (int i = 0; i < 2 * HB; i += HV) {
+    const int from = i + sub, to = 2 * (from % HB);
+    uint4 x = *reinterpret_cast<const uint4*>(codes + (from ^ swz) * 16), lo, hi;
+    if (!live) x = make_uint4(0u, 0u, 0u, 0u);
+    if (HV > 1) __syncwarp();
+    qa_widen16(x, lo, hi);
+    unsigned char* dst = i < HB ? stage + r * HD : codes;
+    *reinterpret_cast<uint4*>(dst + (to ^ swz) * 16) = lo;
+    *reinterpret_cast<uint4*>(dst + ((to + 1) ^ swz) * 16) = hi;
+  }
 }
 
 // the walk of one CTA's run over (token tile, kv head, position tiles)
@@ -313,6 +333,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
     qattn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const QAttnArgs a) {
   using X = QaShape<HD, NP, NC>;
   constexpr int N = X::N, C = X::C, CPC = X::CPC, ST = X::ST, CT = X::CT, NCH = X::NCH, HV = X::HV, NS = X::NS;
+  constexpr int NW = X::NW, WS = X::WS, WP = X::WP, CPW = X::CPW, NCW = X::NCW;
   extern __shared__ unsigned char qraw[];
   const uint32_t s_raw = smem_u32(qraw);
   unsigned char* base = qraw + (((s_raw + 1023u) & ~1023u) - s_raw);
@@ -485,7 +506,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   } else if (warp == 1) {
     // ---- MMA issuer ----
     if (lane == 0) {
-      const uint32_t id_s = idesc_e4m3_f32(kQaTile, N, 0), id_o = idesc_e4m3_f32(HD, N, 1);
+      const uint32_t id_s = idesc_e4m3_f32(kQaTile, N), id_o = idesc_bf16_f32(HD, NW, 1);
       const uint32_t q_addr = smem_u32(qbuf), p_addr = smem_u32(pbuf);
       uint32_t cnt[2] = {0u, 0u};   // tiles whose weights each parity's groups have written
       uint32_t qpar = 0u;
@@ -517,11 +538,11 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
           wait(b_p + 8u * gp, cnt[gp]++ & 1u);
           if (ok) {
             tc_fence_after();
-            const uint32_t v_addr = s_ring + vs * X::STAGE + X::KB;
+            const uint32_t v_addr = s_ring + vs * X::STAGE;
 #pragma unroll
-            for (int kk = 0; kk < kQaTile / 32; ++kk)
-              tc_mma_e4m3(tmem + 2 * N + gp * N, smem_desc(v_addr + kk * 32 * HD, 8 * HD, 8 * HD, X::SWZ),
-                          smem_desc(p_addr + gp * X::PB + kk * 512, 128, 2048, 0), id_o, t > 1 || kk > 0);
+            for (int kk = 0; kk < kQaTile / 16; ++kk)
+              tc_mma_bf16(tmem + 2 * N + gp * NW, smem_desc(v_addr + kk * 16 * HD, X::KB, 8 * HD, X::SWZ),
+                          smem_desc(p_addr + gp * X::PB + kk * 256, 128, 2048, 0), id_o, t > 1 || kk > 0);
             tc_commit(b_pv + 8u * gp);
             tc_commit(b_empty + 8u * vs);
           }
@@ -537,8 +558,8 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
     const int stid = tid - 64, gtid = stid & 127;
     const int c0 = half * CT;               // this thread's columns
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t t_s = tmem + gp * N + c0 * NP + lanes, t_o = tmem + 2 * N + gp * N + c0 * NP + lanes;
-    unsigned char* pmine = pbuf + gp * X::PB + half * NCH * 2048 + (quad * 32 + lane) * 16;
+    const uint32_t t_s = tmem + gp * N + c0 * NP + lanes, t_o = tmem + 2 * N + gp * NW + c0 * WS + lanes;
+    unsigned char* pmine = pbuf + gp * X::PB + half * NCW * 2048 + (quad * 32 + lane) * 16;
     const int H = a.c.kv * a.g;
     auto all_sync = [&]() { named_sync(5, NS); };
     auto group_sync = [&]() { named_sync(1 + group, 128); };
@@ -642,6 +663,8 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         const bool good = !(ks < 0.f) && pos < w.u.last && pos >= w.u.start;
         const bool whole = __all_sync(0xffffffffu, good) && p0 + kQaTile <= w.u.end0;
         const int mypos = good ? pos : 0x7fffffff;
+        const int wr = quad * 32 + (HV == 1 ? lane : half * 16 + (lane & 15));
+        const bool wlive = HV == 1 ? good : __ballot_sync(0xffffffffu, good) >> (wr & 31) & 1u;
         wait(b_s + 8u * gp, cs++ & 1u);
         __syncwarp();
         tc_fence_after();
@@ -692,7 +715,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
           group_sync();
           if (gtid < CT) {
             const float old = ref[gtid];
-            const float top = fmaxf(old, fmaxf(fmaxf(wm[gtid], wm[C + gtid]), fmaxf(wm[2 * C + gtid], wm[3 * C + gtid])) - (t > gp ? kQaTop : kQaFirst<QT>));
+            const float top = fmaxf(old, fmaxf(fmaxf(wm[gtid], wm[C + gtid]), fmaxf(wm[2 * C + gtid], wm[3 * C + gtid])));
             ref[gtid] = top;
             wm[gtid] = top == old ? 1.f : qa_exp2(old - top);
           }
@@ -717,13 +740,13 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
-            for (int ch = 0; ch < NCH; ++ch) {
-              float d[16];
-              tc_ld16(t_o + ch * 16, d);
+            for (int ch = 0; ch < NCW; ++ch) {
+              float d[8];
+              tc_ld8(t_o + ch * 8, d);
               tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) d[i] *= wm[ch * CPC + i / NP] * vcorr;
-              tc_st16(t_o + ch * 16, d);
+              for (int i = 0; i < 8; ++i) d[i] *= wm[ch * CPW + i / WS] * vcorr;
+              tc_st8(t_o + ch * 8, d);
             }
             tc_wait_st();
           }
@@ -737,13 +760,14 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
               if (s[c] > -INFINITY) s[c] = __uint_as_float(0x7fc00000u);
           }
         }
+        qa_widen_row<HD, HV>(base + slot * X::STAGE, wr, lane >> 4 & (HV - 1), wlive);
         if (pend) wait(b_pv + 8u * gp, cpv++ & 1u);  // the weights' buffer is free again
 #pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) {
-          uint32_t o[4];  // 16 codes: CPC columns of NP pieces
+        for (int ch = 0; ch < NCW; ++ch) {
+          uint32_t o[4];  // 8 pieces: CPW columns of WS
 #pragma unroll
-          for (int i = 0; i < CPC; i += 2) {
-            const int c = ch * CPC + i;
+          for (int i = 0; i < CPW; i += 2) {
+            const int c = ch * CPW + i;
             const float2 rv = *reinterpret_cast<const float2*>(ref + c);
             // a weight (0 where the column does not see the position), its sum, and with the value's
             // scale on it
@@ -752,38 +776,28 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
             l[c + 1] += x1;
             x0 *= vr;
             x1 *= vr;
-            uint32_t x[NP];
-            if constexpr (NP == 2) {
-              // (two pieces hold eight bits: the eleven of f16 are enough to take them from, in packed pairs)
-              const uint32_t h = qa_half2(x0, x1);
-              x[0] = qa_e4m3_half2(h);
-              x[1] = qa_e4m3_half2(qa_rest32(h, x[0]));
+            // bf16 pieces: what one leaves over goes into the next
+            const uint32_t w0 = bf16x2(x0, x1);
+            if constexpr (WS == 1) {
+              o[i / 2] = w0;
             } else {
-#pragma unroll
-              for (int y = 0; y < NP; ++y) {
-                x[y] = e4m3x2(x0, x1);
-                if (y + 1 < NP) {
-                  const float2 v = e4m3_pair(x[y]);
-                  x0 = (x0 - v.x) * 32.f;
-                  x1 = (x1 - v.y) * 32.f;
-                }
+              x0 -= bf16_lo(w0);
+              x1 -= bf16_hi(w0);
+              const uint32_t w1 = bf16x2(x0, x1);
+              const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
+              if constexpr (WS == 2) {
+                o[i] = a0;
+                o[i + 1] = a1;
+              } else {
+                const uint32_t w2 = bf16x2(x0 - bf16_lo(w1), x1 - bf16_hi(w1));
+                o[0] = a0;
+                o[1] = w2 & 0xffffu;
+                o[2] = a1;
+                o[3] = w2 >> 16;
               }
-            }
-            if constexpr (NP == 4) {
-              const uint32_t a01 = x[0] | x[1] << 16, a23 = x[2] | x[3] << 16;
-              o[i] = __byte_perm(a01, a23, 0x6420);
-              o[i + 1] = __byte_perm(a01, a23, 0x7531);
-            } else {
-              o[i / 2] = __byte_perm(x[0], x[1], 0x5140);
             }
           }
           *reinterpret_cast<uint4*>(pmine + ch * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        if (mypos == 0x7fffffff && half == 0) {
-          // rows that no column sees hold dead data (any code, NaN among them): zeros
-          uint4* v = reinterpret_cast<uint4*>(base + slot * X::STAGE + X::KB + (quad * 32 + lane) * HD);
-#pragma unroll 1
-          for (int e = 0; e < HD / 16; ++e) v[e] = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -853,16 +867,16 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
       for (int pass = 1; pass >= 0; --pass) {
         if (gp == pass && (both || pass == 0)) {
 #pragma unroll 1
-          for (int ch = 0; ch < NCH && c0 + ch * CPC < used; ++ch) {
-            float d[16];
-            tc_ld16(t_o + ch * 16, d);
+          for (int ch = 0; ch < NCW && c0 + ch * CPW < used; ++ch) {
+            float d[8];
+            tc_ld8(t_o + ch * 8, d);
             tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < CPC; ++i) {
-              const int c = c0 + ch * CPC + i;
-              float v = d[i * NP + NP - 1];
+            for (int i = 0; i < CPW; ++i) {
+              const int c = c0 + ch * CPW + i;
+              float v = d[i * WS + WP - 1];
 #pragma unroll
-              for (int x = NP - 2; x >= 0; --x) v = fmaf(v, 0.03125f, d[i * NP + x]);
+              for (int x = WP - 2; x >= 0; --x) v += d[i * WS + x];
               v *= ffac[pass * C + c];
               if (d_on && c < used) {
                 if (pass == 0 && both) v += other[c * HD + d_row];

@@ -135,13 +135,20 @@ LLM_D void tc_ld16(uint32_t taddr, float (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-// the same 32 x 16 block written back
-LLM_D void tc_st16(uint32_t taddr, const float (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
-      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
-      : "memory");
+// 32 lanes x 8 columns, and the same block written back
+LLM_D void tc_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+LLM_D void tc_st8(uint32_t taddr, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 LLM_D void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 LLM_D void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -159,11 +166,12 @@ LLM_D uint64_t sw128_kmajor_desc(uint32_t saddr) {
   return d;
 }
 
-// Instruction descriptor of kind::f16 with bf16 A and B, f32 accumulator, both K-major:
-// [4,6) D format (1 = f32); [7,10) A format (1 = bf16); [10,13) B format (1 = bf16);
-// [17,23) N >> 3; [24,29) M >> 4.
-LLM_HD uint32_t idesc_bf16_f32(int M, int N) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor of kind::f16 with bf16 A and B, f32 accumulator, both K-major (mn = 1: both
+// stored with their M and N dimension contiguous): [4,6) D format (1 = f32); [7,10) A format
+// (1 = bf16); [10,13) B format (1 = bf16); [15], [16] A, B M/N-major; [17,23) N >> 3; [24,29) M >> 4.
+LLM_HD uint32_t idesc_bf16_f32(int M, int N, int mn = 0) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)mn << 15) | ((uint32_t)mn << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
 }
 
 // Shared-memory matrix descriptor with its offsets and layout given (2 = 128-byte swizzle, 4 =
@@ -173,10 +181,10 @@ LLM_D uint64_t smem_desc(uint32_t saddr, uint32_t lead, uint32_t stride, uint32_
          (uint64_t)1 << 46 | (uint64_t)layout << 61;
 }
 
-// Instruction descriptor of kind::f8f6f4 with e4m3 A and B (formats 0) and an f32 accumulator;
-// mn = 1: A and B are stored with their M and N dimension contiguous (bits 15 and 16).
-LLM_HD uint32_t idesc_e4m3_f32(int M, int N, int mn) {
-  return (1u << 4) | ((uint32_t)mn << 15) | ((uint32_t)mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor of kind::f8f6f4 with e4m3 A and B (formats 0), both K-major, and an f32
+// accumulator.
+LLM_HD uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 }  // namespace llm
