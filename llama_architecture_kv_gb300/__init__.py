@@ -376,11 +376,15 @@ def _rows(t, name, dev, B, S, width):
     return t.data_ptr(), step
 
 
+def _stream(stream, dev):
+    return _torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+
+
 class QCache:
     """An 8-bit key/value cache over torch tensors: codes k, v [rows, kv_heads, max_seq, head]
     (uint8 or float8_e4m3fn) and scales [rows, kv_heads, max_seq // 16] (float32), all zeroed before
     their first use.  The tensors stay the caller's; calls are ordered on `stream` (a cudaStream_t,
-    None: the legacy default stream) and return without waiting.  `pos`, `length`, `count` [B] and
+    None: torch's current stream) and return without waiting.  `pos`, `length`, `count` [B] and
     `table` [B, pages] are int32 CUDA tensors, `status` one int32; rows of tokens are f32 or bf16."""
 
     def __init__(self, k, v, k_scale, v_scale):
@@ -441,7 +445,7 @@ class QCache:
         if step != vstep:
             _bad("k and v must have the same row stride")
         st = self._lib.llm_qcache_write(self._c, kp, vp, self._dtype(k, v), step, B, S, first, count, table, pages, status,
-                                        stream)
+                                        _stream(stream, self._dev))
         if st != LLM_OK:
             _refused("llm_qcache_write", st)
 
@@ -455,7 +459,7 @@ class QCache:
         if step != vstep:
             _bad("k and v must have the same row stride")
         st = self._lib.llm_qcache_read(self._c, B, S, first, count, table, pages, kp, vp, self._dtype(k, v), step, status,
-                                       stream)
+                                       _stream(stream, self._dev))
         if st != LLM_OK:
             _refused("llm_qcache_read", st)
 
@@ -486,7 +490,8 @@ class QCache:
             _bad("workspace must be contiguous CUDA memory beside the cache")
         st = self._lib.llm_qcache_attend(self._c, qp, self._dtype(q, out), qstep, group, B, S, first, count, table, pages,
                                          self._scale if scale is None else scale, op, ostep, workspace.data_ptr(),
-                                         workspace.numel() * workspace.element_size(), status, stream)
+                                         workspace.numel() * workspace.element_size(), status,
+                                         _stream(stream, self._dev))
         if st != LLM_OK:
             _refused("llm_qcache_attend", st)
 
@@ -500,7 +505,8 @@ def _f32s(t, name, dev, n):
 def llm_verify(p, q, drafts, u, ids, accepted, count=None, stream=None):
     """Verification of drafts [B, S] against the target's probabilities p [B, S + 1, V], the draft
     model's q [B, S, V] (None: deterministic drafts) and draws u [B, S + 1], into ids [B, S + 1] and
-    accepted [B] (see include/llm.h); CUDA tensors, f32 and int32."""
+    accepted [B] (see include/llm.h); CUDA tensors, f32 and int32; ordered on `stream` (None: torch's
+    current stream)."""
     torch = _torch or _need_torch()
     if drafts.dim() != 2 or p.dim() != 3:
         _bad("drafts must be [B, S] and p [B, S + 1, V]")
@@ -515,7 +521,7 @@ def llm_verify(p, q, drafts, u, ids, accepted, count=None, stream=None):
     st = lib().llm_verify(_f32s(p, "p", dev, B * (S + 1) * V), None if q is None else _f32s(q, "q", dev, B * S * V),
                           _int32(drafts, "drafts", dev, B * S), None if count is None else _int32(count, "count", dev, B),
                           B, S, V, _f32s(u, "u", dev, B * (S + 1)), _int32(ids, "ids", dev, B * (S + 1)),
-                          _int32(accepted, "accepted", dev, B), stream)
+                          _int32(accepted, "accepted", dev, B), _stream(stream, dev))
     if st != LLM_OK:
         _refused("llm_verify", st)
 
