@@ -275,19 +275,20 @@ namespace {
 // of a row's (token, head) columns, else the largest: a tile's cost grows with its columns (five tokens of
 // a group of four in each of 32 rows of 2048 positions: 66 us with 24 columns, 70 us with 32), and every
 // further tile reads the codes again
+int64_t q_tiles_of(int limit) { return ((int64_t)limit + kQaTile - 1) / kQaTile; }
 struct TcPlanQ {
   int nc, cols, tokens, grid;
 };
-TcPlanQ plan_tc_q(const QCacheView& c, int g, int qt, int64_t rows, int S, int limit, int num_sms) {
+TcPlanQ plan_tc_q(const QCacheView& c, int g, int qt, int64_t rows, int64_t S, int limit, int num_sms) {
   const int np = qt ? 2 : 4, most = qt ? 4 : 8;
   TcPlanQ p;
   p.nc = 1;
   // (f32: 1, 2, 4, 6 or 8; bf16: 1, 2 or 4)
-  while (p.nc < most && (int64_t)p.nc * 16 / np < (int64_t)S * g) p.nc = p.nc < 4 ? p.nc * 2 : p.nc + 2;
+  while (p.nc < most && p.nc * 16 / np < S * g) p.nc = p.nc < 4 ? p.nc * 2 : p.nc + 2;
   p.cols = p.nc * 16 / np;
   p.tokens = p.cols / g;
   const int64_t units = rows * ((S + p.tokens - 1) / p.tokens) * c.kv;
-  const int64_t tiles = units * ((limit + kQaTile - 1) / kQaTile);
+  const int64_t tiles = units * q_tiles_of(limit);
   const int64_t ctas = std::min(num_sms * (p.cols <= 8 ? 2 : 1), kQattnTickets / 4);
   p.grid = (int)std::max<int64_t>(1, std::min(tiles, ctas));
   return p;
@@ -306,7 +307,7 @@ bool qattn_make_map(CUtensorMap* map, const void* codes, int hd, uint64_t rows) 
 bool qattn_fits(const QCacheView& c, int g, int qt, int B, int S, int limit, int num_sms) {
   if (!qattn_uses_tc(c.hd)) return true;
   const TcPlanQ p = plan_tc_q(c, g, qt, B, S, limit, num_sms);
-  return (double)B * ((S + p.tokens - 1) / p.tokens) * c.kv * ((limit + kQaTile - 1) / kQaTile) < 2147483648.0;
+  return (double)B * (((int64_t)S + p.tokens - 1) / p.tokens) * c.kv * q_tiles_of(limit) < 2147483648.0;
 }
 
 uint64_t qattn_workspace(const QCacheView& c, int g, int B, int S, int num_sms) {
@@ -347,7 +348,7 @@ cudaError_t launch_qattn(const QAttnArgs& a0, int qt, int num_sms, cudaStream_t 
     // (a page table can name a page more than once: rows longer than the pool get no more CTAs)
     const TcPlanQ p = plan_tc_q(a.c, a.g, qt, a.r.B, S, std::min(a.r.limit, a.c.rows * a.c.cap), num_sms);
     a.tpt = p.tokens;
-    a.nct = a.r.step ? 1 : (a.r.S + p.tokens - 1) / p.tokens;
+    a.nct = a.r.step ? 1 : (int)(((int64_t)a.r.S + p.tokens - 1) / p.tokens);
     const bool wide = p.nc > 4;
     auto fn = a.c.hd == 64 ? (qt ? qattn_tc64_bf16 : wide ? qattn_tc64_f32_wide : qattn_tc64_f32)
                            : (qt ? qattn_tc128_bf16 : wide ? qattn_tc128_f32_wide : qattn_tc128_f32);

@@ -389,7 +389,9 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   // and the lane whose stretch holds the run's start finds its token tile
   const int nq = a.r.step ? (a.tiles ? a.tiles[1] : a.r.B) : a.r.B * a.nct;
   if (warp == 0) {
-    const int per = (nq + 31) / 32, t0 = min(nq, lane * per), t1 = min(nq, t0 + per);
+    // (unsigned: sums of numbers below 2^31)
+    const uint32_t nu = (uint32_t)nq, pu = (nu + 31u) / 32u, tu = min(nu, lane * pu);
+    const int per = (int)pu, t0 = (int)tu, t1 = (int)min(nu, tu + pu);
     int sum = 0;
 #pragma unroll 1
     for (int t = t0; t < t1; ++t) sum += qa_unit(a, t).nt;
@@ -565,8 +567,8 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
     auto group_sync = [&]() { named_sync(1 + group, 128); };
     // tokens that see nothing and share a tile with none that does: zeros
 #pragma unroll 1
-    for (int t = cta; t < nq; t += gridDim.x) {
-      const QaUnit u = qa_unit(a, t);
+    for (uint32_t t = cta; t < (uint32_t)nq; t += gridDim.x) {
+      const QaUnit u = qa_unit(a, (int)t);
       if (u.nt == 0 && u.ntok > 0)
 #pragma unroll 1
         for (int64_t i = stid; i < (int64_t)u.ntok * H * HD; i += NS) {

@@ -117,7 +117,7 @@ LLM_D float q_scale(float amax) {
 LLM_D float q_recip(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
 // blocks that S tokens can touch
-LLM_HD int q_span(int S) { return (S - 1 + kQBlock - 1) / kQBlock + 1; }
+LLM_HD int q_span(int S) { return (S - 1) / kQBlock + ((S - 1) % kQBlock ? 2 : 1); }
 
 // ---- launches -----------------------------------------------------------------------------
 bool qcache_head_supported(int hd);

@@ -54,6 +54,15 @@ def test_cache_calls_refuse_bad_arguments(lib, call):
     assert lib.llm_last_error(None)
 
 
+@pytest.mark.parametrize("call", [write, read])
+def test_cache_calls_refuse_more_warps_than_a_launch_has(lib, call):
+    # blocks that 2^31 - 1 tokens can touch times 16 heads, and the neighbours of the bound of 2^30
+    wide = dict(rows=1, kv_heads=16, max_seq=16)
+    for S in ((1 << 31) - 1, (1 << 31) - 16, 1 << 30, ((1 << 26) - 2) * 16 + 2):
+        assert call(lib, c=cache(**wide), B=1, S=S, stride=1024) == ARG, S
+        assert b"too large" in lib.llm_last_error(None)
+
+
 def test_attention_refuses_bad_arguments(lib):
     def attend(c=None, q=P, dtype=1, q_stride=256, group=2, B=2, S=1, length=P, count=None, table=None, pages=0,
                scale=0.125, out=P, out_stride=256, ws=P, nbytes=1 << 40, status=None):
