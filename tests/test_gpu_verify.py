@@ -144,3 +144,26 @@ def test_captured_call_replays():
         torch.cuda.synchronize()
         for b in range(B):
             assert (ids[b].tolist(), int(acc[b])) == ref.verify(p[b], q[b], dn[b], None, un[b])
+
+
+@pytest.mark.parametrize("V", [5, 7, 64, 1000, 50001])
+@pytest.mark.parametrize("big", [np.inf, 1e30, 3.0])
+def test_rows_that_are_no_probabilities_draw_an_id_of_the_vocabulary(V, big):
+    # weights above 1 count as 1: up to seven of them are drawn from as defined, more give some id
+    rng = np.random.default_rng(V)
+    B, S = 16, 3
+    p = np.full((B, S + 1, V), big, np.float32)
+    q = softmax(rng.standard_normal((B, S, V)))
+    d = rng.integers(0, V, (B, S))
+    kept = np.arange(B) % (S + 1)
+    d[np.arange(B), np.minimum(kept, S - 1)] = np.where(kept < S, -1, d[np.arange(B), S - 1])   # lost there, or nowhere
+    u = (rng.integers(0, 1 << 24, (B, S + 1)) / (1 << 24)).astype(np.float32)
+    for draft in (q, None):
+        ids, acc = run(p, draft, d, u)
+        assert np.array_equal(acc, kept)
+        for b in range(B):
+            r = kept[b]
+            assert ids[b, :r].tolist() == d[b, :r].tolist() and (ids[b, r + 1:] == -1).all()
+            assert 0 <= ids[b, r] < V
+            if V <= 7:
+                assert (ids[b].tolist(), r) == ref.verify(p[b], None if draft is None else draft[b], d[b], None, u[b])
