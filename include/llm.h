@@ -452,7 +452,7 @@ typedef struct llm_qcache {
  * when it grows; new codes are x / scale to nearest even.  So writing at a position ends what the
  * block held after the new tokens (their codes stay, their scale may not).  A value that is not
  * finite makes its block's scale NaN: all of it reads as NaN until its first position is written anew.
- * Two rows of one call must not write the same block.  B * (S / 16 + 2) * kv_heads below 2^30 always
+ * No block may be written twice by one call (by two rows, or by a row whose table names a page twice).  B * (S / 16 + 2) * kv_heads below 2^30 always
  * fits one call (else LLM_ERR_ARG; of llm_qcache_read too).
  */
 llm_status llm_qcache_write(const llm_qcache* cache, const void* k_dev, const void* v_dev, int32_t dtype,

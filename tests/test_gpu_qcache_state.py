@@ -7,9 +7,13 @@ import llama_architecture_kv_gb300 as pkg
 import synth
 from synth import shrink
 from synth.configs import TINY
-from tests.test_gpu_qcache_model import E4M3, SHAPES, make
+from tests.test_gpu_qcache_model import E4M3, LLAMA8, SHAPES, make
 
 pytestmark = pytest.mark.gpu
+
+# with the head sizes of the attention on CUDA cores
+ALL = SHAPES + [("f32_hd32", shrink(TINY, kv=3, g=2, half=16, ffn=200, vocab=300), 3, 0),
+                ("bf16_hd256", shrink(LLAMA8, layers=2, kv=1, g=2, half=128, ffn=512, vocab=1000), 4, 1)]
 
 
 def bits(x):
@@ -128,7 +132,7 @@ def chain_of(g, start, pos, n):
 
 
 @pytest.mark.parametrize("cache", [pkg.LLM_CACHE_MODEL, E4M3], ids=["model", "e4m3"])
-@pytest.mark.parametrize("name,shape,B,tc", SHAPES, ids=[s[0] for s in SHAPES])
+@pytest.mark.parametrize("name,shape,B,tc", ALL, ids=[s[0] for s in ALL])
 def test_probabilities_do_not_depend_on_later_drafts(name, shape, B, tc, cache):
     n, S, cap = 24, 5, 128
     g = make(shape, 841, B, cap, tc_min_batch=tc, cache_type=cache, wstd=0.2 if not shape.bf16 else 0.06)
@@ -152,7 +156,7 @@ def test_probabilities_do_not_depend_on_later_drafts(name, shape, B, tc, cache):
     g.close()
 
 
-@pytest.mark.parametrize("name,shape,B,tc", SHAPES, ids=[s[0] for s in SHAPES])
+@pytest.mark.parametrize("name,shape,B,tc", ALL, ids=[s[0] for s in ALL])
 def test_drafts_that_are_not_kept_leave_nothing_behind(name, shape, B, tc):
     from tests import qcache_ref as ref
     from tests.test_gpu_qcache_model import wide
