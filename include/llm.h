@@ -473,7 +473,7 @@ llm_status llm_qcache_read(const llm_qcache* cache, int32_t B, int32_t S, const 
  * last `count` of the length, so a token sees those before it and itself):
  *   out = sum softmax(scale * q . k) v,  statistics and sums in f32; a token that sees nothing gets 0.
  * Heads of 64 and 128: a query is held to 2^-19 of its largest element, a weight (times the ratio of its block's
- * value scale to the largest) to 2^-17 (bf16: 2^-8) of itself, down to 2^-100 of the token's largest.
+ * value scale to the largest) to 2^-26 (bf16: 2^-17) of itself, down to 2^-100 of the token's largest.
  * (B * S * kv_heads * positions a row can hold / 128 below 2^31 always fits one call, else LLM_ERR_ARG.)
  * q and out are rows of kv_heads * group * head elements at q_stride and out_stride, both of type
  * dtype; they must not overlap.  group is 1..16 with group * head <= 1024 (else LLM_ERR_CONFIG).

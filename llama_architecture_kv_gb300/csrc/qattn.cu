@@ -273,7 +273,7 @@ namespace {
 
 // the tensor-core kernel's tiles: 16 nc accumulator columns of np pieces, the smallest that holds all
 // of a row's (token, head) columns, else the largest: a tile's cost grows with its columns (five tokens of
-// a group of four in each of 32 rows of 2048 positions: 66 us with 24 columns, 70 us with 32), and every
+// a group of four in each of 32 rows of 2048 positions: 69 us with 24 columns, 74 us with 32), and every
 // further tile reads the codes again
 int64_t q_tiles_of(int limit) { return ((int64_t)limit + kQaTile - 1) / kQaTile; }
 struct TcPlanQ {

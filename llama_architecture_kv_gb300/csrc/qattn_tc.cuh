@@ -42,9 +42,9 @@
 // where a CTA has only a few tiles (a segment costs about 4 us besides its tiles: first loads, the groups'
 // sums, the join).  Widening by integer steps instead of conversions, rolled or before the scores are there,
 // measured the same.  GB300, f32 queries, heads of 128, groups of 4, 8 key/value heads: 8 rows of 32768
-// positions 91 us (538 MB: 5.9 TB/s, 87% of the copy rate); one row of 131072 56 us (4.8 TB/s); 32 rows of up
-// to 2100 34 us (108 MB: 3.2 TB/s); one row of 2048 10.0 us; five tokens in each of 32 rows of 2048 66 us (20
-// columns).  bf16 queries, 8 tokens at 131072 positions (32 columns): 87 us (269 MB: 3.1 TB/s).
+// positions 92 us (538 MB: 5.8 TB/s, 86% of the copy rate); one row of 131072 56 us (4.8 TB/s); 32 rows of up
+// to 2100 34 us (108 MB: 3.2 TB/s); one row of 2048 10.1 us; five tokens in each of 32 rows of 2048 69 us (20
+// columns).  bf16 queries, 8 tokens at 131072 positions (32 columns): 94 us (269 MB: 2.9 TB/s).
 #pragma once
 #include "attention.cuh"
 #include "qcache.cuh"
@@ -55,6 +55,12 @@ namespace llm {
 constexpr int kQaTile = 128;                       // positions per tile
 constexpr uint64_t kQaWaitCycles = 1000000000ull;  // about 0.5 s
 constexpr float kQaMost = 32.0f;                   // log2 of the largest weight that moves no reference
+// Tiles that a group's products are summed over in their accumulator before they are added to the group's sums: a
+// product's additions are not rounded to nearest but cut off (8 per tile, each by up to 2^-23 of the sum), so
+// that with all of a run's tiles in one accumulator digits of one sign are lost.  f32, 8 rows of 32768 positions:
+// 3.9e-6 of the result, with 4 tiles 0.9e-6, with one 0.8e-6 at 1 to 6% more time (f32 sums in one order:
+// 1.4e-6).  bf16: 256 cuts are still 2^-16, well below the output's rounding (32 columns: 94 us, with 4 tiles 96).
+template <int QT> constexpr int kQaRun = QT ? 32 : 4;
 constexpr int kQaNear = 4;                         // most tiles by which a cut moves to a unit's end
 constexpr float kQaNone = -3.0e38f;                // a reference before any score
 constexpr size_t kQaSmem = 232448;                 // shared memory a CTA can have
@@ -64,27 +70,28 @@ struct QaShape {
   static constexpr int N = 16 * NC;                // score columns
   static constexpr int C = N / NP;                 // (token, head) columns
   static constexpr int CPC = 16 / NP;              // of them per 16 score columns
-  // A weight's bf16 pieces, and the columns that they take (at least 16 in all, an MMA's least): one piece for
-  // bf16 queries, whose rounding (2^-8 of the weight) is the output's own, two for f32 (2^-17); where they would
-  // not fill the 16 columns, as many as do (two more and a column of zeros: 2^-26)
-  static constexpr int WS = C * (NP == 4 ? 2 : 1) >= 16 ? (NP == 4 ? 2 : 1) : 16 / C;
-  static constexpr int WP = WS < 4 ? WS : 3;
-  static constexpr int NW = C * WS;                // accumulator columns of the product over the values
-  static constexpr int KB = kQaTile * HD;          // bytes of a tile of keys (or values)
-  static constexpr int STAGE = 2 * KB;
-  static constexpr int QB = N * HD;                // query pieces of a segment
-  static constexpr int PB = 2 * kQaTile * NW;      // weight pieces of one parity's groups
-  static constexpr int COLS = 2 * (N + NW);
-  static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;  // columns
-  // Up to 8 columns two CTAs per SM (16 rows of 5 tokens of 32 heads of 64: 29 us against 42 us with one; 32 rows
-  // of one token of groups of 4: 34 against 41; one row of 131072: 56 against 64), more in one CTA whose groups
-  // halve them (16 rows of 16 columns at 2048 positions: 32 us against 39 us as two CTAs of whole columns)
+  // Up to 8 columns two CTAs per SM (16 rows of 5 tokens of 32 heads of 64: 30 us against 43 us with one; 32 rows
+  // of one token of groups of 4: 34 against 40; one row of 131072: 56 against 64), more in one CTA whose groups
+  // halve them (16 rows of 16 columns at 2048 positions: 33 us against 42 us as two CTAs of whole columns)
   static constexpr int CTAS = C <= 8 ? 2 : 1;
   static constexpr int HV = C <= 8 ? 1 : 2;        // groups that share a tile's columns
   static constexpr int CT = C / HV;                // columns of a thread
   static constexpr int NCH = NC / HV;              // 16-column chunks of scores of a thread
-  static constexpr int CPW = 8 / WS;               // columns per 8 weight pieces (16 bytes)
-  static constexpr int NCW = CT / CPW;             // such chunks of a thread
+  // A weight's bf16 pieces: three for f32 queries (2^-26 of the weight; with two, 2^-17, outputs are twice as far
+  // off as f32 sums leave them), two for bf16 (with one the outputs' error is 2.4e-3 of them instead of the
+  // 1.7e-3 that their own rounding makes).  A thread's pieces y of its columns c lie at y * CTP + c, 8 in 16 bytes.
+  static constexpr int WP = NP == 4 ? 3 : 2;
+  static constexpr int CTP = CT <= 4 ? 4 : (CT + 7) / 8 * 8;
+  static constexpr int NCW = (WP * CTP + 7) / 8;   // 16-byte chunks of pieces of a thread
+  static constexpr int HW = 8 * NCW;               // accumulator columns of a thread
+  static constexpr int NW = (HV * HW + 15) / 16 * 16;  // of the product over the values (an MMA takes multiples of 16;
+                                                       // what is more is never read)
+  static constexpr int KB = kQaTile * HD;          // bytes of a tile of keys (or values)
+  static constexpr int STAGE = 2 * KB;
+  static constexpr int QB = N * HD;                // query pieces of a segment
+  static constexpr int PB = 2 * kQaTile * NW;      // weight pieces of one parity's groups
+  static constexpr int COLS = 2 * (N + NW + C);
+  static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;  // columns
   static constexpr int NS = 256 * HV;              // softmax threads
   static constexpr int NT = NS + 64;               // all threads
   static constexpr size_t MISC = 4096;
@@ -94,7 +101,7 @@ struct QaShape {
   static constexpr size_t SMEM = 1024 + (size_t)ST * STAGE + QB + 2 * PB + MISC;
   static constexpr uint32_t SWZ = HD == 128 ? 2 : 4;  // 128- or 64-byte swizzle
   static_assert(ST >= 2, "ring");
-  static_assert(NCW * CPW == CT && CPW % 2 == 0 && NW % 16 == 0, "weight chunks");
+  static_assert(CT % 4 == 0 && COLS <= 512, "columns");
   // (the weights' buffers hold a segment's sums at its end)
   static_assert(2 * PB >= C * HD * 4 && 2 * PB >= (NS > C * HD / 4 ? NS * 16 : 0), "sums");
 };
@@ -228,7 +235,7 @@ LLM_D float qa_exp2(float x) {
 // T tiles cut into G runs, the first T % G of them one longer; a cut within `near` tiles of a unit's
 // start or end moves there: a segment costs about as much as four tiles besides its tiles, and a cut unit
 // its join, which whole units save at the price of runs that are uneven by as much (16 rows of 5 tokens,
-// 32 heads of 64, about 900 positions: 34 us without, 29 us with; 32 rows of up to 2100 positions, 8 heads of
+// 32 heads of 64, about 900 positions: 35 us without, 30 us with; 32 rows of up to 2100 positions, 8 heads of
 // 128: 33 without, 34 with).
 struct QaCut {
   int q, r, near;
@@ -333,7 +340,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
     qattn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const QAttnArgs a) {
   using X = QaShape<HD, NP, NC>;
   constexpr int N = X::N, C = X::C, CPC = X::CPC, ST = X::ST, CT = X::CT, NCH = X::NCH, HV = X::HV, NS = X::NS;
-  constexpr int NW = X::NW, WS = X::WS, WP = X::WP, CPW = X::CPW, NCW = X::NCW;
+  constexpr int NW = X::NW, WP = X::WP, CTP = X::CTP, NCW = X::NCW;
   extern __shared__ unsigned char qraw[];
   const uint32_t s_raw = smem_u32(qraw);
   unsigned char* base = qraw + (((s_raw + 1023u) & ~1023u) - s_raw);
@@ -544,7 +551,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
 #pragma unroll
             for (int kk = 0; kk < kQaTile / 16; ++kk)
               tc_mma_bf16(tmem + 2 * N + gp * NW, smem_desc(v_addr + kk * 16 * HD, X::KB, 8 * HD, X::SWZ),
-                          smem_desc(p_addr + gp * X::PB + kk * 256, 128, 2048, 0), id_o, t > 1 || kk > 0);
+                          smem_desc(p_addr + gp * X::PB + kk * 256, 128, 2048, 0), id_o, (t >> 1) % kQaRun<QT> != 0 || kk > 0);
             tc_commit(b_pv + 8u * gp);
             tc_commit(b_empty + 8u * vs);
           }
@@ -560,11 +567,27 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
     const int stid = tid - 64, gtid = stid & 127;
     const int c0 = half * CT;               // this thread's columns
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t t_s = tmem + gp * N + c0 * NP + lanes, t_o = tmem + 2 * N + gp * NW + c0 * WS + lanes;
+    const uint32_t t_s = tmem + gp * N + c0 * NP + lanes, t_o = tmem + 2 * N + gp * NW + half * X::HW + lanes,
+                   t_r = tmem + 2 * (N + NW) + gp * C + c0 + lanes;
     unsigned char* pmine = pbuf + gp * X::PB + half * NCW * 2048 + (quad * 32 + lane) * 16;
     const int H = a.c.kv * a.g;
     auto all_sync = [&]() { named_sync(5, NS); };
     auto group_sync = [&]() { named_sync(1 + group, 128); };
+    // four columns of the products: the accumulator's pieces, and what was added up before
+    auto sum4 = [&](int c, bool more, float (&v)[4]) {
+      float d[WP][4], r[4];
+#pragma unroll
+      for (int y = 0; y < WP; ++y) tc_ld4(t_o + y * CTP + c, d[y]);
+      if (more) tc_ld4(t_r + c, r);
+      tc_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = d[WP - 1][i];
+#pragma unroll
+        for (int y = WP - 2; y >= 0; --y) v[i] += d[y][i];
+        if (more) v[i] += r[i];
+      }
+    };
     // tokens that see nothing and share a tile with none that does: zeros
 #pragma unroll 1
     for (uint32_t t = cta; t < (uint32_t)nq; t += gridDim.x) {
@@ -742,13 +765,15 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
-            for (int ch = 0; ch < NCW; ++ch) {
-              float d[8];
-              tc_ld8(t_o + ch * 8, d);
+            for (int k = 0; k < (t >= 2 * kQaRun<QT> ? WP + 1 : WP) * (CT / 4); ++k) {  // (and the sums, once there are some)
+              const int y = k / (CT / 4), c = k % (CT / 4) * 4;
+              const uint32_t at = y < WP ? t_o + y * CTP + c : t_r + c;
+              float d[4];
+              tc_ld4(at, d);
               tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) d[i] *= wm[ch * CPW + i / WS] * vcorr;
-              tc_st8(t_o + ch * 8, d);
+              for (int i = 0; i < 4; ++i) d[i] *= wm[c + i] * vcorr;
+              tc_st4(at, d);
             }
             tc_wait_st();
           }
@@ -764,12 +789,29 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         }
         qa_widen_row<HD, HV>(base + slot * X::STAGE, wr, lane >> 4 & (HV - 1), wlive);
         if (pend) wait(b_pv + 8u * gp, cpv++ & 1u);  // the weights' buffer is free again
+        if (t >= 2 * kQaRun<QT> && (t >> 1) % kQaRun<QT> == 0) {
+          // the accumulator starts anew with this tile: what it holds goes to the sums
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < CT; c += 4) {
+            float v[4];
+            sum4(c, t >= 4 * kQaRun<QT>, v);
+            tc_st4(t_r + c, v);
+          }
+          tc_wait_st();
+        }
 #pragma unroll
-        for (int ch = 0; ch < NCW; ++ch) {
-          uint32_t o[4];  // 8 pieces: CPW columns of WS
+        for (int c8 = 0; c8 < CT; c8 += 8) {
+          uint32_t o[WP][4];  // the pieces of 8 columns, in pairs
 #pragma unroll
-          for (int i = 0; i < CPW; i += 2) {
-            const int c = ch * CPW + i;
+          for (int i = 0; i < 4; ++i) {
+            const int c = c8 + 2 * i;
+            if (c >= CT) {
+#pragma unroll
+              for (int y = 0; y < WP; ++y) o[y][i] = 0u;
+              continue;
+            }
             const float2 rv = *reinterpret_cast<const float2*>(ref + c);
             // a weight (0 where the column does not see the position), its sum, and with the value's
             // scale on it
@@ -778,28 +820,22 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
             l[c + 1] += x1;
             x0 *= vr;
             x1 *= vr;
-            // bf16 pieces: what one leaves over goes into the next
-            const uint32_t w0 = bf16x2(x0, x1);
-            if constexpr (WS == 1) {
-              o[i / 2] = w0;
-            } else {
-              x0 -= bf16_lo(w0);
-              x1 -= bf16_hi(w0);
-              const uint32_t w1 = bf16x2(x0, x1);
-              const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
-              if constexpr (WS == 2) {
-                o[i] = a0;
-                o[i + 1] = a1;
-              } else {
-                const uint32_t w2 = bf16x2(x0 - bf16_lo(w1), x1 - bf16_hi(w1));
-                o[0] = a0;
-                o[1] = w2 & 0xffffu;
-                o[2] = a1;
-                o[3] = w2 >> 16;
-              }
+#pragma unroll
+            for (int y = 0; y < WP; ++y) {  // each piece the rounding of what the ones before left over
+              o[y][i] = bf16x2(x0, x1);
+              x0 -= bf16_lo(o[y][i]);
+              x1 -= bf16_hi(o[y][i]);
             }
           }
-          *reinterpret_cast<uint4*>(pmine + ch * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
+          if constexpr (CT == 4) {
+            static_assert(CT != 4 || WP == 3, "pieces of four columns");
+            *reinterpret_cast<uint4*>(pmine) = make_uint4(o[0][0], o[0][1], o[1][0], o[1][1]);
+            *reinterpret_cast<uint4*>(pmine + 2048) = make_uint4(o[WP - 1][0], o[WP - 1][1], 0u, 0u);
+          } else {
+#pragma unroll
+            for (int y = 0; y < WP; ++y)
+              *reinterpret_cast<uint4*>(pmine + (y * (CTP / 8) + c8 / 8) * 2048) = make_uint4(o[y][0], o[y][1], o[y][2], o[y][3]);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -869,16 +905,13 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
       for (int pass = 1; pass >= 0; --pass) {
         if (gp == pass && (both || pass == 0)) {
 #pragma unroll 1
-          for (int ch = 0; ch < NCW && c0 + ch * CPW < used; ++ch) {
-            float d[8];
-            tc_ld8(t_o + ch * 8, d);
-            tc_wait_ld();
+          for (int c4 = 0; c4 < CT && c0 + c4 < used; c4 += 4) {
+            float v4[4];
+            sum4(c4, n > 2 * kQaRun<QT> + gp, v4);
 #pragma unroll
-            for (int i = 0; i < CPW; ++i) {
-              const int c = c0 + ch * CPW + i;
-              float v = d[i * WS + WP - 1];
-#pragma unroll
-              for (int x = WP - 2; x >= 0; --x) v += d[i * WS + x];
+            for (int i = 0; i < 4; ++i) {
+              const int c = c0 + c4 + i;
+              float v = v4[i];
               v *= ffac[pass * C + c];
               if (d_on && c < used) {
                 if (pass == 0 && both) v += other[c * HD + d_row];

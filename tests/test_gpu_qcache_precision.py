@@ -20,14 +20,14 @@ def want_and_bound(q, k, v, scale, dtype):
     """Attention of q [g, hd] over k, v [n, hd] (float64, as stored), and the bound on an output's error:
     a query enters to 2^-19 of its largest element and hd products are summed in f32, which moves a score by
     ds and a weight and the sum by exp(ds) - 1 each (2.2 ds); the exponential itself is off by 2^-21; a weight
-    enters as two bf16 pieces (f32 queries) or one (bf16), off by 2^-17 or 2^-8 of itself, however small; sums are
+    enters as three bf16 pieces (f32 queries) or two (bf16), off by 2^-26 or 2^-17 of itself, however small; sums are
     f32 (2^-19 of the sum of magnitudes for the lengths here); a bf16 output is off by half a step, 2^-8."""
     s = scale * (q @ k.T)
     w = torch.softmax(s, -1)
     want, mag = w @ v, w @ v.abs()
     sens = abs(scale) * q.abs().amax(-1, keepdim=True) * k.abs().sum(-1).max()
     ds = sens * (2.0 ** -19 + (q.shape[-1] + 32) * 2.0 ** -24)
-    digits = 2.0 ** -17 if dtype == "f32" else 2.0 ** -8
+    digits = 2.0 ** -26 if dtype == "f32" else 2.0 ** -17
     tol = mag * (2.2 * ds + digits + 2.0 ** -21 + 2.0 ** -19) + 1e-37
     return want, tol + (want.abs() * 2.0 ** -8 if dtype == "bf16" else 0)
 
@@ -140,3 +140,36 @@ def test_every_code_counts_at_its_value(hd, g, S, dtype):
     gen = torch.Generator(device="cuda").manual_seed(864)
     q = torch.randn(B, S, kv * g, hd, device="cuda", generator=gen)
     check(c, q.to(DT[dtype]), n, g, dtype, B, kv, hd, range(B), k, v)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hd,kv,g,S,B,n", [(64, 8, 4, 1, 40, 65536), (128, 8, 8, 1, 24, 8192),
+                                           (128, 2, 4, 5, 16, 16384), (64, 2, 1, 8, 16, 16384)])
+def test_long_sums_of_one_sign(hd, kv, g, S, B, n, dtype):
+    # values of one sign and of many sizes: what the additions along a run of tiles lose adds up.  Scores are
+    # products of two numbers that are held exactly, so weights are off by 2^-20 at most; a sum of products by up
+    # to 2^-23 in each of the 32 additions (f32; bf16 256) between two that are rounded to nearest; those, one for
+    # 8 tiles of 128 positions, and the sum of weights, one addition for two tiles and 16 at the end, by 2^-24 each.
+    c = pkg.QCache.empty(B, kv, n, hd)
+    gen = torch.Generator(device="cuda").manual_seed(865)
+    rand = lambda *s: torch.rand(*s, device="cuda", generator=gen)  # noqa: E731
+    k = torch.zeros(B, n, kv, hd, device="cuda")
+    k[..., 0] = torch.floor(rand(B, n, kv) * 9) - 4
+    v = torch.exp2(-6 * rand(B, n, kv, hd))
+    c.write(k, v, i32([0] * B), stream=stream())
+    c.read(i32([0] * B), k, v, stream=stream())
+    q = torch.zeros(B, S, kv * g, hd, device="cuda")
+    q[..., 0] = torch.floor(1 + 3 * rand(B, S, kv * g)) / 4
+    q = q.to(DT[dtype])
+    out = torch.empty_like(q)
+    c.attend(q, i32([n] * B), out, c.workspace(g, B, S), stream=stream())
+    cuts = 32 if dtype == "f32" else 256
+    worst = 0.0
+    for b in range(0, B, 5):
+        for i in range(S):
+            end = n - S + i + 1
+            x, kd, vd = q[b, i].double().reshape(kv, g, hd), k[b, :end].double().transpose(0, 1), v[b, :end].double().transpose(0, 1)
+            want = torch.softmax(hd ** -0.5 * x @ kd.transpose(1, 2), -1) @ vd
+            err = (out[b, i].double().reshape(kv, g, hd) - want).abs() / want
+            worst = max(worst, float(err.max()))
+    assert worst <= 2.0 ** -20 + cuts * 2.0 ** -23 + (n / 1024 + n / 256 + 16) * 2.0 ** -24 + (2.0 ** -8 if dtype == "bf16" else 0), worst
