@@ -36,10 +36,10 @@
 // done, where the last CTA to arrive (a ticket, nobody waits) adds them in CTA order.  So rows of any
 // lengths fill the SMs evenly and the result does not depend on timing.
 //
-// Bound by HBM where a tile's columns are few and rows long (shared memory is next: the loads, the widening
-// and both products move 128 KB per tile of 128 x 128, three quarters of what it can at that rate), by the
-// latency of a tile's chain (scores, widening, weights, products) from about 16 columns on, and by latencies
-// where a CTA has only a few tiles (a segment costs about 4 us besides its tiles: first loads, the groups'
+// Bound by HBM where a tile's columns are few and rows long, by the latency of a tile's chain (scores, widening,
+// weights, products) from about 16 columns on (32 columns: 49% of issue slots busy, shared memory below half, the
+// tensor pipe at 14%), and by latencies where a CTA has only a few tiles (a segment costs about 4 us besides its
+// tiles: first loads, the groups'
 // sums, the join).  Widening by integer steps instead of conversions, rolled or before the scores are there,
 // measured the same.  GB300, f32 queries, heads of 128, groups of 4, 8 key/value heads: 8 rows of 32768
 // positions 92 us (538 MB: 5.8 TB/s, 86% of the copy rate); one row of 131072 56 us (4.8 TB/s); 32 rows of up

@@ -84,9 +84,9 @@ LLM_D void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
-// order this thread's earlier generic-proxy shared-memory accesses before later bulk copies
 // this thread's writes to global memory, before bulk copies that read them
 LLM_D void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+// order this thread's earlier generic-proxy shared-memory accesses before later bulk copies
 LLM_D void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ---- tcgen05 ----------------------------------------------------------------------------
