@@ -298,8 +298,8 @@ llm_status llm_generate_dev(llm_handle* h, const int32_t* tokens_dev, int32_t B,
  * next step starts at positions_host[b] + accepted + 1, which rewinds over the drafts not kept.
  * On an 8-bit cache the tokens are stored and attended one after the other, as single steps would, so that
  * no probability depends on a later draft (a block's scale covers all that it holds), and the drafts that
- * are not kept leave no trace in the blocks before the next step's position; what lies behind it is dead
- * although the filled length counts it.  The first call on such a handle allocates room for a pass's keys
+ * are not kept leave no trace in the block of the next step's position, nor in those before and behind it;
+ * the positions from there on are dead although the filled length counts them.  The first call on such a handle allocates room for a pass's keys
  * and values of every layer (else LLM_ERR_OOM).
  */
 llm_status llm_verify_step(llm_handle* h, const int32_t* tokens_host, int32_t B, int32_t S,

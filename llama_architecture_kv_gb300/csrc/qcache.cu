@@ -227,12 +227,14 @@ __global__ void __launch_bounds__(kQThreads) qcache_settle_kernel(const QVerify 
   if (kept_drafts >= v.T - 1) return;         // nothing else was written
   const int p0 = row_pos(v.r.step, e), last = p0 + kept_drafts;
   const int t1 = last % kQBlock + 1;          // tokens of the block up to the last that was kept
-  if (t1 == kQBlock) return;                  // the others are in blocks of their own
   int row, pp;
   cache_slot(v.r.step, v.c.cap, e, last, row, pp);
   const size_t head = ((size_t)l * v.c.rows + row) * v.c.kv + h;
   uint8_t* codes = (side ? v.c.v : v.c.k) + (head * v.c.cap + (pp + 1 - t1)) * HD;
   float* scale = (side ? v.c.vs : v.c.ks) + head * (v.c.cap / kQBlock) + pp / kQBlock;
+  // the blocks behind hold nothing
+  for (int i = 1 + lane; i <= (p0 + v.T - 1) / kQBlock - last / kQBlock; i += 32) scale[i] = 0.f;
+  if (t1 == kQBlock) return;
   const int t0 = max(0, p0 - (last + 1 - t1));  // tokens of the block before this call's
   if (t0 > 0) {
     const size_t kept = ((size_t)l * v.c.rows + b) * v.c.kv + h;

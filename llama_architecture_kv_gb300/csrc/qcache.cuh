@@ -131,7 +131,8 @@ cudaError_t launch_qcache_write_step(const QCacheView& c, const QRows& r, const 
 // Verification passes: entry b * T + i of the step is token i of row b.  keep: the codes and scales of the
 // blocks that the rows' first tokens go into (where their positions before hold something) to the kept_*
 // arrays; settle: after accepted[b] of the T - 1 drafts were kept, the block that ends with the last of the kept
-// tokens as if no other had been written, from what was kept and the tokens' staged values.
+// tokens as if no other had been written, from what was kept and the tokens' staged values, and the blocks behind it
+// empty.
 struct QVerify {
   QCacheView c;                // layer 0; the others follow
   int32_t layers, T;

@@ -211,3 +211,24 @@ def test_drafts_that_are_not_kept_leave_nothing_behind(name, shape, B, tc):
         assert np.array_equal(wide(gk), wk) and np.array_equal(wide(gv), wv), b
     plain.close()
     g.close()
+
+
+@pytest.mark.parametrize("name,shape,B,tc", ALL, ids=[s[0] for s in ALL])
+def test_blocks_of_lost_drafts_alone_are_empty(name, shape, B, tc):
+    from tests.test_gpu_qcache_model import wide
+    n, S, cap = 31, 20, 128
+    g = make(shape, 871, B, cap, tc_min_batch=tc, cache_type=E4M3, wstd=0.2 if not shape.bf16 else 0.06)
+    toks = synth.tokens(872, 0, B * n, shape.vocab).reshape(B, n)
+    g.prefill(toks[:, :n], 0, logits=False)
+    pos = np.array([n - b % 17 for b in range(B)])             # 15 .. 31: the last of a block among them
+    drafts = synth.tokens(873, 0, B * (S + 1), shape.vocab).reshape(B, S + 1)
+    drafts[:, 0] = toks[np.arange(B), np.minimum(pos, n - 1)]
+    # no probability is above a draw times 1 that is above 1: nothing is kept
+    _, acc, _ = g.verify_step(drafts, pos, np.full((B, S + 1), 2.0, np.float32))
+    assert (acc == 0).all()
+    for b in range(B):
+        behind, end = int(pos[b]) // 16 * 16 + 16, int(pos[b]) + S + 1
+        for layer in range(shape.layers):
+            k, v = g.kv_export(layer, b, behind, end - behind)
+            assert (wide(k) == 0).all() and (wide(v) == 0).all()   # (codes keep their signs)
+    g.close()
