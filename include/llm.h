@@ -91,7 +91,10 @@ typedef struct llm_config {
   int32_t cache_type;   /* LLM_CACHE_MODEL (0): the cache holds dtype; LLM_CACHE_E4M3: 8-bit codes with
                            block scales (see llm_qcache), in about half the bytes of a bf16 cache.
                            Keys and values are rounded to dtype, then quantised as llm_qcache_write
-                           does; every entry works on it (step_kernel is ignored).  A step at a
+                           does; every entry works on it (step_kernel is ignored).  The tokens that a
+                           prefill pass writes into a block share its scale, so logits inside a prompt
+                           can differ by roundings with the tokens behind them (llm_verify_step's
+                           probabilities do not).  A step at a
                            position that is not a multiple of 16 ends what its block of 16 held after
                            it: with llm_decode_paged, write a page's positions in order; llm_kv_import
                            and llm_prefill_packed refuse to end inside a block whose later positions
