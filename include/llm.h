@@ -322,7 +322,7 @@ float* llm_logits_buffer(llm_handle* h);
 int32_t llm_filled(const llm_handle* h, int32_t b);
 
 /* A message for the last failure on h (owned by h; valid until the next call); with h == NULL,
- * why the last llm_create, llm_qcache_* or llm_verify on the calling thread failed.  And a name
+ * why the last llm_create, llm_qcache_*, llm_pages_*, llm_sample_rows or llm_verify on the calling thread failed.  And a name
  * for a status code. */
 const char* llm_last_error(const llm_handle* h);
 const char* llm_status_string(llm_status s);
@@ -491,6 +491,90 @@ llm_status llm_qcache_attend(const llm_qcache* cache, const void* q_dev, int32_t
                              const int32_t* count_dev, const int32_t* table_dev, int32_t pages_per_row,
                              float scale, void* out_dev, int64_t out_stride, void* workspace_dev,
                              uint64_t workspace_bytes, int32_t* status_dev, void* cuda_stream);
+
+/*
+ * The same attention for rows that share places: rows groups_dev[i] .. groups_dev[i + 1] - 1 of the call take
+ * their positions below shared_dev[i] from the places of the group's first row (its pages, or its cache row),
+ * whatever their own tables say there, and the others from their own.  Each group's shared positions are read
+ * once for all its rows (heads of 64 and 128; other heads read them row by row).  groups_dev [groups + 1]
+ * ascends from 0 to B (a group may be empty) and shared_dev [groups] is 0 .. the positions a row can hold:
+ * else LLM_ERR_ARG or LLM_ERR_POS_RANGE is stored, and no row (of the group) shares anything.  What a token sees
+ * goes by its row's length as above: a row shorter than what its group shares sees that much of it.  With rows whose
+ * tables name the same pages for what they share this is llm_qcache_attend, but for roundings.  groups is
+ * 1..B.  The workspace is as large as llm_qcache_shared_workspace says, for the same cache, group, B, S and
+ * groups; it need not be cleared.  Calls that overlap on the GPU need workspaces of their own.
+ */
+llm_status llm_qcache_shared_workspace(const llm_qcache* cache, int32_t group, int32_t B, int32_t S, int32_t groups, uint64_t* bytes);
+llm_status llm_qcache_attend_shared(const llm_qcache* cache, const void* q_dev, int32_t dtype, int64_t q_stride,
+                                    int32_t group, int32_t B, int32_t S, const int32_t* length_dev,
+                                    const int32_t* count_dev, const int32_t* table_dev, int32_t pages_per_row,
+                                    const int32_t* groups_dev, const int32_t* shared_dev, int32_t groups, float scale,
+                                    void* out_dev, int64_t out_stride, void* workspace_dev, uint64_t workspace_bytes,
+                                    int32_t* status_dev, void* cuda_stream);
+
+/*
+ * Page tables whose rows fork, shrink, grow and are freed (device memory of the caller; the pages are numbers 0
+ * .. pages - 1 of a pool such as a cache's, rows * (max_seq / 64), or a handle's).  Row r holds length[r] positions, in
+ * pages table[r][0 .. ceil(length[r] / 64) - 1]; what its table says after them means nothing.  A page is in use while
+ * a row holds it; rows can hold a page together.  rows x (pages_per_row + 1) < 2^31, pages <= 2^28.
+ *
+ * llm_pages_update writes to *to what *from becomes (two tables of one shape that do not overlap), for all rows at
+ * once: row r becomes the first length_dev[r] positions of row parent_dev[r] -- parent -1: it is emptied (its pages
+ * are free if no row holds them); parent_dev NULL: every row its own; length_dev NULL: the parent's length.  Where
+ * length_dev[r] exceeds the parent's, the row has pages for positions still to be written.  Whole pages are held together.  A page that more
+ * than one row would write next (its positions end inside it) stays with one row and is copied for the others, and
+ * so is one that another row holds whole.  Pages are taken lowest first, a row's copy before its
+ * new ones, in the order of the rows; entries behind a row's pages are -1.  compact moves the pages in use to
+ * numbers 0 .. used - 1 with the fewest copies, ascending.
+ * moves_dev [m][2] receives the copies to make, from and to page, then -1 (llm_qcache_copy_pages and
+ * llm_copy_pages make them; they can be made in any order): m is rows for an update and max(1, pages / 2) for compact.  counts_dev
+ * [2] receives their number and the pages in use after them.
+ * A parent, length or page out of range, or too few free pages, is stored in *status_dev where given
+ * (LLM_ERR_ARG, LLM_ERR_POS_RANGE, LLM_ERR_OOM); *to then equals *from, there are no moves and counts_dev is 0, -1.
+ * The workspace need not be cleared; calls that overlap on the GPU need their own.  cuda_stream as above;
+ * the calls return without waiting, allocate nothing and may be captured.
+ */
+typedef struct llm_pages {
+  int32_t* table;   /* [rows][pages_per_row] */
+  int32_t* length;  /* [rows]                */
+  int32_t rows, pages_per_row, pages;
+} llm_pages;
+llm_status llm_pages_workspace(const llm_pages* pages, uint64_t* bytes);
+llm_status llm_pages_update(const llm_pages* from, const llm_pages* to, const int32_t* parent_dev,
+                            const int32_t* length_dev, int32_t* moves_dev, int32_t* counts_dev, void* workspace_dev,
+                            uint64_t workspace_bytes, int32_t* status_dev, void* cuda_stream);
+llm_status llm_pages_compact(const llm_pages* from, const llm_pages* to, int32_t* moves_dev, int32_t* counts_dev,
+                             void* workspace_dev, uint64_t workspace_bytes, int32_t* status_dev, void* cuda_stream);
+
+/*
+ * Copy pages (codes and scales, keys and values) in n caches of one shape, the layers of a model: for i < m (and
+ * i < counts_dev[0] where given) page moves_dev[i][0] to page moves_dev[i][1]; both negative: none.  No page may be
+ * the target of two moves, nor the target of one and the source of another.  A page outside the pool stores LLM_ERR_ARG and is skipped.
+ * m x kv_heads < 2^32 / 96.  llm_copy_pages does it for every layer of a handle's pool (llm_decode_paged), of
+ * either cache type: moves_host [m][2] is host memory, read before the call returns; the copies are ordered on the
+ * handle's stream; pages outside the pool and targets named twice or also as a source are refused (LLM_ERR_ARG).
+ */
+llm_status llm_qcache_copy_pages(const llm_qcache* caches, int32_t n, const int32_t* moves_dev, int32_t m,
+                                 const int32_t* counts_dev, int32_t* status_dev, void* cuda_stream);
+llm_status llm_copy_pages(llm_handle* h, const int32_t* moves_host, int32_t m);
+
+/*
+ * Sampling with settings of each row's own, without a handle.  Row b of logits_dev (rows of V floats, stride apart) is
+ * drawn from with temp_dev[b], k_dev[b], p_dev[b], min_p_dev[b] (arrays may be NULL: 1, V, 1, 0) and u_dev[b] into
+ * ids_dev[b].  temp == 0: the first index of the largest logit.  Else, with top the largest logit, a
+ * candidate's distance is d = floor(2^27 min((top - v) * r, 30)), r = min(1 / temp, the largest f32), each of these an f32
+ * operation, and its weight w = round(2^31 exp(-d / 2^27)), the exp that of llm_sample.  In the order of d (ties: lower id
+ * first), top-k keeps the first k, top-p of them those whose weights before them sum to less than floor(floor(2^24 p) sum / 2^24) (always
+ * the first), min-p those with w >= floor(2^31 min_p), and the id is the first whose running sum is above
+ * floor(floor(2^24 u) total / 2^24), total the sum of what all three keep.  Sums are exact, so an id does not
+ * depend on any order of summation.  NaN logits are never drawn, nor is -inf; a row of nothing else gives 0.  A row whose
+ * settings are out of range (temp >= 0 and finite, k >= 1, 0 < p <= 1, 0 <= min_p <= 1, 0 <= u < 1; for
+ * temp == 0 only temp counts) gives -1, and LLM_ERR_ARG in *status_dev (may be NULL) if that holds 0.  V is 1..524280.  Device memory of the
+ * current device; ordered on cuda_stream, returns without waiting, allocates nothing, may be captured.
+ */
+llm_status llm_sample_rows(const float* logits_dev, int64_t stride, int32_t B, int32_t V, const float* temp_dev,
+                           const int32_t* k_dev, const float* p_dev, const float* min_p_dev, const float* u_dev,
+                           int32_t* ids_dev, int32_t* status_dev, void* cuda_stream);
 
 /*
  * Verify drafted tokens, without a handle (speculative sampling: the tokens that come out are

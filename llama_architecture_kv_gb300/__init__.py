@@ -27,7 +27,9 @@ EXPORTS = ("llm_weight_count", "llm_create", "llm_destroy", "llm_reset", "llm_pr
            "llm_step_rows_dev", "llm_generate", "llm_generate_dev", "llm_decode_paged",
            "llm_decode_paged_dev", "llm_step_paged", "llm_step_paged_dev", "llm_check_wait_timeout",
            "llm_prefill_packed", "llm_qcache_write", "llm_qcache_read", "llm_qcache_workspace",
-           "llm_qcache_attend", "llm_verify", "llm_verify_step")
+           "llm_qcache_attend", "llm_verify", "llm_verify_step", "llm_qcache_shared_workspace",
+           "llm_qcache_attend_shared", "llm_pages_workspace", "llm_pages_update", "llm_pages_compact",
+           "llm_qcache_copy_pages", "llm_copy_pages", "llm_sample_rows")
 
 
 class LlmConfig(ctypes.Structure):
@@ -49,6 +51,11 @@ class LlmQcache(ctypes.Structure):
                 ("max_seq", ctypes.c_int32), ("head", ctypes.c_int32)]
 
 
+class LlmPages(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("length", ctypes.c_void_p), ("rows", ctypes.c_int32),
+                ("pages_per_row", ctypes.c_int32), ("pages", ctypes.c_int32)]
+
+
 class LlmError(RuntimeError):
     def __init__(self, status, msg):
         super().__init__(f"{msg} (status {status})")
@@ -59,6 +66,7 @@ class LlmError(RuntimeError):
 _i32, _i64, _u64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float, ctypes.c_void_p
 _pcfg = ctypes.POINTER(LlmConfig)
 _pqc = ctypes.POINTER(LlmQcache)
+_ppg = ctypes.POINTER(LlmPages)
 SIGNATURES = {
     "llm_weight_count": ([_pcfg], _u64),
     "llm_create": ([_pcfg, _vp, _u64, _i32, _vp, ctypes.POINTER(_vp)], _i32),
@@ -103,6 +111,15 @@ SIGNATURES = {
                            _vp, _vp], _i32),
     "llm_verify_step": ([_vp, _vp, _i32, _i32, _vp, _f32, _vp, _vp, _vp, _vp, _vp], _i32),
     "llm_verify": ([_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp], _i32),
+    "llm_qcache_shared_workspace": ([_pqc, _i32, _i32, _i32, _i32, ctypes.POINTER(_u64)], _i32),
+    "llm_qcache_attend_shared": ([_pqc, _vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _f32, _vp,
+                                  _i64, _vp, _u64, _vp, _vp], _i32),
+    "llm_pages_workspace": ([_ppg, ctypes.POINTER(_u64)], _i32),
+    "llm_pages_update": ([_ppg, _ppg, _vp, _vp, _vp, _vp, _vp, _u64, _vp, _vp], _i32),
+    "llm_pages_compact": ([_ppg, _ppg, _vp, _vp, _vp, _u64, _vp, _vp], _i32),
+    "llm_qcache_copy_pages": ([_vp, _i32, _vp, _i32, _vp, _vp, _vp], _i32),
+    "llm_copy_pages": ([_vp, _vp, _i32], _i32),
+    "llm_sample_rows": ([_vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
     }
 
 _lib = None
@@ -268,6 +285,10 @@ def llm_prefill_packed(h, tokens, rows, positions, segments, P, last, nlast, log
 def llm_verify_step(h, tokens, B, S, positions, temp, q, u, p, ids, accepted):
     _check(h, lib().llm_verify_step(h, _ptr(tokens), B, S, _ptr(positions), temp, _ptr(q), _ptr(u), _ptr(p),
                                     _ptr(ids), _ptr(accepted)))
+
+
+def llm_copy_pages(h, moves, m):
+    _check(h, lib().llm_copy_pages(h, _ptr(moves), m))
 
 
 def llm_synchronize(h):
@@ -496,6 +517,138 @@ class QCache:
             _refused("llm_qcache_attend", st)
 
 
+    def workspace_shared(self, group, B, S, groups):
+        """A workspace for attend_shared() with this group, rows, tokens per row and groups of rows."""
+        if _torch.cuda.current_device() != self._dev:
+            _bad(f"the cache lies on cuda:{self._dev} and another CUDA device is current")
+        n = ctypes.c_uint64()
+        st = self._lib.llm_qcache_shared_workspace(self._c, group, B, S, groups, ctypes.byref(n))
+        if st != LLM_OK:
+            _refused("llm_qcache_shared_workspace", st)
+        return _torch.empty(max(16, n.value), dtype=_torch.uint8, device=self.device)
+
+    def attend_shared(self, q, length, groups, shared, out, workspace, count=None, table=None, scale=None, status=None,
+                      stream=None):
+        """attend() for rows that share places: rows groups[i] .. groups[i + 1] - 1 take their positions below
+        shared[i] from the places of the group's first row, which are read once for all of them
+        (llm_qcache_attend_shared).  groups [G + 1] and shared [G] are int32 CUDA tensors."""
+        B, S = q.shape[:2]
+        per = self.kv * self.hd
+        n = q.numel()
+        group = n // (B * S * per) if B * S else 0
+        if n != B * S * group * per:
+            _bad("q must hold a whole number of heads per key/value head")
+        first, count, table, pages, status = self._call_rows(B, length, "length", count, table, status)
+        if shared is None or groups is None:
+            _bad("groups and shared are missing")
+        G = shared.numel()
+        dev = self._dev
+        bound, part = _int32(groups, "groups", dev, G + 1), _int32(shared, "shared", dev, G)
+        qp, qstep = _rows(q, "q", dev, B, S, group * per)
+        op, ostep = _rows(out, "out", dev, B, S, group * per)
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _bad("workspace must be contiguous CUDA memory beside the cache")
+        st = self._lib.llm_qcache_attend_shared(self._c, qp, self._dtype(q, out), qstep, group, B, S, first, count, table, pages,
+                                                bound, part, G, self._scale if scale is None else scale, op, ostep,
+                                                workspace.data_ptr(), workspace.numel() * workspace.element_size(), status,
+                                                _stream(stream, dev))
+        if st != LLM_OK:
+            _refused("llm_qcache_attend_shared", st)
+
+
+class QCacheLayers:
+    """The 8-bit caches of a model's layers, all of one shape (QCache), whose pages are copied together."""
+
+    def __init__(self, caches):
+        caches = list(caches)
+        if not caches:
+            _bad("at least one cache is needed")
+        if any(c._dev != caches[0]._dev for c in caches):
+            _bad("the caches must lie on one device")
+        self.caches = caches
+        self._dev, self._lib = caches[0]._dev, lib()
+        self._array = (LlmQcache * len(caches))(*[c.c for c in caches])
+
+    def copy(self, moves, counts=None, status=None, stream=None):
+        """Copy pages moves[i][0] to moves[i][1] in every layer (llm_qcache_copy_pages): moves [m, 2] and counts (the
+        first of its elements: how many of them there are) int32 CUDA tensors, as Pages.update and compact write them."""
+        dev = self._dev
+        if _torch.cuda.current_device() != dev:
+            _bad(f"the caches lie on cuda:{dev} and another CUDA device is current")
+        m = moves.shape[0] if moves.dim() == 2 else -1
+        if m == 0:
+            return
+        st = self._lib.llm_qcache_copy_pages(self._array, len(self.caches), _int32(moves, "moves", dev, 2 * m), m,
+                                             None if counts is None else _int32(counts, "counts", dev, 2),
+                                             None if status is None else _int32(status, "status", dev, 1), _stream(stream, dev))
+        if st != LLM_OK:
+            _refused("llm_qcache_copy_pages", st)
+
+
+class Pages:
+    """A page table [rows, pages_per_row] and lengths [rows] (int32 CUDA tensors) over a pool of `pages`
+    pages of 64 positions (llm_pages).  update and compact write what becomes of it into another Pages of
+    the same shape; calls are ordered on `stream` (None: torch's current stream) and return without waiting."""
+
+    def __init__(self, table, length, pages):
+        torch = _need_torch()
+        for t, name in ((table, "table"), (length, "length")):
+            if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+                _bad(f"{name} must be a contiguous int32 tensor in CUDA memory")
+        if table.dim() != 2 or tuple(length.shape) != (table.shape[0],) or length.device != table.device:
+            _bad("table must be [rows, pages_per_row] and length [rows] beside it")
+        self.table, self.length, self.pages = table, length, int(pages)
+        self._dev = table.get_device()
+        self.c = LlmPages(table.data_ptr(), length.data_ptr(), table.shape[0], table.shape[1], self.pages)
+        self._c, self._lib = ctypes.byref(self.c), lib()
+
+    @classmethod
+    def empty(cls, rows, pages_per_row, pages, device="cuda"):
+        """Rows that hold nothing."""
+        torch = _need_torch()
+        return cls(torch.full((rows, pages_per_row), -1, dtype=torch.int32, device=device),
+                   torch.zeros(rows, dtype=torch.int32, device=device), pages)
+
+    def workspace(self):
+        """A workspace for update() and compact()."""
+        n = ctypes.c_uint64()
+        st = self._lib.llm_pages_workspace(self._c, ctypes.byref(n))
+        if st != LLM_OK:
+            _refused("llm_pages_workspace", st)
+        return _torch.empty(n.value // 4, dtype=_torch.int32, device=self.table.device)
+
+    def _call(self, out, moves, m, counts, workspace, status):
+        dev = self._dev
+        if _torch.cuda.current_device() != dev:
+            _bad(f"the table lies on cuda:{dev} and another CUDA device is current")
+        if out._dev != dev or workspace.get_device() != dev or not workspace.is_contiguous():
+            _bad("out and workspace must lie beside the table, the workspace contiguous")
+        if moves is None or counts is None:
+            _bad("moves and counts are missing")
+        return (_int32(moves, "moves", dev, 2 * m), _int32(counts, "counts", dev, 2), workspace.data_ptr(),
+                workspace.numel() * workspace.element_size(), None if status is None else _int32(status, "status", dev, 1))
+
+    def update(self, out, moves, counts, workspace, parent=None, length=None, status=None, stream=None):
+        """Row r of out becomes the first length[r] positions of row parent[r] of this table (parent -1: empty;
+        None: every row its own; length None: the parent's), with pages for positions it does not hold yet.
+        moves [rows, 2] receives the pages to copy (QCacheLayers.copy), counts [2] their number and the
+        pages in use (llm_pages_update)."""
+        moves, counts, ws, n, status = self._call(out, moves, self.c.rows, counts, workspace, status)
+        st = self._lib.llm_pages_update(self._c, out._c, None if parent is None else _int32(parent, "parent", self._dev, self.c.rows),
+                                        None if length is None else _int32(length, "length", self._dev, self.c.rows), moves, counts,
+                                        ws, n, status, _stream(stream, self._dev))
+        if st != LLM_OK:
+            _refused("llm_pages_update", st)
+
+    def compact(self, out, moves, counts, workspace, status=None, stream=None):
+        """The pages in use as numbers 0 .. used - 1 in out; moves [max(1, pages // 2), 2] and counts as
+        for update (llm_pages_compact)."""
+        moves, counts, ws, n, status = self._call(out, moves, max(1, self.pages // 2), counts, workspace, status)
+        st = self._lib.llm_pages_compact(self._c, out._c, moves, counts, ws, n, status, _stream(stream, self._dev))
+        if st != LLM_OK:
+            _refused("llm_pages_compact", st)
+
+
 def _f32s(t, name, dev, n):
     if t.dtype is not _torch.float32 or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
         _bad(f"{name} must be a contiguous float32 tensor of {n} elements on cuda:{dev}")
@@ -524,6 +677,31 @@ def llm_verify(p, q, drafts, u, ids, accepted, count=None, stream=None):
                           _int32(accepted, "accepted", dev, B), _stream(stream, dev))
     if st != LLM_OK:
         _refused("llm_verify", st)
+
+
+def llm_sample_rows(logits, temp, u, ids, k=None, p=None, min_p=None, status=None, stream=None):
+    """One token per row of logits [B, V] (rows may be a slice of wider ones), drawn with the row's own temp, k,
+    p, min_p and u [B] into ids [B] (see include/llm.h); CUDA tensors, f32 and int32 (k, ids, status); temp None: 1,
+    k None: V, p None: 1, min_p None: 0; ordered on `stream` (None: torch's current stream)."""
+    torch = _torch or _need_torch()
+    if logits.dim() != 2 or logits.dtype is not torch.float32:
+        _bad("logits must be float32 [B, V]")
+    B, V = logits.shape
+    dev = logits.get_device()
+    if dev < 0 or torch.cuda.current_device() != dev:
+        _bad("logits must lie on the current CUDA device")
+    step, one = logits.stride()
+    if V > 1 and one != 1:
+        _bad("the logits of a row must be contiguous")
+    if u is None or ids is None:
+        _bad("u and ids are missing")
+    st = lib().llm_sample_rows(logits.data_ptr(), step if B > 1 else max(step, V), B, V, None if temp is None else _f32s(temp, "temp", dev, B),
+                               None if k is None else _int32(k, "k", dev, B), None if p is None else _f32s(p, "p", dev, B),
+                               None if min_p is None else _f32s(min_p, "min_p", dev, B), _f32s(u, "u", dev, B),
+                               _int32(ids, "ids", dev, B), None if status is None else _int32(status, "status", dev, 1),
+                               _stream(stream, dev))
+    if st != LLM_OK:
+        _refused("llm_sample_rows", st)
 
 
 # ---- a small convenience wrapper --------------------------------------------------------
@@ -642,6 +820,12 @@ class Model:
         llm_verify_step(self.h, tokens, B, S, positions, temp, qd, ud, p, ids, acc)
         self.synchronize()
         return ids.cpu().numpy(), acc.cpu().numpy(), p.cpu().numpy()
+
+    def copy_pages(self, moves):
+        """Copy pages moves[i][0] to moves[i][1] of the paged steps' pool, in every layer."""
+        moves = np.ascontiguousarray(moves, np.int32).reshape(-1, 2)
+        if len(moves):
+            llm_copy_pages(self.h, moves, len(moves))
 
     def sample(self, logits, temp, k, p, u):
         logits = np.ascontiguousarray(logits, np.float32)

@@ -23,6 +23,7 @@
 #include "mega.cuh"
 #include "gemv.cuh"
 #include "llm.h"
+#include "pages.cuh"
 #include "qcache.cuh"
 #include "sampler.cuh"
 #include "tc.cuh"
@@ -2001,6 +2002,44 @@ llm_status llm_kv_import(llm_handle* h, int32_t layer, int32_t row, int32_t pos0
 
 llm_status llm_kv_export(llm_handle* h, int32_t layer, int32_t row, int32_t pos0, int32_t n, void* k_host, void* v_host) {
   return kv_copy(h, layer, row, pos0, n, k_host, v_host, false);
+}
+
+llm_status llm_copy_pages(llm_handle* h, const int32_t* moves_host, int32_t m) {
+  if (!h || !moves_host || m < 1) return LLM_ERR_ARG;
+  if (!h->page_table)
+    return fail(h, LLM_ERR_CONFIG, "pages need max_seq (%d) to be a multiple of %d", h->cfg.max_seq, kPage);
+  const int64_t pool = (int64_t)h->cfg.max_batch * (h->cfg.max_seq / kPage);
+  std::vector<uint8_t> use((size_t)pool, 0);  // 1: a source, 2: a target
+  for (int32_t i = 0; i < m; ++i)
+    for (int y = 0; y < 2; ++y) {
+      const int32_t page = moves_host[2 * (size_t)i + y];
+      if (page < 0 || page >= pool) return fail(h, LLM_ERR_ARG, "move %d: page %d outside the pool of %lld", i, page, (long long)pool);
+      if (use[page] & (y ? 3 : 2))
+        return fail(h, LLM_ERR_ARG, "move %d: page %d is a target, and named by another move or as its source", i, page);
+      use[page] |= y ? 2 : 1;
+    }
+  CopyArgs a = {};
+  a.rows = h->cfg.max_batch; a.kv = h->cfg.kv_heads; a.cap = h->q8 ? h->qcap : h->cfg.max_seq;
+  a.bytes = h->q8 ? h->hd : h->hd * (h->wt ? 2 : 4);
+  a.moves = h->page_table;
+  const size_t codes = (size_t)a.rows * a.kv * a.cap * a.bytes, scales = (size_t)a.rows * a.kv * (a.cap / kQBlock);
+  // (the page table of the paged steps holds half as many moves as the pool has pages, at a time: a pool of one page has none)
+  const int32_t most = (int32_t)std::max<int64_t>(1, pool / 2);
+  for (int32_t i = 0; i < m; i += most) {
+    a.m = std::min(m - i, most);
+    CUDA_TRY(h, cudaMemcpyAsync(h->page_table, moves_host + 2 * (size_t)i, (size_t)a.m * 8, cudaMemcpyHostToDevice, h->stream));
+    for (int l0 = 0; l0 < h->L; l0 += kCopyLayers) {
+      a.layers = std::min(h->L - l0, kCopyLayers);
+      for (int l = 0; l < a.layers; ++l) {
+        a.k[l] = (uint8_t*)(h->q8 ? (void*)h->qk : h->kc) + (l0 + l) * codes;
+        a.v[l] = (uint8_t*)(h->q8 ? (void*)h->qv : h->vc) + (l0 + l) * codes;
+        a.ks[l] = h->q8 ? h->qks + (l0 + l) * scales : nullptr;
+        a.vs[l] = h->q8 ? h->qvs + (l0 + l) * scales : nullptr;
+      }
+      CUDA_TRY(h, launch_copy_pages(a, h->stream));
+    }
+  }
+  return LLM_OK;
 }
 
 llm_status llm_step_kernels(llm_handle* h, int32_t B, float temp, int32_t k, int32_t* kernels) {

@@ -1,12 +1,14 @@
-// Entry points of the operators that need no handle (include/llm.h): 8-bit key/value caches and the
-// verification of drafted tokens.  Each checks its arguments on the host, then launches on the
+// Entry points of the operators that need no handle (include/llm.h): 8-bit key/value caches, page tables
+// that fork, the verification of drafted tokens and the sampler with settings per row.  Each checks its arguments on the host, then launches on the
 // caller's stream; what only device memory knows (positions, counts, pages) the kernels check.
 #include <math.h>
 #include <stdio.h>
 
 #include "attention.cuh"
 #include "llm.h"
+#include "pages.cuh"
 #include "qcache.cuh"
+#include "sampler.cuh"
 #include "verify.cuh"
 
 using namespace llm;
@@ -160,6 +162,155 @@ llm_status llm_qcache_attend(const llm_qcache* cache, const void* q_dev, int32_t
   a.q = q_dev; a.out = out_dev; a.q_stride = q_stride; a.out_stride = out_stride; a.g = group; a.scale = scale;
   a.ws = (unsigned char*)workspace_dev;
   return launched(launch_qattn(a, dtype, sms, (cudaStream_t)cuda_stream, false));
+}
+
+llm_status llm_qcache_shared_workspace(const llm_qcache* cache, int32_t group, int32_t B, int32_t S, int32_t groups, uint64_t* bytes) {
+  REFUSE(!cache || !bytes, LLM_ERR_ARG, "NULL argument");
+  TRY(check_cache(cache));
+  REFUSE(!attn_supported(cache->head, group), LLM_ERR_CONFIG, "group must be 1..16 with group x head size at most 1024");
+  REFUSE(B < 1, LLM_ERR_BATCH, "batch must be at least 1");
+  REFUSE(S < 1 || (int64_t)B * S >= (int64_t)1 << 31, LLM_ERR_ARG, "tokens per row out of range");
+  REFUSE(groups < 1 || groups > B, LLM_ERR_ARG, "groups must be 1..B");
+  int sms = 0;
+  TRY(device_sms(&sms));
+  const QCacheView c = {nullptr, nullptr, nullptr, nullptr, cache->rows, cache->kv_heads, cache->max_seq, cache->head};
+  *bytes = qattn_shared_workspace(c, group, B, S, sms);
+  return LLM_OK;
+}
+
+llm_status llm_qcache_attend_shared(const llm_qcache* cache, const void* q_dev, int32_t dtype, int64_t q_stride, int32_t group,
+                                    int32_t B, int32_t S, const int32_t* length_dev, const int32_t* count_dev,
+                                    const int32_t* table_dev, int32_t pages_per_row, const int32_t* groups_dev,
+                                    const int32_t* shared_dev, int32_t groups, float scale, void* out_dev, int64_t out_stride,
+                                    void* workspace_dev, uint64_t workspace_bytes, int32_t* status_dev, void* cuda_stream) {
+  REFUSE(!cache, LLM_ERR_ARG, "NULL cache");
+  QAttnArgs a = {};
+  TRY(check_cache(cache));
+  TRY(check_rows(cache, B, S, length_dev, count_dev, table_dev, pages_per_row, status_dev, &a.c, &a.r));
+  REFUSE(!attn_supported(cache->head, group), LLM_ERR_CONFIG, "group must be 1..16 with group x head size at most 1024");
+  const int64_t width = (int64_t)a.c.kv * group * a.c.hd;
+  TRY(check_buffer(q_dev, dtype, q_stride, width));
+  TRY(check_buffer(out_dev, dtype, out_stride, width));
+  REFUSE(!isfinite(scale), LLM_ERR_ARG, "scale must be finite");
+  REFUSE(groups < 1 || groups > B, LLM_ERR_ARG, "groups must be 1..B");
+  REFUSE(!groups_dev || !shared_dev || !aligned4(groups_dev) || !aligned4(shared_dev), LLM_ERR_ARG,
+         "the groups' bounds and shared positions must be given, as aligned int32 arrays");
+  int sms = 0;
+  TRY(device_sms(&sms));
+  REFUSE(!qattn_fits(a.c, group, dtype, B, S, a.r.limit, sms), LLM_ERR_ARG,
+         "too large for one call: rows x tokens x kv heads x 128-position tiles must stay below 2^31");
+  const uint64_t need = qattn_shared_workspace(a.c, group, B, S, sms);
+  if (need > 0) {
+    REFUSE(!workspace_dev || workspace_bytes < need, LLM_ERR_ARG, "workspace smaller than llm_qcache_shared_workspace says");
+    REFUSE(!aligned16(workspace_dev), LLM_ERR_ARG, "the workspace must be aligned to 16 bytes");
+  }
+  a.q = q_dev; a.out = out_dev; a.q_stride = q_stride; a.out_stride = out_stride; a.g = group; a.scale = scale;
+  a.ws = (unsigned char*)workspace_dev;
+  a.groups = groups_dev; a.shared = shared_dev; a.ngroups = groups;
+  return launched(launch_qattn_shared(a, dtype, sms, (cudaStream_t)cuda_stream));
+}
+
+llm_status llm_qcache_copy_pages(const llm_qcache* caches, int32_t n, const int32_t* moves_dev, int32_t m,
+                                 const int32_t* counts_dev, int32_t* status_dev, void* cuda_stream) {
+  REFUSE(!caches || n < 1, LLM_ERR_ARG, "at least one cache is needed");
+  REFUSE(!moves_dev || m < 1, LLM_ERR_ARG, "at least one move is needed");
+  REFUSE(!aligned4(moves_dev) || !aligned4(counts_dev) || !aligned4(status_dev), LLM_ERR_ARG, "int32 arrays must be aligned");
+  for (int32_t i = 0; i < n; ++i) {
+    TRY(check_cache(caches + i));
+    REFUSE(caches[i].rows != caches[0].rows || caches[i].kv_heads != caches[0].kv_heads ||
+               caches[i].max_seq != caches[0].max_seq || caches[i].head != caches[0].head,
+           LLM_ERR_CONFIG, "the caches of a call must have one shape");
+  }
+  REFUSE(caches->max_seq % kPage, LLM_ERR_CONFIG, "pages need max_seq to be a multiple of 64");
+  REFUSE((int64_t)m * caches->kv_heads >= ((int64_t)1 << 32) / kCopyLayers, LLM_ERR_ARG,
+         "too large for one call: moves x kv heads must stay below 2^32 / 96");
+  CopyArgs a = {};
+  a.rows = caches->rows; a.kv = caches->kv_heads; a.cap = caches->max_seq; a.bytes = caches->head;
+  a.moves = moves_dev; a.m = m; a.counts = counts_dev; a.status = status_dev;
+  for (int32_t i = 0; i < n; i += kCopyLayers) {
+    a.layers = n - i < kCopyLayers ? n - i : kCopyLayers;
+    for (int32_t l = 0; l < a.layers; ++l) {
+      a.k[l] = (uint8_t*)caches[i + l].k;
+      a.v[l] = (uint8_t*)caches[i + l].v;
+      a.ks[l] = caches[i + l].k_scale;
+      a.vs[l] = caches[i + l].v_scale;
+    }
+    TRY(launched(launch_copy_pages(a, (cudaStream_t)cuda_stream)));
+  }
+  return LLM_OK;
+}
+
+static llm_status check_pages(const llm_pages* p) {
+  REFUSE(!p->table || !p->length || !aligned4(p->table) || !aligned4(p->length), LLM_ERR_ARG,
+         "a page table and lengths are needed, aligned to 4 bytes");
+  REFUSE(p->rows < 1 || p->pages_per_row < 1 || p->pages < 1, LLM_ERR_CONFIG, "rows, pages per row and pages must be at least 1");
+  REFUSE(p->pages > 1 << 28 || p->pages_per_row > 1 << 24 || (int64_t)p->rows * (p->pages_per_row + 1) > 0x7fffffff, LLM_ERR_CONFIG,
+         "too large: pages at most 2^28, pages per row 2^24, rows x (pages per row + 1) below 2^31");
+  return LLM_OK;
+}
+
+static bool overlap(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + (uintptr_t)m * 4 && y < x + (uintptr_t)n * 4;
+}
+
+// the two books of an update or a compaction, and where its copies and counts go
+static llm_status check_books(const llm_pages* from, const llm_pages* to, const int32_t* moves, const int32_t* counts,
+                              const void* ws, uint64_t ws_bytes, const int32_t* status, PageBook* x, PageBook* y) {
+  REFUSE(!from || !to, LLM_ERR_ARG, "NULL pages");
+  TRY(check_pages(from));
+  TRY(check_pages(to));
+  REFUSE(from->rows != to->rows || from->pages_per_row != to->pages_per_row || from->pages != to->pages, LLM_ERR_CONFIG,
+         "both tables must have one shape, over one pool");
+  const int64_t R = from->rows, n = R * from->pages_per_row;
+  REFUSE(overlap(from->table, n, to->table, n) || overlap(from->length, R, to->length, R) ||
+             overlap(from->table, n, to->length, R) || overlap(from->length, R, to->table, n),
+         LLM_ERR_ARG, "the new table and lengths must not overlap the old ones");
+  REFUSE(!moves || !counts || !aligned4(moves) || !aligned4(counts) || !aligned4(status), LLM_ERR_ARG,
+         "moves and counts are needed, as aligned int32 arrays");
+  REFUSE(!ws || !aligned4(ws) || ws_bytes < pages_workspace(from->rows, from->pages) * 4, LLM_ERR_ARG,
+         "workspace smaller than llm_pages_workspace says");
+  *x = PageBook{from->table, from->length, from->rows, from->pages_per_row, from->pages};
+  *y = PageBook{to->table, to->length, to->rows, to->pages_per_row, to->pages};
+  return LLM_OK;
+}
+
+llm_status llm_pages_workspace(const llm_pages* pages, uint64_t* bytes) {
+  REFUSE(!pages || !bytes, LLM_ERR_ARG, "NULL argument");
+  TRY(check_pages(pages));
+  *bytes = pages_workspace(pages->rows, pages->pages) * 4;
+  return LLM_OK;
+}
+
+llm_status llm_pages_update(const llm_pages* from, const llm_pages* to, const int32_t* parent_dev, const int32_t* length_dev,
+                            int32_t* moves_dev, int32_t* counts_dev, void* workspace_dev, uint64_t workspace_bytes,
+                            int32_t* status_dev, void* cuda_stream) {
+  PageBook x, y;
+  TRY(check_books(from, to, moves_dev, counts_dev, workspace_dev, workspace_bytes, status_dev, &x, &y));
+  REFUSE(!aligned4(parent_dev) || !aligned4(length_dev), LLM_ERR_ARG, "int32 arrays must be aligned");
+  return launched(launch_pages_update(x, y, parent_dev, length_dev, moves_dev, counts_dev, (int32_t*)workspace_dev, status_dev,
+                                      (cudaStream_t)cuda_stream));
+}
+
+llm_status llm_pages_compact(const llm_pages* from, const llm_pages* to, int32_t* moves_dev, int32_t* counts_dev,
+                             void* workspace_dev, uint64_t workspace_bytes, int32_t* status_dev, void* cuda_stream) {
+  PageBook x, y;
+  TRY(check_books(from, to, moves_dev, counts_dev, workspace_dev, workspace_bytes, status_dev, &x, &y));
+  return launched(launch_pages_compact(x, y, moves_dev, counts_dev, (int32_t*)workspace_dev, status_dev, (cudaStream_t)cuda_stream));
+}
+
+llm_status llm_sample_rows(const float* logits_dev, int64_t stride, int32_t B, int32_t V, const float* temp_dev,
+                           const int32_t* k_dev, const float* p_dev, const float* min_p_dev, const float* u_dev,
+                           int32_t* ids_dev, int32_t* status_dev, void* cuda_stream) {
+  REFUSE(!logits_dev || !u_dev || !ids_dev, LLM_ERR_ARG, "NULL argument");
+  REFUSE(B < 1 || B > 1 << 24, LLM_ERR_BATCH, "batch out of range");
+  REFUSE(V < 1 || V > kSampleRowsMost, LLM_ERR_ARG, "the vocabulary must be in 1..524280");
+  REFUSE(stride < V, LLM_ERR_ARG, "rows overlap: the stride is below the vocabulary");
+  REFUSE(!aligned4(logits_dev) || !aligned4(temp_dev) || !aligned4(k_dev) || !aligned4(p_dev) || !aligned4(min_p_dev) ||
+             !aligned4(u_dev) || !aligned4(ids_dev) || !aligned4(status_dev),
+         LLM_ERR_ARG, "arrays must be aligned to 4 bytes");
+  const SampleRowsArgs a = {logits_dev, stride, B, V, temp_dev, k_dev, p_dev, min_p_dev, u_dev, ids_dev, status_dev};
+  return launched(launch_sample_rows(a, (cudaStream_t)cuda_stream));
 }
 
 llm_status llm_verify(const float* p_dev, const float* q_dev, const int32_t* drafts_dev, const int32_t* count_dev,

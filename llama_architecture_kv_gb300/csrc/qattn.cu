@@ -68,8 +68,35 @@ LLM_D bool token_place(const QRows& r, const QCacheView& c, int b, int pos, int&
   return true;
 }
 
-// HD: head size; GM: bound of the group size; QT: 0 f32, 1 bf16 queries and outputs
-template <int HD, int GM, int QT>
+// Whether the group bounds of a call with shared positions ascend from 0 to B (else an error is recorded and no
+// row shares anything); every thread of the CTA calls it
+LLM_D bool groups_fine(const QAttnArgs& a) {
+  bool fine = true;
+  for (int i = threadIdx.x; i < a.ngroups; i += blockDim.x) {
+    const int lo = a.groups[i], hi = a.groups[i + 1];
+    fine &= lo <= hi && (i > 0 || lo == 0) && (i + 1 < a.ngroups || hi == a.r.B);
+  }
+  fine = __syncthreads_and(fine);
+  if (!fine) q_report(a.r.status, kErrArg);
+  return fine;
+}
+// the positions that row b shares, and the row whose places hold them
+LLM_D int row_shares(const QAttnArgs& a, int b, int& leader) {
+  int lo = 0, hi = a.ngroups - 1;  // the last group that starts at b or before (empty groups before it start there too)
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.groups[mid] <= b) lo = mid;
+    else hi = mid - 1;
+  }
+  leader = a.groups[lo];
+  const int n = a.shared[lo];
+  if (n >= 0 && n <= a.r.limit) return n;
+  q_report(a.r.status, kErrPosRange);
+  return 0;
+}
+
+// HD: head size; GM: bound of the group size; QT: 0 f32, 1 bf16 queries and outputs; SH: rows share positions
+template <int HD, int GM, int QT, bool SH>
 __global__ void __launch_bounds__(kSimpleThreads) qattn_simple_kernel(const QAttnArgs a) {
   constexpr int NW = kSimpleThreads / 32;
   constexpr int DPL = HD >= 32 ? HD / 32 : 1;  // dimensions per lane of the values
@@ -80,6 +107,7 @@ __global__ void __launch_bounds__(kSimpleThreads) qattn_simple_kernel(const QAtt
   __shared__ __align__(16) float qs[GM * HD];
   __shared__ __align__(16) float wb[NW][32 * GM];
   __shared__ float part[NW][GM * (HD + 2)];
+  const bool sharing = SH && groups_fine(a);
   for (int64_t t64 = blockIdx.z; t64 < (int64_t)a.r.B * a.r.S; t64 += gridDim.z) {
     const int t = (int)t64;
     int b, start, end;
@@ -87,7 +115,14 @@ __global__ void __launch_bounds__(kSimpleThreads) qattn_simple_kernel(const QAtt
     const int64_t qrow = a.r.step ? b : t64;
     // this part's positions: a whole number of 32-position chunks, aligned so that none crosses a page
     const int base = start & ~31;
-    const int nch = end > start ? (end - base + 31) / 32 : 0;
+    int nch = end > start ? (end - base + 31) / 32 : 0;
+    // (shared positions: chunks of their own, the last of them cut where they end)
+    int leader = 0, sh = 0, nsh = 0;
+    if constexpr (SH) {
+      if (sharing) sh = min(row_shares(a, b, leader), end);
+      nsh = (sh + 31) / 32;
+      nch = nsh + (end > sh ? (end - (sh & ~31) + 31) / 32 : 0);
+    }
     const int c0 = (int)((int64_t)nch * split / a.splits), c1 = (int)((int64_t)nch * (split + 1) / a.splits);
     __syncthreads();  // the previous token's shared memory is free
     for (int i = tid; i < g * HD; i += kSimpleThreads)
@@ -102,13 +137,14 @@ __global__ void __launch_bounds__(kSimpleThreads) qattn_simple_kernel(const QAtt
       for (int e = 0; e < DPL; ++e) o[h][e] = 0.f;
     }
     for (int ch = c0 + warp; ch < c1; ch += NW) {
-      const int pb = base + ch * 32;
+      const bool in_shared = SH && ch < nsh;
+      const int pb = !SH || in_shared ? base + ch * 32 : (sh & ~31) + (ch - nsh) * 32;
       int row, pp;
-      if (!token_place(a.r, a.c, b, pb, row, pp)) continue;
+      if (!token_place(a.r, a.c, in_shared ? leader : b, pb, row, pp)) continue;
       const size_t head = (size_t)row * a.c.kv + j;
       const uint8_t* kp = a.c.k + (head * a.c.cap + pp) * HD;
       const uint8_t* vp = a.c.v + (head * a.c.cap + pp) * HD;
-      const int lo = max(0, start - pb), hi = min(32, end - pb);
+      const int lo = max(0, (SH && !in_shared ? sh : start) - pb), hi = min(32, (in_shared ? sh : end) - pb);
       const bool seen = lane >= lo && lane < hi;
       float acc[GM];
 #pragma unroll
@@ -240,16 +276,16 @@ int simple_splits(const QCacheView& c, int64_t tokens, int limit, int num_sms) {
   return (int)std::max<int64_t>(1, std::min<int64_t>({want, kSimpleSplits, limit / 128}));
 }
 
-template <int HD, int QT>
+template <int HD, int QT, bool SH = false>
 cudaError_t launch_simple(const QAttnArgs& a0, int num_sms, cudaStream_t s, bool pdl) {
   QAttnArgs a = a0;
   const int64_t tokens = (int64_t)a.r.B * a.r.S;
   a.splits = simple_splits(a.c, tokens, std::min(a.r.limit, a.c.rows * a.c.cap), num_sms);
   void (*fn)(const QAttnArgs) = nullptr;
-  if (a.g <= 4) fn = qattn_simple_kernel<HD, 4, QT>;
+  if (a.g <= 4) fn = qattn_simple_kernel<HD, 4, QT, SH>;
   else if constexpr (HD <= 128) {
-    if (a.g <= 8) fn = qattn_simple_kernel<HD, 8, QT>;
-    else if constexpr (HD <= 64) fn = qattn_simple_kernel<HD, 16, QT>;
+    if (a.g <= 8) fn = qattn_simple_kernel<HD, 8, QT, SH>;
+    else if constexpr (HD <= 64) fn = qattn_simple_kernel<HD, 16, QT, SH>;
   }
   if (!fn) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
@@ -360,6 +396,25 @@ cudaError_t launch_qattn(const QAttnArgs& a0, int qt, int num_sms, cudaStream_t 
     case 256: return qt ? launch_simple<256, 1>(a, num_sms, s, pdl) : launch_simple<256, 0>(a, num_sms, s, pdl);
     default: return cudaErrorInvalidValue;
   }
+}
+
+uint64_t qattn_shared_workspace(const QCacheView& c, int g, int B, int S, int num_sms) {
+  const int splits = simple_splits(c, (int64_t)B * S, c.rows * c.cap, num_sms);
+  return splits == 1 ? 0 : kQattnTickets + (uint64_t)B * S * c.kv * g * splits * (c.hd + 2) * 4;
+}
+
+cudaError_t launch_qattn_shared(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s) {
+#define LLM_CASE(HD) \
+  case HD: return qt ? launch_simple<HD, 1, true>(a, num_sms, s, false) : launch_simple<HD, 0, true>(a, num_sms, s, false);
+  switch (a.c.hd) {
+    LLM_CASE(16)
+    LLM_CASE(32)
+    LLM_CASE(64)
+    LLM_CASE(128)
+    LLM_CASE(256)
+    default: return cudaErrorInvalidValue;
+  }
+#undef LLM_CASE
 }
 
 }  // namespace llm

@@ -167,6 +167,10 @@ struct QAttnArgs {
   // quantises into the cache (tensor cores only); null where they are there already
   const void *new_k, *new_v;
   int32_t new_t;
+  // Rows that share places: rows groups[i] .. groups[i + 1] - 1 of the call take their positions below shared[i]
+  // from the places of the group's first row (ngroups groups; 0: every row has its own)
+  const int32_t *groups, *shared;
+  int32_t ngroups;
   // set by launch_qattn: parts of a token's positions (CUDA cores), or tokens per tile and tiles per row
   int32_t splits, tpt, nct;
 };
@@ -179,6 +183,9 @@ uint64_t qattn_step_workspace(const QCacheView& c, int g, int NT, int num_sms);
 // kmap, vmap: tensor maps of qattn_make_map over the whole caches; null: made for this call
 cudaError_t launch_qattn(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s, bool pdl,
                          const CUtensorMap* kmap = nullptr, const CUtensorMap* vmap = nullptr);
+// the same with groups of rows that share positions, read once for all rows of a group (heads of 64 and 128)
+uint64_t qattn_shared_workspace(const QCacheView& c, int g, int B, int S, int num_sms);
+cudaError_t launch_qattn_shared(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s);
 bool qattn_uses_tc(int hd);
 bool qattn_make_map(CUtensorMap* map, const void* codes, int hd, uint64_t rows);
 // tokens of one sequence that share a tile of the tensor-core kernel (f32 queries)

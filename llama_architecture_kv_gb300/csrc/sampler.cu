@@ -25,31 +25,6 @@ namespace llm {
 constexpr int kSampThreads = 1024;
 constexpr int kSortMaxSlices = kSortMaxSlicesPerRow;
 
-LLM_D float exp_s(float x) {
-  if (x != x) return x;
-  if (x > 88.5f) return INFINITY;
-  if (x < -104.0f) return 0.0f;
-  const float LOG2E = 1.44269504088896340736f;
-  const float LN2_HI = 0.693145751953125f;  // ln 2 to 16 significant bits: n * LN2_HI is exact
-  const float LN2_LO = (float)(0.69314718055994530942 - 0.693145751953125);
-  const float nf = rintf(__fmul_rn(x, LOG2E));
-  const int n = (int)nf;
-  float r = __fmaf_rn(-nf, LN2_HI, x);
-  r = __fmaf_rn(-nf, LN2_LO, r);
-  float p = (float)(1.0 / 40320.0);
-  p = __fmaf_rn(p, r, (float)(1.0 / 5040.0));
-  p = __fmaf_rn(p, r, (float)(1.0 / 720.0));
-  p = __fmaf_rn(p, r, (float)(1.0 / 120.0));
-  p = __fmaf_rn(p, r, (float)(1.0 / 24.0));
-  p = __fmaf_rn(p, r, (float)(1.0 / 6.0));
-  p = __fmaf_rn(p, r, 0.5f);
-  p = __fmaf_rn(p, r, 1.0f);
-  p = __fmaf_rn(p, r, 1.0f);
-  if (n >= -126) return __fmul_rn(p, __uint_as_float((uint32_t)(n + 127) << 23));
-  return __fmul_rn(__fmul_rn(p, __uint_as_float((uint32_t)(n + 64 + 127) << 23)),
-                   __uint_as_float((uint32_t)(-64 + 127) << 23));
-}
-
 // order-preserving key, largest value first (ascending key); -0 and +0 equal
 LLM_D uint32_t desc_key(float v) {
   uint32_t u = __float_as_uint(v);
