@@ -14,7 +14,9 @@ LIB = os.path.join(HERE, "libllm.so")
 SOURCES = ["llm.cu", "gemv.cu", "gemm.cu", "attention.cu", "sampler.cu", "noalloc.cu", "mega.cu", "qcache.cu",
            "qattn.cu", "verify.cu", "pages.cu", "sample_rows.cu", "ops.cu"]
 # the longest first
-SOURCES = [f"qattn_tc{hd}_{t}.cu" for t in ("f32", "f32_wide", "bf16") for hd in (128, 64)] + SOURCES
+SOURCES = ([f"qattn_tc{hd}_{t}.cu" for t in ("f32", "f32_wide", "bf16") for hd in (128, 64)]
+           + [f"qshare{hd}_{t}.cu" for t in ("f32", "bf16") for hd in (128, 64)]
+           + [f"qattn_sh{hd}_{t}.cu" for t in ("f32", "bf16") for hd in (128, 64)] + ["qshare.cu"] + SOURCES)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE]
 

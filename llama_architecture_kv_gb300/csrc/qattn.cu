@@ -399,22 +399,19 @@ cudaError_t launch_qattn(const QAttnArgs& a0, int qt, int num_sms, cudaStream_t 
 }
 
 uint64_t qattn_shared_workspace(const QCacheView& c, int g, int B, int S, int num_sms) {
+  if (qattn_uses_tc(c.hd)) return qshare_workspace(c, g, B, S, num_sms);
   const int splits = simple_splits(c, (int64_t)B * S, c.rows * c.cap, num_sms);
   return splits == 1 ? 0 : kQattnTickets + (uint64_t)B * S * c.kv * g * splits * (c.hd + 2) * 4;
 }
 
 cudaError_t launch_qattn_shared(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s) {
-#define LLM_CASE(HD) \
-  case HD: return qt ? launch_simple<HD, 1, true>(a, num_sms, s, false) : launch_simple<HD, 0, true>(a, num_sms, s, false);
+  if (qattn_uses_tc(a.c.hd)) return launch_qshare_all(a, qt, num_sms, s);
   switch (a.c.hd) {
-    LLM_CASE(16)
-    LLM_CASE(32)
-    LLM_CASE(64)
-    LLM_CASE(128)
-    LLM_CASE(256)
+    case 16: return qt ? launch_simple<16, 1, true>(a, num_sms, s, false) : launch_simple<16, 0, true>(a, num_sms, s, false);
+    case 32: return qt ? launch_simple<32, 1, true>(a, num_sms, s, false) : launch_simple<32, 0, true>(a, num_sms, s, false);
+    case 256: return qt ? launch_simple<256, 1, true>(a, num_sms, s, false) : launch_simple<256, 0, true>(a, num_sms, s, false);
     default: return cudaErrorInvalidValue;
   }
-#undef LLM_CASE
 }
 
 }  // namespace llm

@@ -149,6 +149,103 @@ LLM_D QaUnit qa_unit(const QAttnArgs& a, int t) {
   return u;
 }
 
+// ---- rows that share positions (qshare.cuh) ----
+// whether the groups' bounds ascend from 0 to B (else no row shares anything); every thread of the CTA calls it
+LLM_D bool sh_fine(const QAttnArgs& a) {
+  bool fine = true;
+  for (int i = threadIdx.x; i < a.ngroups; i += blockDim.x) {
+    const int lo = a.groups[i], hi = a.groups[i + 1];
+    fine &= lo <= hi && (i > 0 || lo == 0) && (i + 1 < a.ngroups || hi == a.r.B);
+  }
+  fine = __syncthreads_and(fine);
+  if (!fine && threadIdx.x == 0) q_report(a.r.status, kErrArg);
+  return fine;
+}
+// the group of row b: positions that it shares, the row that has them, and where the group ends
+LLM_D int sh_group(const QAttnArgs& a, int b, int& lead, int& end) {
+  int lo = 0, hi = a.ngroups - 1;  // the last group that starts at b or before (empty ones before it start there too)
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.groups[mid] <= b) lo = mid;
+    else hi = mid - 1;
+  }
+  lead = a.groups[lo];
+  end = a.groups[lo + 1];
+  const int n = a.shared[lo];
+  if (n >= 0 && n <= a.r.limit) return n;
+  q_report(a.r.status, kErrPosRange);
+  return 0;
+}
+// the positions that token i of row b sees end here (0: it is not there)
+LLM_D int sh_end(const QAttnArgs& a, int b, int i) {
+  const int n = q_count(a.r, b);
+  int len = a.r.first[b];
+  if (len < 0 || len > a.r.limit) {
+    q_report(a.r.status, kErrPosRange);
+    len = 0;
+  }
+  return i < n ? max(0, len - n + i + 1) : 0;
+}
+// Unit s: of B * cpr prefix units (only the first of each that holds several rows has tiles), then B * cpr suffix
+// units.  end0 is not used: the columns' ends are looked up one by one.
+template <int TN, bool EXACT = true>
+LLM_D QaUnit sh_unit(const QAttnArgs& a, int s, bool sharing) {
+  const ShSide& x = a.sh;
+  const int half = a.r.B * x.cpr;
+  const bool prefix = s < half;
+  const int t = prefix ? s : s - half, b = t / x.cpr, c = t - b * x.cpr;
+  int lead = b, end = b + 1;
+  const int sh = sharing ? sh_group(a, b, lead, end) : 0;
+  QaUnit u;
+  u.qrow = (int64_t)b * a.r.S + c * x.tpt;
+  u.end0 = u.tile0 = u.nt = 0;
+  if (prefix) {
+    const int rows = x.cpr > 1 ? 1 : min(x.rpt, end - b);
+    u.b = lead;
+    u.ntok = x.cpr > 1 ? min(x.tpt, a.r.S - c * x.tpt) : rows * a.r.S;
+    u.start = u.last = 0;
+    if ((x.sides & 1) && sh > 0 && (x.rpt == 1 || (b - lead) % x.rpt == 0)) {
+      u.last = sh;
+      if constexpr (EXACT) {  // (no further than any of the rows sees)
+        int most = 0;
+#pragma unroll 8
+        for (int i = 0; i < rows; ++i) most = max(most, sh_end(a, b + i, q_count(a.r, b + i) - 1));
+        u.last = min(sh, most);
+      }
+      u.nt = (u.last + TN - 1) / TN;
+    }
+  } else {
+    u.b = b;
+    u.ntok = min(x.tpt, a.r.S - c * x.tpt);
+    u.start = sh;
+    // (of the tokens that are there the last sees most)
+    const int n = min(q_count(a.r, b), c * x.tpt + u.ntok);
+    u.last = (x.sides & 2) && n > c * x.tpt ? sh_end(a, b, n - 1) : 0;
+    u.tile0 = sh / TN;
+    if (u.last > sh) u.nt = (u.last + TN - 1) / TN - u.tile0;
+  }
+  return u;
+}
+// the next unit that can have tiles
+LLM_D int sh_next(const QAttnArgs& a, int s, bool sharing) {
+  if (s >= a.r.B * a.sh.cpr || a.sh.rpt == 1 || !sharing) return s + 1;
+  int lead, end;  // (cpr is 1)
+  sh_group(a, s, lead, end);
+  return min(s + a.sh.rpt - (s - lead) % a.sh.rpt, end);
+}
+// where a column's sums go, and its statistics (part 0, 1: a unit's first run, of a prefix or a row's own; 2: a later one)
+LLM_D float* sh_put(const QAttnArgs& a, int part, int half, int64_t col, int place, float m, float l, int cta, int cta0, int ctas) {
+  const int64_t cols = (int64_t)a.r.B * a.r.S * a.c.kv * a.g;
+  if (part == 2) {
+    const int64_t at = ((int64_t)cta * a.sh.groups + half) * a.sh.pitch + place;
+    a.sh.mstats[at] = make_float2(m, l);
+    return a.sh.more + at * a.c.hd;
+  }
+  const int64_t at = (part * 2 + half) * cols + col;
+  a.sh.stats[at] = make_float4(m, l, __int_as_float(cta0), __int_as_float(ctas << 8 | place));
+  return a.sh.parts + at * a.c.hd;
+}
+
 LLM_D bool qa_place(const QAttnArgs& a, int b, int pos, int& row, int& pp) {
   if (!a.r.step) return q_place(a.r, a.c, b, pos, row, pp);
   cache_slot(a.r.step, a.c.cap, b, pos, row, pp);
@@ -300,19 +397,42 @@ LLM_D void qa_widen_row(unsigned char* stage, int r, int sub, bool live) {
   }
 }
 
-// the walk of one CTA's run over (token tile, kv head, position tiles)
+// the walk of one CTA's run over (token tile, kv head, position tiles); SH: over the units of a call whose rows share
+// positions
+template <bool SH>
 struct QaWalk {
   QaUnit u;
   int t, j, k0, k1;
   int st, end, off;  // off: place of (t, head 0) in the sequence
+  bool sharing;
+  LLM_D QaUnit unit(const QAttnArgs& a, int i) const {
+    if constexpr (SH) return sh_unit<kQaTile>(a, i, sharing);
+    else return qa_unit(a, i);
+  }
+  LLM_D void skip(const QAttnArgs& a) {
+    if constexpr (SH) {
+      const int n = 2 * a.r.B * a.sh.cpr;
+      do {
+        t = sh_next(a, t, sharing);
+        if (t >= n) {  // (only if lengths or groups change while the call runs)
+          st = end;
+          return;
+        }
+        u = unit(a, t);
+      } while (u.nt == 0);
+    } else {
+      do u = qa_unit(a, ++t);
+      while (u.nt == 0);
+    }
+  }
   LLM_D void begin(const QAttnArgs& a, int t_, int off_, int c0, int c1) {
     t = t_; off = off_; st = c0; end = c1;
     if (st >= end) return;
-    u = qa_unit(a, t);
+    u = unit(a, t);
     if (st - off == a.c.kv * u.nt) {  // (a cut moved to the end of its token tile)
       off = st;
-      do u = qa_unit(a, ++t);
-      while (u.nt == 0);
+      skip(a);
+      if (SH && st >= end) return;
     }
     j = (int)((uint32_t)(st - off) / (uint32_t)u.nt);
     k0 = st - off - j * u.nt;
@@ -328,14 +448,14 @@ struct QaWalk {
     if (++j == a.c.kv) {
       j = 0;
       off += a.c.kv * u.nt;
-      do u = qa_unit(a, ++t);
-      while (u.nt == 0);
+      skip(a);
+      if (SH && st >= end) return;
     }
     cut();
   }
 };
 
-template <int HD, int NP, int NC, int QT>
+template <int HD, int NP, int NC, int QT, bool SH>
 __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::CTAS)
     qattn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const QAttnArgs a) {
   using X = QaShape<HD, NP, NC>;
@@ -394,8 +514,62 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   // previous kernel, below)
   // this CTA's run: the token tiles' position tiles are counted lane by lane (contiguous stretches),
   // and the lane whose stretch holds the run's start finds its token tile
-  const int nq = a.r.step ? (a.tiles ? a.tiles[1] : a.r.B) : a.r.B * a.nct;
-  if (warp == 0) {
+  const int nq = SH ? 2 * a.r.B * a.sh.cpr : a.r.step ? (a.tiles ? a.tiles[1] : a.r.B) : a.r.B * a.nct;
+  bool sharing = false;
+  int* before = reinterpret_cast<int*>(base);  // SH: [nq] tiles of the units before (the ring is idle yet)
+  __shared__ int s_sum[SH ? X::NT / 32 : 1];
+  if constexpr (SH) {
+    // (counted by all threads: a unit's count is a chain of reads)
+    sharing = sh_fine(a);
+    const int per = (nq + X::NT - 1) / X::NT, u0 = min(nq, tid * per), u1 = min(nq, u0 + per);
+    int sum = 0;
+    for (int t = u0; t < u1; ++t) {
+      before[t] = sum;
+      sum += sh_unit<kQaTile>(a, t, sharing).nt;
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    int lead = incl - sum, all = 0;
+    for (int i = 0; i < X::NT / 32; ++i) {
+      if (i < warp) lead += s_sum[i];
+      all += s_sum[i];
+    }
+    for (int t = u0; t < u1; ++t) before[t] += lead;
+    __syncthreads();
+    if (warp == 0 && lane < 2) {  // the run's start, and its end
+      const int total = all * a.c.kv, ge = min((int)gridDim.x, total);
+      if (lane == 0) s_total = s_begin = s_end = total;
+      __syncwarp(3u);
+      const int x = cta < ge ? [&] { QaCut cut; cut.make(total, ge); return cut.begin(cta + lane); }() : total;
+      if (x < total) {
+        // the last unit that starts at x or before
+        const int goal = x / a.c.kv;
+        int lo = 0, hi = nq - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (before[mid] <= goal) lo = mid;
+          else hi = mid - 1;
+        }
+        const int off = before[lo] * a.c.kv, nt = (lo + 1 < nq ? before[lo + 1] : all) - before[lo];
+        QaCut cut;
+        cut.make(total, ge);
+        const int to = cut.moved(x, x - (int)((uint32_t)(x - off) % (uint32_t)nt), nt);
+        if (lane) {
+          s_end = to;
+        } else {
+          s_t = lo;
+          s_off = off;
+          s_begin = to;
+        }
+      }
+    }
+  } else if (warp == 0) {
     // (unsigned: sums of numbers below 2^31)
     const uint32_t nu = (uint32_t)nq, pu = (nu + 31u) / 32u, tu = min(nu, lane * pu);
     const int per = (int)pu, t0 = (int)tu, t1 = (int)min(nu, tu + pu);
@@ -446,7 +620,8 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   // while this kernel waits for the tensor memory)
   grid_dep_launch();
   const uint32_t tmem = s_tmem;
-  QaWalk w;
+  QaWalk<SH> w;
+  w.sharing = sharing;
   w.begin(a, s_t, s_off, s_begin, s_end);
   grid_dep_wait();
   bool ok = true;  // a wait that gave up: no further waits, but every loop and barrier is still walked
@@ -475,10 +650,18 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         // the place of this lane's block, and with it of its half of the tile (pages hold 64 positions)
         const int p0 = (w.u.tile0 + k) * kQaTile, pos = p0 + kQBlock * blk;
         int row = 0, pp = 0;
-        const bool seen = pos < w.u.last && qa_place(a, w.u.b, pos, row, pp);
-        const int y = a.krow0 + (row * a.c.kv + w.j) * a.c.cap + pp;
-        const int y0 = __shfl_sync(0xffffffffu, y, 0), y1 = __shfl_sync(0xffffffffu, y, 4);
-        const uint32_t have = __ballot_sync(0xffffffffu, seen);
+        const bool seen = pos < w.u.last && (!SH || pos + kQBlock > w.u.start) && qa_place(a, w.u.b, pos, row, pp);
+        int y = a.krow0 + (row * a.c.kv + w.j) * a.c.cap + pp;
+        uint32_t have = __ballot_sync(0xffffffffu, seen);
+        int l0 = 0, l1 = 4;
+        if constexpr (SH) {  // (a half tile is there if one of its blocks is: one may start inside it)
+          y -= pos & (kPage - 1);
+          const uint32_t h0 = have & 15u, h1 = have & 0xf0u;
+          l0 = h0 ? __ffs(h0) - 1 : 0;
+          l1 = h1 ? __ffs(h1) - 1 : 4;
+          have = (h0 != 0u) | (h1 != 0u) << 4;
+        }
+        const int y0 = __shfl_sync(0xffffffffu, y, l0), y1 = __shfl_sync(0xffffffffu, y, l1);
         wait(b_empty + 8u * slot, par);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -590,7 +773,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
     };
     // tokens that see nothing and share a tile with none that does: zeros
 #pragma unroll 1
-    for (uint32_t t = cta; t < (uint32_t)nq; t += gridDim.x) {
+    for (uint32_t t = SH ? (uint32_t)nq : (uint32_t)cta; t < (uint32_t)nq; t += gridDim.x) {
       const QaUnit u = qa_unit(a, (int)t);
       if (u.nt == 0 && u.ntok > 0)
 #pragma unroll 1
@@ -662,7 +845,12 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         if (lane == 0) {
           // a query that is not finite makes its scores NaN
           qsc[c] = c < used ? (fine ? s * (a.scale * 1.4426950408889634f) : __uint_as_float(0x7fc00000u)) : 0.f;
-          cend[c] = c < used ? w.u.end0 + tok : 0;
+          if constexpr (SH) {
+            const int gt = (int)w.u.qrow + tok, b = gt / a.r.S;
+            cend[c] = c < used ? min(w.u.last, sh_end(a, b, gt - b * a.r.S)) : 0;
+          } else {
+            cend[c] = c < used ? w.u.end0 + tok : 0;
+          }
         }
       }
       fence_proxy_async_smem();
@@ -673,6 +861,12 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
       group_sync();
       const float* qsg = qsc + c0;
       const int* ceg = cend + c0;
+      int all_end = 0x7fffffff;             // the least that a column sees
+      if constexpr (SH) {
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+          if (c0 + c < used) all_end = min(all_end, ceg[c]);
+      }
       uint32_t slot = sb + gp, fpar = spar;  // ring slot and phase of this group's next tile
       if (slot >= ST) slot -= ST, fpar ^= 1u;
       float l[CT];
@@ -686,7 +880,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         wait(b_full + 8u * slot, fpar);
         const float ks = ssc[slot * 16 + quad * 2 + (lane >> 4)], vs = ssc[slot * 16 + 8 + quad * 2 + (lane >> 4)];
         const bool good = !(ks < 0.f) && pos < w.u.last && pos >= w.u.start;
-        const bool whole = __all_sync(0xffffffffu, good) && p0 + kQaTile <= w.u.end0;
+        const bool whole = __all_sync(0xffffffffu, good) && p0 + kQaTile <= (SH ? all_end : w.u.end0);
         const int mypos = good ? pos : 0x7fffffff;
         const int wr = quad * 32 + (HV == 1 ? lane : half * 16 + (lane & 15));
         const bool wlive = HV == 1 ? good : __ballot_sync(0xffffffffu, good) >> (wr & 31) & 1u;
@@ -877,7 +1071,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         if (gtid == 0) gvs[group] = vref;
       }
       all_sync();  // (every product is done: the weights' buffers are free)
-      const bool both = n > 1, alone = w.k0 == 0 && w.k1 == w.u.nt;  // alone: this CTA holds the whole unit
+      const bool both = n > 1, alone = !SH && w.k0 == 0 && w.k1 == w.u.nt;  // alone: this CTA holds the whole unit
       // parts of units cut across CTAs: [CTA][the unit's first part?]{[C][HD] sums, [C] (reference, weight)}
       float* parts = reinterpret_cast<float*>(a.ws + kQattnTickets);
       float* mine = parts + ((size_t)cta * 2 + (w.k0 == 0 ? 1 : 0)) * C * (HD + 2);
@@ -893,8 +1087,18 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         ffac[c] = f0 * gvs[2 * hv] * r;
         ffac[C + c] = f1 * (both ? gvs[2 * hv + 1] : 0.f) * r;
         const int tok = c / a.g;
-        coff[c] = tok * a.out_stride + (c - tok * a.g) * HD;
-        if (!alone) *reinterpret_cast<float2*>(mine + C * HD + 2 * c) = make_float2(M, L);
+        if constexpr (SH) {
+          const bool all = w.k0 == 0 && w.k1 == w.u.nt;
+          QaCut cut;
+          cut.make(s_total, min((int)gridDim.x, s_total));
+          const int first = all ? cta : cut.first(w.unit0()), ctas = all ? 0 : cut.last(w.unit0(), w.u.nt) - first;
+          const int part = w.k0 > 0 ? 2 : w.t < a.r.B * a.sh.cpr ? 0 : 1;
+          float* dst = sh_put(a, part, 0, ((int64_t)w.j * a.r.B * a.r.S + w.u.qrow) * a.g + c, c, M, L, cta, first, ctas);
+          coff[c] = dst - a.sh.parts;
+        } else {
+          coff[c] = tok * a.out_stride + (c - tok * a.g) * HD;
+          if (!alone) *reinterpret_cast<float2*>(mine + C * HD + 2 * c) = make_float2(M, L);
+        }
       }
       all_sync();
       const int d_row = HD == 128 ? quad * 32 + lane : quad * 16 + (lane & 15);  // the dimension of this lane
@@ -919,6 +1123,8 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
                   const int64_t at = obase + coff[c] + d_row;
                   if constexpr (QT) static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v);
                   else static_cast<float*>(a.out)[at] = v;
+                } else if (SH && pass == 0) {
+                  a.sh.parts[coff[c] + d_row] = v;
                 } else {
                   (pass ? other : mine)[c * HD + d_row] = v;
                 }
@@ -928,7 +1134,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         }
         if (pass == 1 && both) all_sync();
       }
-      if (!alone) {
+      if (!SH && !alone) {
         if (stid == 0) {
           QaCut cut;
           cut.make(s_total, min((int)gridDim.x, s_total));
@@ -1034,11 +1240,11 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
 }
 
 // one instantiation per translation unit (they take half a minute each to compile)
-template <int HD, int NP, int NC, int QT>
+template <int HD, int NP, int NC, int QT, bool SH = false>
 cudaError_t launch_qattn_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const QAttnArgs& a, int grid,
                             cudaStream_t s, bool pdl) {
   constexpr size_t smem = QaShape<HD, NP, NC>::SMEM;
-  auto fn = qattn_tc_kernel<HD, NP, NC, QT>;
+  auto fn = qattn_tc_kernel<HD, NP, NC, QT, SH>;
   // (the limit belongs to the device's context: set on every call, a fraction of a microsecond)
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -1064,5 +1270,10 @@ LLM_QATTN_TC(qattn_tc64_bf16);
 LLM_QATTN_TC(qattn_tc128_f32);
 LLM_QATTN_TC(qattn_tc128_f32_wide);
 LLM_QATTN_TC(qattn_tc128_bf16);
+// of rows that share positions
+LLM_QATTN_TC(qattn_sh64_f32);
+LLM_QATTN_TC(qattn_sh64_bf16);
+LLM_QATTN_TC(qattn_sh128_f32);
+LLM_QATTN_TC(qattn_sh128_bf16);
 
 }  // namespace llm

@@ -150,6 +150,25 @@ cudaError_t launch_qcache_clear(const QCacheView& c, int layers, int row, int bl
 cudaError_t launch_qcache_read(const QCacheView& c, const QRows& r, void* k, void* v, int st, int64_t stride,
                                cudaStream_t s);
 
+// Attention of rows that share positions (qshare.cuh): how a kernel splits its part of a call into units, and where
+// what it sums goes.  A unit is the positions that a group shares, for up to rpt rows or tpt tokens of one (a prefix
+// unit), or a row's own, for up to tpt of its tokens (a suffix unit); its columns are the (token, query head) pairs.
+struct ShSide {
+  int32_t tpt, cpr, rpt;  // tokens of a unit at most, units per row, rows of a prefix unit at most
+  int32_t sides;          // 1: prefix units, 2: suffix units, 3: both
+  int32_t ctas;           // of the launch
+  int32_t pitch;          // columns of a unit at most
+  // What each of a CTA's one or two groups comes to, by column (j * tokens + token) * g + head of key/value head j: sums
+  // over a unit's first run of tiles [2: prefix, own][2: group][columns][hd], with {reference, sum of weights, first CTA,
+  // CTAs after it << 8 | place in the unit}; and over the runs of other CTAs that go on with it [CTA][groups][pitch][hd], with
+  // {reference, sum of weights}.  Where the sum of weights is 0 there are no sums.
+  int32_t groups;
+  float* parts;
+  float4* stats;
+  float* more;
+  float2* mstats;
+};
+
 // attention of the rows' tokens (a row's `first` is its length): q and out are rows of H * hd
 // elements (H = kv * g) at the given strides, f32 (qt 0) or bf16 (qt 1)
 struct QAttnArgs {
@@ -171,6 +190,7 @@ struct QAttnArgs {
   // from the places of the group's first row (ngroups groups; 0: every row has its own)
   const int32_t *groups, *shared;
   int32_t ngroups;
+  ShSide sh;              // (set by launch_qattn_shared)
   // set by launch_qattn: parts of a token's positions (CUDA cores), or tokens per tile and tiles per row
   int32_t splits, tpt, nct;
 };
@@ -186,6 +206,10 @@ cudaError_t launch_qattn(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s
 // the same with groups of rows that share positions, read once for all rows of a group (heads of 64 and 128)
 uint64_t qattn_shared_workspace(const QCacheView& c, int g, int B, int S, int num_sms);
 cudaError_t launch_qattn_shared(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s);
+// (its tensor-core part, qshare.cu; whether a call's units and columns can be counted)
+bool qshare_fits(const QCacheView& c, int g, int qt, int B, int S, int ngroups, int limit);
+uint64_t qshare_workspace(const QCacheView& c, int g, int B, int S, int num_sms);
+cudaError_t launch_qshare_all(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s);
 bool qattn_uses_tc(int hd);
 bool qattn_make_map(CUtensorMap* map, const void* codes, int hd, uint64_t rows);
 // tokens of one sequence that share a tile of the tensor-core kernel (f32 queries)
