@@ -64,6 +64,7 @@ template <int QT> constexpr int kQaRun = QT ? 32 : 4;
 constexpr int kQaNear = 4;                         // most tiles by which a cut moves to a unit's end
 constexpr float kQaNone = -3.0e38f;                // a reference before any score
 constexpr size_t kQaSmem = 232448;                 // shared memory a CTA can have
+constexpr int kShUnits = 8192;                     // units per key/value head of a call whose rows share positions
 
 template <int HD, int NP, int NC>
 struct QaShape {
@@ -233,6 +234,32 @@ LLM_D int sh_next(const QAttnArgs& a, int s, bool sharing) {
   sh_group(a, s, lead, end);
   return min(s + a.sh.rpt - (s - lead) % a.sh.rpt, end);
 }
+// Equal shares of units that differ in length: a unit of nt tiles counts nt + kShCost, what its start and end cost being
+// put before its tiles (256 of them, of one to four tiles each, took 74 us in equal runs of tiles, 30 us so).  A cut
+// there, or within kShNear tiles of the unit's end, moves to its start or end.
+constexpr int kShCost = 4, kShNear = 2;
+struct ShCut {
+  int q, r;
+  LLM_D void make(int T, int G) {
+    q = T / G;
+    r = T - q * G;
+  }
+  LLM_D int begin(int c) const { return c * q + min(c, r); }
+  // the last CTA whose share starts at y or before
+  LLM_D int owner(int y) const {
+    const int head = r * (q + 1);
+    return y < head ? y / (q + 1) : r + (y - head) / q;
+  }
+  // tile of a unit at which a cut at place o of it lies
+  LLM_D static int tile(int o, int nt) {
+    const int k = o - kShCost;
+    return k <= 0 ? 0 : k >= nt - kShNear ? nt : k;
+  }
+  // the first and the last CTA that have tiles of the unit of nt tiles at place y
+  LLM_D int first(int y) const { return owner(y + kShCost); }
+  LLM_D int last(int y, int nt) const { return owner(y + kShCost + max(0, nt - kShNear - 1)); }
+};
+
 // where a column's sums go, and its statistics (part 0, 1: a unit's first run, of a prefix or a row's own; 2: a later one)
 LLM_D float* sh_put(const QAttnArgs& a, int part, int half, int64_t col, int place, float m, float l, int cta, int cta0, int ctas) {
   const int64_t cols = (int64_t)a.r.B * a.r.S * a.c.kv * a.g;
@@ -405,6 +432,7 @@ struct QaWalk {
   int t, j, k0, k1;
   int st, end, off;  // off: place of (t, head 0) in the sequence
   bool sharing;
+  int offw;          // SH: the same with what units cost (ShCut)
   LLM_D QaUnit unit(const QAttnArgs& a, int i) const {
     if constexpr (SH) return sh_unit<kQaTile>(a, i, sharing);
     else return qa_unit(a, i);
@@ -431,6 +459,7 @@ struct QaWalk {
     u = unit(a, t);
     if (st - off == a.c.kv * u.nt) {  // (a cut moved to the end of its token tile)
       off = st;
+      if constexpr (SH) offw += a.c.kv * (u.nt + kShCost);
       skip(a);
       if (SH && st >= end) return;
     }
@@ -448,6 +477,7 @@ struct QaWalk {
     if (++j == a.c.kv) {
       j = 0;
       off += a.c.kv * u.nt;
+      if constexpr (SH) offw += a.c.kv * (u.nt + kShCost);
       skip(a);
       if (SH && st >= end) return;
     }
@@ -516,56 +546,74 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   // and the lane whose stretch holds the run's start finds its token tile
   const int nq = SH ? 2 * a.r.B * a.sh.cpr : a.r.step ? (a.tiles ? a.tiles[1] : a.r.B) : a.r.B * a.nct;
   bool sharing = false;
-  int* before = reinterpret_cast<int*>(base);  // SH: [nq] tiles of the units before (the ring is idle yet)
-  __shared__ int s_sum[SH ? X::NT / 32 : 1];
+  int2* before = reinterpret_cast<int2*>(base);  // SH: [nq] tiles of the units before, and how many have any (the ring is idle yet)
+  __shared__ int2 s_sum[SH ? X::NT / 32 : 1];
+  __shared__ int s_offw;
+  static_assert(!SH || ST * X::STAGE >= kShUnits * 8, "the counts of a call's units");
   if constexpr (SH) {
     // (counted by all threads: a unit's count is a chain of reads)
     sharing = sh_fine(a);
     const int per = (nq + X::NT - 1) / X::NT, u0 = min(nq, tid * per), u1 = min(nq, u0 + per);
-    int sum = 0;
+    int2 sum = make_int2(0, 0);  // tiles, and units that have some
     for (int t = u0; t < u1; ++t) {
       before[t] = sum;
-      sum += sh_unit<kQaTile>(a, t, sharing).nt;
+      const int nt = sh_unit<kQaTile>(a, t, sharing).nt;
+      sum.x += nt;
+      sum.y += nt > 0;
     }
-    int incl = sum;
+    int2 incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+      if (lane >= o) {
+        incl.x += x;
+        incl.y += y;
+      }
     }
     if (lane == 31) s_sum[warp] = incl;
     __syncthreads();
-    int lead = incl - sum, all = 0;
+    int2 lead = make_int2(incl.x - sum.x, incl.y - sum.y), all = make_int2(0, 0);
     for (int i = 0; i < X::NT / 32; ++i) {
-      if (i < warp) lead += s_sum[i];
-      all += s_sum[i];
+      if (i < warp) {
+        lead.x += s_sum[i].x;
+        lead.y += s_sum[i].y;
+      }
+      all.x += s_sum[i].x;
+      all.y += s_sum[i].y;
     }
-    for (int t = u0; t < u1; ++t) before[t] += lead;
+    for (int t = u0; t < u1; ++t) {
+      before[t].x += lead.x;
+      before[t].y += lead.y;
+    }
     __syncthreads();
     if (warp == 0 && lane < 2) {  // the run's start, and its end
-      const int total = all * a.c.kv, ge = min((int)gridDim.x, total);
-      if (lane == 0) s_total = s_begin = s_end = total;
+      const int total = (all.x + kShCost * all.y) * a.c.kv, ge = min((int)gridDim.x, total);
+      if (lane == 0) {
+        s_total = total;
+        s_begin = s_end = all.x * a.c.kv;
+      }
       __syncwarp(3u);
-      const int x = cta < ge ? [&] { QaCut cut; cut.make(total, ge); return cut.begin(cta + lane); }() : total;
-      if (x < total) {
-        // the last unit that starts at x or before
-        const int goal = x / a.c.kv;
+      if (cta + lane < ge) {
+        ShCut cut;
+        cut.make(total, ge);
+        const int y = cut.begin(cta + lane);
+        auto at = [&](int t) { return (before[t].x + kShCost * before[t].y) * a.c.kv; };
+        // the last unit that starts at y or before
         int lo = 0, hi = nq - 1;
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
-          if (before[mid] <= goal) lo = mid;
+          if (at(mid) <= y) lo = mid;
           else hi = mid - 1;
         }
-        const int off = before[lo] * a.c.kv, nt = (lo + 1 < nq ? before[lo + 1] : all) - before[lo];
-        QaCut cut;
-        cut.make(total, ge);
-        const int to = cut.moved(x, x - (int)((uint32_t)(x - off) % (uint32_t)nt), nt);
+        const int off = before[lo].x * a.c.kv, nt = (lo + 1 < nq ? before[lo + 1].x : all.x) - before[lo].x, o = y - at(lo);
+        const int j = o / (nt + kShCost), to = off + j * nt + ShCut::tile(o - j * (nt + kShCost), nt);
         if (lane) {
           s_end = to;
         } else {
           s_t = lo;
           s_off = off;
           s_begin = to;
+          s_offw = at(lo);
         }
       }
     }
@@ -622,6 +670,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   const uint32_t tmem = s_tmem;
   QaWalk<SH> w;
   w.sharing = sharing;
+  w.offw = SH ? s_offw : 0;
   w.begin(a, s_t, s_off, s_begin, s_end);
   grid_dep_wait();
   bool ok = true;  // a wait that gave up: no further waits, but every loop and barrier is still walked
@@ -1088,10 +1137,9 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         ffac[C + c] = f1 * (both ? gvs[2 * hv + 1] : 0.f) * r;
         const int tok = c / a.g;
         if constexpr (SH) {
-          const bool all = w.k0 == 0 && w.k1 == w.u.nt;
-          QaCut cut;
+          ShCut cut;
           cut.make(s_total, min((int)gridDim.x, s_total));
-          const int first = all ? cta : cut.first(w.unit0()), ctas = all ? 0 : cut.last(w.unit0(), w.u.nt) - first;
+          const int y = w.offw + w.j * (w.u.nt + kShCost), first = cut.first(y), ctas = cut.last(y, w.u.nt) - first;
           const int part = w.k0 > 0 ? 2 : w.t < a.r.B * a.sh.cpr ? 0 : 1;
           float* dst = sh_put(a, part, 0, ((int64_t)w.j * a.r.B * a.r.S + w.u.qrow) * a.g + c, c, M, L, cta, first, ctas);
           coff[c] = dst - a.sh.parts;

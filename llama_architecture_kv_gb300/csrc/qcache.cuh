@@ -163,6 +163,8 @@ struct ShSide {
   // CTAs after it << 8 | place in the unit}; and over the runs of other CTAs that go on with it [CTA][groups][pitch][hd], with
   // {reference, sum of weights}.  Where the sum of weights is 0 there are no sums.
   int32_t groups;
+  uint8_t* qp;     // queries in e4m3 pieces [pieces][columns][hd], and their scales [columns]
+  float* qs;
   float* parts;
   float4* stats;
   float* more;

@@ -13,15 +13,15 @@ namespace llm {
 
 namespace {
 
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 256;
 
-// Thread = (column, four dimensions).  Bound by the reads of the sums, which lie in L2.
-template <int QT>
+// Warp = column: its parts' statistics a lane each, then their sums, eight loads in flight (heads of 64: two parts at a
+// time, half a warp each).  Bound by the reads of the sums, which lie in L2.
+template <int HD, int QT>
 __global__ void __launch_bounds__(kMergeThreads) qshare_merge_kernel(const QAttnArgs a, const ShSide prefix, const ShSide own) {
-  const int q4 = a.c.hd / 4, BS = a.r.B * a.r.S, cols = BS * a.c.kv * a.g;
+  const int BS = a.r.B * a.r.S, cols = BS * a.c.kv * a.g, lane = threadIdx.x & 31;
   const bool sharing = sh_fine(a);
-  const int64_t t = (int64_t)blockIdx.x * kMergeThreads + threadIdx.x;
-  const int col = (int)(t / q4), k4 = (int)(t - (int64_t)col * q4);
+  const int col = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
   if (col >= cols) return;
   const int jt = col / a.g, h = col - jt * a.g, j = jt / BS, gt = jt - j * BS, b = gt / a.r.S, i = gt - b * a.r.S;
   if (i >= q_count(a.r, b)) return;
@@ -30,47 +30,140 @@ __global__ void __launch_bounds__(kMergeThreads) qshare_merge_kernel(const QAttn
   // (a column that sees something of a side is in a unit that has tiles there)
   const bool there[2] = {sh > 0 && end > 0, end > sh};
   grid_dep_wait();
-  // the parts: by side and group, each the unit's first run and those of the CTAs that go on with it
+  // parts, by side and group: the unit's first run, then those of the CTAs that go on with it
   float4 st[4] = {};
-  int first[4] = {}, runs[4] = {}, at[4] = {};
-  float M = kQaNone, L = 0.f;
+  int before[5] = {0, 0, 0, 0, 0};
 #pragma unroll
   for (int y = 0; y < 4; ++y) {
     const ShSide& x = y / 2 ? own : prefix;
-    if (!there[y / 2] || y % 2 >= x.groups) continue;
-    st[y] = __ldcg(x.stats + (int64_t)y * cols + col);
-    M = fmaxf(M, st[y].x);
-    first[y] = __float_as_int(st[y].z) + 1;
-    runs[y] = __float_as_int(st[y].w) >> 8;
-    at[y] = min(__float_as_int(st[y].w) & 255, x.pitch - 1);
-    // (where a wait gave up, there is nothing to go by)
-    if (first[y] < 1 || runs[y] < 0 || runs[y] > x.ctas - first[y]) runs[y] = 0;
-#pragma unroll 4
-    for (int c = 0; c < runs[y]; ++c) M = fmaxf(M, __ldcg(x.mstats + ((first[y] + c) * x.groups + y % 2) * x.pitch + at[y]).x);
+    int n = 0;
+    if (there[y / 2] && y % 2 < x.groups) {
+      st[y] = __ldcg(x.stats + (int64_t)y * cols + col);
+      const int c0 = __float_as_int(st[y].z), runs = __float_as_int(st[y].w) >> 8;
+      // (where a wait gave up, there is nothing to go by)
+      n = c0 < 0 || runs < 0 || runs >= x.ctas - c0 ? 1 : runs + 1;
+    }
+    before[y + 1] = before[y] + n;
   }
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  // (a part without weight has no sums)
-  auto plus = [&](float m, float l, const float* v) {
-    if (l == 0.f) return;
-    const float f = qa_exp2(m - M);
-    const float4 s = __ldcg(reinterpret_cast<const float4*>(v) + k4);
-    L = fmaf(f, l, L);
-    o.x = fmaf(f, s.x, o.x); o.y = fmaf(f, s.y, o.y); o.z = fmaf(f, s.z, o.z); o.w = fmaf(f, s.w, o.w);
-  };
-#pragma unroll
-  for (int y = 0; y < 4; ++y) {
+  const int np = before[4];
+  // a part's statistics, and where its sums are
+  auto part = [&](int p, const float*& at) {
+    const int y = (p >= before[1]) + (p >= before[2]) + (p >= before[3]);
     const ShSide& x = y / 2 ? own : prefix;
-    if (!there[y / 2] || y % 2 >= x.groups) continue;
-    plus(st[y].x, st[y].y, x.parts + ((int64_t)y * cols + col) * a.c.hd);
-#pragma unroll 4
-    for (int c = 0; c < runs[y]; ++c) {
-      const int64_t part = (int64_t)((first[y] + c) * x.groups + y % 2) * x.pitch + at[y];
-      const float2 s = __ldcg(x.mstats + part);
-      plus(s.x, s.y, x.more + part * a.c.hd);
+    const float4 s = y == 0 ? st[0] : y == 1 ? st[1] : y == 2 ? st[2] : st[3];
+    const int c = p - (y == 0 ? 0 : y == 1 ? before[1] : y == 2 ? before[2] : before[3]);
+    if (c == 0) {
+      at = x.parts + ((int64_t)y * cols + col) * HD;
+      return make_float2(s.x, s.y);
+    }
+    const int64_t place = (int64_t)((__float_as_int(s.z) + c) * x.groups + y % 2) * x.pitch + min(__float_as_int(s.w) & 255, x.pitch - 1);
+    at = x.more + place * HD;
+    return __ldcg(x.mstats + place);
+  };
+  float M = kQaNone;
+  const float* at = nullptr;
+  float2 mine = make_float2(kQaNone, 0.f);
+  for (int p0 = 0; p0 < np; p0 += 32) {
+    if (p0 + lane < np) mine = part(p0 + lane, at);
+    M = fmaxf(M, mine.x);
+  }
+  M = warp_max(M);
+  constexpr int W = HD / 4, SIDE = 32 / W;  // lanes of a part, parts at a time
+  const int k4 = lane % W, sub = lane / W;
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p0 = 0; p0 < np; p0 += 32) {
+    if (np > 32) mine = p0 + lane < np ? part(p0 + lane, at) : make_float2(kQaNone, 0.f);
+    // (a part without weight has no sums)
+    const float f = mine.y == 0.f ? 0.f : qa_exp2(mine.x - M);
+    L = fmaf(f, mine.y, L);
+    const int n = min(32, np - p0);
+    constexpr int U = 8;
+    for (int q0 = 0; q0 < n; q0 += U * SIDE) {
+      float4 v[U];
+      float fp[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int q = q0 + u * SIDE + sub, from = min(q, 31);
+        const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(at), from));
+        fp[u] = __shfl_sync(0xffffffffu, f, from);
+        if (q >= n) fp[u] = 0.f;
+        v[u] = fp[u] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcg(reinterpret_cast<const float4*>(src) + k4);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        o.x = fmaf(fp[u], v[u].x, o.x);
+        o.y = fmaf(fp[u], v[u].y, o.y);
+        o.z = fmaf(fp[u], v[u].z, o.z);
+        o.w = fmaf(fp[u], v[u].w, o.w);
+      }
     }
   }
+  L = warp_sum(L);
+  if constexpr (SIDE == 2) {
+    o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
+    o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+    o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
+    o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+  }
   const float r = L == 0.f ? 0.f : 1.f / L;
-  qa_put4<QT>(a.out, (int64_t)gt * a.out_stride + (int64_t)(j * a.g + h) * a.c.hd + 4 * k4, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
+  if (sub == 0)
+    qa_put4<QT>(a.out, (int64_t)gt * a.out_stride + (int64_t)(j * a.g + h) * HD + 4 * k4, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
+}
+
+// Queries in e4m3 pieces (qshare.cuh), warp = column; of tokens that are not there: zeros.  As a kernel of its own
+// (2 us) they are made once; four warps of each CTA of the attention took 13 us for 128 columns.
+template <int HD, int QT>
+__global__ void __launch_bounds__(kMergeThreads) qshare_pieces_kernel(const QAttnArgs a) {
+  constexpr int NP = QT ? 2 : 4, E = HD / 32;
+  grid_dep_launch();
+  const int BS = a.r.B * a.r.S, cols = BS * a.c.kv * a.g, lane = threadIdx.x & 31;
+  const int col = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  if (col >= cols) return;
+  const int jt = col / a.g, h = col - jt * a.g, j = jt / BS, gt = jt - j * BS, b = gt / a.r.S;
+  float v[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) v[i] = 0.f;
+  if (gt - b * a.r.S < q_count(a.r, b)) {
+    const int64_t at = (int64_t)gt * a.q_stride + (int64_t)(j * a.g + h) * HD + lane * E;
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      if constexpr (QT) {
+        const uint32_t f = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + at + i);
+        v[i] = bf16_lo(f);
+        v[i + 1] = bf16_hi(f);
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at + i);
+        v[i] = f.x;
+        v[i + 1] = f.y;
+      }
+    }
+  }
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < E; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  top = __reduce_max_sync(0xffffffffu, top);
+  const bool fine = top < 0x7f800000u;
+  const float s = q_scale(fine ? __uint_as_float(top) * 1.75f : 0.f), r = a.scale < 0.f ? -q_recip(s) : q_recip(s);  // |x| r <= 256
+#pragma unroll
+  for (int i = 0; i < E; ++i) v[i] = fine ? v[i] * r : 0.f;
+#pragma unroll
+  for (int y = 0; y < NP; ++y) {
+    uint32_t code = 0u;
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      const uint32_t p = e4m3x2(v[i], v[i + 1]);
+      const float2 f = e4m3_pair(p);
+      v[i] = (v[i] - f.x) * (y == 1 ? 1024.f : 1.f);
+      v[i + 1] = (v[i + 1] - f.y) * (y == 1 ? 1024.f : 1.f);
+      code |= p << (8 * i);
+    }
+    uint8_t* dst = a.sh.qp + ((int64_t)y * cols + col) * HD + lane * E;
+    if constexpr (E == 4) *reinterpret_cast<uint32_t*>(dst) = code;
+    else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)code;
+  }
+  // (a query that is not finite makes its scores NaN)
+  if (lane == 0) a.sh.qs[col] = fine ? s * (fabsf(a.scale) * 1.4426950408889634f) : __uint_as_float(0x7fc00000u);
 }
 
 // Which kernel takes the prefixes: that of many columns where a group has more than kShFew on average
@@ -111,17 +204,35 @@ bool qshare_fits(const QCacheView& c, int g, int qt, int B, int S, int ngroups, 
   const ShPlan p = plan_of(c, g, qt, B, S, ngroups);
   const ShSide x = side_of(B, S, g, p.cols, 3, 1);
   const int64_t units = 2 * (int64_t)B * x.cpr;
-  return units <= kShSlots && p.columns < (1ll << 31) / c.hd && units * c.kv * ((int64_t)limit / 64 + 2) < 1ll << 31;
+  return units <= kShUnits && p.columns < (1ll << 31) / c.hd && units * c.kv * ((int64_t)limit / 64 + 2) < 1ll << 31;
 }
 
 uint64_t qshare_workspace(const QCacheView& c, int g, int B, int S, int num_sms) {
   const uint64_t columns = (uint64_t)B * S * c.kv * g;
-  return 4 * columns * (c.hd * 4 + 16) + (uint64_t)num_sms * (2 * kShRows + 2 * 32) * (c.hd * 4 + 8);
+  return 4 * columns * (c.hd * 4 + 16) + columns * (4 * c.hd + 16) + (uint64_t)num_sms * (2 * kShRows + 2 * 32) * (c.hd * 4 + 8);
 }
 
+namespace {
+cudaError_t launch(void* fn, int64_t grid, void** args, cudaStream_t s, bool pdl) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+}  // namespace
+
+// The kernels of a call follow one another programmatically: each but the first may start before the one before
+// is done, waits for it before it reads what that wrote, and is done only after it.
 cudaError_t launch_qshare_all(const QAttnArgs& a0, int qt, int num_sms, cudaStream_t s) {
   QAttnArgs a = a0;
   const int64_t B = a.r.B, S = a.r.S;
+  const int hd = a.c.hd, np = qt ? 2 : 4;
   const ShPlan p = plan_of(a.c, a.g, qt, B, S, a.ngroups);
   ShSide few = side_of(B, S, a.g, p.cols, p.many ? 2 : 3, 1), many = side_of(B, S, a.g, kShRows, 1, 2);
   few.ctas = few_ctas(p.cols, num_sms);
@@ -132,37 +243,44 @@ cudaError_t launch_qshare_all(const QAttnArgs& a0, int qt, int num_sms, cudaStre
     w += n;
     return at;
   };
-  few.parts = many.parts = reinterpret_cast<float*>(take(4 * (uint64_t)p.columns * a.c.hd * 4));
-  few.stats = many.stats = reinterpret_cast<float4*>(take(4 * (uint64_t)p.columns * 16));
+  const uint64_t columns = (uint64_t)p.columns;
+  few.parts = many.parts = reinterpret_cast<float*>(take(4 * columns * hd * 4));
+  few.stats = many.stats = reinterpret_cast<float4*>(take(4 * columns * 16));
+  many.qp = take(columns * 4 * hd);
+  many.qs = reinterpret_cast<float*>(take(columns * 16));
   for (ShSide* x : {&few, &many}) {
     const uint64_t n = (uint64_t)x->ctas * x->groups * x->pitch;
-    x->more = reinterpret_cast<float*>(take(n * a.c.hd * 4));
+    x->more = reinterpret_cast<float*>(take(n * hd * 4));
     x->mstats = reinterpret_cast<float2*>(take(n * 8));
   }
-  CUtensorMap kmap, vmap;
+  CUtensorMap kmap, vmap, qmap;
   const uint64_t rows = (uint64_t)a.c.rows * a.c.kv * a.c.cap;
-  if (!qattn_make_map(&kmap, a.c.k, a.c.hd, rows) || !qattn_make_map(&vmap, a.c.v, a.c.hd, rows)) return cudaErrorInvalidValue;
+  if (!qattn_make_map(&kmap, a.c.k, hd, rows) || !qattn_make_map(&vmap, a.c.v, hd, rows)) return cudaErrorInvalidValue;
+  const int64_t grid = (p.columns + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
+  cudaError_t e = cudaSuccess;
+  if (p.many) {
+    if (!qattn_make_map(&qmap, many.qp, hd, np * columns)) return cudaErrorInvalidValue;
+    a.sh = many;
+    void* args[] = {&a};
+    auto fn = hd == 64 ? (qt ? qshare_pieces_kernel<64, 1> : qshare_pieces_kernel<64, 0>)
+                       : (qt ? qshare_pieces_kernel<128, 1> : qshare_pieces_kernel<128, 0>);
+    e = launch((void*)fn, grid, args, s, false);
+    if (e != cudaSuccess) return e;
+  }
   a.sh = few;
-  auto fn = a.c.hd == 64 ? (qt ? qattn_sh64_bf16 : qattn_sh64_f32) : (qt ? qattn_sh128_bf16 : qattn_sh128_f32);
-  cudaError_t e = fn(kmap, vmap, a, p.nc, few.ctas, s, false);
+  auto fn = hd == 64 ? (qt ? qattn_sh64_bf16 : qattn_sh64_f32) : (qt ? qattn_sh128_bf16 : qattn_sh128_f32);
+  e = fn(kmap, vmap, a, p.nc, few.ctas, s, p.many);
   if (e != cudaSuccess) return e;
   if (p.many) {
     a.sh = many;
-    auto fm = a.c.hd == 64 ? (qt ? qshare64_bf16 : qshare64_f32) : (qt ? qshare128_bf16 : qshare128_f32);
-    e = fm(kmap, vmap, a, many.ctas, s, true);
+    auto fm = hd == 64 ? (qt ? qshare64_bf16 : qshare64_f32) : (qt ? qshare128_bf16 : qshare128_f32);
+    e = fm(kmap, vmap, qmap, a, many.ctas, s, true);
     if (e != cudaSuccess) return e;
   }
-  const int64_t threads = p.columns * (a.c.hd / 4);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((threads + kMergeThreads - 1) / kMergeThreads));
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, qt ? qshare_merge_kernel<1> : qshare_merge_kernel<0>, a, p.many ? many : few, few);
+  void* args[] = {&a, p.many ? &many : &few, &few};
+  auto fj = hd == 64 ? (qt ? qshare_merge_kernel<64, 1> : qshare_merge_kernel<64, 0>)
+                     : (qt ? qshare_merge_kernel<128, 1> : qshare_merge_kernel<128, 0>);
+  return launch((void*)fj, grid, args, s, true);
 }
 
 }  // namespace llm

@@ -36,7 +36,6 @@ namespace llm {
 
 constexpr int kShRows = 128;         // columns of a unit: the M side
 constexpr int kShSegs = 8;           // segments told ahead
-constexpr int kShSlots = 8192;       // units per key/value head that the walk can count
 constexpr int kShWarps = 16;         // loads, products, walk, an idle one; two softmax groups of four; four that widen
 constexpr int kShThreads = 32 * kShWarps;
 constexpr int kShWiden = 128;        // threads that widen
@@ -58,21 +57,7 @@ struct ShShape {
   static constexpr uint32_t SWZ = HD == 128 ? 2 : 4;
   static constexpr uint32_t BUF = 128;               // tensor-memory columns of a group's scores; the groups' O behind both
   static_assert(SMEM <= kQaSmem, "shared memory");
-  static_assert((KS + VS) * KB >= kShSlots * 4, "the walk's counts");
-};
-
-// equal runs of T tiles over G CTAs
-struct ShCut {
-  int q, r;
-  LLM_D void make(int T, int G) {
-    q = T / G;
-    r = T - q * G;
-  }
-  LLM_D int begin(int c) const { return c * q + min(c, r); }
-  LLM_D int owner(int i) const {
-    const int head = r * (q + 1);
-    return i < head ? i / (q + 1) : r + (i - head) / q;
-  }
+  static_assert((KS + VS) * KB >= kShUnits * 4, "the walk's counts");
 };
 
 // what the walk tells the others of a segment
@@ -89,7 +74,8 @@ struct ShSeg {
 
 template <int HD, int QT>
 __global__ void __launch_bounds__(kShThreads, 1)
-    qshare_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const QAttnArgs a) {
+    qshare_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap,
+                  const QAttnArgs a) {
   using X = ShShape<HD, QT>;
   constexpr int NP = X::NP, WP = X::WP, TN = X::TN, NB = X::NB, KS = X::KS, VS = X::VS;
   extern __shared__ unsigned char qraw[];
@@ -138,7 +124,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
     mbar_init(b_end, 1);
     mbar_init(b_qe, 1);
     for (int i = 0; i < kShSegs; ++i) {
-      mbar_init(b_qf + 8u * i, kShWiden);
+      mbar_init(b_qf + 8u * i, 33);          // the loads, and the lanes that copy the scales
       mbar_init(b_gf + 8u * i, 32);
       mbar_init(b_ge + 8u * i, 2 + 12);
     }
@@ -282,17 +268,39 @@ __global__ void __launch_bounds__(kShThreads, 1)
     mbar_arrive(b_gf + 8u * gs);
   } else if (warp == 0) {
     // ---- the loads ----
+    grid_dep_wait();  // (the queries' pieces are the work of a kernel before)
+    fence_proxy_async_global();
     if (lane == 0) {
       tma_prefetch_map(&kmap);
       tma_prefetch_map(&vmap);
+      tma_prefetch_map(&qmap);
     }
-    uint32_t ks = 0u, kpar = 1u, vs = 0u, vpar = 1u, nk = 0u;
+    uint32_t ks = 0u, kpar = 1u, vs = 0u, vpar = 1u, nk = 0u, qpar = 1u;
     const float* sc = lane < NB ? a.c.ks : a.c.vs;
     const int blk = lane & (NB - 1);
     // places of 32 pages, one per lane: of row `held` from page `page0` on (of a unit's heads all the same)
     int held = -1, held_start = 0, held_stop = 0, page0 = 0, prow = -1, ppos = 0;
     while (const int n = next_seg()) {
       const int p0 = segs[gslot].p0, start = segs[gslot].start, stop = segs[gslot].stop, place = segs[gslot].place, j = segs[gslot].j;
+      {
+        // the queries, once the products of the segment before have read theirs (the rows behind the unit's columns are
+        // others' or what was there: finite, and of no use)
+        const int col = (j * a.r.B * a.r.S + segs[gslot].gt) * a.g, used = segs[gslot].used, cols = a.r.B * a.r.S * a.c.kv * a.g;
+        wait(b_qe, qpar);
+        qpar ^= 1u;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t bar = b_qf + 8u * gslot;
+        if (lane == 0) {
+          const int boxes = used > 64 ? 2 : 1;
+          mbar_expect_tx(bar, NP * boxes * 64 * HD);
+          for (int p = 0; p < NP; ++p)
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(smem_u32(qbuf) + (p * kShRows + 64 * i) * HD, &qmap, bar, 0, p * cols + col + 64 * i);
+        }
+        for (int c = lane; c < used; c += 32) qa_copy4(smem_u32(qsc + gslot * kShRows + c), a.sh.qs + col + c);
+        qa_copy_arrive(bar);
+      }
       seg_done();
 #pragma unroll 1
       for (int k = 0; k < n; ++k, ++nk) {
@@ -351,7 +359,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
       }
       if (!ok) break;
     }
-    // no copy may still be writing shared memory when the CTA exits
+    // no copy may still be writing shared memory when the CTA exits (the queries' have been waited for with their use)
     ok = true;
 #pragma unroll 1
     for (uint32_t i = nk > KS ? nk - KS : 0u; i < nk; ++i) wait(b_kf + 8u * (i % KS), (i / KS) & 1u);
@@ -698,92 +706,12 @@ __global__ void __launch_bounds__(kShThreads, 1)
       flush(mine - 1u, true);
     }
   } else {
-    // ---- query pieces, and values widened ----
-    const int wid = tid - 384, ww = warp - 12;
-    uint32_t vs = 0u, vpar = 0u, it = 0u, qpar = 1u;
-    // the next segment's query pieces, once the products of the one before have read theirs: its tiles, or 0
-    auto queries = [&]() {
-      const int n = next_seg();
-      if (n == 0) return 0;
-      // warp = column, eight at a time
-      constexpr int E = HD / 32, QU = 8;
-      const ShSeg& g = segs[gslot];
-      const float sign = a.scale < 0.f ? -1.f : 1.f;
-      const int used = g.used, rows = (used + 31) & ~31;
-      const int64_t q0 = (int64_t)g.gt * a.q_stride + (int64_t)g.j * a.g * HD + lane * E;
-#pragma unroll 1
-      for (int c0 = ww; c0 < rows; c0 += 4 * QU) {
-        float w[QU][E];
-#pragma unroll
-        for (int y = 0; y < QU; ++y) {
-          const int c = c0 + 4 * y, tok = c / a.g;
-#pragma unroll
-          for (int i = 0; i < E; ++i) w[y][i] = 0.f;
-          if (c >= used) continue;
-          const int64_t at = q0 + (int64_t)tok * a.q_stride + (c - tok * a.g) * HD;
-          if constexpr (QT == 0) {
-            const float* p = static_cast<const float*>(a.q) + at;
-            if constexpr (E == 4) {
-              const float4 f = *reinterpret_cast<const float4*>(p);
-              w[y][0] = f.x; w[y][1] = f.y; w[y][2] = f.z; w[y][3] = f.w;
-            } else {
-              const float2 f = *reinterpret_cast<const float2*>(p);
-              w[y][0] = f.x; w[y][1] = f.y;
-            }
-          } else if constexpr (E == 4) {
-            const uint2 f = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + at);
-            w[y][0] = bf16_lo(f.x); w[y][1] = bf16_hi(f.x); w[y][2] = bf16_lo(f.y); w[y][3] = bf16_hi(f.y);
-          } else {
-            const uint32_t f = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + at);
-            w[y][0] = bf16_lo(f); w[y][1] = bf16_hi(f);
-          }
-        }
-        if (c0 == ww) {  // (the loads are under way)
-          wait(b_qe, qpar);
-          qpar ^= 1u;
-          __syncwarp();
-        }
-#pragma unroll
-        for (int y8 = 0; y8 < QU; ++y8) {
-          float (&v)[E] = w[y8];
-          const int c = c0 + 4 * y8;
-          uint32_t top = 0u;
-#pragma unroll
-          for (int i = 0; i < E; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-          top = __reduce_max_sync(0xffffffffu, top);
-          const bool fine = top < 0x7f800000u;
-          const float s = q_scale(fine ? __uint_as_float(top) * 1.75f : 0.f), r = q_recip(s) * sign;  // |x| r <= 256
-#pragma unroll
-          for (int i = 0; i < E; ++i) v[i] = fine ? v[i] * r : 0.f;
-#pragma unroll
-          for (int y = 0; y < NP; ++y) {
-            uint32_t code = 0u;
-#pragma unroll
-            for (int i = 0; i < E; i += 2) {
-              const uint32_t p = e4m3x2(v[i], v[i + 1]);
-              const float2 f = e4m3_pair(p);
-              v[i] = (v[i] - f.x) * (y == 1 ? 1024.f : 1.f);
-              v[i + 1] = (v[i + 1] - f.y) * (y == 1 ? 1024.f : 1.f);
-              code |= p << (8 * i);
-            }
-            unsigned char* dst = qbuf + (y * kShRows + c) * HD;
-            if constexpr (HD == 128)
-              *reinterpret_cast<uint32_t*>(dst + (((lane >> 2) ^ (c & 7)) << 4) + (lane & 3) * 4) = code;
-            else
-              *reinterpret_cast<uint16_t*>(dst + (((lane >> 3) ^ ((c >> 1) & 3)) << 4) + (lane & 7) * 2) = (uint16_t)code;
-          }
-          // a query that is not finite makes its scores NaN
-          if (lane == 0) qsc[gslot * kShRows + c] = fine ? s * (fabsf(a.scale) * 1.4426950408889634f) : __uint_as_float(0x7fc00000u);
-        }
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(b_qf + 8u * gslot);
-      return n;
-    };
-    int n = queries();
-    while (n) {
+    // ---- values widened ----
+    const int wid = tid - 384;
+    uint32_t vs = 0u, vpar = 0u, it = 0u;
+    while (const int n = next_seg()) {
       const int start = segs[gslot].start, stop = segs[gslot].stop;
-      int p0 = segs[gslot].p0, next = 0;
+      int p0 = segs[gslot].p0;
       seg_done();
 #pragma unroll 1
       for (int k = 0; k < n; ++k, ++it, p0 += TN) {
@@ -813,21 +741,18 @@ __global__ void __launch_bounds__(kShThreads, 1)
         if (lane == 0) mbar_arrive(b_ve + 8u * vs);
         if (++vs == VS) vs = 0u, vpar ^= 1u;
       }
-      // (the next segment's queries at once: its first scores are to be there when this segment's last tile is done)
-      next = queries();
-      n = next;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
-  grid_dep_wait();  // (the kernel before may still be at its part of the call: what waits for this one waits for both)
+
 }
 
 // one instantiation per translation unit
 template <int HD, int QT>
-cudaError_t launch_qshare(const CUtensorMap& kmap, const CUtensorMap& vmap, const QAttnArgs& a, int grid, cudaStream_t s, bool pdl) {
+cudaError_t launch_qshare(const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap, const QAttnArgs& a, int grid, cudaStream_t s, bool pdl) {
   constexpr size_t smem = ShShape<HD, QT>::SMEM;
   auto fn = qshare_kernel<HD, QT>;
   // (the limit belongs to the device's context: set on every call, a fraction of a microsecond)
@@ -843,10 +768,11 @@ cudaError_t launch_qshare(const CUtensorMap& kmap, const CUtensorMap& vmap, cons
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, kmap, vmap, a);
+  return cudaLaunchKernelEx(&cfg, fn, kmap, vmap, qmap, a);
 }
 
-#define LLM_QSHARE(NAME) cudaError_t NAME(const CUtensorMap& kmap, const CUtensorMap& vmap, const QAttnArgs& a, int grid, cudaStream_t s, bool pdl)
+#define LLM_QSHARE(NAME) \
+  cudaError_t NAME(const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap, const QAttnArgs& a, int grid, cudaStream_t s, bool pdl)
 LLM_QSHARE(qshare64_f32);
 LLM_QSHARE(qshare64_bf16);
 LLM_QSHARE(qshare128_f32);

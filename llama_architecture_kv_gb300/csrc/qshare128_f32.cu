@@ -3,6 +3,6 @@
 
 namespace llm {
 
-LLM_QSHARE(qshare128_f32) { return launch_qshare<128, 0>(kmap, vmap, a, grid, s, pdl); }
+LLM_QSHARE(qshare128_f32) { return launch_qshare<128, 0>(kmap, vmap, qmap, a, grid, s, pdl); }
 
 }  // namespace llm

@@ -3,6 +3,6 @@
 
 namespace llm {
 
-LLM_QSHARE(qshare64_bf16) { return launch_qshare<64, 1>(kmap, vmap, a, grid, s, pdl); }
+LLM_QSHARE(qshare64_bf16) { return launch_qshare<64, 1>(kmap, vmap, qmap, a, grid, s, pdl); }
 
 }  // namespace llm
