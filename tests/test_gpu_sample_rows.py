@@ -50,6 +50,24 @@ def test_large_vocabularies(V):
     check(rng.standard_normal((B, V)) * 2.5, [1.0, 0.8, 0.0, 2.0], [V, 50, 1, V // 3], [0.95, 1.0, 1.0, 0.9], [0, 0, 0, 1e-3], rng.random(B))
 
 
+@pytest.mark.parametrize("B,V", [(20, 32771), (39, 16387), (153, 2049), (40, 100003), (3, 65537)])
+def test_numbers_of_rows_and_ids(B, V):
+    # rows take fewer CTAs the more there are, and more where a part of a row has no room on chip
+    rng = np.random.default_rng(B)
+    check(rng.standard_normal((B, V)) * rng.choice([0.5, 2.5, 6.0], (B, 1)), *settings(rng, B, V))
+
+
+def test_places_whose_candidates_just_fit_or_just_do_not():
+    # n logits in one of the 2048 steps into which the distances are sorted first, n about the room for a place's
+    # and for all places' candidates, the rest far apart
+    rng = np.random.default_rng(6)
+    for n in (1000, 1023, 1024, 1025, 2046, 2047, 2048, 2049, 2100):
+        V = n + 500
+        v = np.concatenate([[0.0], np.linspace(-20, -1, V - n - 1), -0.5 - 1e-4 * rng.random(n)])
+        v = np.stack([rng.permutation(v) for _ in range(6)])
+        check(v, [1.0] * 6, [V, n // 2, n + 1, V, 3, V], [0.9, 1.0, 0.5, 1.0, 0.9, 0.3], [0, 0, 0.1, 0.6, 0.6065, 0.60651], rng.random(6))
+
+
 def test_equal_logits_and_logits_within_a_step():
     # every candidate at one distance, more than are put in order at once; and distances of a few units of 2^-27
     V, rng = 20000, np.random.default_rng(1)
