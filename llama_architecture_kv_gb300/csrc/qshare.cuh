@@ -580,6 +580,9 @@ __global__ void __launch_bounds__(kShThreads, 1)
                                fmaxf(__uint_as_float(v[16 * b + 8 + i]), __uint_as_float(v[16 * b + 12 + i])));
                 if (see[b]) m = fmaxf(m, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * f1[b]);
               }
+              // (a lane without a column has the scores of whatever queries were there: they move no reference of the others,
+              // whose roundings would depend on what ran before)
+              if (row >= used) m = kQaNone;
               // (references move when a weight exceeds 2^24, or a value's scale 2^16 times, what they are relative to: rarely
               // but with a segment's first tile)
               if (__any_sync(0xffffffffu, m > ref + kShMost) || vtop > vref * 65536.f) {

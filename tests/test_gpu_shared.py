@@ -23,6 +23,13 @@ def tolerance(dtype, hd, want, mag, sens):
     return mag * (2.2 * ds + 2.0 ** -21 + digits + 2.0 ** -19) + (np.abs(want) * 2.0 ** -8 if dtype == "bf16" else 0) + 1e-37
 
 
+def wide_table(r, B, table=None):
+    """The rows' page table, or that of rows in place, with columns for 2^18 positions, which no row has."""
+    per = r.k.shape[2] // 64
+    table = np.arange(B)[:, None] * per + np.arange(per)[None] if table is None else np.asarray(table)
+    return np.concatenate([table, np.full((B, 4096 - table.shape[1]), -1)], 1).astype(np.int32)
+
+
 def check(c, r, rng, S, g, dtype, length, groups, shared, count=None, table=None, scale=None, spread=1.0, ws=None, status=0, want_with=None):
     B, hd = len(length), r.hd
     q, qn = rows_of(rng, (B, S, r.kv * g, hd), dtype, spread)
@@ -31,10 +38,17 @@ def check(c, r, rng, S, g, dtype, length, groups, shared, count=None, table=None
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     c.attend_shared(q, i32(length), i32(groups), i32(shared), out, ws, count=None if count is None else i32(count),
                     table=None if table is None else i32(table), scale=scale, status=st)
+    outs = [out]
+    if status == 0 and r.k.shape[2] % 64 == 0:
+        # the same through a page table that has room for far more, which calls that read the shared positions once go by
+        outs.append(torch.full_like(q, 9.0))
+        t = wide_table(r, B) if table is None else wide_table(r, B, table)
+        c.attend_shared(q, i32(length), i32(groups), i32(shared), outs[1], ws, count=None if count is None else i32(count),
+                        table=i32(t), scale=scale, status=st)
     length, groups, shared = want_with or (length, groups, shared)
     want, mag, sens, _ = shared_ref.attend_shared(r, qn, length, groups, shared, count, table, scale, out=np.full(q.shape, 9.0))
-    got = out.double().cpu().numpy()
     assert int(st) == status
+    got = np.stack([x.double().cpu().numpy() for x in outs])
     err, tol = np.abs(got - want), tolerance(dtype, hd, want, mag, sens)
     bad = ~(err <= tol)
     assert not bad.any(), (f"{int(bad.sum())} of {bad.size} off, first at {np.argwhere(bad)[0].tolist()}, "
@@ -300,3 +314,41 @@ def test_a_run_of_fork_write_attention_and_draws():
     assert int(st) == 0
     update([0, -1, 0, -1], [length[0], 0, 65, 0])
     assert counts.tolist()[1] == shared_ref.pages_of(length[0]) + 1
+
+
+@pytest.mark.parametrize("dtype,hd,S", [("bf16", 128, 1), ("f32", 64, 3)])
+def test_captured_calls_that_read_the_shared_positions_once(dtype, hd, S):
+    # as above, for calls whose tables have room for more: several kernels each, workspaces that held anything
+    rng = np.random.default_rng(32)
+    B, kv, g, cap = 7, 2, 4, 640
+    c, r = make(B, kv, cap, hd, garbage=4)
+    fill(c, r, rng, 600)
+    table = i32(wide_table(r, B))
+    length, groups, shared = i32([600 - 7 * b for b in range(B)]), i32([0, 2, B]), i32([300, 500])
+    q, _ = rows_of(rng, (B, S, kv * g, hd), dtype)
+    ws = [c.workspace_shared(g, B, S, 2) for _ in range(2)]
+    out = [torch.zeros_like(q) for _ in range(2)]
+    graphs = []
+    for i in range(2):
+        ws[i].fill_(255)
+        c.attend_shared(q, length, groups, shared, out[i], ws[i], table=table)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            c.attend_shared(q, length, groups, shared, out[i], ws[i], table=table)
+    s = [torch.cuda.Stream() for _ in range(2)]
+    for L, sh in (([600] * B, [300, 500]), ([250, 600, 0, 64, 500, 10, 3], [64, 65]), ([600 - 7 * b for b in range(B)], [0, 600])):
+        length.copy_(i32(L))
+        shared.copy_(i32(sh))
+        want, few = torch.zeros_like(q), torch.zeros_like(q)
+        c.attend_shared(q, length, groups, shared, want, ws[0], table=table)
+        c.attend_shared(q, length, groups, shared, few, ws[0])      # (the other way: the same workspace)
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for i in range(2):
+                with torch.cuda.stream(s[i]):
+                    graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want) and torch.equal(out[1], want)
+        ref, mag, sens, _ = shared_ref.attend_shared(r, q.double().cpu().numpy(), L, [0, 2, B], sh)
+        for x in (want, few):
+            assert (np.abs(x.double().cpu().numpy() - ref) <= tolerance(dtype, hd, ref, mag, sens)).all()
