@@ -16,7 +16,7 @@ SOURCES = ["llm.cu", "gemv.cu", "gemm.cu", "attention.cu", "sampler.cu", "noallo
 # the longest first
 SOURCES = ([f"qattn_tc{hd}_{t}.cu" for t in ("f32", "f32_wide", "bf16") for hd in (128, 64)]
            + [f"qshare{hd}_{t}.cu" for t in ("f32", "bf16") for hd in (128, 64)]
-           + [f"qattn_sh{hd}_{t}.cu" for t in ("f32", "bf16") for hd in (128, 64)] + ["qshare.cu"] + SOURCES)
+           + [f"qattn_{k}{hd}_{t}.cu" for k in ("by", "sh") for t in ("f32", "bf16") for hd in (128, 64)] + ["qshare.cu"] + SOURCES)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE]
 

@@ -368,6 +368,23 @@ uint64_t qattn_step_workspace(const QCacheView& c, int g, int NT, int num_sms) {
   return most;
 }
 
+// Whether rows that share positions are attended one by one (QAttnArgs::groups): where every row is a group, or they can
+// hold so few tiles of positions per SM that reading the shared ones once, with the two to four kernels that it takes, saves
+// nothing.  Row by row, and shared: 4 rows of about 1000 positions (2 tiles per SM) 16 and 18 us, 16 of 2176 (14) 25 and 39, 24 of
+// 5300 in 3 groups (26) 41 and 39, 16 with 5 tokens of 4400 (29) 60 and 70, 2 of 65536 (54) 47 and 43, 32 of 8400 (111) 88 and 54.
+constexpr int kByTiles = 32;
+static __global__ void q_clear_tickets_kernel(uint4* tickets) {
+  grid_dep_launch();
+  static_assert(kQattnTickets == 256 * 16, "a thread's tickets");
+  tickets[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+}
+static bool q_by_rows(const QAttnArgs& a, int qt, int num_sms) {
+  if (!qattn_fits(a.c, a.g, qt, a.r.B, a.r.S, std::min<int64_t>((int64_t)a.r.limit + 2 * kQaTile, 0x7fffffff), num_sms)) return false;
+  const TcPlanQ p = plan_tc_q(a.c, a.g, qt, a.r.B, a.r.S, a.r.limit, num_sms);
+  const int64_t tiles = (int64_t)a.r.B * (((int64_t)a.r.S + p.tokens - 1) / p.tokens) * a.c.kv * q_tiles_of(a.r.limit);
+  return a.ngroups == a.r.B || tiles <= (int64_t)num_sms * kByTiles;
+}
+
 cudaError_t launch_qattn(const QAttnArgs& a0, int qt, int num_sms, cudaStream_t s, bool pdl, const CUtensorMap* kmap,
                          const CUtensorMap* vmap) {
   QAttnArgs a = a0;
@@ -388,6 +405,7 @@ cudaError_t launch_qattn(const QAttnArgs& a0, int qt, int num_sms, cudaStream_t 
     const bool wide = p.nc > 4;
     auto fn = a.c.hd == 64 ? (qt ? qattn_tc64_bf16 : wide ? qattn_tc64_f32_wide : qattn_tc64_f32)
                            : (qt ? qattn_tc128_bf16 : wide ? qattn_tc128_f32_wide : qattn_tc128_f32);
+    if (a.ngroups > 0) fn = a.c.hd == 64 ? (qt ? qattn_by64_bf16 : qattn_by64_f32) : (qt ? qattn_by128_bf16 : qattn_by128_f32);
     return fn(*kmap, *vmap, a, p.nc, p.grid, s, pdl);
   }
   switch (a.c.hd) {
@@ -399,13 +417,19 @@ cudaError_t launch_qattn(const QAttnArgs& a0, int qt, int num_sms, cudaStream_t 
 }
 
 uint64_t qattn_shared_workspace(const QCacheView& c, int g, int B, int S, int num_sms) {
-  if (qattn_uses_tc(c.hd)) return qshare_workspace(c, g, B, S, num_sms);
+  if (qattn_uses_tc(c.hd)) return std::max(qattn_workspace(c, g, B, S, num_sms), qshare_workspace(c, g, B, S, num_sms));
   const int splits = simple_splits(c, (int64_t)B * S, c.rows * c.cap, num_sms);
   return splits == 1 ? 0 : kQattnTickets + (uint64_t)B * S * c.kv * g * splits * (c.hd + 2) * 4;
 }
 
 cudaError_t launch_qattn_shared(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s) {
-  if (qattn_uses_tc(a.c.hd)) return launch_qshare_all(a, qt, num_sms, s);
+  if (qattn_uses_tc(a.c.hd)) {
+    if (!q_by_rows(a, qt, num_sms)) return launch_qshare_all(a, qt, num_sms, s);
+    // (the workspace may hold anything; 1 us)
+    q_clear_tickets_kernel<<<1, 256, 0, s>>>(reinterpret_cast<uint4*>(a.ws));
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_qattn(a, qt, num_sms, s, true, nullptr, nullptr);
+  }
   switch (a.c.hd) {
     case 16: return qt ? launch_simple<16, 1, true>(a, num_sms, s, false) : launch_simple<16, 0, true>(a, num_sms, s, false);
     case 32: return qt ? launch_simple<32, 1, true>(a, num_sms, s, false) : launch_simple<32, 0, true>(a, num_sms, s, false);

@@ -1,0 +1,15 @@
+// Attention of rows that share positions, each row by itself (qshare.cu): head size 128, f32 queries.
+#include "qattn_tc.cuh"
+
+namespace llm {
+
+LLM_QATTN_TC(qattn_by128_f32) {
+  if (nc == 1) return launch_qattn_tc<128, 4, 1, 0, 2>(kmap, vmap, a, grid, s, pdl);
+  if (nc == 2) return launch_qattn_tc<128, 4, 2, 0, 2>(kmap, vmap, a, grid, s, pdl);
+  if (nc == 4) return launch_qattn_tc<128, 4, 4, 0, 2>(kmap, vmap, a, grid, s, pdl);
+  if (nc == 6) return launch_qattn_tc<128, 4, 6, 0, 2>(kmap, vmap, a, grid, s, pdl);
+  if (nc == 8) return launch_qattn_tc<128, 4, 8, 0, 2>(kmap, vmap, a, grid, s, pdl);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace llm

@@ -4,10 +4,10 @@
 namespace llm {
 
 LLM_QATTN_TC(qattn_sh128_f32) {
-  if (nc == 1) return launch_qattn_tc<128, 4, 1, 0, true>(kmap, vmap, a, grid, s, pdl);
-  if (nc == 2) return launch_qattn_tc<128, 4, 2, 0, true>(kmap, vmap, a, grid, s, pdl);
-  if (nc == 4) return launch_qattn_tc<128, 4, 4, 0, true>(kmap, vmap, a, grid, s, pdl);
-  if (nc == 8) return launch_qattn_tc<128, 4, 8, 0, true>(kmap, vmap, a, grid, s, pdl);
+  if (nc == 1) return launch_qattn_tc<128, 4, 1, 0, 1>(kmap, vmap, a, grid, s, pdl);
+  if (nc == 2) return launch_qattn_tc<128, 4, 2, 0, 1>(kmap, vmap, a, grid, s, pdl);
+  if (nc == 4) return launch_qattn_tc<128, 4, 4, 0, 1>(kmap, vmap, a, grid, s, pdl);
+  if (nc == 8) return launch_qattn_tc<128, 4, 8, 0, 1>(kmap, vmap, a, grid, s, pdl);
   return cudaErrorInvalidValue;
 }
 

@@ -4,9 +4,9 @@
 namespace llm {
 
 LLM_QATTN_TC(qattn_sh64_bf16) {
-  if (nc == 1) return launch_qattn_tc<64, 2, 1, 1, true>(kmap, vmap, a, grid, s, pdl);
-  if (nc == 2) return launch_qattn_tc<64, 2, 2, 1, true>(kmap, vmap, a, grid, s, pdl);
-  if (nc == 4) return launch_qattn_tc<64, 2, 4, 1, true>(kmap, vmap, a, grid, s, pdl);
+  if (nc == 1) return launch_qattn_tc<64, 2, 1, 1, 1>(kmap, vmap, a, grid, s, pdl);
+  if (nc == 2) return launch_qattn_tc<64, 2, 2, 1, 1>(kmap, vmap, a, grid, s, pdl);
+  if (nc == 4) return launch_qattn_tc<64, 2, 4, 1, 1>(kmap, vmap, a, grid, s, pdl);
   return cudaErrorInvalidValue;
 }
 

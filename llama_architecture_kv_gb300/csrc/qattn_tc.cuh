@@ -114,7 +114,22 @@ struct QaUnit {
   int64_t qrow;
   int start, end0, last;  // last: positions the last token sees end here
   int tile0, nt;  // its position tiles
+  // rows by themselves (SH 2): the first np of the tiles hold positions below `shared` at the places of row `lead`, the
+  // others the row's own from tile0 on
+  int lead, shared, np;
 };
+// where a tile's positions lie: those from lo to hi of the 128 from p0 on, at the places of row b
+struct QaTileAt {
+  int p0, lo, hi, b;
+};
+template <int SH>
+LLM_D QaTileAt qa_tile(const QaUnit& u, int k) {
+  if constexpr (SH == 2) {
+    if (k < u.np) return QaTileAt{k * kQaTile, 0, u.shared, u.lead};
+    return QaTileAt{(u.tile0 + k - u.np) * kQaTile, u.shared, u.last, u.b};
+  }
+  return QaTileAt{(u.tile0 + k) * kQaTile, u.start, u.last, u.b};
+}
 
 LLM_D QaUnit qa_unit(const QAttnArgs& a, int t) {
   QaUnit u;
@@ -151,13 +166,23 @@ LLM_D QaUnit qa_unit(const QAttnArgs& a, int t) {
 }
 
 // ---- rows that share positions (qshare.cuh) ----
+// What a unit is follows from its row's group, length and count: this thread's part of them is read at once, before the
+// first of the reads that depend on one another
+LLM_D int sh_touch(const QAttnArgs& a) {
+  int x = 0;
+  for (int i = threadIdx.x; i < a.ngroups; i += blockDim.x) x ^= a.shared[i];
+  for (int i = threadIdx.x; i < a.r.B; i += blockDim.x) x ^= a.r.first[i] ^ q_count(a.r, i);
+  return x;
+}
 // whether the groups' bounds ascend from 0 to B (else no row shares anything); every thread of the CTA calls it
 LLM_D bool sh_fine(const QAttnArgs& a) {
   bool fine = true;
+  const int touched = sh_touch(a);
   for (int i = threadIdx.x; i < a.ngroups; i += blockDim.x) {
     const int lo = a.groups[i], hi = a.groups[i + 1];
     fine &= lo <= hi && (i > 0 || lo == 0) && (i + 1 < a.ngroups || hi == a.r.B);
   }
+  asm volatile("" ::"r"(touched));
   fine = __syncthreads_and(fine);
   if (!fine && threadIdx.x == 0) q_report(a.r.status, kErrArg);
   return fine;
@@ -259,6 +284,19 @@ struct ShCut {
   LLM_D int first(int y) const { return owner(y + kShCost); }
   LLM_D int last(int y, int nt) const { return owner(y + kShCost + max(0, nt - kShNear - 1)); }
 };
+
+// A row by itself: a tile of its tokens as in a call without groups, its positions in two runs of tiles
+LLM_D QaUnit sh_row(const QAttnArgs& a, int t, bool sharing) {
+  QaUnit u = qa_unit(a, t);
+  int end;
+  u.lead = u.b;
+  u.shared = u.nt > 0 && sharing ? min(sh_group(a, u.b, u.lead, end), u.last) : 0;
+  if (u.lead == u.b) u.shared = 0;
+  u.np = (u.shared + kQaTile - 1) / kQaTile;
+  u.tile0 = u.shared / kQaTile;
+  if (u.nt > 0) u.nt = u.np + (u.last > u.shared ? (u.last + kQaTile - 1) / kQaTile - u.tile0 : 0);
+  return u;
+}
 
 // where a column's sums go, and its statistics (part 0, 1: a unit's first run, of a prefix or a row's own; 2: a later one)
 LLM_D float* sh_put(const QAttnArgs& a, int part, int half, int64_t col, int place, float m, float l, int cta, int cta0, int ctas) {
@@ -424,9 +462,9 @@ LLM_D void qa_widen_row(unsigned char* stage, int r, int sub, bool live) {
   }
 }
 
-// the walk of one CTA's run over (token tile, kv head, position tiles); SH: over the units of a call whose rows share
-// positions
-template <bool SH>
+// The walk of one CTA's run over (token tile, kv head, position tiles).  SH, of a call whose rows share positions: 1: over
+// the units of its groups, whose sums another kernel joins; 2: over its rows, each by itself
+template <int SH>
 struct QaWalk {
   QaUnit u;
   int t, j, k0, k1;
@@ -434,11 +472,12 @@ struct QaWalk {
   bool sharing;
   int offw;          // SH: the same with what units cost (ShCut)
   LLM_D QaUnit unit(const QAttnArgs& a, int i) const {
-    if constexpr (SH) return sh_unit<kQaTile>(a, i, sharing);
+    if constexpr (SH == 1) return sh_unit<kQaTile>(a, i, sharing);
+    else if constexpr (SH == 2) return sh_row(a, i, sharing);
     else return qa_unit(a, i);
   }
   LLM_D void skip(const QAttnArgs& a) {
-    if constexpr (SH) {
+    if constexpr (SH == 1) {
       const int n = 2 * a.r.B * a.sh.cpr;
       do {
         t = sh_next(a, t, sharing);
@@ -449,7 +488,7 @@ struct QaWalk {
         u = unit(a, t);
       } while (u.nt == 0);
     } else {
-      do u = qa_unit(a, ++t);
+      do u = unit(a, ++t);
       while (u.nt == 0);
     }
   }
@@ -459,9 +498,9 @@ struct QaWalk {
     u = unit(a, t);
     if (st - off == a.c.kv * u.nt) {  // (a cut moved to the end of its token tile)
       off = st;
-      if constexpr (SH) offw += a.c.kv * (u.nt + kShCost);
+      if constexpr (SH == 1) offw += a.c.kv * (u.nt + kShCost);
       skip(a);
-      if (SH && st >= end) return;
+      if (SH == 1 && st >= end) return;
     }
     j = (int)((uint32_t)(st - off) / (uint32_t)u.nt);
     k0 = st - off - j * u.nt;
@@ -477,15 +516,15 @@ struct QaWalk {
     if (++j == a.c.kv) {
       j = 0;
       off += a.c.kv * u.nt;
-      if constexpr (SH) offw += a.c.kv * (u.nt + kShCost);
+      if constexpr (SH == 1) offw += a.c.kv * (u.nt + kShCost);
       skip(a);
-      if (SH && st >= end) return;
+      if (SH == 1 && st >= end) return;
     }
     cut();
   }
 };
 
-template <int HD, int NP, int NC, int QT, bool SH>
+template <int HD, int NP, int NC, int QT, int SH>
 __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::CTAS)
     qattn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const QAttnArgs a) {
   using X = QaShape<HD, NP, NC>;
@@ -544,15 +583,19 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   // previous kernel, below)
   // this CTA's run: the token tiles' position tiles are counted lane by lane (contiguous stretches),
   // and the lane whose stretch holds the run's start finds its token tile
-  const int nq = SH ? 2 * a.r.B * a.sh.cpr : a.r.step ? (a.tiles ? a.tiles[1] : a.r.B) : a.r.B * a.nct;
+  const int nq = SH == 1 ? 2 * a.r.B * a.sh.cpr : a.r.step ? (a.tiles ? a.tiles[1] : a.r.B) : a.r.B * a.nct;
   bool sharing = false;
   int2* before = reinterpret_cast<int2*>(base);  // SH: [nq] tiles of the units before, and how many have any (the ring is idle yet)
-  __shared__ int2 s_sum[SH ? X::NT / 32 : 1];
+  __shared__ int2 s_sum[SH == 1 ? X::NT / 32 : 1];
   __shared__ int s_offw;
-  static_assert(!SH || ST * X::STAGE >= kShUnits * 8, "the counts of a call's units");
-  if constexpr (SH) {
+  static_assert(SH != 1 || ST * X::STAGE >= kShUnits * 8, "the counts of a call's units");
+  if constexpr (SH) sharing = sh_fine(a);
+  auto row_unit = [&](int t) {
+    if constexpr (SH == 2) return sh_row(a, t, sharing);
+    else return qa_unit(a, t);
+  };
+  if constexpr (SH == 1) {
     // (counted by all threads: a unit's count is a chain of reads)
-    sharing = sh_fine(a);
     const int per = (nq + X::NT - 1) / X::NT, u0 = min(nq, tid * per), u1 = min(nq, u0 + per);
     int2 sum = make_int2(0, 0);  // tiles, and units that have some
     for (int t = u0; t < u1; ++t) {
@@ -623,7 +666,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
     const int per = (int)pu, t0 = (int)tu, t1 = (int)min(nu, tu + pu);
     int sum = 0;
 #pragma unroll 1
-    for (int t = t0; t < t1; ++t) sum += qa_unit(a, t).nt;
+    for (int t = t0; t < t1; ++t) sum += row_unit(t).nt;
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -646,7 +689,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         int off = lo, t = t0, nt = sum;  // (one token tile per lane: it is the one)
 #pragma unroll 1
         for (; per > 1; ++t) {
-          nt = qa_unit(a, t).nt;
+          nt = row_unit(t).nt;
           if (x < off + nt * a.c.kv) break;
           off += nt * a.c.kv;
         }
@@ -670,7 +713,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
   const uint32_t tmem = s_tmem;
   QaWalk<SH> w;
   w.sharing = sharing;
-  w.offw = SH ? s_offw : 0;
+  w.offw = SH == 1 ? s_offw : 0;
   w.begin(a, s_t, s_off, s_begin, s_end);
   grid_dep_wait();
   bool ok = true;  // a wait that gave up: no further waits, but every loop and barrier is still walked
@@ -697,9 +740,10 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
           if (a.new_k && k == w.u.nt - 1) qa_store_new<HD>(a, w.u.b, w.j);
         }
         // the place of this lane's block, and with it of its half of the tile (pages hold 64 positions)
-        const int p0 = (w.u.tile0 + k) * kQaTile, pos = p0 + kQBlock * blk;
+        const QaTileAt at = qa_tile<SH>(w.u, k);
+        const int pos = at.p0 + kQBlock * blk;
         int row = 0, pp = 0;
-        const bool seen = pos < w.u.last && (!SH || pos + kQBlock > w.u.start) && qa_place(a, w.u.b, pos, row, pp);
+        const bool seen = pos < at.hi && (!SH || pos + kQBlock > at.lo) && qa_place(a, at.b, pos, row, pp);
         int y = a.krow0 + (row * a.c.kv + w.j) * a.c.cap + pp;
         uint32_t have = __ballot_sync(0xffffffffu, seen);
         int l0 = 0, l1 = 4;
@@ -822,7 +866,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
     };
     // tokens that see nothing and share a tile with none that does: zeros
 #pragma unroll 1
-    for (uint32_t t = SH ? (uint32_t)nq : (uint32_t)cta; t < (uint32_t)nq; t += gridDim.x) {
+    for (uint32_t t = SH == 1 ? (uint32_t)nq : (uint32_t)cta; t < (uint32_t)nq; t += gridDim.x) {
       const QaUnit u = qa_unit(a, (int)t);
       if (u.nt == 0 && u.ntok > 0)
 #pragma unroll 1
@@ -894,7 +938,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         if (lane == 0) {
           // a query that is not finite makes its scores NaN
           qsc[c] = c < used ? (fine ? s * (a.scale * 1.4426950408889634f) : __uint_as_float(0x7fc00000u)) : 0.f;
-          if constexpr (SH) {
+          if constexpr (SH == 1) {
             const int gt = (int)w.u.qrow + tok, b = gt / a.r.S;
             cend[c] = c < used ? min(w.u.last, sh_end(a, b, gt - b * a.r.S)) : 0;
           } else {
@@ -911,7 +955,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
       const float* qsg = qsc + c0;
       const int* ceg = cend + c0;
       int all_end = 0x7fffffff;             // the least that a column sees
-      if constexpr (SH) {
+      if constexpr (SH == 1) {
 #pragma unroll
         for (int c = 0; c < CT; ++c)
           if (c0 + c < used) all_end = min(all_end, ceg[c]);
@@ -925,11 +969,12 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
       bool pend = false;                    // a product over the values not waited for yet
 #pragma unroll 1
       for (int t = gp; t < n; t += 2) {
-        const int p0 = (w.u.tile0 + w.k0 + t) * kQaTile, pos = p0 + quad * 32 + lane;
+        const QaTileAt at = qa_tile<SH>(w.u, w.k0 + t);
+        const int p0 = at.p0, pos = p0 + quad * 32 + lane;
         wait(b_full + 8u * slot, fpar);
         const float ks = ssc[slot * 16 + quad * 2 + (lane >> 4)], vs = ssc[slot * 16 + 8 + quad * 2 + (lane >> 4)];
-        const bool good = !(ks < 0.f) && pos < w.u.last && pos >= w.u.start;
-        const bool whole = __all_sync(0xffffffffu, good) && p0 + kQaTile <= (SH ? all_end : w.u.end0);
+        const bool good = !(ks < 0.f) && pos < at.hi && pos >= at.lo;
+        const bool whole = __all_sync(0xffffffffu, good) && p0 + kQaTile <= (SH == 1 ? all_end : w.u.end0);
         const int mypos = good ? pos : 0x7fffffff;
         const int wr = quad * 32 + (HV == 1 ? lane : half * 16 + (lane & 15));
         const bool wlive = HV == 1 ? good : __ballot_sync(0xffffffffu, good) >> (wr & 31) & 1u;
@@ -1120,7 +1165,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         if (gtid == 0) gvs[group] = vref;
       }
       all_sync();  // (every product is done: the weights' buffers are free)
-      const bool both = n > 1, alone = !SH && w.k0 == 0 && w.k1 == w.u.nt;  // alone: this CTA holds the whole unit
+      const bool both = n > 1, alone = SH != 1 && w.k0 == 0 && w.k1 == w.u.nt;  // alone: this CTA holds the whole unit
       // parts of units cut across CTAs: [CTA][the unit's first part?]{[C][HD] sums, [C] (reference, weight)}
       float* parts = reinterpret_cast<float*>(a.ws + kQattnTickets);
       float* mine = parts + ((size_t)cta * 2 + (w.k0 == 0 ? 1 : 0)) * C * (HD + 2);
@@ -1136,7 +1181,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         ffac[c] = f0 * gvs[2 * hv] * r;
         ffac[C + c] = f1 * (both ? gvs[2 * hv + 1] : 0.f) * r;
         const int tok = c / a.g;
-        if constexpr (SH) {
+        if constexpr (SH == 1) {
           ShCut cut;
           cut.make(s_total, min((int)gridDim.x, s_total));
           const int y = w.offw + w.j * (w.u.nt + kShCost), first = cut.first(y), ctas = cut.last(y, w.u.nt) - first;
@@ -1171,7 +1216,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
                   const int64_t at = obase + coff[c] + d_row;
                   if constexpr (QT) static_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v);
                   else static_cast<float*>(a.out)[at] = v;
-                } else if (SH && pass == 0) {
+                } else if (SH == 1 && pass == 0) {
                   a.sh.parts[coff[c] + d_row] = v;
                 } else {
                   (pass ? other : mine)[c * HD + d_row] = v;
@@ -1182,7 +1227,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
         }
         if (pass == 1 && both) all_sync();
       }
-      if (!SH && !alone) {
+      if (SH != 1 && !alone) {
         if (stid == 0) {
           QaCut cut;
           cut.make(s_total, min((int)gridDim.x, s_total));
@@ -1288,7 +1333,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
 }
 
 // one instantiation per translation unit (they take half a minute each to compile)
-template <int HD, int NP, int NC, int QT, bool SH = false>
+template <int HD, int NP, int NC, int QT, int SH = 0>
 cudaError_t launch_qattn_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const QAttnArgs& a, int grid,
                             cudaStream_t s, bool pdl) {
   constexpr size_t smem = QaShape<HD, NP, NC>::SMEM;
@@ -1318,10 +1363,14 @@ LLM_QATTN_TC(qattn_tc64_bf16);
 LLM_QATTN_TC(qattn_tc128_f32);
 LLM_QATTN_TC(qattn_tc128_f32_wide);
 LLM_QATTN_TC(qattn_tc128_bf16);
-// of rows that share positions
+// of rows that share positions: units of groups, and rows by themselves
 LLM_QATTN_TC(qattn_sh64_f32);
 LLM_QATTN_TC(qattn_sh64_bf16);
 LLM_QATTN_TC(qattn_sh128_f32);
 LLM_QATTN_TC(qattn_sh128_bf16);
+LLM_QATTN_TC(qattn_by64_f32);
+LLM_QATTN_TC(qattn_by64_bf16);
+LLM_QATTN_TC(qattn_by128_f32);
+LLM_QATTN_TC(qattn_by128_bf16);
 
 }  // namespace llm
