@@ -1,4 +1,5 @@
-// Attention of rows that share positions: which kernel takes which part of a call, and the join of what they sum.
+// Attention of rows that share positions, read once for all that share them: which kernel takes which part of a call, and the join
+// of what they sum.  (Calls that gain nothing from it are attended row by row, qattn.cu.)
 //
 // Both kernels sum over a share of the units' position tiles per CTA and leave their sums in the workspace.  Units of
 // few columns -- a row's own positions, or a prefix that few rows share -- run on the kernel of the ordinary attention
@@ -16,7 +17,8 @@ namespace {
 constexpr int kMergeThreads = 256;
 
 // Warp = column: its parts' statistics a lane each, then their sums, eight loads in flight (heads of 64: two parts at a
-// time, half a warp each).  Bound by the reads of the sums, which lie in L2.
+// time, half a warp each).  Bound by the reads of the sums, which lie in L2 (1024 columns of 5 to 9 parts: 8 us with eight loads in
+// flight; 32 rows of 32 heads behind 8192 positions).
 template <int HD, int QT>
 __global__ void __launch_bounds__(kMergeThreads) qshare_merge_kernel(const QAttnArgs a, const ShSide prefix, const ShSide own) {
   const int BS = a.r.B * a.r.S, cols = BS * a.c.kv * a.g, lane = threadIdx.x & 31;
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(kMergeThreads) qshare_merge_kernel(const QAttn
 }
 
 // Queries in e4m3 pieces (qshare.cuh), warp = column; of tokens that are not there: zeros.  As a kernel of its own
-// (2 us) they are made once; four warps of each CTA of the attention took 13 us for 128 columns.
+// (3 us) they are made once; four warps of each CTA of the attention took 13 us for 128 columns.
 template <int HD, int QT>
 __global__ void __launch_bounds__(kMergeThreads) qshare_pieces_kernel(const QAttnArgs a) {
   constexpr int NP = QT ? 2 : 4, E = HD / 32;
@@ -166,8 +168,11 @@ __global__ void __launch_bounds__(kMergeThreads) qshare_pieces_kernel(const QAtt
   if (lane == 0) a.sh.qs[col] = fine ? s * (fabsf(a.scale) * 1.4426950408889634f) : __uint_as_float(0x7fc00000u);
 }
 
-// Which kernel takes the prefixes: that of many columns where a group has more than kShFew on average
-constexpr int kShFew = 40;
+// Which kernel takes the prefixes: that of many columns where a group has more than this on average.  Its tile costs the
+// same for any number of columns, twice as much with f32 queries as with bf16; the other's grows with every 32 (8 kv heads
+// of 128, 4 groups behind 16000 positions, microseconds with the kernel for many and the one for few: bf16 24 columns 88 and 71, 32 92
+// and 98, 40 98 and 108, 64 102 and 153; f32 32 columns 190 and 104, 64 201 and 161, 128 (2 groups) 153 and 147)
+constexpr int kShFew[2] = {100, 40};  // f32, bf16
 struct ShPlan {
   bool many;
   int nc, cols;        // the other kernel's accumulator columns in 16s, and columns of a unit
@@ -176,7 +181,7 @@ struct ShPlan {
 ShPlan plan_of(const QCacheView& c, int g, int qt, int64_t B, int64_t S, int64_t ngroups) {
   ShPlan p;
   const int64_t group = (B * S * g + ngroups - 1) / ngroups;
-  p.many = group > kShFew;
+  p.many = group > kShFew[qt];
   const int np = qt ? 2 : 4, most = qt ? 4 : 8;
   const int64_t want = std::min<int64_t>(32, std::max(S * g, p.many ? 0 : group));
   p.nc = 1;
@@ -228,7 +233,9 @@ cudaError_t launch(void* fn, int64_t grid, void** args, cudaStream_t s, bool pdl
 }  // namespace
 
 // The kernels of a call follow one another programmatically: each but the first may start before the one before
-// is done, waits for it before it reads what that wrote, and is done only after it.
+// is done, waits for it before it reads what that wrote, and is done only after it.  (Side by side, each on SMs of its own in
+// proportion to its work, they took 45 us in place of 54 behind 8192 positions, but 302 in place of 274 behind 131072: CTAs of one
+// next to SMs that run the other are up to 15% slower, and the slowest decides.)
 cudaError_t launch_qshare_all(const QAttnArgs& a0, int qt, int num_sms, cudaStream_t s) {
   QAttnArgs a = a0;
   const int64_t B = a.r.B, S = a.r.S;

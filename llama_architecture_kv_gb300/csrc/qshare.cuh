@@ -1,32 +1,37 @@
-// Attention of rows that share positions over an 8-bit cache, on the 5th-generation tensor cores (head sizes 64
-// and 128): the kernel template (an instantiation each in qshare<head size>_<type>.cu).
+// Attention over positions that many columns share, in an 8-bit cache, on the 5th-generation tensor cores (head sizes
+// 64 and 128): the kernel template (an instantiation each in qshare<head size>_<type>.cu).
 //
-// The (token, query head) pairs that read a key/value head at the same places are columns of one product, up
-// to 128 of them: all tokens of a group's rows for the positions that the group shares (a prefix unit), the tokens of one
-// row for its own (a suffix unit).  Queries are on the M side, positions on the N side, so that a thread has a
-// column's scores to itself:
+// The (token, query head) pairs of a group's rows that read a key/value head at the same places are columns of one
+// product, up to 128 of them.  Queries are on the M side, positions on the N side, so that a thread has a column's scores
+// to itself:
 //   S [128 columns][TN positions] = Q K^T     A = query pieces (shared memory), B = keys' codes as they lie
-//   softmax                                   thread = column: maximum, weights, their sum
-//   O [128][HD]                   = P V       A = weight pieces (tensor memory), B = widened values
-// A tile's weights are relative to its own largest score (rounded up to a power of two, so that what follows is
-// exact); O of a tile is read from tensor memory as soon as it is there and added to the sums, which
-// stay in registers, by their common reference.  So tiles do not depend on one another, nothing is rescaled
-// in tensor memory, and sums are rounded to nearest from tile to tile.
+//   softmax                                   thread = column: weights against a reference, their sum
+//   O [128][HD]                  += P V       A = weight pieces (tensor memory), B = widened values
+// The reference is a power of two that follows the column's largest score lazily: it moves when a weight would
+// exceed 2^24, which after a run's first tile is rare, and what was added up so far is then rescaled in tensor memory
+// (exactly).  So weights go from 2^24 down to 2^-126 of it with all their digits, no maximum is waited for, and a tile's
+// products go on top of those before.  The blocks' value scales ride on the weights, relative to a power of two that moves in the
+// same way.  O is read after RUN of a group's tiles (kQaRun says what longer runs lose) into sums in local memory.
 //
 // Pieces.  A query is scaled by a power of two to at most 256 and enters as e4m3 pieces, each the
-// rounding of what the ones before left over: two (bf16: its eight bits, of elements down to 2^-9 of the largest), summed
-// in one accumulator; or four (f32), the last two 2^10 times larger in an accumulator of their own, which leaves 2^-17 of an
-// element and at most 2^-19 of the largest.  The softmax weights are bf16 pieces, two (bf16 queries: 2^-17
-// of a weight, half of 2^-9 being the output's own rounding) or three (f32: 2^-26), over values widened to bf16, exactly;
-// bf16 has f32's exponents, so that a weight keeps its digits however small it is.  The blocks' value scales ride on
-// the weights relative to the tile's largest.
+// rounding of what the ones before left over (made once for the call, qshare.cu): two (bf16: its eight bits, of elements down
+// to 2^-9 of the largest), summed in one accumulator; or four (f32), the last two 2^10 times larger in an accumulator of their
+// own, which leaves 2^-17 of an element and at most 2^-19 of the largest.  The softmax weights are bf16 pieces, two (bf16 queries:
+// 2^-17 of a weight, half of 2^-9 being the output's own rounding) or three (f32: 2^-26), over values widened to bf16,
+// exactly; bf16 has f32's exponents, so that a weight keeps its digits however small it is.
 //
-// One CTA per SM: warp 0 walks the CTA's share of the work (segments: runs of tiles of one unit) ahead of all others,
-// loads the tiles by TMA, and tells the others each segment; warp 1 issues the products; two groups of four softmax
-// warps take the tiles in turn; eight helper warps split the queries into pieces, widen the values and add up O.  Three score
-// buffers in tensor memory, each reused for its tile's weights.  The units' tiles are shared out in equal runs; a
-// unit's sums over a CTA's run go to global memory, and a second kernel joins each column's: its prefix's and its own, in
-// CTA order, so the result does not depend on timing.
+// One CTA per SM, 16 warps: warp 0 loads the tiles and queries by TMA; warp 1 issues the products; warp 2 walks the CTA's share of
+// the work (segments: runs of tiles of one unit) ahead of the others and tells them each segment; four warps widen values; two
+// groups of four softmax warps take the tiles in turn, each with scores, sums and references of its own in tensor memory, so that one
+// group's products run while the other weighs.  The units' tiles are shared out in equal runs; a unit's sums over a CTA's
+// run go to global memory, a part for each group, and another kernel joins each column's parts in CTA order, so the result does
+// not depend on timing.
+//
+// What bounds it (131072 positions, 64 rows of 32 heads of 128 behind them, bf16: 235 us of a call's 274, where the products alone would
+// take 71): a tile of 128 x 128 takes 4070 clocks, its softmax 4840 in either group, of which the 32-score steps
+// take 1000 each: two pieces of a weight are some 14 instructions a score, of which a scheduler issues 0.7 per clock with its two
+// softmax warps.  f32 queries: 3700 clocks a tile of 64 positions.  The value product in halves, and more registers for the softmax
+// warps (setmaxnreg), were slower.
 #pragma once
 #include <type_traits>
 
@@ -207,9 +212,6 @@ __global__ void __launch_bounds__(kShThreads, 1)
     if (lane == 0) mbar_arrive(b_ge + 8u * gslot);
     if (++gslot == kShSegs) gslot = 0u, gpar ^= 1u;
   };
-
-
-
 
   if (warp == 2) {
     // ---- the walk: what each segment is, and where its columns' positions end ----
@@ -750,7 +752,6 @@ __global__ void __launch_bounds__(kShThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
-
 }
 
 // one instantiation per translation unit

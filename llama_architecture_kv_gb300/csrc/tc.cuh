@@ -259,8 +259,4 @@ LLM_D uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// ---- registers from one warpgroup to another (all four warps; the shares must fit the launch's total) -----
-template <int N> LLM_D void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> LLM_D void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
 }  // namespace llm
