@@ -39,7 +39,6 @@ constexpr int kSrBits = 11;
 constexpr int kSrMost = 1024;                 // candidates of a bin that are put in order
 constexpr int kSrList = 2 * kSrMost;          // and of the bins of all places
 constexpr uint32_t kSrNear = 1u << 12;        // what a distance found by logf may be off, and the weights' rounding
-constexpr uint32_t kSrFar = 30u << 27;        // the largest distance
 constexpr uint32_t kSrNothing = 2977044472u;  // exp(-d / 2^27) < 2^-32 from here on: the weight is 0
 constexpr uint32_t kSrNone = 0xffffffffu;     // no candidate: it weighs nothing
 
@@ -118,12 +117,13 @@ struct alignas(16) SrShared {
   uint64_t weight[kSrBins];         // the row's: sums of weights of the bins before
   uint32_t count[kSrBins];          // counts of the bins before
   uint32_t listed[4];
-  uint64_t top[kSrCluster];         // the CTAs' largest logits, as key and -id
-  uint32_t low[kSrCluster];         // and the keys of their smallest
+  uint32_t top[kSrCluster];         // the keys of the CTAs' largest logits
+  uint32_t low[kSrCluster];         // and of their smallest
   uint64_t above[kSrCluster];       // sums of weights that min-p keeps
   uint32_t same[kSrCluster];        // candidates at one distance
   uint64_t sum[32];                 // by warp
   uint32_t num[32];
+  uint32_t low_of[32];
   uint64_t all_weight[2];
   uint32_t all_count[2];
   uint64_t upto[3];
@@ -200,39 +200,40 @@ struct SrRow {
   LLM_D uint4 d(int j) const { return kept ? kept[j] : far(logits(j)); }
   LLM_D int id(int j) const { return id0 + 4 * j - pad; }
   LLM_D uint32_t dist(float x) const {
-    // (NaN, and what is infinitely far: nothing; all of +inf at the top are at it)
-    if (!(x > -INFINITY)) return kSrNone;
-    const float a = x == top ? 0.0f : __fmul_rn(__fsub_rn(top, x), scale);
-    const uint32_t d = a < 30.0f ? (uint32_t)(a * 134217728.0f) : kSrFar;
-    return d >= kSrNothing ? kSrNone : d;
+    // (all of +inf at the top are at it; NaN, and what weighs nothing: none.  kSrNothing's f32 is the least at or above it)
+    const float f = __fmul_rn(__fmul_rn(x == top ? 0.0f : __fsub_rn(top, x), scale), 134217728.0f);
+    return f < (float)kSrNothing ? (uint32_t)f : kSrNone;
   }
 };
 
-// counts and weights of the candidates with d >> (shift + bits) == bin, by the `bits` bits below; the sums of the
-// bins before each, for the whole row, in every CTA.  FIRST: of all candidates, whose distances stay in r.kept
-template <int NT, bool FIRST>
-LLM_D void sr_histogram(SrShared& s, const SrRow& r, int shift, int bits, uint32_t bin) {
+// Counts and weights of the candidates with d >> (shift + bits) == bin, by the `bits` bits below; the sums of the
+// bins before each, for the whole row, in every CTA.  FIRST: of all candidates; `fresh`: r.kept holds logits yet, and
+// distances from then on.  WEIGHTS false: counts alone
+template <int NT, bool FIRST, bool WEIGHTS>
+LLM_D void sr_histogram(SrShared& s, const SrRow& r, int shift, int bits, uint32_t bin, bool fresh) {
   constexpr int T = kSrBins / NT, R = (T + 1) / 2;
   uint64_t* weight = FIRST ? s.weight : s.split.weight;
   uint32_t* count = FIRST ? s.count : s.split.count;
-  if (!FIRST) {
+  if (!fresh) {
     sr_sync();  // (the cluster's reads of what this overwrites)
     for (int i = threadIdx.x; i < 3 * kSrBins; i += NT) s.hist[0][i] = 0u;
     __syncthreads();
   }
   auto put = [&](uint32_t d) {
     const bool in = FIRST ? d != kSrNone : d != kSrNone && (uint32_t)((uint64_t)d >> (shift + bits)) == bin;
-    const uint32_t w = sr_weight(d), b = FIRST ? d >> shift : d >> shift & ((1u << bits) - 1u);
+    const uint32_t w = WEIGHTS ? sr_weight(d) : 0u, b = FIRST ? d >> shift : d >> shift & ((1u << bits) - 1u);
     if (in) {
       atomicAdd(&s.hist[0][b], 1u);
-      atomicAdd(&s.hist[1][b], w & 0xffffu);
-      atomicAdd(&s.hist[2][b], w >> 16);
+      if (WEIGHTS) {
+        atomicAdd(&s.hist[1][b], w & 0xffffu);
+        atomicAdd(&s.hist[2][b], w >> 16);
+      }
     }
   };
 #pragma unroll 2
   for (int j = threadIdx.x; j < r.quads; j += NT) {
     uint4 d;
-    if (FIRST) {
+    if (FIRST && fresh) {
       d = r.far(r.logits(j));
       if (r.kept) r.kept[j] = d;
     } else {
@@ -261,8 +262,10 @@ LLM_D void sr_histogram(SrShared& s, const SrRow& r, int shift, int bits, uint32
         n[c] = lo[c] = hi[c] = make_uint2(0u, 0u);
         if (c < r.size) {
           n[c] = sr_get64(&s.hist[0][b], c);
-          lo[c] = sr_get64(&s.hist[1][b], c);
-          hi[c] = sr_get64(&s.hist[2][b], c);
+          if (WEIGHTS) {
+            lo[c] = sr_get64(&s.hist[1][b], c);
+            hi[c] = sr_get64(&s.hist[2][b], c);
+          }
         }
       }
 #pragma unroll
@@ -283,8 +286,10 @@ LLM_D void sr_histogram(SrShared& s, const SrRow& r, int shift, int bits, uint32
       for (uint32_t c = 0; c < kSrCluster; ++c)
         if (c < r.size) {
           sr_put(reinterpret_cast<uint64_t*>(&count[b]), c, (uint64_t)jn[y][1] << 32 | jn[y][0]);
-          sr_put(&weight[b], c, jw[y][0]);
-          sr_put(&weight[b + 1], c, jw[y][1]);
+          if (WEIGHTS) {
+            sr_put(&weight[b], c, jw[y][0]);
+            sr_put(&weight[b + 1], c, jw[y][1]);
+          }
         }
     }
   }
@@ -295,7 +300,7 @@ LLM_D void sr_histogram(SrShared& s, const SrRow& r, int shift, int bits, uint32
 #pragma unroll
   for (int y = 0; y < T; ++y) {
     n[y] = count[threadIdx.x * T + y];
-    w[y] = weight[threadIdx.x * T + y];
+    w[y] = WEIGHTS ? weight[threadIdx.x * T + y] : 0ull;
     sn += n[y];
     sw += w[y];
   }
@@ -303,7 +308,7 @@ LLM_D void sr_histogram(SrShared& s, const SrRow& r, int shift, int bits, uint32
 #pragma unroll
   for (int y = 0; y < T; ++y) {
     count[threadIdx.x * T + y] = n0;
-    weight[threadIdx.x * T + y] = w0;
+    if (WEIGHTS) weight[threadIdx.x * T + y] = w0;
     n0 += n[y];
     w0 += w[y];
   }
@@ -387,7 +392,7 @@ LLM_D SrPlace sr_find(SrShared& s, const SrRow& r, int shift, uint64_t t, bool w
     bits = min(shift, kSrBits);
     shift -= bits;
     split = true;
-    sr_histogram<NT, false>(s, r, shift, bits, bin);
+    sr_histogram<NT, false, true>(s, r, shift, bits, bin, false);
   }
   if (split) sr_sync();  // (the split's sums are read by all before the list takes their place)
   if (in_bin > kSrMost) {
@@ -517,14 +522,15 @@ LLM_D int32_t sr_one_by_one(SrShared& s, const SrRow& r, int shift, uint32_t k, 
 }
 
 // The places together.  The histogram bounds the sum that each place keeps, so the bins that the next can be in: one
-// gathering of the candidates of all these bins, and the rest is the first CTA's alone.  False if they are too many.
-template <int NT>
+// gathering of the candidates of all these bins, and the rest is the first CTA's alone.  HEAD, for a small k: all up to
+// the k-th candidate's bin, of which only the counts are known.  False if they are too many.
+template <int NT, bool HEAD>
 LLM_D bool sr_together(SrShared& s, const SrRow& r, int shift, uint32_t k, uint32_t part, uint32_t least, uint32_t u, int32_t& id) {
   constexpr int T = kSrBins / NT;
   const int tid = threadIdx.x;
-  const uint64_t all = s.all_weight[0];
+  const uint64_t all = HEAD ? (uint64_t)0 : s.all_weight[0];
   const uint32_t count = s.all_count[0];
-  auto weight_at = [&](uint32_t b) { return b < kSrBins ? s.weight[b] : all; };
+  auto weight_at = [&](uint32_t b) { return HEAD ? (uint64_t)0 : b < kSrBins ? s.weight[b] : all; };
   auto count_at = [&](uint32_t b) { return b < kSrBins ? s.count[b] : count; };
   uint64_t w[T + 1];
 #pragma unroll
@@ -543,12 +549,14 @@ LLM_D bool sr_together(SrShared& s, const SrRow& r, int shift, uint32_t k, uint3
       if (count_at(tid * T + y) <= k - 1 && k - 1 < count_at(tid * T + y + 1)) s.bin[0] = tid * T + y;
     __syncthreads();
     const uint32_t b = s.bin[0];
-    in[0] = SrBinRange{b, 1u};
+    in[0] = HEAD ? SrBinRange{0u, b + 1u} : SrBinRange{b, 1u};
     lo = weight_at(b);
     hi = weight_at(b + 1);
+  } else if (HEAD) {
+    in[0] = SrBinRange{0u, (uint32_t)kSrBins};
   }
   auto before = [](uint64_t limit) { return limit ? limit - 1 : 0ull; };
-  if (part < 1u << 24) {
+  if (!HEAD && part < 1u << 24) {
     mark(before(sr_share(lo, part)), 1);
     mark(before(sr_share(hi, part)), 2);
     __syncthreads();
@@ -561,14 +569,23 @@ LLM_D bool sr_together(SrShared& s, const SrRow& r, int shift, uint32_t k, uint3
     const uint32_t d = (uint32_t)fmaxf(-logf(((float)least - 0.5f) * 0x1p-31f) * 134217728.0f, 0.0f);
     least_lo = min((d > kSrNear ? d - kSrNear : 0u) >> shift, (uint32_t)kSrBins - 1);
     least_hi = min((d + kSrNear) >> shift, (uint32_t)kSrBins - 1);
-    in[2] = SrBinRange{least_lo, least_hi - least_lo + 1};
-    lo = min(lo, weight_at(least_lo));
-    hi = min(hi, weight_at(least_hi + 1));
+    if (HEAD) {
+      // (all of the bins in which a weight can be on either side of `least`, or none)
+      if (least_lo < in[0].len) in[0].len = max(in[0].len, least_hi + 1);
+      least_lo = 0u;
+      least_hi = kSrBins - 1;
+    } else {
+      in[2] = SrBinRange{least_lo, least_hi - least_lo + 1};
+      lo = min(lo, weight_at(least_lo));
+      hi = min(hi, weight_at(least_hi + 1));
+    }
   }
-  mark(sr_share(lo, u), 3);
-  mark(sr_share(hi, u), 4);
-  __syncthreads();
-  in[3] = SrBinRange{s.bin[3], s.bin[4] - s.bin[3] + 1};
+  if (!HEAD) {
+    mark(sr_share(lo, u), 3);
+    mark(sr_share(hi, u), 4);
+    __syncthreads();
+    in[3] = SrBinRange{s.bin[3], s.bin[4] - s.bin[3] + 1};
+  }
   // in order, those that touch as one
   auto swap = [&](int a, int b) {
     if (in[a].lo > in[b].lo) {
@@ -658,7 +675,7 @@ LLM_D bool sr_together(SrShared& s, const SrRow& r, int shift, uint32_t k, uint3
       }
     run += wt[e];
   }
-  uint64_t kept = all;
+  uint64_t kept = HEAD ? wall : all;
   if (k < count) {
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -724,13 +741,12 @@ __global__ void __launch_bounds__(NT) sample_rows_kernel(const SampleRowsArgs a,
   }
   if (tid < 4) s.listed[tid] = 0u;
   sr_arrive();
-  // ---- the largest logit and its first id; the smallest that is not -inf ----
+  // ---- the largest logit, and the smallest that is not -inf ----
   r.pad = (int)(reinterpret_cast<uintptr_t>(r.v) >> 2 & 3u);
   r.quads = r.n > 0 ? (r.pad + r.n + 3) >> 2 : 0;
   r.kept = nullptr;
   uint4* kept = reinterpret_cast<uint4*>(raw + sizeof(SrShared));
-  uint32_t top_key = 0u, low = 0xffffffffu;
-  int top_id = 0x7fffffff;
+  float most_v = -INFINITY, least_v = INFINITY;
   const float4* v4 = reinterpret_cast<const float4*>(r.v - r.pad);  // (read where all four are the stretch's)
 #pragma unroll 8
   for (int j = tid; j < r.quads; j += NT) {
@@ -738,71 +754,87 @@ __global__ void __launch_bounds__(NT) sample_rows_kernel(const SampleRowsArgs a,
     if (4 * j >= r.pad && 4 * j + 4 <= r.pad + r.n) x = *reinterpret_cast<const uint4*>(v4 + j);
     else x = r.logits(j);
     if (keep) kept[j] = x;
-    auto see = [&](uint32_t bits, int id) {
-      const uint32_t key = sr_key(__uint_as_float(bits));
-      if (key > top_key) {  // (a thread's ids rise)
-        top_key = key;
-        top_id = id;
-      }
-      if (key > 0x007fffffu) low = min(low, key);
+    auto see = [&](uint32_t bits) {  // (maxima and minima leave NaN out)
+      const float v = __uint_as_float(bits);
+      most_v = fmaxf(most_v, v);
+      least_v = fminf(least_v, v == -INFINITY ? INFINITY : v);
     };
-    see(x.x, r.id(j));
-    see(x.y, r.id(j) + 1);
-    see(x.z, r.id(j) + 2);
-    see(x.w, r.id(j) + 3);
+    see(x.x);
+    see(x.y);
+    see(x.z);
+    see(x.w);
   }
   if (keep) r.kept = kept;
-  uint64_t top = (uint64_t)top_key << 32 | (uint32_t)~top_id;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const uint64_t x = __shfl_xor_sync(0xffffffffu, top, o);
-    top = x > top ? x : top;
-  }
-  low = __reduce_min_sync(0xffffffffu, low);
+  // (as keys, which are whole numbers; an empty stretch: those of -inf and +inf)
+  const uint32_t top = __reduce_max_sync(0xffffffffu, sr_key(most_v)), low = __reduce_min_sync(0xffffffffu, sr_key(least_v));
   if (lane == 0) {
-    s.sum[warp] = top;
-    s.num[warp] = low;
+    s.num[warp] = top;
+    s.low_of[warp] = low;
   }
   for (int i = tid; i < 3 * kSrBins / 4; i += NT) reinterpret_cast<uint4*>(s.hist[0])[i] = make_uint4(0u, 0u, 0u, 0u);
   // (every CTA has started and set its lists' lengths before another writes to it)
   __syncthreads();
   sr_wait();
   if (warp == 0) {
-    uint64_t x = lane < NT / 32 ? s.sum[lane] : 0ull;
-    uint32_t y = lane < NT / 32 ? s.num[lane] : 0xffffffffu;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const uint64_t z = __shfl_xor_sync(0xffffffffu, x, o);
-      x = z > x ? z : x;
-    }
-    y = __reduce_min_sync(0xffffffffu, y);
+    const uint32_t x = __reduce_max_sync(0xffffffffu, lane < NT / 32 ? s.num[lane] : 0u);
+    const uint32_t y = __reduce_min_sync(0xffffffffu, lane < NT / 32 ? s.low_of[lane] : 0xffffffffu);
     if (lane < r.size) {
-      sr_put(&s.top[r.rank], lane, x);
+      sr_put32(&s.top[r.rank], lane, x);
       sr_put32(&s.low[r.rank], lane, y);
     }
   }
   sr_sync();
+  uint32_t key = 0u, low_key = 0xffffffffu;
   for (uint32_t i = 0; i < r.size; ++i) {
-    top = s.top[i] > top ? s.top[i] : top;
-    low = min(low, s.low[i]);
+    key = max(key, s.top[i]);
+    low_key = min(low_key, s.low[i]);
   }
-  const uint32_t key = (uint32_t)(top >> 32);
-  const bool none = key <= 0x007fffffu;  // every logit is -inf or NaN
-  if (none || greedy) {
-    if (r.rank == 0 && tid == 0) a.ids[b] = none ? 0 : (int32_t)~(uint32_t)top;
+  if (key <= 0x007fffffu) {  // every logit is -inf or NaN
+    if (r.rank == 0 && tid == 0) a.ids[b] = 0;
     return;
   }
   r.top = sr_unkey(key);
+  if (greedy) {
+    // the first that is as large
+    int first = 0x7fffffff;
+    for (int j = tid; j < r.quads; j += NT) {
+      const uint4 x = r.logits(j);
+      const int id = r.id(j);
+      const int y = __uint_as_float(x.x) == r.top ? 0 : __uint_as_float(x.y) == r.top ? 1 : __uint_as_float(x.z) == r.top ? 2 : __uint_as_float(x.w) == r.top ? 3 : 4;
+      if (y < 4) first = min(first, id + y);
+    }
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) s.num[warp] = (uint32_t)first;
+    __syncthreads();
+    if (warp == 0) {
+      first = (int)__reduce_min_sync(0xffffffffu, lane < NT / 32 ? s.num[lane] : 0x7fffffffu);
+      if (lane == 0) sr_put32(&s.same[r.rank], 0, (uint32_t)first);
+    }
+    sr_sync();
+    if (r.rank == 0 && tid == 0) {
+      for (uint32_t i = 0; i < r.size; ++i) first = min(first, (int)s.same[i]);
+      a.ids[b] = first;
+    }
+    return;
+  }
   r.scale = fminf(__fdiv_rn(1.0f, temp), 3.402823466e38f);
   // ---- the histogram over the range that the distances have ----
-  const float span = __fmul_rn(__fsub_rn(r.top, sr_unkey(low)), r.scale);
+  const float span = __fmul_rn(__fsub_rn(r.top, sr_unkey(low_key)), r.scale);
   const uint32_t most = span < 22.2f ? (uint32_t)(span * 134217728.0f) : 0xb1a00000u;
   const int shift = max(0, 32 - __clz((int)most) - kSrBits);
-  sr_histogram<NT, true>(s, r, shift, kSrBits, 0u);
-  // ---- what is kept, and the draw from it ----
   const uint32_t part = sr_part(p), least = (uint32_t)(min_p * 2147483648.0f);
   int32_t id = 0;
-  if (!sr_together<NT>(s, r, shift, (uint32_t)k, part, least, sr_part(u), id))
+  const bool small = k <= kSrMost;  // (one addition a candidate, and no weight, in place of three)
+  if (small) {
+    sr_histogram<NT, true, false>(s, r, shift, kSrBits, 0u, true);
+    if (sr_together<NT, true>(s, r, shift, (uint32_t)k, part, least, sr_part(u), id)) {
+      if (r.rank == 0 && tid == 0) a.ids[b] = id;
+      return;
+    }
+  }
+  sr_histogram<NT, true, true>(s, r, shift, kSrBits, 0u, !small);
+  // ---- what is kept, and the draw from it ----
+  if (!sr_together<NT, false>(s, r, shift, (uint32_t)k, part, least, sr_part(u), id))
     id = sr_one_by_one<NT>(s, r, shift, (uint32_t)k, part, least, sr_part(u));
   if (r.rank == 0 && tid == 0) a.ids[b] = id;
 }

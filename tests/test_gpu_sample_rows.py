@@ -68,6 +68,17 @@ def test_places_whose_candidates_just_fit_or_just_do_not():
         check(v, [1.0] * 6, [V, n // 2, n + 1, V, 3, V], [0.9, 1.0, 0.5, 1.0, 0.9, 0.3], [0, 0, 0.1, 0.6, 0.6065, 0.60651], rng.random(6))
 
 
+@pytest.mark.parametrize("k", [1, 2, 1000, 1023, 1024, 1025, 2000])
+def test_top_k_about_the_room_for_its_candidates(k):
+    # as many candidates in the k-th one's step as just fit with those before, or do not; with each of the other settings
+    rng = np.random.default_rng(k)
+    V = 6000
+    for n in (1, 900, 1500, 2500):
+        v = np.concatenate([np.linspace(0, -2, k - 1), np.full(n, -2.5), np.linspace(-9, -25, V - n - k + 1)])
+        v = np.stack([rng.permutation(v) for _ in range(6)])
+        check(v, [1.0, 0.7, 1.3, 1.0, 0.0, 1.0], [k] * 6, [1.0, 0.9, 1.0, 0.5, 1.0, 0.999], [0, 0, np.exp(-2.5), 0.3, 0, 0.0820849], rng.random(6))
+
+
 def test_equal_logits_and_logits_within_a_step():
     # every candidate at one distance, more than are put in order at once; and distances of a few units of 2^-27
     V, rng = 20000, np.random.default_rng(1)
