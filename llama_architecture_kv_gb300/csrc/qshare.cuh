@@ -20,17 +20,17 @@
 // 2^-17 of a weight, half of 2^-9 being the output's own rounding) or three (f32: 2^-26), over values widened to bf16,
 // exactly; bf16 has f32's exponents, so that a weight keeps its digits however small it is.
 //
-// One CTA per SM, 16 warps: warp 0 loads the tiles and queries by TMA; warp 1 issues the products; warp 2 walks the CTA's share of
+// One CTA per SM, 16 warps: warp 0 loads the tiles and queries by TMA; warps 1 and 3 issue the products; warp 2 walks the CTA's share of
 // the work (segments: runs of tiles of one unit) ahead of the others and tells them each segment; four warps widen values; two
 // groups of four softmax warps take the tiles in turn, each with scores, sums and references of its own in tensor memory, so that one
 // group's products run while the other weighs.  The units' tiles are shared out in equal runs; a unit's sums over a CTA's
 // run go to global memory, a part for each group, and another kernel joins each column's parts in CTA order, so the result does
 // not depend on timing.
 //
-// What bounds it (131072 positions, 64 rows of 32 heads of 128 behind them, bf16: 235 us of a call's 274, where the products alone would
-// take 71): a tile of 128 x 128 takes 4070 clocks, its softmax 4840 in either group, of which the 32-score steps
+// What bounds it (131072 positions, 64 rows of 32 heads of 128 behind them, bf16: 230 us of a call's 269, where the products alone would
+// take 71): a tile of 128 x 128 takes about 4100 clocks, its softmax 4800 in either group, of which the 32-score steps
 // take 1000 each: two pieces of a weight are some 14 instructions a score, of which a scheduler issues 0.7 per clock with its two
-// softmax warps.  f32 queries: 3700 clocks a tile of 64 positions.  The value product in halves, and more registers for the softmax
+// softmax warps.  f32 queries: 3400 clocks a tile of 64 positions.  The value product in halves, and more registers for the softmax
 // warps (setmaxnreg), were slower.
 #pragma once
 #include <type_traits>
@@ -41,7 +41,7 @@ namespace llm {
 
 constexpr int kShRows = 128;         // columns of a unit: the M side
 constexpr int kShSegs = 8;           // segments told ahead
-constexpr int kShWarps = 16;         // loads, products, walk, an idle one; two softmax groups of four; four that widen
+constexpr int kShWarps = 16;         // loads, scores, walk, values' products; two softmax groups of four; four that widen
 constexpr int kShThreads = 32 * kShWarps;
 constexpr int kShWiden = 128;        // threads that widen
 constexpr float kShMost = 24.0f;     // log2 of the largest weight that moves no reference
@@ -56,12 +56,14 @@ struct ShShape {
   static constexpr int QB = NP * kShRows * HD;       // query pieces
   static constexpr int VB = 2 * TN * HD;             // widened values of a tile
   static constexpr int KS = HD == 64 || !QT ? 6 : 4, VS = HD == 64 || !QT ? 6 : 3;  // ring stages
-  static constexpr int RUN = QT ? 32 : 8;            // a group's tiles whose products are summed in tensor memory
+  static constexpr int RUN = (QT ? 4096 : 512) / TN;            // a group's tiles whose products are summed in tensor memory
   static constexpr size_t MISC = 14336;
   static constexpr size_t SMEM = 1024 + (size_t)(KS + VS) * KB + QB + 2 * VB + MISC;
   static constexpr uint32_t SWZ = HD == 128 ? 2 : 4;
-  static constexpr uint32_t BUF = 128;               // tensor-memory columns of a group's scores; the groups' O behind both
-  static_assert(SMEM <= kQaSmem, "shared memory");
+  // Tensor memory: a group's scores, in 128 columns (f32: coarse and fine pieces apart) that its weights reuse; behind both
+  // groups' their O
+  static constexpr uint32_t BUF = 128, O = 2 * BUF;
+  static_assert(SMEM <= kQaSmem && O + 2 * HD <= 512, "memory");
   static_assert((KS + VS) * KB >= kShUnits * 4, "the walk's counts");
 };
 
@@ -99,8 +101,8 @@ __global__ void __launch_bounds__(kShThreads, 1)
   const uint32_t b_kf = bars, b_ke = b_kf + 8 * KS, b_vf = b_ke + 8 * KS, b_ve = b_vf + 8 * VS, b_wf = b_ve + 8 * VS,
                  b_we = b_wf + 16, b_sf = b_we + 16, b_pf = b_sf + 16, b_of = b_pf + 16, b_oe = b_of + 16, b_qe = b_oe + 16,
                  b_qf = b_qe + 8, b_gf = b_qf + 8 * kShSegs, b_ge = b_gf + 8 * kShSegs,
-                 b_end = b_ge + 8 * kShSegs;
-  static_assert(64 * VS + 8 * 128 * kShSegs + 512 + sizeof(ShSeg) * kShSegs + 16 * (KS + VS) + 136 + 24 * kShSegs + 8 <= X::MISC,
+                 b_end = b_ge + 8 * kShSegs, b_end2 = b_end + 8;
+  static_assert(64 * VS + 8 * 128 * kShSegs + 512 + sizeof(ShSeg) * kShSegs + 16 * (KS + VS) + 144 + 24 * kShSegs + 8 <= X::MISC,
                 "shared memory");
   __shared__ uint32_t s_tmem;
   __shared__ int s_warp[kShWarps], s_total, s_slot, s_at;
@@ -127,11 +129,12 @@ __global__ void __launch_bounds__(kShThreads, 1)
       mbar_init(b_oe + 8u * i, 128);
     }
     mbar_init(b_end, 1);
+    mbar_init(b_end2, 1);
     mbar_init(b_qe, 1);
     for (int i = 0; i < kShSegs; ++i) {
       mbar_init(b_qf + 8u * i, 33);          // the loads, and the lanes that copy the scales
       mbar_init(b_gf + 8u * i, 32);
-      mbar_init(b_ge + 8u * i, 2 + 12);
+      mbar_init(b_ge + 8u * i, 3 + 12);
     }
     mbar_fence_init();
   }
@@ -368,28 +371,21 @@ __global__ void __launch_bounds__(kShThreads, 1)
 #pragma unroll 1
     for (uint32_t i = nk > VS ? nk - VS : 0u; i < nk; ++i) wait(b_vf + 8u * (i % VS), (i / VS) & 1u);
   } else if (warp == 1) {
-    // ---- the products: scores run two tiles ahead of the values ----
-    const uint32_t id_s = idesc_e4m3_f32(kShRows, TN), id_o = idesc_bf16_f32(kShRows, HD) | 1u << 16;
-    const uint32_t q_addr = smem_u32(qbuf), w_addr = smem_u32(wide), k_ring = smem_u32(kring);
-    uint32_t ks = 0u, kpar = 0u, it = 0u, scored = 0u;
-    uint32_t fresh = 0u;                  // bit t % 32: tile t starts a run of its group
-    uint32_t placed = 0u, opar[2] = {1u, 1u};
-    bool more = true;
-    int left = 0;  // tiles of the segment that are not scored yet
+    // ---- the products of queries and keys: a group's next as soon as its columns are free ----
+    const uint32_t id_s = idesc_e4m3_f32(kShRows, TN);
+    const uint32_t q_addr = smem_u32(qbuf), k_ring = smem_u32(kring);
+    uint32_t ks = 0u, kpar = 0u, it = 0u;
     const uint32_t one = lane == 0;  // (the lane that issues: the addresses stay uniform over the warp)
-    auto score = [&]() {
-      if (left == 0 && more) {
-        left = __reduce_max_sync(0xffffffffu, next_seg());
-        placed = 0u;
-        more = left > 0;
-        if (!more) return;
-        wait(b_qf + 8u * gslot, gpar);
-        seg_done();
-      }
-      if (!more) return;
-      wait(b_kf + 8u * ks, kpar);
-      const uint32_t gp = scored & 1u;
-      if (ok) {
+    while (const int n = __reduce_max_sync(0xffffffffu, next_seg())) {
+      wait(b_qf + 8u * gslot, gpar);
+      seg_done();
+#pragma unroll 1
+      for (int k = 0; k < n; ++k, ++it) {
+        const uint32_t gp = it & 1u;
+        if (it >= 2u) wait(b_of + 8u * gp, (it >> 1 & 1u) ^ 1u);  // (the product has read the weights there)
+        wait(b_kf + 8u * ks, kpar);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t k_addr = k_ring + ks * X::KB;
 #pragma unroll
@@ -400,29 +396,36 @@ __global__ void __launch_bounds__(kShThreads, 1)
                            smem_desc(k_addr + i * 32, 16, 8 * HD, X::SWZ), id_s, (p & 1) != 0 || i > 0, one);
         tc_commit_if(b_sf + 8u * gp, one);
         tc_commit_if(b_ke + 8u * ks, one);
-        if (left == 1) tc_commit_if(b_qe, one);
+        if (k + 1 == n) tc_commit_if(b_qe, one);
+        __syncwarp();
+        if (++ks == KS) ks = 0u, kpar ^= 1u;
       }
-      __syncwarp();
-      const uint32_t bit = 1u << (scored & 31u);
-      fresh = (placed++ >> 1) % X::RUN == 0u ? fresh | bit : fresh & ~bit;
-      --left;
-      ++scored;
-      if (++ks == KS) ks = 0u, kpar ^= 1u;
-    };
-    score();
-    score();
-    while (it < scored) {
-      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const uint32_t gp = it & 1u, ph = it >> 1 & 1u;  // the tile's group, and the phase of its barriers
-      wait(b_wf + 8u * gp, ph);
-      wait(b_pf + 8u * gp, ph);
-      const bool start = fresh >> (it & 31u) & 1u;
-      if (start) {  // (the sums of the run before have been read)
-        wait(b_oe + 8u * gp, opar[gp]);
-        opar[gp] ^= 1u;
-      }
-      if (ok) {
+    }
+    if (!ok) {  // (no product may be at work when the CTA exits)
+      tc_commit_if(b_end, one);
+      mbar_wait(b_end, 0u, kQaWaitCycles);
+    }
+  } else if (warp == 3) {
+    // ---- the products of weights and values, from a warp of its own: in one, each kind's issue waits for the other's (131072
+    // positions 274 us against 269, 32768 with f32 queries 108 against 100) ----
+    const uint32_t id_o = idesc_bf16_f32(kShRows, HD) | 1u << 16, w_addr = smem_u32(wide);
+    uint32_t it = 0u, opar[2] = {1u, 1u};
+    const uint32_t one = lane == 0;
+    while (const int n = __reduce_max_sync(0xffffffffu, next_seg())) {
+      seg_done();
+#pragma unroll 1
+      for (int k = 0; k < n; ++k, ++it) {
+        const uint32_t gp = it & 1u, ph = it >> 1 & 1u;  // the tile's group, and the phase of its barriers
+        wait(b_wf + 8u * gp, ph);
+        wait(b_pf + 8u * gp, ph);
+        const bool start = (k >> 1) % X::RUN == 0;  // of a run of the group's tiles
+        if (start) {  // (the sums of the run before have been read)
+          wait(b_oe + 8u * gp, opar[gp]);
+          opar[gp] ^= 1u;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t v_addr = w_addr + gp * X::VB;
 #pragma unroll
@@ -430,35 +433,30 @@ __global__ void __launch_bounds__(kShThreads, 1)
           const uint64_t vd = smem_desc(v_addr + kk * 16 * HD, X::KB, 8 * HD, X::SWZ);
 #pragma unroll
           for (int y = 0; y < WP; ++y)
-            tc_mma_bf16_ts(tmem + 2 * X::BUF + gp * HD, tmem + gp * X::BUF + kk * 16 + (y < 2 ? y * 8 : 64), vd, id_o,
+            tc_mma_bf16_ts(tmem + X::O + gp * HD, tmem + gp * X::BUF + kk * 16 + (y < 2 ? y * 8 : 64), vd, id_o,
                            !start || kk > 0 || y > 0, one);
         }
         tc_commit_if(b_of + 8u * gp, one);
         tc_commit_if(b_we + 8u * gp, one);
+        __syncwarp();
       }
-      __syncwarp();
-      ++it;
-      // the group's next tile, in the same columns: once the product has read the weights there
-      wait(b_of + 8u * gp, ph);
-      score();
+      if (!ok) break;
     }
-    if (!ok) {  // (no product may be at work when the CTA exits)
-      tc_commit_if(b_end, one);
-      mbar_wait(b_end, 0u, kQaWaitCycles);
+    if (!ok) {
+      tc_commit_if(b_end2, one);
+      mbar_wait(b_end2, 0u, kQaWaitCycles);
     }
-  } else if (warp < 4) {
-    // (the others of these four have no work)
   } else if (warp < 12) {
     // ---- softmax: thread = column; the groups take the tiles in turn, each with scores, sums and references of its own ----
     const uint32_t group = (warp - 4) >> 2;
     const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t t_s = tmem + group * X::BUF + lanes, t_o = tmem + 2 * X::BUF + group * HD + lanes;
+    const uint32_t t_s = tmem + group * X::BUF + lanes, t_o = tmem + X::O + group * HD + lanes;
     float* sc = wsc + (warp - 4) * 16;
     float sums[HD];                          // of the runs before (local memory: rarely touched)
     float ref = kQaNone, l = 0.f;            // reference of the column's weights, and their sum
     float vref = 0.f;                        // a power of two that the values' scales are relative to
-    uint32_t it = 0u, vs = 0u, vpar = 0u, mine = 0u;  // mine: tiles of this group
+    uint32_t it = 0u, vs = 0u, vpar = 0u;
     // what waits to be read from tensor memory until the next tile's weights are on their way: a segment's end
     bool pend = false, earlier = false;      // earlier: the segment has sums of runs before
     uint32_t pslot = 0u;
@@ -467,9 +465,9 @@ __global__ void __launch_bounds__(kShThreads, 1)
     auto place = [&](const ShSeg& o, float m, float sum) {
       return sh_put(a, o.part, group, ((int64_t)o.j * a.r.B * a.r.S + o.gt) * a.g + row, row, m, sum, cta, o.cta0, o.ctas);
     };
-    // the products of the group's tiles up to number t: to the sums, or with the segment's end to global memory
+    // the products of the group's tiles up to tile t: to the sums, or with the segment's end to global memory
     auto flush = [&](uint32_t t, bool ends) {
-      wait(b_of + 8u * group, t & 1u);
+      wait(b_of + 8u * group, t >> 1 & 1u);
       __syncwarp();
       const uint32_t slot = ends ? pslot : gslot;
       const int used = segs[slot].used;
@@ -516,7 +514,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
         if ((it & 1u) == group) {
           // (scores first: once they are there the tile before this one in the ring's stage has been used up, so the
           // stage's barrier, which this group looks at in some of its phases only, can be no phase behind)
-          wait(b_sf + 8u * group, mine & 1u);
+          wait(b_sf + 8u * group, it >> 1 & 1u);
           wait(b_vf + 8u * vs, vpar);
           __syncwarp();
           const float x0 = lane < 2 * NB ? ssc[vs * 16 + lane] : 0.f;
@@ -614,7 +612,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
                 }
                 if (own > 0) {
                   // what has been added up so far, once the product before is in it
-                  wait(b_of + 8u * group, (mine - 1u) & 1u);
+                  wait(b_of + 8u * group, (it - 2u) >> 1 & 1u);
                   __syncwarp();
                   tc_fence_after();
 #pragma unroll 1
@@ -686,10 +684,9 @@ __global__ void __launch_bounds__(kShThreads, 1)
           }
           mbar_arrive(b_pf + 8u * group);
           // the run before, so that this one's products can start
-          if (pend) flush(mine - 1u, true);
-          else if (own > 0 && own % X::RUN == 0) flush(mine - 1u, false);
+          if (pend) flush(it - 2u, true);
+          else if (own > 0 && own % X::RUN == 0) flush(it - 2u, false);
           ++own;
-          ++mine;
         }
         if (++vs == VS) vs = 0u, vpar ^= 1u;
       }
@@ -708,7 +705,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
       pm = ref;
       pl = l;
       pback = vref;
-      flush(mine - 1u, true);
+      flush(((it - 1u) & 1u) == group ? it - 1u : it - 2u, true);  // (the group's last tile)
     }
   } else {
     // ---- values widened ----
