@@ -29,9 +29,10 @@
 //
 // What bounds it (131072 positions, 64 rows of 32 heads of 128 behind them, bf16: 230 us of a call's 269, where the products alone would
 // take 71): a tile of 128 x 128 takes about 4100 clocks, its softmax 4800 in either group, of which the 32-score steps
-// take 1000 each: two pieces of a weight are some 14 instructions a score, of which a scheduler issues 0.7 per clock with its two
-// softmax warps.  f32 queries: 3400 clocks a tile of 64 positions.  The value product in halves, and more registers for the softmax
-// warps (setmaxnreg), were slower.
+// take 1000 each (293 instructions for 32 scores; the schedulers issue 47% of the time), then 1400 for its product and 750 for
+// its next scores.  f32 queries: 3400 clocks a tile of 64 positions.  Slower: the value product's columns in halves, more registers for
+// the softmax warps (setmaxnreg), tiles of 64 with two score buffers a group (289 us).  The product's positions in halves, the
+// first under way while the second is weighed: 266 us, for two more barriers a group.
 #pragma once
 #include <type_traits>
 

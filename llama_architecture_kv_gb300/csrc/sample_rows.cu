@@ -20,10 +20,13 @@
 // bin split by the next 11 bits of d until its candidates fit or d is the same for all, where the order is that
 // of the ids.  Candidates that weigh nothing are in no bin.
 //
-// What bounds it: for one row barriers of the cluster and the block, some thirty one after the other (16 us at 49152;
-// 29 with the places one after the other and every pass from global memory); for many rows the histogram, whose
-// three additions a candidate each serve the 32 banks' longest queue (about 5 clocks a warp; 32 rows of 128256: 35 us, 86
-// before; 256 of 50257: 83, 249 before).
+// For k up to 1024 the histogram is of counts alone, one addition a candidate and no weight, and all candidates up to the
+// k-th one's bin are gathered.
+//
+// What bounds it: for one row barriers of the cluster and the block, some thirty one after the other (15 us at 49152;
+// 29 with the places one after the other and every pass from global memory); for many rows a candidate's weight (some
+// 40 instructions; 56% of issue slots busy) and the histogram, whose three additions each serve the 32 banks' longest
+// queue (32 rows of 128256: 32 us, 86 before; 256 of 50257: 75, 249 before).
 #include <math.h>
 
 #include "sampler.cuh"
@@ -868,11 +871,11 @@ cudaError_t launch_sample_rows(const SampleRowsArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   // CTAs of a row: as many as have an SM each, so that few rows take little time and many few barriers and joins
-  // (8 / 4 / 2 / 1: 1 row of 49152 16 / 18 / 22 / 38 us, 32 of 128256 40 / 35 / 54 / 54, 256 of 50257 151 / 92 / 83 / 88);
+  // (8 / 4 / 2: 1 row of 49152 15 / 17 / 21 us, 32 of 128256 42 / 32 / 48, 256 of 50257 183 / 109 / 75);
   // more where a stretch has no room in shared memory, or a bin's sum none in 32 bits
   int size = (int64_t)a.B * 8 <= sms ? 8 : (int64_t)a.B * 4 <= sms ? 4 : 2;
   while (size < kSrCluster && sizeof(SrShared) + (size_t)a.V / size * 4 > 226u * 1024u) size *= 2;
-  // (512 threads: 16 us for that row, 1024 17)
+  // (512 threads: 15 us for that row, 1024 16)
   return (a.V + size - 1) / size <= 8192 ? sr_launch<512>(a, size, s) : sr_launch<1024>(a, size, s);
 }
 
