@@ -137,6 +137,7 @@ LLM_D void pg_hand_on(const PageBook& from, const PageBook& to, int32_t* moves, 
 __global__ void __launch_bounds__(kPgThreads)
     pages_update_kernel(const PageBook from, const PageBook to, const int32_t* parent, const int32_t* length, int32_t* moves,
                         int32_t* counts, int32_t* ws, int32_t* status) {
+  grid_dep_launch();
   const PgCluster c = pg_cluster();
   const int t = c.rank * kPgThreads + threadIdx.x, nt = c.size * kPgThreads;
   const int lane = threadIdx.x & 31, warp = t >> 5, nw = nt >> 5;
@@ -268,6 +269,7 @@ __global__ void __launch_bounds__(kPgThreads)
 __global__ void __launch_bounds__(kPgThreads)
     pages_compact_kernel(const PageBook from, const PageBook to, int32_t* moves, int m, int32_t* counts, int32_t* ws,
                          int32_t* status) {
+  grid_dep_launch();
   const PgCluster c = pg_cluster();
   const int t = c.rank * kPgThreads + threadIdx.x, nt = c.size * kPgThreads;
   const int lane = threadIdx.x & 31, warp = t >> 5, nw = nt >> 5;
@@ -363,6 +365,7 @@ __global__ void __launch_bounds__(kPgThreads)
 // 16-byte loads in flight as a lane has registers for, and its four scales.  Bound by HBM.
 constexpr int kCopyThreads = 128;
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyArgs a) {
+  grid_dep_wait();
   const int lane = threadIdx.x & 31;
   const int per = a.layers * a.kv * 2;           // warps of a move
   const int64_t w = (int64_t)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
@@ -429,8 +432,17 @@ cudaError_t launch_pages_compact(const PageBook& from, const PageBook& to, int32
 
 cudaError_t launch_copy_pages(const CopyArgs& a, cudaStream_t s) {
   const int64_t warps = (int64_t)a.m * a.layers * a.kv * 2;
-  copy_pages_kernel<<<(unsigned)((warps + kCopyThreads / 32 - 1) / (kCopyThreads / 32)), kCopyThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((warps + kCopyThreads / 32 - 1) / (kCopyThreads / 32)));
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = s;
+  // (behind an update of the table it is on the SMs when that is done: one row forked into four 10.9 to 10.4 us)
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, copy_pages_kernel, a);
 }
 
 }  // namespace llm

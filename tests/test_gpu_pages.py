@@ -163,6 +163,54 @@ def test_copied_pages_equal_and_nothing_else_changes(hd, kv, rows, cap):
             same(c, r)
 
 
+def test_captured_copies_behind_a_fill_a_copy_of_memory_and_an_update():
+    # what a copy of pages follows in a captured graph: a memory copy of its moves, an update that writes them, another copy
+    rng = np.random.default_rng(9)
+    R, per, pages = 3, 4, 16
+    c = pkg.QCache.empty(1, 2, pages * 64, 64)
+    layers = pkg.QCacheLayers([c])
+    book = [pkg.Pages.empty(R, per, pages) for _ in range(2)]
+    ws = book[0].workspace()
+    counts = torch.zeros(2, dtype=torch.int32, device="cuda")
+    moves, given, second = (torch.zeros(R, 2, dtype=torch.int32, device="cuda") for _ in range(3))
+    parent, length = (torch.zeros(R, dtype=torch.int32, device="cuda") for _ in range(2))
+    second.copy_(torch.tensor([[1, 11], [-1, -1], [11, 12]], dtype=torch.int32))
+
+    def run():
+        moves.copy_(given)                      # (a memory copy)
+        layers.copy(moves)
+        layers.copy(second[:1].contiguous())
+        layers.copy(second[2:].contiguous())
+        book[0].update(book[1], moves, counts, ws, parent=parent, length=length)
+        layers.copy(moves, counts=counts)
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        run()
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for trial in range(6):
+        codes = torch.from_numpy(rng.integers(0, 256, (1, 2, pages * 64, 64)).astype(np.uint8)).cuda()
+        c.tensors[0].copy_(codes)
+        first = rng.permutation(10)[:6].reshape(3, 2)
+        given.copy_(torch.from_numpy(first.astype(np.int32)))
+        # row 0 holds pages 13 and 14, the latter in part; the others go on from it
+        book[0].table.fill_(-1)
+        book[0].table[0, :2] = torch.tensor([13, 14])
+        book[0].length.copy_(torch.tensor([64 + 10 + trial, 0, 0]))
+        length.fill_(64 + 10 + trial)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        want = codes.cpu().numpy().reshape(2, pages, 64, 64).copy()
+        for a, b in [*[(a, b) for a, b in first], (1, 11), (11, 12), *moves.tolist()[:int(counts[0])]]:
+            want[:, b] = want[:, a]
+        assert int(counts[0]) == 2 and moves[:2, 0].tolist() == [14, 14]
+        assert (c.tensors[0].cpu().numpy().reshape(want.shape) == want).all()
+
+
 def test_pages_outside_the_pool_are_reported_and_skipped():
     c, r = make(2, 2, 128, 64, garbage=1)
     for move in ([4, 0], [0, 4], [-1, 0], [0, -1], [1 << 30, 1], [0, -(1 << 31)]):
