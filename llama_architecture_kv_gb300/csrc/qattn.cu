@@ -71,12 +71,14 @@ LLM_D bool token_place(const QRows& r, const QCacheView& c, int b, int pos, int&
 // Whether the group bounds of a call with shared positions ascend from 0 to B (else an error is recorded and no
 // row shares anything); every thread of the CTA calls it
 LLM_D bool groups_fine(const QAttnArgs& a) {
-  bool fine = true;
+  bool fine = true, held = true;
   for (int i = threadIdx.x; i < a.ngroups; i += blockDim.x) {
-    const int lo = a.groups[i], hi = a.groups[i + 1];
+    const int lo = a.groups[i], hi = a.groups[i + 1], n = a.shared[i];
     fine &= lo <= hi && (i > 0 || lo == 0) && (i + 1 < a.ngroups || hi == a.r.B);
+    held &= n >= 0 && n <= a.r.limit;
   }
   fine = __syncthreads_and(fine);
+  if (fine && !held) q_report(a.r.status, kErrPosRange);
   if (!fine) q_report(a.r.status, kErrArg);
   return fine;
 }

@@ -166,24 +166,21 @@ LLM_D QaUnit qa_unit(const QAttnArgs& a, int t) {
 }
 
 // ---- rows that share positions (qshare.cuh) ----
-// What a unit is follows from its row's group, length and count: this thread's part of them is read at once, before the
-// first of the reads that depend on one another
-LLM_D int sh_touch(const QAttnArgs& a) {
-  int x = 0;
-  for (int i = threadIdx.x; i < a.ngroups; i += blockDim.x) x ^= a.shared[i];
-  for (int i = threadIdx.x; i < a.r.B; i += blockDim.x) x ^= a.r.first[i] ^ q_count(a.r, i);
-  return x;
-}
-// whether the groups' bounds ascend from 0 to B (else no row shares anything); every thread of the CTA calls it
+// Whether the groups' bounds ascend from 0 to B (else no row shares anything); every thread of the CTA calls it.  What a unit is
+// follows from its row's group, length and count: a thread's part of all these is read at once here, before the first of
+// the reads that depend on one another.
 LLM_D bool sh_fine(const QAttnArgs& a) {
-  bool fine = true;
-  const int touched = sh_touch(a);
+  bool fine = true, held = true;
+  int touched = 0;
+  for (int i = threadIdx.x; i < a.r.B; i += blockDim.x) touched ^= a.r.first[i] ^ q_count(a.r, i);
   for (int i = threadIdx.x; i < a.ngroups; i += blockDim.x) {
-    const int lo = a.groups[i], hi = a.groups[i + 1];
+    const int lo = a.groups[i], hi = a.groups[i + 1], n = a.shared[i];
     fine &= lo <= hi && (i > 0 || lo == 0) && (i + 1 < a.ngroups || hi == a.r.B);
+    held &= n >= 0 && n <= a.r.limit;
   }
   asm volatile("" ::"r"(touched));
   fine = __syncthreads_and(fine);
+  if (fine && !held) q_report(a.r.status, kErrPosRange);
   if (!fine && threadIdx.x == 0) q_report(a.r.status, kErrArg);
   return fine;
 }

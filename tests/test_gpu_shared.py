@@ -169,6 +169,25 @@ def test_bad_groups_shared_parts_lengths_and_pages():
 
 
 @pytest.mark.parametrize("hd", [32, 64, 128])
+def test_shared_parts_out_of_range_are_reported_whoever_has_them(hd):
+    # a group without rows, one of empty rows, one whose rows have no tokens in the call; each way a call can go
+    kv, g, B = 2, 4, 4
+    c, r = make(B, kv, 128, hd, garbage=2)
+    fill(c, r, np.random.default_rng(16), 100)
+    q = torch.ones(B, 1, kv * g, hd, device="cuda")
+    for table in (None, wide_table(r, B)):
+        for groups, shared, length, count in (([0, 2, 2, 4], [10, -1, 20], [100] * 4, None), ([0, 2, 4, 4], [10, 20, 1 << 30], [100] * 4, None),
+                                              ([0, 2, 4], [10, -7], [100, 100, 0, 0], None), ([0, 2, 4], [1 << 29, 10], [100] * 4, [0, 0, 1, 1])):
+            st, out = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full_like(q, 9.0)
+            c.attend_shared(q, i32(length), i32(groups), i32(shared), out, c.workspace_shared(g, B, 1, len(shared)),
+                            count=None if count is None else i32(count), table=None if table is None else i32(table), status=st)
+            want, mag, sens, _ = shared_ref.attend_shared(r, q.double().cpu().numpy(), length, groups, [0 if not 0 <= n <= 128 else n for n in shared],
+                                                          count, None, out=np.full(q.shape, 9.0))
+            assert int(st) == pkg.LLM_ERR_POS_RANGE
+            assert (np.abs(out.double().cpu().numpy() - want) <= tolerance("f32", hd, want, mag, sens)).all()
+
+
+@pytest.mark.parametrize("hd", [32, 64, 128])
 def test_nothing_to_see(hd):
     kv, g, B = 2, 4, 3
     c, _ = make(B, kv, 64, hd, garbage=2)
