@@ -135,25 +135,27 @@ def test_slices_of_wider_rows_and_other_scales():
         check(c, r, rng, 1, g, "f32", length, [0, B], [100], scale=scale, spread=2.0)
 
 
-def test_bad_groups_shared_parts_lengths_and_pages():
+@pytest.mark.parametrize("wide", [False, True])
+def test_bad_groups_shared_parts_lengths_and_pages(wide):
     rng = np.random.default_rng(15)
     for hd in (128, 64, 32):
         kv, g, cap, B = 2, 4, 256, 4
         c, r = make(B, kv, cap, hd, garbage=3)
         fill(c, r, rng, 256)
+        t, most = (wide_table(r, B), 1 << 18) if wide else (None, cap)
         L = [256, 200, 70, 130]
         # bounds that do not ascend from 0 to B: no row shares
         for groups in ([0, 3], [1, 4], [0, 5], [0, 3, 2, 4], [0, 4, 4, 3], [-1, 4], [0, 1 << 30, 4], [0, -5, 4]):
             n = len(groups) - 1
-            check(c, r, rng, 1, g, "f32", L, groups, [64] * n, status=pkg.LLM_ERR_ARG, want_with=(L, [0, 4], [0]) if n == 1 else (L, [0, 4], [0]))
+            check(c, r, rng, 1, g, "f32", L, groups, [64] * n, status=pkg.LLM_ERR_ARG, want_with=(L, [0, 4], [0]) if n == 1 else (L, [0, 4], [0]), table=t)
         # shared parts out of range: the rows of that group share nothing
-        for bad in (-1, cap + 1, 1 << 30):
-            check(c, r, rng, 1, g, "f32", L, [0, 2, 4], [bad, 60], status=pkg.LLM_ERR_POS_RANGE, want_with=(L, [0, 2, 4], [0, 60]))
+        for bad in (-1, most + 1, 1 << 30):
+            check(c, r, rng, 1, g, "f32", L, [0, 2, 4], [bad, 60], status=pkg.LLM_ERR_POS_RANGE, want_with=(L, [0, 2, 4], [0, 60]), table=t)
         # lengths and counts out of range: those rows are empty
-        check(c, r, rng, 1, g, "f32", [256, -1, cap + 1, 130], [0, 4], [100], status=pkg.LLM_ERR_POS_RANGE,
-              want_with=([256, 0, 0, 130], [0, 4], [100]))
+        check(c, r, rng, 1, g, "f32", [256, -1, most + 1, 130], [0, 4], [100], status=pkg.LLM_ERR_POS_RANGE,
+              want_with=([256, 0, 0, 130], [0, 4], [100]), table=t)
         # a page of the shared part outside the pool is unseen by all, one of a row's own by that row
-        table = np.arange(B * 4, dtype=np.int32).reshape(B, 4)
+        table = wide_table(r, B) if wide else np.arange(B * 4, dtype=np.int32).reshape(B, 4)
         for b, i in ((0, 1), (3, 1)):
             bad = table.copy()
             bad[b, i] = B * 4
@@ -188,25 +190,28 @@ def test_shared_parts_out_of_range_are_reported_whoever_has_them(hd):
 
 
 @pytest.mark.parametrize("hd", [32, 64, 128])
-def test_nothing_to_see(hd):
+@pytest.mark.parametrize("wide", [False, True])
+def test_nothing_to_see(hd, wide):
     kv, g, B = 2, 4, 3
-    c, _ = make(B, kv, 64, hd, garbage=2)
-    ws = c.workspace_shared(g, B, 2, 2)
+    c, r = make(B, kv, 64, hd, garbage=2)
+    ws, table = c.workspace_shared(g, B, 2, 2), i32(wide_table(r, B)) if wide else None
     q = torch.ones(B, 2, kv * g, hd, device="cuda")
     for length, count, shared, want in (([0] * B, None, [0, 0], 0.0), ([0] * B, None, [64, 30], 0.0), ([0] * B, [0] * B, [10, 0], 9.0),
                                         ([40, 64, 1], [0] * B, [40, 64], 9.0)):
         out = torch.full_like(q, 9.0)
-        c.attend_shared(q, i32(length), i32([0, 1, 3]), i32(shared), out, ws, count=None if count is None else i32(count))
+        c.attend_shared(q, i32(length), i32([0, 1, 3]), i32(shared), out, ws, count=None if count is None else i32(count), table=table)
         assert (out == want).all()
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_nan_reaches_only_the_tokens_that_see_it(dtype):
+def test_nan_reaches_only_the_tokens_that_see_it(dtype, wide):
     rng = np.random.default_rng(14)
     for hd, g in ((128, 4), (64, 1), (32, 2)):
         kv, n, B = 2, 160, 3
         c, r = make(B, kv, 192, hd)
         fill(c, r, rng, n)
+        table = i32(wide_table(r, B)) if wide else None
         bad, zero = torch.zeros(1, 1, kv, hd, device="cuda"), torch.zeros(1, 1, kv, hd, device="cuda")
         bad[0, 0, 1, 3] = float("nan")        # head 1 of the first row's token at position 160, alone in its block
         for k, v in ((bad, zero), (zero, bad)):
@@ -215,7 +220,7 @@ def test_nan_reaches_only_the_tokens_that_see_it(dtype):
             out = torch.zeros_like(q)
             # shared: seen by the last token of the rows that reach it; not shared: by the first row's alone
             for shared, seers in (([176], (0, 2)), ([160], (0,)), ([16], (0,))):
-                c.attend_shared(q, i32([161, 160, 161]), i32([0, B]), i32(shared), out, c.workspace_shared(g, B, 3, 1))
+                c.attend_shared(q, i32([161, 160, 161]), i32([0, B]), i32(shared), out, c.workspace_shared(g, B, 3, 1), table=table)
                 for b in range(B):
                     for i in range(3):
                         sees = b in seers and i == 2
@@ -227,7 +232,7 @@ def test_nan_reaches_only_the_tokens_that_see_it(dtype):
             q, _ = rows_of(rng, (B, 3, kv * g, hd), dtype)
             q[1, 1, g, 5] = value
             out = torch.zeros_like(q)
-            c.attend_shared(q, i32([160] * B), i32([0, B]), i32([100]), out, c.workspace_shared(g, B, 3, 1))
+            c.attend_shared(q, i32([160] * B), i32([0, B]), i32([100]), out, c.workspace_shared(g, B, 3, 1), table=table)
             wrong = ~torch.isfinite(out)
             assert wrong[1, 1, g].all() and int(wrong.sum()) == hd
 
@@ -371,3 +376,34 @@ def test_captured_calls_that_read_the_shared_positions_once(dtype, hd, S):
         ref, mag, sens, _ = shared_ref.attend_shared(r, q.double().cpu().numpy(), L, [0, 2, B], sh)
         for x in (want, few):
             assert (np.abs(x.double().cpu().numpy() - ref) <= tolerance(dtype, hd, ref, mag, sens)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_nan_beside_many_columns(dtype):
+    # a group of 132 columns, whose shared positions the kernel for many takes: a NaN among them, behind what some rows see;
+    # a query that is not finite
+    rng = np.random.default_rng(17)
+    hd, kv, g, B = 128, 2, 4, 33
+    c, r = make(1, kv, 640, hd)
+    fill(c, r, rng, 592)          # (whole blocks: a value that is not finite makes its block's scale NaN)
+    bad, zero = torch.zeros(1, 1, kv, hd, device="cuda"), torch.zeros(1, 1, kv, hd, device="cuda")
+    bad[0, 0, 1, 3] = float("nan")
+    table = i32(np.concatenate([np.tile(np.arange(10), (B, 1)), np.full((B, 4086), -1)], 1))
+    length = [593 if b % 3 == 0 else 592 if b % 3 == 1 else 77 for b in range(B)]
+    for k, v in ((bad, zero), (zero, bad)):
+        c.write(k, v, i32([592]))
+        q, _ = rows_of(rng, (B, 1, kv * g, hd), dtype)
+        out = torch.zeros_like(q)
+        c.attend_shared(q, i32(length), i32([0, B]), i32([593]), out, c.workspace_shared(g, B, 1, 1), table=table)
+        wrong = ~torch.isfinite(out[:, 0])
+        assert not wrong[:, :g].any()
+        for b in range(B):
+            assert wrong[b, g:].all() if length[b] == 593 else not wrong[b].any()
+    c.write(zero, zero, i32([592]))
+    for value in (float("nan"), float("inf")):
+        q, _ = rows_of(rng, (B, 1, kv * g, hd), dtype)
+        q[31, 0, 5, 100] = value
+        out = torch.zeros_like(q)
+        c.attend_shared(q, i32([592] * B), i32([0, B]), i32([590]), out, c.workspace_shared(g, B, 1, 1), table=table)
+        wrong = ~torch.isfinite(out)
+        assert wrong[31, 0, 5].all() and int(wrong.sum()) == hd
