@@ -197,7 +197,8 @@ llm_status llm_qcache_attend_shared(const llm_qcache* cache, const void* q_dev, 
          "the groups' bounds and shared positions must be given, as aligned int32 arrays");
   int sms = 0;
   TRY(device_sms(&sms));
-  REFUSE(!(qattn_uses_tc(a.c.hd) ? qshare_fits(a.c, group, dtype, B, S, groups, a.r.limit) : qattn_fits(a.c, group, dtype, B, S, a.r.limit, sms)), LLM_ERR_ARG,
+  REFUSE(!(qattn_uses_tc(a.c.hd) ? qshare_fits(a.c, group, dtype, B, S, groups, a.r.limit)
+                                 : qattn_fits(a.c, group, dtype, B, S, a.r.limit, sms)), LLM_ERR_ARG,
          "too large for one call: rows x tokens / (32 / group) at most 4096, these x kv heads x 64-position tiles below 2^30, "
          "and the outputs' elements below 2^31");
   const uint64_t need = qattn_shared_workspace(a.c, group, B, S, sms);

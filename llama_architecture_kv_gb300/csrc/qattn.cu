@@ -8,7 +8,8 @@
 // Head sizes 64 and 128 run on the tensor cores (qattn_tc.cuh: 32 rows of up to 2100 positions, 8 heads
 // of 128, groups of 4, in 34 us, against 170 us with the kernel here).  qattn_simple_kernel takes the
 // others (16, 32, 256; on the tensor cores they would take other tiles: a 32-byte swizzle and value products of
-// 64 rows for 32, two boxes a row and two value products for 256): a CTA of four warps takes one token, one key/value head and one contiguous part of the positions.  Each warp takes 32 positions at a
+// 64 rows for 32, two boxes a row and two value products for 256): a CTA of four warps takes one token, one key/value
+// head and one contiguous part of the positions.  Each warp takes 32 positions at a
 // time: lane = position for the scores of the group's heads (the codes widened to f32, the scale applied
 // to the dot product once), a warp-wide running maximum and sum per head, then lane = dimensions for the
 // values.  Statistics, weights and sums are f32.  The parts of a token meet in qattn_merge_kernel in their

@@ -803,8 +803,10 @@ __global__ void __launch_bounds__(NT) sample_rows_kernel(const SampleRowsArgs a,
     for (int j = tid; j < r.quads; j += NT) {
       const uint4 x = r.logits(j);
       const int id = r.id(j);
-      const int y = __uint_as_float(x.x) == r.top ? 0 : __uint_as_float(x.y) == r.top ? 1 : __uint_as_float(x.z) == r.top ? 2 : __uint_as_float(x.w) == r.top ? 3 : 4;
-      if (y < 4) first = min(first, id + y);
+      const float v[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        if (v[y] == r.top) first = min(first, id + y);
     }
     first = __reduce_min_sync(0xffffffffu, first);
     if (lane == 0) s.num[warp] = (uint32_t)first;
