@@ -16,19 +16,19 @@ namespace {
 
 constexpr int kMergeThreads = 256;
 
-// Warp = column: its parts' statistics a lane each, then their sums, eight loads in flight (heads of 64: two parts at a
-// time, half a warp each).  Bound by the reads of the sums, which lie in L2 (1024 columns of 5 to 9 parts: 8 us with eight loads in
-// flight; 32 rows of 32 heads behind 8192 positions).
+// One, two or four warps to a column (`split`): its parts' statistics a lane each in every one of them, then the parts' sums,
+// eight loads in flight, by turns (heads of 64: two parts at a time, half a warp each).  Bound by the reads of the sums, which
+// lie in L2 (32 rows of 32 heads behind 8192 positions: 1024 columns of some 40 parts, 21 MB).
 template <int HD, int QT>
-__global__ void __launch_bounds__(kMergeThreads) qshare_merge_kernel(const QAttnArgs a, const ShSide prefix, const ShSide own) {
-  const int BS = a.r.B * a.r.S, cols = BS * a.c.kv * a.g, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kMergeThreads) qshare_merge_kernel(const QAttnArgs a, const ShSide prefix, const ShSide own, int split) {
+  __shared__ float4 half[kMergeThreads];
+  const int BS = a.r.B * a.r.S, cols = BS * a.c.kv * a.g, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool sharing = sh_fine(a);
-  const int col = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
-  if (col >= cols) return;
+  const int at_warp = blockIdx.x * (kMergeThreads / 32) + warp, col = at_warp / split, mine_of = at_warp - col * split;
   const int jt = col / a.g, h = col - jt * a.g, j = jt / BS, gt = jt - j * BS, b = gt / a.r.S, i = gt - b * a.r.S;
-  if (i >= q_count(a.r, b)) return;
+  const bool live = col < cols && i < q_count(a.r, b);
   int lead, last;
-  const int sh = sharing ? sh_group(a, b, lead, last) : 0, end = sh_end(a, b, i);
+  const int sh = live && sharing ? sh_group(a, b, lead, last) : 0, end = live ? sh_end(a, b, i) : 0;
   // (a column that sees something of a side is in a unit that has tiles there)
   const bool there[2] = {sh > 0 && end > 0, end > sh};
   grid_dep_wait();
@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(kMergeThreads) qshare_merge_kernel(const QAttn
     const int n = min(32, np - p0);
     constexpr int U = 8;
     for (int q0 = 0; q0 < n; q0 += U * SIDE) {
+      if ((p0 + q0) / (U * SIDE) % split != mine_of) continue;
       float4 v[U];
       float fp[U];
 #pragma unroll
@@ -108,6 +109,16 @@ __global__ void __launch_bounds__(kMergeThreads) qshare_merge_kernel(const QAttn
     o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
     o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
   }
+  if (split > 1) {  // (a column's warps, in their order)
+    half[threadIdx.x] = o;
+    __syncthreads();
+    if (!live || mine_of > 0) return;
+    for (int w = 1; w < split; ++w) {
+      const float4 x = half[threadIdx.x + 32 * w];
+      o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+    }
+  }
+  if (!live) return;
   const float r = L == 0.f ? 0.f : 1.f / L;
   if (sub == 0)
     qa_put4<QT>(a.out, (int64_t)gt * a.out_stride + (int64_t)(j * a.g + h) * HD + 4 * k4, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
@@ -263,7 +274,7 @@ cudaError_t launch_qshare_all(const QAttnArgs& a0, int qt, int num_sms, cudaStre
   CUtensorMap kmap, vmap, qmap;
   const uint64_t rows = (uint64_t)a.c.rows * a.c.kv * a.c.cap;
   if (!qattn_make_map(&kmap, a.c.k, hd, rows) || !qattn_make_map(&vmap, a.c.v, hd, rows)) return cudaErrorInvalidValue;
-  const int64_t grid = (p.columns + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
+  auto grid = [&](int64_t warps) { return (warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32); };
   cudaError_t e = cudaSuccess;
   if (p.many) {
     if (!qattn_make_map(&qmap, many.qp, hd, np * columns)) return cudaErrorInvalidValue;
@@ -271,7 +282,7 @@ cudaError_t launch_qshare_all(const QAttnArgs& a0, int qt, int num_sms, cudaStre
     void* args[] = {&a};
     auto fn = hd == 64 ? (qt ? qshare_pieces_kernel<64, 1> : qshare_pieces_kernel<64, 0>)
                        : (qt ? qshare_pieces_kernel<128, 1> : qshare_pieces_kernel<128, 0>);
-    e = launch((void*)fn, grid, args, s, false);
+    e = launch((void*)fn, grid(p.columns), args, s, false);
     if (e != cudaSuccess) return e;
   }
   a.sh = few;
@@ -284,10 +295,14 @@ cudaError_t launch_qshare_all(const QAttnArgs& a0, int qt, int num_sms, cudaStre
     e = fm(kmap, vmap, qmap, a, many.ctas, s, true);
     if (e != cudaSuccess) return e;
   }
-  void* args[] = {&a, p.many ? &many : &few, &few};
+  // warps of a column: as many as the SMs hold at once, two CTAs each (1 / 2 / 4: 1024 columns behind 8192 positions 54 / 52 / 57
+  // us a call, 64 behind 65536 45 / 43 / 42, 1536 behind 2047 72 / 75 / 78)
+  int split = 1;
+  while (split < 4 && p.columns * split * 2 <= (int64_t)num_sms * (2 * kMergeThreads / 32)) split *= 2;
+  void* args[] = {&a, p.many ? &many : &few, &few, &split};
   auto fj = hd == 64 ? (qt ? qshare_merge_kernel<64, 1> : qshare_merge_kernel<64, 0>)
                      : (qt ? qshare_merge_kernel<128, 1> : qshare_merge_kernel<128, 0>);
-  return launch((void*)fj, grid, args, s, true);
+  return launch((void*)fj, grid(p.columns * split), args, s, true);
 }
 
 }  // namespace llm
