@@ -701,6 +701,7 @@ __global__ void __launch_bounds__(QaShape<HD, NP, NC>::NT, QaShape<HD, NP, NC>::
       }
     }
   }
+  if constexpr (SH == 1) fence_proxy_async_smem();  // the counts, written and read above, come before the copies that fill the ring
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
     s_slot = lo;
     s_at = before[lo] * a.c.kv;
   }
+  fence_proxy_async_smem();  // the counts, written and read here, come before the copies that fill the rings
   __syncthreads();
 
   bool ok = true;  // a wait that gave up: no further waits, but every loop is still walked to its end

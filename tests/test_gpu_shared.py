@@ -407,3 +407,27 @@ def test_nan_beside_many_columns(dtype):
         c.attend_shared(q, i32([592] * B), i32([0, B]), i32([590]), out, c.workspace_shared(g, B, 1, 1), table=table)
         wrong = ~torch.isfinite(out)
         assert wrong[31, 0, 5].all() and int(wrong.sum()) == hd
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("G", [1, 1000])
+def test_calls_of_many_units(G, dtype):
+    # thousands of units, whose counts lie where the first tiles go: one group (the kernel for many columns, the rows' own
+    # positions on that for few), and groups of four rows (the kernel for few); the same bits every time
+    rng = np.random.default_rng(18)
+    B, kv, g, hd, n = 4000, 2, 1, 64, 150
+    c, r = make(2, kv, 256, hd, garbage=5)
+    fill(c, r, rng, 256, np.arange(8).reshape(2, 4))
+    table = np.full((B, 4096), -1)
+    table[:, :3] = rng.integers(0, 8, (B, 3))
+    length = (n - np.arange(B) % 37).tolist()
+    groups, shared = np.linspace(0, B, G + 1).astype(int).tolist(), (100 + np.arange(G) % 29).tolist()
+    q, qn = rows_of(rng, (B, 1, kv * g, hd), dtype)
+    ws, outs = c.workspace_shared(g, B, 1, G), []
+    for i in range(8):
+        outs.append(torch.full_like(q, 9.0))
+        c.attend_shared(q, i32(length), i32(groups), i32(shared), outs[i], ws, table=i32(table))
+        ws.fill_(255 if i % 2 else 0)
+    want, mag, sens, _ = shared_ref.attend_shared(r, qn, length, groups, shared, None, table[:, :3])
+    assert (np.abs(outs[0].double().cpu().numpy() - want) <= tolerance(dtype, hd, want, mag, sens)).all()
+    assert all(torch.equal(x, outs[0]) for x in outs)
