@@ -594,7 +594,8 @@ __global__ void __launch_bounds__(kShThreads, 1)
                 ref = to;
                 l *= corr;
                 vref = vto;
-                // the weights of the steps before
+                // the weights of the steps before, once they are there
+                if (h > 0) tc_wait_st();
 #pragma unroll 1
                 for (int c = 0; c < h * SB * WP; ++c) {
                   const uint32_t at = t_s + 16 * (c / WP) + (c % WP < 2 ? 8 * (c % WP) : 64);

@@ -133,6 +133,28 @@ def test_scores_that_climb_and_fall_far(way, hd, g, B, S, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("way,hd,g,B,S", WAYS)
+def test_references_that_move_within_a_tile(way, hd, g, B, S, dtype):
+    # weights that rise by 2^26 with every block of 16 positions, eight times over, and start again: what was weighed a step before
+    # is rescaled before its product, and as the heaviest 32 positions of 128 are 0 it is the result; the same bits every time
+    r, n = rand(867), 1500
+    c = Case(way, hd, B, n)
+    k, v = torch.zeros(n, c.kv, hd, device="cuda"), 0.5 + 0.5 * r(n, c.kv, hd)
+    block = torch.arange(n, device="cuda") // 16 % 8
+    k[..., 0] = block[:, None].float()
+    k[..., 1] = torch.floor(r(n, c.kv) * 3)
+    v[block >= 6] = 0.0
+    c.put(k, v)
+    q = torch.zeros(B, S, c.kv * g, hd, device="cuda")
+    q[..., 0] = (26.0 + r(B, S, c.kv * g)) * LN2 * hd ** 0.5
+    q[..., 1] = LN2 * hd ** 0.5
+    q = q.to(DT[dtype])
+    c.check(q, g, dtype, 1400)
+    first = c.run(q, g, 1400)
+    assert all(torch.equal(c.run(q, g, 1400), first) for _ in range(8))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("way,hd,g,B,S", WAYS)
 def test_every_code_counts_at_its_value(way, hd, g, B, S, dtype):
     # all finite codes, subnormal ones among them, along the positions and dimensions
     n = 640
