@@ -898,6 +898,19 @@ llm_status run_step(llm_handle* h, int B, int mode, bool pass = false, int verif
   return LLM_OK;
 }
 
+// Host memory to the device in stream order, whatever memory it is read before this returns: a copy straight from
+// page-locked memory reads it when the stream gets there.  From ordinary memory copies of up to 64 KB are read at once and
+// without waiting for the stream (larger ones wait), so the bytes go through some of that, piece by piece.
+llm_status upload(llm_handle* h, void* dst, const void* src, size_t bytes) {
+  unsigned char piece[16384];
+  for (size_t at = 0; at < bytes; at += sizeof piece) {
+    const size_t n = std::min(bytes - at, sizeof piece);
+    memcpy(piece, static_cast<const unsigned char*>(src) + at, n);
+    CUDA_TRY(h, cudaMemcpyAsync(static_cast<unsigned char*>(dst) + at, piece, n, cudaMemcpyHostToDevice, h->stream));
+  }
+  return LLM_OK;
+}
+
 // the step prologue; rows at their own positions when pos_host is given (copied to pos_buf)
 llm_status begin(llm_handle* h, int pos, int B, const int32_t* tok_host, const int32_t* tok_dev, int tok_stride,
                  int tok_col, float temp, int k, float p, const float* u_host, const float* u_dev,
@@ -2027,7 +2040,7 @@ llm_status llm_copy_pages(llm_handle* h, const int32_t* moves_host, int32_t m) {
   const int32_t most = (int32_t)std::max<int64_t>(1, pool / 2);
   for (int32_t i = 0; i < m; i += most) {
     a.m = std::min(m - i, most);
-    CUDA_TRY(h, cudaMemcpyAsync(h->page_table, moves_host + 2 * (size_t)i, (size_t)a.m * 8, cudaMemcpyHostToDevice, h->stream));
+    TRY(upload(h, h->page_table, moves_host + 2 * (size_t)i, (size_t)a.m * 8));
     for (int l0 = 0; l0 < h->L; l0 += kCopyLayers) {
       a.layers = std::min(h->L - l0, kCopyLayers);
       for (int l = 0; l < a.layers; ++l) {

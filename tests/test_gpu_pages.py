@@ -313,3 +313,32 @@ def test_every_page_of_a_handle_can_be_moved_at_once():
         m.copy_pages([[0, 1]])
     assert e.value.status == pkg.LLM_ERR_CONFIG
     m.close()
+
+
+@pytest.mark.parametrize("pinned", [False, True])
+def test_moves_are_read_before_the_call_returns(pinned):
+    # the handle's stream is busy when pages are copied, and the array is used again at once, from ordinary memory and from
+    # memory that the device reads by itself; few moves, and more than one transfer takes
+    w = WORKLOADS["tiny_f32"]
+    s = w.shape
+    for rows, seq, moves, later in ((2, 192, [[0, 5], [0, 1], [4, 2], [0, 3]], [[4, 5], [4, 1], [0, 2], [4, 3]]),
+                                    (8, 1 << 16, [[3, p] for p in range(8192) if p not in (3, 4)], [[4, p] for p in range(8192) if p not in (3, 4)])):
+        m = pkg.Model(s, synth.model_blob(s, w.seed_weights), max_batch=rows, max_seq=seq)
+        per = seq // 64
+        k = np.random.default_rng(4).standard_normal((s.layers, s.kv, min(seq, 320), s.hd)).astype(np.float32)
+        for l in range(s.layers):
+            for r in range(2 if rows == 2 else 1):
+                m.kv_import(l, r, 0, k[l] * (1 + r), -k[l])
+        page = lambda l, p: k[l, :, p % per * 64:p % per * 64 + 64] * (1 + p // per)  # noqa: E731
+        host = torch.tensor(moves, dtype=torch.int32)
+        host = host.pin_memory() if pinned else host
+        with torch.cuda.stream(torch.cuda.ExternalStream(pkg.llm_stream(m.h))):
+            torch.cuda._sleep(200_000_000)
+        pkg.llm_copy_pages(m.h, host, len(moves))
+        host.copy_(torch.tensor(later, dtype=torch.int32))
+        m.synchronize()
+        for l in range(s.layers):
+            for a, b in moves[:2] + moves[-2:] + moves[len(moves) // 3::1000]:
+                got = m.kv_export(l, b // per, b % per * 64, 64)
+                assert np.array_equal(got[0], page(l, a)), (a, b)
+        m.close()
