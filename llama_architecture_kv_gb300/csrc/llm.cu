@@ -902,7 +902,7 @@ llm_status run_step(llm_handle* h, int B, int mode, bool pass = false, int verif
 // page-locked memory reads it when the stream gets there.  From ordinary memory copies of up to 64 KB are read at once and
 // without waiting for the stream (larger ones wait), so the bytes go through some of that, piece by piece.
 llm_status upload(llm_handle* h, void* dst, const void* src, size_t bytes) {
-  unsigned char piece[16384];
+  unsigned char piece[49152];
   for (size_t at = 0; at < bytes; at += sizeof piece) {
     const size_t n = std::min(bytes - at, sizeof piece);
     memcpy(piece, static_cast<const unsigned char*>(src) + at, n);
@@ -924,7 +924,7 @@ llm_status begin(llm_handle* h, int pos, int B, const int32_t* tok_host, const i
     if (B <= kInline) {
       for (int b = 0; b < B; ++b) a.pos_inline[b] = pos_host[b];
     } else {
-      CUDA_TRY(h, cudaMemcpyAsync(h->pos_buf, pos_host, (size_t)B * 4, cudaMemcpyHostToDevice, h->stream));
+      TRY(upload(h, h->pos_buf, pos_host, (size_t)B * 4));
       a.pos_dev = h->pos_buf;
     }
   }
@@ -1564,7 +1564,7 @@ static llm_status paged_impl(llm_handle* h, const int32_t* tok_host, const int32
   if (u_host && temp > 0.0f)
     for (int b = 0; b < B; ++b)
       if (!(u_host[b] >= 0.0f && u_host[b] < 1.0f)) return fail(h, LLM_ERR_ARG, "u[%d] outside [0, 1)", b);
-  CUDA_TRY(h, cudaMemcpyAsync(h->page_table, table, (size_t)B * pages_per_row * 4, cudaMemcpyHostToDevice, h->stream));
+  TRY(upload(h, h->page_table, table, (size_t)B * pages_per_row * 4));
   TRY(begin(h, 0, B, tok_host, tok_dev, 1, 0, temp, k, p, u_host, u_dev, pos, h->page_table, pages_per_row));
   TRY(run_step(h, B, mode));
   if (host) {

@@ -128,3 +128,39 @@ def test_paged_errors():
         h.decode_paged(toks, np.zeros(3, np.int32), np.zeros((3, 1), np.int32))
     assert e.value.status == pkg.LLM_ERR_CONFIG
     h.close()
+
+
+@pytest.mark.parametrize("pinned", [False, True])
+def test_positions_and_tables_are_read_before_a_call_returns(pinned):
+    # the handle's stream is busy, and the arrays are used again at once: from ordinary memory, and from page-locked memory, which
+    # the device could read by itself later; more rows than travel with the step's arguments
+    torch = pytest.importorskip("torch")
+    shape, B, cap, P = CASES[0][1], 65, 128, 100
+    g = pkg.Model(shape, synth.model_blob(shape, 541), max_batch=B, max_seq=cap)
+    toks = synth.tokens(542, 0, B * P, shape.vocab).reshape(B, P)
+    g.prefill(toks, 0, logits=False)
+    tok = torch.from_numpy(toks[:, 7].copy()).cuda()
+    place = (lambda x: torch.tensor(x, dtype=torch.int32).pin_memory()) if pinned else (lambda x: torch.tensor(x, dtype=torch.int32))
+    pos, other = [P - 1 - b for b in range(B)], [b for b in range(B)]
+    table, wrong = [[2 * b, 2 * b + 1] for b in range(B)], [[2 * (B - 1 - b), 2 * (B - 1 - b) + 1] for b in range(B)]
+    out = torch.empty(B, shape.vocab, device="cuda")
+    ids = torch.empty(B, dtype=torch.int32, device="cuda")
+    calls = [lambda p, t: pkg.llm_decode_rows_dev(g.h, tok, B, p, out), lambda p, t: pkg.llm_step_rows_dev(g.h, tok, B, p, 0.0, 1, 1.0, None, ids, out),
+             lambda p, t: pkg.llm_decode_paged_dev(g.h, tok, B, p, t, 2, out),
+             lambda p, t: pkg.llm_step_paged_dev(g.h, tok, B, p, t, 2, 0.0, 1, 1.0, None, ids, out)]
+    for call in calls:
+        got = []
+        for busy in (False, True):
+            p, t = place(pos), place(table)
+            g.prefill(toks, 0, logits=False)
+            if busy:
+                with torch.cuda.stream(torch.cuda.ExternalStream(pkg.llm_stream(g.h))):
+                    torch.cuda._sleep(200_000_000)
+            call(p, t)
+            if busy:
+                p.copy_(torch.tensor(other, dtype=torch.int32))
+                t.copy_(torch.tensor(wrong, dtype=torch.int32))
+            g.synchronize()
+            got.append(out.clone())
+        assert torch.equal(*got)
+    g.close()

@@ -322,7 +322,7 @@ def test_moves_are_read_before_the_call_returns(pinned):
     w = WORKLOADS["tiny_f32"]
     s = w.shape
     for rows, seq, moves, later in ((2, 192, [[0, 5], [0, 1], [4, 2], [0, 3]], [[4, 5], [4, 1], [0, 2], [4, 3]]),
-                                    (8, 1 << 16, [[3, p] for p in range(8192) if p not in (3, 4)], [[4, p] for p in range(8192) if p not in (3, 4)])):
+                                    (16, 1 << 16, [[3, p] for p in range(1 << 14) if p not in (3, 4)], [[4, p] for p in range(1 << 14) if p not in (3, 4)])):
         m = pkg.Model(s, synth.model_blob(s, w.seed_weights), max_batch=rows, max_seq=seq)
         per = seq // 64
         k = np.random.default_rng(4).standard_normal((s.layers, s.kv, min(seq, 320), s.hd)).astype(np.float32)
