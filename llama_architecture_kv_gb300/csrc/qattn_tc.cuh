@@ -229,11 +229,18 @@ LLM_D QaUnit sh_unit(const QAttnArgs& a, int s, bool sharing) {
     u.start = u.last = 0;
     if ((x.sides & 1) && sh > 0 && (x.rpt == 1 || (b - lead) % x.rpt == 0)) {
       u.last = sh;
-      if constexpr (EXACT) {  // (no further than any of the rows sees)
+      if constexpr (EXACT) {  // (no further than any of the unit's tokens sees)
         int most = 0;
 #pragma unroll 8
-        for (int i = 0; i < rows; ++i) most = max(most, sh_end(a, b + i, q_count(a.r, b + i) - 1));
+        for (int i = 0; i < rows; ++i) {
+          const int n = min(q_count(a.r, b + i), x.cpr > 1 ? c * x.tpt + u.ntok : a.r.S);
+          most = max(most, n > c * x.tpt ? sh_end(a, b + i, n - 1) : 0);
+        }
         u.last = min(sh, most);
+      } else if (a.r.count) {  // (nothing, where none of its tokens is there)
+        bool any = false;
+        for (int i = 0; i < rows && !any; ++i) any = q_count(a.r, b + i) > c * x.tpt;
+        if (!any) u.last = 0;
       }
       u.nt = (u.last + TN - 1) / TN;
     }

@@ -431,3 +431,34 @@ def test_calls_of_many_units(G, dtype):
     want, mag, sens, _ = shared_ref.attend_shared(r, qn, length, groups, shared, None, table[:, :3])
     assert (np.abs(outs[0].double().cpu().numpy() - want) <= tolerance(dtype, hd, want, mag, sens)).all()
     assert all(torch.equal(x, outs[0]) for x in outs)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hd,g,S", [(32, 2, 1), (64, 1, 3), (128, 4, 1), (128, 8, 33), (64, 4, 128)])
+def test_rows_without_tokens_have_no_pages(hd, g, S, dtype):
+    # rows that take no part in a call, whole groups of them and single ones, whose tables were never set: nothing of theirs is
+    # looked at or reported, and their outputs stay; a group's first row holds its pages with or without tokens of its own.  128
+    # tokens of 4 heads: the kernel for many columns
+    rng = np.random.default_rng(hd + S)
+    rows, kv, B = 6, 2, 8
+    c, r = make(rows, kv, 256, hd, garbage=8)
+    table = np.zeros((B, 4), np.int32)
+    table[[0, 3, 6]] = pages(rng, 3, 256, rows)
+    fill(c, r, rng, 256, table[[0, 3, 6]])
+    for b, lead in ((1, 0), (2, 0), (4, 3), (5, 3), (7, 6)):
+        table[b] = table[lead]
+    length, groups, shared = [250, 249, 170, 200, 190, 180, 256, 140], [0, 3, 6, 8], [129, 100, 64]
+    q, qn = rows_of(rng, (B, S, kv * g, hd), dtype)
+    ws = c.workspace_shared(g, B, S, 3)
+    for count in ([S, 0, 1, 0, 0, 0, 0, S], [0, 0, S, 0, 0, 0, (S + 1) // 2, 0], [0] * B):
+        view = table.copy()
+        for b in range(B):
+            i = max(x for x in range(3) if groups[x] <= b)
+            if count[b] == 0 and (b != groups[i] or not any(count[groups[i]:groups[i + 1]])):
+                view[b] = -1 if b % 2 else 1 << 30
+        want, mag, sens, _ = shared_ref.attend_shared(r, qn, length, groups, shared, count, table, out=np.full(q.shape, 9.0))
+        for t in (view, wide_table(r, B, view)):
+            out, st = torch.full_like(q, 9.0), torch.zeros(1, dtype=torch.int32, device="cuda")
+            c.attend_shared(q, i32(length), i32(groups), i32(shared), out, ws, count=i32(count), table=i32(t), status=st)
+            assert int(st) == 0
+            assert (np.abs(out.double().cpu().numpy() - want) <= tolerance(dtype, hd, want, mag, sens)).all()
