@@ -496,8 +496,9 @@ llm_status llm_qcache_attend(const llm_qcache* cache, const void* q_dev, int32_t
  * The same attention for rows that share places: rows groups_dev[i] .. groups_dev[i + 1] - 1 of the call take
  * their positions below shared_dev[i] from the places of the group's first row (its pages, or its cache row),
  * whatever their own tables say there, and the others from their own.  Each group's shared positions are read
- * once for all its rows (heads of 64 and 128, where the rows can hold enough positions for that to pay; else row by row; the
- * two differ in roundings).  A query is held to 2^-16 of each element (bf16: exactly, elements below 2^-9 of the largest
+ * once for all its rows (heads of 64 and 128, where the rows can hold enough positions for that to pay and B x ceil(S /
+ * floor(32 / group)) is at most 4096; else row by row; the two differ in roundings).  (B * S * kv_heads * (positions a row can
+ * hold / 128 + 2) below 2^31 always fits one call, else LLM_ERR_ARG.)  A query is held to 2^-16 of each element (bf16: exactly, elements below 2^-9 of the largest
  * to 2^-17 of that), a weight as above.  groups_dev [groups + 1]
  * ascends from 0 to B (a group may be empty) and shared_dev [groups] is 0 .. the positions a row can hold:
  * else LLM_ERR_ARG or LLM_ERR_POS_RANGE is stored, and no row (of the group) shares anything.  What a token sees

@@ -197,18 +197,17 @@ llm_status llm_qcache_attend_shared(const llm_qcache* cache, const void* q_dev, 
          "the groups' bounds and shared positions must be given, as aligned int32 arrays");
   int sms = 0;
   TRY(device_sms(&sms));
-  REFUSE(!(qattn_uses_tc(a.c.hd) ? qshare_fits(a.c, group, dtype, B, S, groups, a.r.limit)
-                                 : qattn_fits(a.c, group, dtype, B, S, a.r.limit, sms)), LLM_ERR_ARG,
-         "too large for one call: rows x tokens / (32 / group) at most 4096, these x kv heads x 64-position tiles below 2^30, "
-         "and the outputs' elements below 2^31");
+  a.g = group; a.ngroups = groups;
+  REFUSE(qattn_shared_way(a, dtype, sms) == kSharedTooLarge, LLM_ERR_ARG,
+         "too large for one call: rows x tokens x kv heads x 128-position tiles must stay below 2^31");
   const uint64_t need = qattn_shared_workspace(a.c, group, B, S, sms);
   if (need > 0) {
     REFUSE(!workspace_dev || workspace_bytes < need, LLM_ERR_ARG, "workspace smaller than llm_qcache_shared_workspace says");
     REFUSE(!aligned16(workspace_dev), LLM_ERR_ARG, "the workspace must be aligned to 16 bytes");
   }
-  a.q = q_dev; a.out = out_dev; a.q_stride = q_stride; a.out_stride = out_stride; a.g = group; a.scale = scale;
+  a.q = q_dev; a.out = out_dev; a.q_stride = q_stride; a.out_stride = out_stride; a.scale = scale;
   a.ws = (unsigned char*)workspace_dev;
-  a.groups = groups_dev; a.shared = shared_dev; a.ngroups = groups;
+  a.groups = groups_dev; a.shared = shared_dev;
   return launched(launch_qattn_shared(a, dtype, sms, (cudaStream_t)cuda_stream));
 }
 

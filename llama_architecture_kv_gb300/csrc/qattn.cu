@@ -371,9 +371,9 @@ uint64_t qattn_step_workspace(const QCacheView& c, int g, int NT, int num_sms) {
   return most;
 }
 
-// Whether rows that share positions are attended one by one (QAttnArgs::groups): where every row is a group, or they can
-// hold so few tiles of positions per SM that reading the shared ones once, with the two to four kernels that it takes, saves
-// nothing.  Row by row, and shared: 4 rows of about 1000 positions (2 tiles per SM) 16 and 18 us, 16 of 2176 (14) 25 and 39, 24 of
+// Rows that share positions are attended one by one (QAttnArgs::groups) where a call has more units than are counted, where
+// there are as many groups as rows, or where the rows can hold so few tiles of positions per SM that reading the shared ones
+// once, with the two to four kernels that it takes, saves nothing.  Row by row, and shared: 4 rows of about 1000 positions (2 tiles per SM) 16 and 18 us, 16 of 2176 (14) 25 and 39, 24 of
 // 5300 in 3 groups (26) 41 and 39, 16 with 5 tokens of 4400 (29) 60 and 70, 2 of 65536 (54) 47 and 43, 32 of 8400 (111) 88 and 54.
 constexpr int kByTiles = 32;
 static __global__ void q_clear_tickets_kernel(uint4* tickets) {
@@ -381,11 +381,16 @@ static __global__ void q_clear_tickets_kernel(uint4* tickets) {
   static_assert(kQattnTickets == 256 * 16, "a thread's tickets");
   tickets[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
 }
-static bool q_by_rows(const QAttnArgs& a, int qt, int num_sms) {
-  if (!qattn_fits(a.c, a.g, qt, a.r.B, a.r.S, std::min<int64_t>((int64_t)a.r.limit + 2 * kQaTile, 0x7fffffff), num_sms)) return false;
-  const TcPlanQ p = plan_tc_q(a.c, a.g, qt, a.r.B, a.r.S, a.r.limit, num_sms);
-  const int64_t tiles = (int64_t)a.r.B * (((int64_t)a.r.S + p.tokens - 1) / p.tokens) * a.c.kv * q_tiles_of(a.r.limit);
-  return a.ngroups == a.r.B || tiles <= (int64_t)num_sms * kByTiles;
+QSharedWay qattn_shared_way(const QAttnArgs& a, int qt, int num_sms) {
+  const int B = a.r.B, S = a.r.S;
+  // (a row by itself has up to two tiles more)
+  const bool rows = qattn_fits(a.c, a.g, qt, B, S, std::min<int64_t>((int64_t)a.r.limit + 2 * kQaTile, 0x7fffffff), num_sms);
+  if (!qattn_uses_tc(a.c.hd)) return rows ? kSharedByRows : kSharedTooLarge;
+  const bool once = qshare_fits(a.c, a.g, qt, B, S, a.ngroups, a.r.limit);
+  if (!rows || !once) return rows ? kSharedByRows : once ? kSharedOnce : kSharedTooLarge;
+  const TcPlanQ p = plan_tc_q(a.c, a.g, qt, B, S, a.r.limit, num_sms);
+  const int64_t tiles = (int64_t)B * (((int64_t)S + p.tokens - 1) / p.tokens) * a.c.kv * q_tiles_of(a.r.limit);
+  return a.ngroups == B || tiles <= (int64_t)num_sms * kByTiles ? kSharedByRows : kSharedOnce;
 }
 
 cudaError_t launch_qattn(const QAttnArgs& a0, int qt, int num_sms, cudaStream_t s, bool pdl, const CUtensorMap* kmap,
@@ -427,7 +432,7 @@ uint64_t qattn_shared_workspace(const QCacheView& c, int g, int B, int S, int nu
 
 cudaError_t launch_qattn_shared(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s) {
   if (qattn_uses_tc(a.c.hd)) {
-    if (!q_by_rows(a, qt, num_sms)) return launch_qshare_all(a, qt, num_sms, s);
+    if (qattn_shared_way(a, qt, num_sms) == kSharedOnce) return launch_qshare_all(a, qt, num_sms, s);
     // (the workspace may hold anything; 1 us)
     q_clear_tickets_kernel<<<1, 256, 0, s>>>(reinterpret_cast<uint4*>(a.ws));
     const cudaError_t e = cudaGetLastError();

@@ -462,3 +462,39 @@ def test_rows_without_tokens_have_no_pages(hd, g, S, dtype):
             c.attend_shared(q, i32(length), i32(groups), i32(shared), out, ws, count=i32(count), table=i32(t), status=st)
             assert int(st) == 0
             assert (np.abs(out.double().cpu().numpy() - want) <= tolerance(dtype, hd, want, mag, sens)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hd,g,B,S,per", [(64, 1, 4096, 1, 160), (64, 1, 4097, 1, 160), (128, 1, 4500, 1, 3), (64, 16, 4, 2048, 512), (64, 16, 4, 2050, 512)])
+def test_both_sides_of_the_most_units(hd, g, B, S, per, dtype):
+    # up to 4096 units a side the shared positions can be read once; calls of more go row by row, as the ordinary attention takes them
+    rng = np.random.default_rng(B + S)
+    kv, n = 1, 140
+    c, r = make(2, kv, 320, hd, garbage=5)
+    fill(c, r, rng, 320, np.arange(10).reshape(2, 5))
+    table = np.full((B, per), -1)
+    table[:, :3] = rng.integers(0, 10, (B, 3))
+    length, G = (n - np.arange(B) % 37).tolist(), min(B, 9) // 3
+    groups, shared = np.linspace(0, B, G + 1).astype(int).tolist(), (60 + np.arange(G) * 5).tolist()
+    count = None if S == 1 else [S, 1, 3, 2][:B]
+    if S > 1:
+        length = [140, 120, 133, 64]
+    q, qn = rows_of(rng, (B, S, kv * g, hd), dtype)
+    out, st = torch.full_like(q, 9.0), torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.attend_shared(q, i32(length), i32(groups), i32(shared), out, c.workspace_shared(g, B, S, G), table=i32(table), status=st,
+                    count=None if count is None else i32(count))
+    assert int(st) == 0
+    want, mag, sens, _ = shared_ref.attend_shared(r, qn, length, groups, shared, count, table[:, :3], out=np.full(q.shape, 9.0))
+    assert (np.abs(out.double().cpu().numpy() - want) <= tolerance(dtype, hd, want, mag, sens)).all()
+
+
+def test_a_call_that_no_way_takes_is_refused():
+    c = pkg.QCache.empty(1, 8, 64, 64)
+    q = torch.zeros(1, 1, 8, 64, device="cuda").expand(4096, 1, 8, 64)
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda").expand(4096, 1 << 16)
+    lib, P = pkg.lib(), q.data_ptr()          # (refused on the host: nothing is read)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    for B, S, G in ((1 << 20, 1 << 10, 1), (1 << 20, 1 << 10, 1 << 20)):
+        st = lib.llm_qcache_attend_shared(c._c, P, 0, 512, 1, B, S, P, None, table.data_ptr(), 1 << 16, P, P, G, 0.1, P, 512, ws.data_ptr(),
+                                          1 << 60, None, None)
+        assert st == pkg.LLM_ERR_ARG and b"too large" in lib.llm_last_error(None)
