@@ -505,7 +505,8 @@ llm_status llm_qcache_attend(const llm_qcache* cache, const void* q_dev, int32_t
  * goes by its row's length as above: a row shorter than what its group shares sees that much of it.  With rows whose
  * tables name the same pages for what they share this is llm_qcache_attend, but for roundings.  groups is
  * 1..B.  The workspace is as large as llm_qcache_shared_workspace says, for the same cache, group, B, S and
- * groups; it need not be cleared.  Calls that overlap on the GPU need workspaces of their own.
+ * groups; it need not be cleared, and calls leave one that llm_qcache_attend can use (zero before its first use) ready for
+ * that.  Calls that overlap on the GPU need workspaces of their own.
  */
 llm_status llm_qcache_shared_workspace(const llm_qcache* cache, int32_t group, int32_t B, int32_t S, int32_t groups, uint64_t* bytes);
 llm_status llm_qcache_attend_shared(const llm_qcache* cache, const void* q_dev, int32_t dtype, int64_t q_stride,

@@ -225,7 +225,7 @@ bool qshare_fits(const QCacheView& c, int g, int qt, int B, int S, int ngroups, 
 
 uint64_t qshare_workspace(const QCacheView& c, int g, int B, int S, int num_sms) {
   const uint64_t columns = (uint64_t)B * S * c.kv * g;
-  return 4 * columns * (c.hd * 4 + 16) + columns * (4 * c.hd + 16) + (uint64_t)num_sms * (2 * kShRows + 2 * 32) * (c.hd * 4 + 8);
+  return kQattnTickets + 4 * columns * (c.hd * 4 + 16) + columns * (4 * c.hd + 16) + (uint64_t)num_sms * (2 * kShRows + 2 * 32) * (c.hd * 4 + 8);
 }
 
 namespace {
@@ -255,7 +255,7 @@ cudaError_t launch_qshare_all(const QAttnArgs& a0, int qt, int num_sms, cudaStre
   ShSide few = side_of(B, S, a.g, p.cols, p.many ? 2 : 3, 1), many = side_of(B, S, a.g, kShRows, 1, 2);
   few.ctas = few_ctas(p.cols, num_sms);
   many.ctas = num_sms;
-  unsigned char* w = a.ws;
+  unsigned char* w = a.ws + kQattnTickets;  // (the ordinary attention's tickets stay as they are)
   auto take = [&](uint64_t n) {
     unsigned char* at = w;
     w += n;

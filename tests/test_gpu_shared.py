@@ -498,3 +498,23 @@ def test_a_call_that_no_way_takes_is_refused():
         st = lib.llm_qcache_attend_shared(c._c, P, 0, 512, 1, B, S, P, None, table.data_ptr(), 1 << 16, P, P, G, 0.1, P, 512, ws.data_ptr(),
                                           1 << 60, None, None)
         assert st == pkg.LLM_ERR_ARG and b"too large" in lib.llm_last_error(None)
+
+
+@pytest.mark.parametrize("hd", [32, 64, 128])
+def test_a_zeroed_workspace_serves_both_attentions_by_turns(hd):
+    rng = np.random.default_rng(19)
+    B, kv, g, cap = 5, 2, 4, 640
+    c, r = make(B, kv, cap, hd, garbage=4)
+    fill(c, r, rng, 600)
+    table = i32(wide_table(r, B))
+    length, groups, shared = i32([600 - 7 * b for b in range(B)]), i32([0, 2, B]), i32([300, 500])
+    q, _ = rows_of(rng, (B, 8, kv * g, hd), "bf16")
+    ws = torch.zeros(max(c.workspace(g, B, 8).numel(), c.workspace_shared(g, B, 8, 2).numel()), dtype=torch.uint8, device="cuda")
+    want, out, other = (torch.empty_like(q) for _ in range(3))
+    c.attend(q, length, want, c.workspace(g, B, 8))
+    for t in (table, None, table, table):
+        c.attend_shared(q, length, groups, shared, other, ws, table=t)
+        for _ in range(2):
+            out.fill_(9.0)
+            c.attend(q, length, out, ws)
+            assert torch.equal(out, want)
