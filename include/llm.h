@@ -498,8 +498,10 @@ llm_status llm_qcache_attend(const llm_qcache* cache, const void* q_dev, int32_t
  * whatever their own tables say there, and the others from their own.  Each group's shared positions are read
  * once for all its rows (heads of 64 and 128, where the rows can hold enough positions for that to pay and B x ceil(S /
  * floor(32 / group)) is at most 4096; else row by row; the two differ in roundings).  (B * S * kv_heads * (positions a row can
- * hold / 128 + 2) below 2^31 always fits one call, else LLM_ERR_ARG.)  A query is held to 2^-16 of each element (bf16: exactly, elements below 2^-9 of the largest
- * to 2^-17 of that), a weight as above.  groups_dev [groups + 1]
+ * hold / 128 + 2) below 2^31 always fits one call, else LLM_ERR_ARG.)  An f32 query is held to 2^-19 of each element or 2^-27 of its largest, whichever is more (so beside an
+ * element 2^27 times larger it counts for nothing, whatever the keys are there); a bf16 query exactly, but for elements below 2^-9
+ * of the largest, which are held to 2^-17 of that.  Row by row, and behind few columns, they are held to 2^-32 (bf16: elements below
+ * 2^-14 to 2^-22) of the largest.  A weight is held as above.  groups_dev [groups + 1]
  * ascends from 0 to B (a group may be empty) and shared_dev [groups] is 0 .. the positions a row can hold:
  * else LLM_ERR_ARG or LLM_ERR_POS_RANGE is stored, and no row (of the group) shares anything.  What a token sees
  * goes by its row's length as above: a row shorter than what its group shares sees that much of it.  With rows whose

@@ -4,8 +4,9 @@
 // The codes go from HBM to shared memory by TMA, the keys' from there into e4m3 MMAs as they are.  The
 // f32 (bf16) queries that meet them enter as NP e4m3 pieces, x = 2^e (x_0 + x_1 / 32 + x_2 / 32^2 + ...)
 // with |x| / 2^e <= 256, each piece the rounding of what the ones before left over (at most half a step, 8
-// of 256, so 32 times it is in range again).  A piece takes four bits: four pieces leave 2^-16 of an element
-// at worst, or 2^-33 of the largest where it is tiny (f32); two hold a bf16 query's eight bits.  The pieces
+// of 256, so 32 times it is in range again).  A piece takes four bits and the next one's sign a
+// fifth: four pieces leave 2^-19 of an element at worst, or 2^-32 of the largest where it is tiny (f32); two hold a bf16 query's
+// eight bits, down to 2^-14 of the largest.  The pieces
 // are columns of their own, so every accumulator sums like with like in f32 and the powers of 32 are applied
 // once, in registers.  The values are widened to bf16 (exact) in shared memory, in the place of the tile's
 // keys and values: their softmax weights, as bf16 pieces, have the exponents of f32, so that a weight keeps its

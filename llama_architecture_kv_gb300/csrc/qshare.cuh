@@ -13,12 +13,14 @@
 // products go on top of those before.  The blocks' value scales ride on the weights, relative to a power of two that moves in the
 // same way.  O is read after RUN of a group's tiles (kQaRun says what longer runs lose) into sums in local memory.
 //
-// Pieces.  A query is scaled by a power of two to at most 256 and enters as e4m3 pieces, each the
-// rounding of what the ones before left over (made once for the call, qshare.cu): two (bf16: its eight bits, of elements down
-// to 2^-9 of the largest), summed in one accumulator; or four (f32), the last two 2^10 times larger in an accumulator of their
-// own, which leaves 2^-17 of an element and at most 2^-19 of the largest.  The softmax weights are bf16 pieces, two (bf16 queries:
-// 2^-17 of a weight, half of 2^-9 being the output's own rounding) or three (f32: 2^-26), over values widened to bf16,
-// exactly; bf16 has f32's exponents, so that a weight keeps its digits however small it is.
+// Pieces.  A query is scaled by a power of two so that its largest element is between 128 and 256, and enters as e4m3 pieces, each
+// the rounding of what the ones before left over (made once for the call, qshare.cu).  A piece takes four bits and the sign of what
+// is left a fifth, so two leave 2^-9 of an element's binade, or 2^-10, half the least step of e4m3.  bf16: two, summed in one accumulator,
+// which are an element's eight bits down to 2^-9 of the largest and leave 2^-17 of the largest of smaller ones.  f32: four, the last two
+// 2^10 times larger in an accumulator of their own, which leave 2^-19 of an element or 2^-20, 2^-27 of the largest.  (The kernel for few
+// columns has an accumulator a piece, each 2^5 times larger than the one before: 2^-32 of the largest.)  The softmax weights are
+// bf16 pieces, two (bf16 queries: 2^-17 of a weight, half of 2^-9 being the output's own rounding) or three (f32: 2^-26), over values
+// widened to bf16, exactly; bf16 has f32's exponents, so that a weight keeps its digits however small it is.
 //
 // One CTA per SM, 16 warps: warp 0 loads the tiles and queries by TMA; warps 1 and 3 issue the products; warp 2 walks the CTA's share of
 // the work (segments: runs of tiles of one unit) ahead of the others and tells them each segment; four warps widen values; two

@@ -153,6 +153,43 @@ def test_references_that_move_within_a_tile(way, hd, g, B, S, dtype):
     assert all(torch.equal(c.run(q, g, 1400), first) for _ in range(8))
 
 
+@pytest.mark.parametrize("dtype,up", [("f32", 12), ("f32", 16), ("f32", 20), ("bf16", 8), ("bf16", 10), ("bf16", 12)])
+@pytest.mark.parametrize("way,hd,g,B,S", WAYS)
+def test_an_element_far_above_the_others(way, hd, g, B, S, dtype, up):
+    # a query's first element is 2^up times the others, and the keys are 0 there: the others decide the scores.  An element is
+    # held to 2^-19 of itself (bf16: exactly) or, where pieces end, to a share of the largest, f << 1: f32 2^-27 with the shared
+    # positions read once for many columns, else 2^-32; bf16 2^-17 of elements below 2^-9 of it, else 2^-22 of those below 2^-14.
+    # Products are summed in f32: (hd + 32) 2^-24 of the sum of magnitudes.  Scores off by ds move a weight and the sum of weights by
+    # exp(ds) - 1 each, together exp(2 ds) - 1; the rest as in Case.check.
+    r, n = rand(868), 700
+    c = Case(way, hd, B, n)
+    k, v = 2.0 * r(n, c.kv, hd) - 1.0, 2.0 * r(n, c.kv, hd) - 1.0
+    k[..., 0] = 0.0
+    c.put(k, v)
+    q = 2.0 * r(B, S, c.kv * g, hd) - 1.0
+    q[..., 0] = 2.0 ** up * (1.0 + r(B, S, c.kv * g))
+    q = q.to(DT[dtype])
+    out, scale = c.run(q, g, 600), hd ** -0.5
+    many = way == "many"
+    for i in range(S):
+        end = n - S + i + 1
+        for j in range(c.kv):
+            x = q[:, i, j * g:(j + 1) * g].double().flatten(0, 1)
+            top = x.abs().amax(-1, keepdim=True)
+            if dtype == "f32":
+                dq = torch.maximum(2.0 ** -19 * x.abs(), (2.0 ** -27 if many else 2.0 ** -32) * top)
+            else:
+                dq = torch.where(x.abs() < (2.0 ** -9 if many else 2.0 ** -14) * top, (2.0 ** -17 if many else 2.0 ** -22) * top, 0 * top)
+            kk, vv = c.k[:end, j], c.v[:end, j]
+            w = torch.softmax(scale * (x @ kk.T), -1)
+            want, mag = w @ vv, w @ vv.abs()
+            ds = scale * (dq @ kk.abs().T + (hd + 32) * 2.0 ** -24 * (x.abs() @ kk.abs().T)).amax(-1, keepdim=True)
+            tol = mag * (torch.expm1(2 * ds) + (2.0 ** -26 if dtype == "f32" else 2.0 ** -17) + 2.0 ** -21 + 2.0 ** -19)
+            tol = tol + (want.abs() * 2.0 ** -8 if dtype == "bf16" else 0)
+            err = (out[:, i, j * g:(j + 1) * g].double().flatten(0, 1) - want).abs()
+            assert (err <= tol).all(), f"token {i} head {j}: {float((err / tol).max()):.3g} of the bound"
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("way,hd,g,B,S", WAYS)
 def test_every_code_counts_at_its_value(way, hd, g, B, S, dtype):
