@@ -495,10 +495,14 @@ llm_status llm_qcache_attend(const llm_qcache* cache, const void* q_dev, int32_t
 /*
  * The same attention for rows that share places: rows groups_dev[i] .. groups_dev[i + 1] - 1 of the call take
  * their positions below shared_dev[i] from the places of the group's first row (its pages, or its cache row),
- * whatever their own tables say there, and the others from their own.  Each group's shared positions are read
- * once for all its rows (heads of 64 and 128, where the rows can hold enough positions for that to pay and B x ceil(S /
- * floor(32 / group)) is at most 4096; else row by row; the two differ in roundings).  (B * S * kv_heads * (positions a row can
- * hold / 128 + 2) below 2^31 always fits one call, else LLM_ERR_ARG.)  An f32 query is held to 2^-19 of each element or 2^-27 of its largest, whichever is more (so beside an
+ * whatever their own tables say there, and the others from their own.  How a call goes is chosen from what the host
+ * knows: B, S, groups and the positions a row can hold.  Row by row, every row reading all that it sees as in llm_qcache_attend: heads of
+ * 16, 32 and 256; groups equal to B; rows that can hold at most 32 tiles of 128 positions per SM in all; and B x ceil(S /
+ * floor(32 / group)) above 4096.  Otherwise a group's shared positions are read once for up to 128 of its (token, head of a key/value head)
+ * pairs, if B * S * group / groups, what a group has on average, is above 100 (bf16: 40), or else once for as many as that, at most 32.
+ * So name as many groups as there are: empty ones lower the average, and with groups equal to B nothing is read once.  The
+ * ways differ in roundings.  (B * S * kv_heads * (positions a row can hold / 128 + 2) below 2^31 always fits one call, else
+ * LLM_ERR_ARG.)  An f32 query is held to 2^-19 of each element or 2^-27 of its largest, whichever is more (so beside an
  * element 2^27 times larger it counts for nothing, whatever the keys are there); a bf16 query exactly, but for elements below 2^-9
  * of the largest, which are held to 2^-17 of that.  Row by row, and behind few columns, they are held to 2^-32 (bf16: elements below
  * 2^-14 to 2^-22) of the largest.  A weight is held as above.  groups_dev [groups + 1]

@@ -530,8 +530,8 @@ class QCache:
     def attend_shared(self, q, length, groups, shared, out, workspace, count=None, table=None, scale=None, status=None,
                       stream=None):
         """attend() for rows that share places: rows groups[i] .. groups[i + 1] - 1 take their positions below
-        shared[i] from the places of the group's first row, which are read once for all of them where that pays
-        (llm_qcache_attend_shared).  groups [G + 1] and shared [G] are int32 CUDA tensors."""
+        shared[i] from the places of the group's first row, which are read once for many of them where that pays by B, S, the
+        number of groups and the table's width (llm_qcache_attend_shared; with as many groups as rows it is not).  groups [G + 1] and shared [G] are int32 CUDA tensors."""
         B, S = q.shape[:2]
         per = self.kv * self.hd
         n = q.numel()

@@ -518,3 +518,19 @@ def test_a_zeroed_workspace_serves_both_attentions_by_turns(hd):
             out.fill_(9.0)
             c.attend(q, length, out, ws)
             assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hd,g,S", [(64, 2, 1), (128, 4, 1), (128, 4, 4)])
+def test_uneven_groups_and_empty_ones(hd, g, S, dtype):
+    # as many groups as rows, most of them empty (all rows in the first, in the last, in one between); one group of most rows beside single
+    # ones; more empty groups than others
+    rng = np.random.default_rng(20)
+    kv, B = 2, 40
+    c, r = make(B, kv, 256, hd, garbage=6)
+    fill(c, r, rng, 250)
+    length = [250 - 3 * (b % 7) for b in range(B)]
+    for groups, shared in (([0] + [B] * B, [200] + [70] * (B - 1)), ([0] * B + [B], [70] * (B - 1) + [200]),
+                           ([0] * 11 + [B] * (B - 10), [70] * 10 + [200] + [70] * (B - 11)),
+                           ([0, 31] + list(range(32, B + 1)), [200] + [129] * (B - 31)), ([0, 0, 0, 3, 3, 3, 39, 39, 39, 40], [1, 2, 130, 3, 4, 200, 5, 6, 60])):
+        check(c, r, rng, S, g, dtype, length, groups, shared)
