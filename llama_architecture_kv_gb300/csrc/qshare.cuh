@@ -78,7 +78,7 @@ struct ShSeg {
   int place;         // the row whose places hold them
   int gt, used;      // first token, columns
   int j;             // key/value head
-  int part;          // 0, 1: the unit's first run, of a prefix or of a row's own; 2: a run that goes on
+  int part;          // as sh_put takes it: 0: the unit's first run, 2: a run that goes on
   int cta0, ctas;    // CTAs that hold the unit: the first, and how many come after it
 };
 
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
   }
   // ---- the units' tiles, counted by all threads; the unit that this CTA's run starts in ----
   const bool sharing = sh_fine(a);
-  const int slots = 2 * a.r.B * a.sh.cpr;
+  const int slots = a.r.B * a.sh.cpr;  // (prefix units alone: the rows' own positions are the other kernel's)
   int* before = reinterpret_cast<int*>(kring);  // [slots] (the rings are idle yet)
   int G = gridDim.x;
   {
@@ -262,8 +262,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
       for (int i = 0; i < kShRows / 32; ++i) lim[gs * kShRows + lane + 32 * i] = e[i];
       if (lane == 0) {
         const int first = at + j * u.nt, c0 = cut.owner(first);
-        segs[gs] = ShSeg{n, (u.tile0 + k0) * TN, u.start, last, u.b, (int)u.qrow, u.ntok * a.g, j, k0 > 0 ? 2 : s < a.r.B * a.sh.cpr ? 0 : 1, c0,
-                         cut.owner(first + u.nt - 1) - c0};
+        segs[gs] = ShSeg{n, (u.tile0 + k0) * TN, u.start, last, u.b, (int)u.qrow, u.ntok * a.g, j, k0 > 0 ? 2 : 0, c0, cut.owner(first + u.nt - 1) - c0};
       }
       __syncwarp();
       mbar_arrive(b_gf + 8u * gs);
