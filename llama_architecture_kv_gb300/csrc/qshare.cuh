@@ -47,6 +47,9 @@ constexpr int kShSegs = 8;           // segments told ahead
 constexpr int kShWarps = 16;         // loads, scores, walk, values' products; two softmax groups of four; four that widen
 constexpr int kShThreads = 32 * kShWarps;
 constexpr int kShWiden = 128;        // threads that widen
+// A wait's limit, about 4 s: all warps but that of the loads wait for data from when the CTA starts, and with that for the rest of the
+// kernel before, which may be a long one.  (A wait for that kernel alone in each warp took 3 to 9 us of the 269 above more.)
+constexpr uint64_t kShWaitCycles = 8 * kQaWaitCycles;
 constexpr float kShMost = 24.0f;     // log2 of the largest weight that moves no reference
 
 template <int HD, int QT>
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
 
   bool ok = true;  // a wait that gave up: no further waits, but every loop is still walked to its end
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (ok && !mbar_wait(bar, parity, kQaWaitCycles)) {
+    if (ok && !mbar_wait(bar, parity, kShWaitCycles)) {
       ok = false;
       q_report(a.r.status, kErrDeviceTimeout);
     }
@@ -407,7 +410,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
     }
     if (!ok) {  // (no product may be at work when the CTA exits)
       tc_commit_if(b_end, one);
-      mbar_wait(b_end, 0u, kQaWaitCycles);
+      mbar_wait(b_end, 0u, kShWaitCycles);
     }
   } else if (warp == 3) {
     // ---- the products of weights and values, from a warp of its own: in one, each kind's issue waits for the other's (131072
@@ -447,7 +450,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
     }
     if (!ok) {
       tc_commit_if(b_end2, one);
-      mbar_wait(b_end2, 0u, kQaWaitCycles);
+      mbar_wait(b_end2, 0u, kShWaitCycles);
     }
   } else if (warp < 12) {
     // ---- softmax: thread = column; the groups take the tiles in turn, each with scores, sums and references of its own ----
