@@ -539,7 +539,7 @@ llm_status llm_qcache_attend_shared(const llm_qcache* cache, const void* q_dev, 
  * moves_dev [m][2] receives the copies to make, from and to page, then -1 (llm_qcache_copy_pages and
  * llm_copy_pages make them; they can be made in any order): m is rows for an update and max(1, pages / 2) for compact.  counts_dev
  * [2] receives their number and the pages in use after them.
- * A parent, length or page out of range, or too few free pages, is stored in *status_dev where given
+ * A parent, length or page out of range (a row that is emptied has no length), or too few free pages, is stored in *status_dev where given
  * (LLM_ERR_ARG, LLM_ERR_POS_RANGE, LLM_ERR_OOM); *to then equals *from, there are no moves and counts_dev is 0, -1.
  * The workspace need not be cleared; calls that overlap on the GPU need their own.  cuda_stream as above;
  * the calls return without waiting, allocate nothing and may be captured.

@@ -29,8 +29,8 @@
 // run go to global memory, a part for each group, and another kernel joins each column's parts in CTA order, so the result does
 // not depend on timing.
 //
-// What bounds it (131072 positions, 64 rows of 32 heads of 128 behind them, bf16: 230 us of a call's 269, where the products alone would
-// take 71): a tile of 128 x 128 takes about 4100 clocks, its softmax 4800 in either group, of which the 32-score steps
+// What bounds it (131072 positions, 64 rows of 32 heads of 128 behind them, bf16: 230 us of a call's 269, for 85 of which the tensor pipe
+// is busy): a tile of 128 x 128 takes about 4100 clocks, its softmax 4800 in either group, of which the 32-score steps
 // take 1000 each (293 instructions for 32 scores; the schedulers issue 47% of the time), then 1400 for its product and 750 for
 // its next scores.  f32 queries: 3400 clocks a tile of 64 positions.  Slower: the value product's columns in halves, more registers for
 // the softmax warps (setmaxnreg), tiles of 64 with two score buffers a group (289 us).  The product's positions in halves, the

@@ -25,7 +25,7 @@
 //
 // What bounds it: for one row barriers of the cluster and the block, some thirty one after the other (15 us at 49152;
 // 29 with the places one after the other and every pass from global memory); for many rows a candidate's weight (some
-// 40 instructions; 56% of issue slots busy) and the histogram, whose three additions each serve the 32 banks' longest
+// 40 instructions; 48% of issue slots busy) and the histogram, whose three additions each serve the 32 banks' longest
 // queue (32 rows of 128256: 32 us, 86 before; 256 of 50257: 75, 249 before).
 #include <math.h>
 

@@ -193,7 +193,7 @@ LLM_D void tc_st4(uint32_t taddr, const float (&v)[4]) {
                "f"(v[3])
                : "memory");
 }
-// 32 lanes x 8 or 16 columns written
+// 32 lanes x 8 columns written
 LLM_D void tc_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
