@@ -174,7 +174,7 @@ llm_status llm_qcache_shared_workspace(const llm_qcache* cache, int32_t group, i
   int sms = 0;
   TRY(device_sms(&sms));
   const QCacheView c = {nullptr, nullptr, nullptr, nullptr, cache->rows, cache->kv_heads, cache->max_seq, cache->head};
-  *bytes = qattn_shared_workspace(c, group, B, S, sms);
+  *bytes = qattn_shared_workspace(c, group, B, S, groups, sms);
   return LLM_OK;
 }
 
@@ -200,7 +200,7 @@ llm_status llm_qcache_attend_shared(const llm_qcache* cache, const void* q_dev, 
   a.g = group; a.ngroups = groups;
   REFUSE(qattn_shared_way(a, dtype, sms) == kSharedTooLarge, LLM_ERR_ARG,
          "too large for one call: rows x tokens x kv heads x 128-position tiles must stay below 2^31");
-  const uint64_t need = qattn_shared_workspace(a.c, group, B, S, sms);
+  const uint64_t need = qattn_shared_workspace(a.c, group, B, S, groups, sms);
   if (need > 0) {
     REFUSE(!workspace_dev || workspace_bytes < need, LLM_ERR_ARG, "workspace smaller than llm_qcache_shared_workspace says");
     REFUSE(!aligned16(workspace_dev), LLM_ERR_ARG, "the workspace must be aligned to 16 bytes");

@@ -387,7 +387,7 @@ QSharedWay qattn_shared_way(const QAttnArgs& a, int qt, int num_sms) {
   const bool rows = qattn_fits(a.c, a.g, qt, B, S, std::min<int64_t>((int64_t)a.r.limit + 2 * kQaTile, 0x7fffffff), num_sms);
   if (!qattn_uses_tc(a.c.hd)) return rows ? kSharedByRows : kSharedTooLarge;
   const bool once = qshare_fits(a.c, a.g, qt, B, S, a.ngroups, a.r.limit);
-  if (!rows || !once) return rows ? kSharedByRows : once ? kSharedOnce : kSharedTooLarge;
+  if (!rows || !once) return rows ? kSharedByRows : kSharedTooLarge;  // (what can be read once fits row by row: fewer tiles)
   const TcPlanQ p = plan_tc_q(a.c, a.g, qt, B, S, a.r.limit, num_sms);
   const int64_t tiles = (int64_t)B * (((int64_t)S + p.tokens - 1) / p.tokens) * a.c.kv * q_tiles_of(a.r.limit);
   return a.ngroups == B || tiles <= (int64_t)num_sms * kByTiles ? kSharedByRows : kSharedOnce;
@@ -424,8 +424,12 @@ cudaError_t launch_qattn(const QAttnArgs& a0, int qt, int num_sms, cudaStream_t 
   }
 }
 
-uint64_t qattn_shared_workspace(const QCacheView& c, int g, int B, int S, int num_sms) {
-  if (qattn_uses_tc(c.hd)) return std::max(qattn_workspace(c, g, B, S, num_sms), qshare_workspace(c, g, B, S, num_sms));
+uint64_t qattn_shared_workspace(const QCacheView& c, int g, int B, int S, int ngroups, int num_sms) {
+  if (qattn_uses_tc(c.hd)) {
+    // (more rows than can go any way but row by row need no more than the ordinary attention does)
+    const bool once = ngroups < B && (qshare_fits(c, g, 0, B, S, ngroups, 0) || qshare_fits(c, g, 1, B, S, ngroups, 0));
+    return std::max(qattn_workspace(c, g, B, S, num_sms), once ? qshare_workspace(c, g, B, S, num_sms) : 0);
+  }
   const int splits = simple_splits(c, (int64_t)B * S, c.rows * c.cap, num_sms);
   return splits == 1 ? 0 : kQattnTickets + (uint64_t)B * S * c.kv * g * splits * (c.hd + 2) * 4;
 }

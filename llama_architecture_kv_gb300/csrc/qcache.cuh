@@ -206,7 +206,7 @@ uint64_t qattn_step_workspace(const QCacheView& c, int g, int NT, int num_sms);
 cudaError_t launch_qattn(const QAttnArgs& a, int qt, int num_sms, cudaStream_t s, bool pdl,
                          const CUtensorMap* kmap = nullptr, const CUtensorMap* vmap = nullptr);
 // the same with groups of rows that share positions, read once for all rows of a group (heads of 64 and 128)
-uint64_t qattn_shared_workspace(const QCacheView& c, int g, int B, int S, int num_sms);
+uint64_t qattn_shared_workspace(const QCacheView& c, int g, int B, int S, int ngroups, int num_sms);
 // which way a call goes: row by row, or with the shared positions read once; or neither, its tiles being too many to count
 enum QSharedWay { kSharedTooLarge, kSharedByRows, kSharedOnce };
 QSharedWay qattn_shared_way(const QAttnArgs& a, int qt, int num_sms);

@@ -534,3 +534,11 @@ def test_uneven_groups_and_empty_ones(hd, g, S, dtype):
                            ([0] * 11 + [B] * (B - 10), [70] * 10 + [200] + [70] * (B - 11)),
                            ([0, 31] + list(range(32, B + 1)), [200] + [129] * (B - 31)), ([0, 0, 0, 3, 3, 3, 39, 39, 39, 40], [1, 2, 130, 3, 4, 200, 5, 6, 60])):
         check(c, r, rng, S, g, dtype, length, groups, shared)
+
+
+def test_workspaces_of_calls_that_go_row_by_row():
+    # as many groups as rows, or more rows than are counted: as much as the ordinary attention needs
+    c = pkg.QCache.empty(2, 8, 256, 128)
+    for g, B, S, G in ((4, 5000, 1, 7), (4, 64, 1, 64), (4, 600, 64, 1)):
+        assert c.workspace_shared(g, B, S, G).numel() == c.workspace(g, B, S).numel()
+    assert c.workspace_shared(4, 64, 1, 63).numel() > c.workspace(4, 64, 1).numel()
