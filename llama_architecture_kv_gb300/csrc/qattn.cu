@@ -373,8 +373,10 @@ uint64_t qattn_step_workspace(const QCacheView& c, int g, int NT, int num_sms) {
 
 // Rows that share positions are attended one by one (QAttnArgs::groups) where a call has more units than are counted, where
 // there are as many groups as rows, or where the rows can hold so few tiles of positions per SM that reading the shared ones
-// once, with the two to four kernels that it takes, saves nothing.  Row by row, and shared: 4 rows of about 1000 positions (2 tiles per SM) 16 and 18 us, 16 of 2176 (14) 25 and 39, 24 of
-// 5300 in 3 groups (26) 41 and 39, 16 with 5 tokens of 4400 (29) 60 and 70, 2 of 65536 (54) 47 and 43, 32 of 8400 (111) 88 and 54.
+// once, with the two to four kernels that it takes, saves nothing.  Row by row, and shared: 4 rows of about 1000 positions (2 tiles
+// per SM) 16 and 18 us, 16 of 2176 (14) 25 and 39, 24 of 5300 in 3 groups (26) 41 and 39, 16 with 5 tokens of 4400 (29) 60 and 70,
+// 2 of 65536 (54) 47 and 43, 32 of 8400 (111) 88 and 54.  (Rows that are groups of one, read once: 16 of 8192 59 and 64 us, 32 of
+// 16384 177 and 182.)
 constexpr int kByTiles = 32;
 static __global__ void q_clear_tickets_kernel(uint4* tickets) {
   grid_dep_launch();
